@@ -50,6 +50,7 @@ extern "C" {
 #define PE_REQ_CAPACITY    1    /* entries needed exceed max_pages * page_size */
 #define PE_REQ_BAD_PAGE    2    /* a needed page-table entry is outside [0, num_pages) */
 #define PE_REQ_BAD_INPUT   3    /* token id outside [0, V), negative length */
+#define PE_REQ_TIMEOUT     4    /* pe_attention_kv8: a device-side wait gave up; the request's output is zero */
 
 /* bits of the device error word (pe_device_errors) */
 #define PE_DEVERR_GEMM_TIMEOUT  1u
@@ -336,6 +337,102 @@ int pe_linear_fp8(int32_t M, int32_t N, int32_t Kd, const void* w, const float* 
  *    by the caller. Each call clears the tickets it uses on its stream. */
 int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const void* w, const void* x, float* y,
                       void* stream);
+
+/* Linear layer with 4-bit weights and group scales, for the few token rows of
+ * a draft pass (beside pe_linear_fp8):
+ *   y[n, m] = sum_k (c[m, k] - z[m, k / group]) * s[m, k / group] * x[n, k]
+ *  w       [M, Kd/2] uint8: code c (0..15) of column 2i in the low half of byte i, of 2i+1 in the high half
+ *  w_scale [M, ceil(Kd/group)] of scale_dtype (PE_DTYPE_BF16 or PE_DTYPE_FP32); w_zero the same shape, uint8
+ *          (0..255), or NULL: every zero point is 8
+ *  x       [N, Kd] bf16, rows ld_x elements apart; y [N, M] fp32 OUT, rows ld_y apart
+ * group is 32, 64 or 128 (the last group of a row may be short); Kd a
+ * multiple of 32; w and x 16-byte aligned, ld_x a multiple of 8. Products and
+ * sums in fp32; the weights are not rounded. The inputs are finite: a row of
+ * x that holds an infinity or NaN gives NaN in its row of y. No scratch; the
+ * device that holds the tensors must be current. Rows of x go 16 at a time, and
+ * each 16 read the weights again. */
+int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,
+                 const void* w_scale, const uint8_t* w_zero, const void* x, int64_t ld_x, float* y, int64_t ld_y,
+                 void* stream);
+
+/* Pages for a growing batch, on the device (no host round trip between a
+ * verify and the next pass): request b holds page_counts[b] pages, the first
+ * entries of its page_table row, and seq_lens[b] committed entries, and is to
+ * take new_lens[b] more. What is missing comes from the top of a stack of free
+ * pages (free_pages[0 .. free_count)), in request order.
+ *  seq_lens, new_lens, page_counts [B] int32; new_lens in 0..n_max
+ *  page_table   [B, max_pages] int32 in/out: entries page_counts[b] .. are written
+ *  free_pages   [free_cap] int32, free_count [1] int32
+ *  page_counts_out [B], free_count_out [1] OUT; must not alias their inputs
+ *  slot_mapping [B, n_max] int32 OUT: slot (page*16 + offset) of entries
+ *               S_b .. S_b+n_b-1, then -1
+ *  status       [B] OUT: PE_REQ_BAD_INPUT (a length out of range, or fewer
+ *               pages than seq_lens needs), PE_REQ_CAPACITY (max_pages, or the
+ *               stack runs out: this request and every later one that needs
+ *               pages get none), PE_REQ_BAD_PAGE (a page of the new entries is
+ *               outside [0, num_pages); the pages it took stay with it). The
+ *               slots of a request that is not OK are -1. */
+int pe_assign_pages(int32_t B, const int32_t* seq_lens, const int32_t* new_lens, const int32_t* page_counts,
+                    int32_t* page_counts_out, int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                    const int32_t* free_pages, int32_t free_cap, const int32_t* free_count, int32_t* free_count_out,
+                    int32_t n_max, int32_t* slot_mapping, int32_t* status, void* stream);
+
+/* The way back: request b keeps the pages of its first keep_lens[b] entries
+ * (0: it is finished) and pushes the others, in request and page order, onto
+ * the stack; their page_table entries become -1. page_counts_out and
+ * free_count_out may alias their inputs. status: PE_REQ_BAD_INPUT (keep_lens
+ * beyond the request's pages), PE_REQ_BAD_PAGE (one of the pages is outside
+ * [0, num_pages)), PE_REQ_CAPACITY (the stack is full: this request and every
+ * later one keep theirs); a request that is not OK keeps everything. */
+int pe_release_pages(int32_t B, const int32_t* keep_lens, const int32_t* page_counts, int32_t* page_counts_out,
+                     int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t* free_pages, int32_t free_cap,
+                     const int32_t* free_count, int32_t* free_count_out, int32_t* status, void* stream);
+
+/* A paged KV cache in 8 bits, half the bytes of the bf16 one:
+ *  k_codes, v_codes [num_pages][nkv][16][hd] uint8: E4M3 codes
+ *  k_scale, v_scale [num_pages][nkv] fp32: entry = code * scale of its page and head
+ * One layer's cache; the layers of a model are as many of them.
+ *
+ * pe_kv8_append stores rows[b] (NULL: n_max) new rows of request b at its
+ * entries S_b, S_b+1, ...:
+ *  k, v  [B, n_max, nkv, hd] bf16, rows ld_k / ld_v elements apart (columns of
+ *        a fused projection's output will do); rows past rows[b] are not read
+ *  status [B] OUT; a request that is not OK writes nothing.
+ * The scale of a page and head is the smallest power of two (2^-126 at least)
+ * under which the new rows' largest finite magnitude is at most 448; codes are
+ * the nearest (ties to even). A page with committed entries keeps its scale if
+ * that is larger; if not, their codes are moved to the new one. Infinities
+ * become +-448, a NaN the NaN code. Nothing else of the cache is touched;
+ * codes behind the last new row keep their bytes. Pages that two requests
+ * share must be full: two that append to one page race.
+ * k, v 8-byte aligned, ld_k and ld_v multiples of 4, codes 16-byte aligned. */
+int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void* k, int64_t ld_k, const void* v,
+                  int64_t ld_v, const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table,
+                  int32_t max_pages, int32_t num_pages, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
+                  float* v_scale, int32_t* status, void* stream);
+
+/* Attention of the K rows of each request over that cache: row j < rows[b]
+ * (NULL: K) of request b attends to entries 0 .. S_b + j (its own row is
+ * appended before), query head h over kv head h / (nq/nkv), softmax of
+ * scale * q.k in fp32.
+ *  q      [B, K, nq, hd] bf16, rows ld_q elements apart
+ *  out    [B, K, nq, hd] bf16 OUT, rows ld_out apart; rows past rows[b], and
+ *         all rows of a request that is not OK, are zero
+ *  ws     scratch of pe_attention_kv8_scratch floats, 16-byte aligned; needs no
+ *         initial value, and calls that can overlap need one each
+ *  status [B] OUT; a page-table entry of a needed page that is outside
+ *         [0, num_pages) is PE_REQ_BAD_PAGE
+ * K * (nq/nkv) <= 128, hd 64 or 128; q, out and codes 16-byte aligned, ld_q and
+ * ld_out multiples of 8; B * nkv * ceil(K*nq/nkv/16) * max_pages < 2^30.
+ * Entries that no row sees may hold anything. A NaN among the entries that
+ * only some rows of the pass see makes those rows NaN and no others. */
+int pe_attention_kv8_scratch(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             int32_t max_pages, int64_t* ws_floats);
+int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,
+                     int64_t ld_q, const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table,
+                     int32_t max_pages, int32_t num_pages, const uint8_t* k_codes, const uint8_t* v_codes,
+                     const float* k_scale, const float* v_scale, float scale, void* out, int64_t ld_out, float* ws,
+                     int64_t ws_floats, int32_t* status, void* stream);
 
 /* One whole step (pe_draft, then pe_verify_rebuild on its drafts) captured
  * once into a CUDA graph and replayed with a single launch. The arguments are

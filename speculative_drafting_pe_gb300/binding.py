@@ -14,7 +14,7 @@ import torch
 from . import build as _build
 
 PE_OK = 0
-PE_REQ_OK, PE_REQ_CAPACITY, PE_REQ_BAD_PAGE, PE_REQ_BAD_INPUT = 0, 1, 2, 3
+PE_REQ_OK, PE_REQ_CAPACITY, PE_REQ_BAD_PAGE, PE_REQ_BAD_INPUT, PE_REQ_TIMEOUT = 0, 1, 2, 3, 4
 PE_DTYPE_BF16, PE_DTYPE_FP32, PE_DTYPE_FP8W = 0, 1, 2
 PE_DEVERR_GEMM_TIMEOUT, PE_DEVERR_ATTN_TIMEOUT, PE_DEVERR_CHAIN_TIMEOUT = 1, 2, 4
 PE_DRAFT_PARALLEL, PE_DRAFT_SEQUENTIAL = 0, 1
@@ -27,6 +27,8 @@ EXPORTS = (
     "pe_linear_noalloc", "pe_test_stall_chain", "pe_draft_sequential", "pe_step_graph_create_ex",
     "pe_init_drafter_fp8", "pe_linear_fp8", "pe_draft_refeed", "pe_verify_rebuild_refeed",
     "pe_sample_drafts", "pe_verify_stochastic",
+    "pe_linear_w4", "pe_assign_pages", "pe_release_pages", "pe_kv8_append", "pe_attention_kv8_scratch",
+    "pe_attention_kv8",
 )
 KERNEL_KINDS = ("fc", "row_build", "rmsnorm", "qkv", "attention", "o_proj", "gate_up", "down", "lm_head", "argmax",
                 "layer_chain")
@@ -147,6 +149,17 @@ def load():
     lib.pe_step_graph_launch_count.restype = ctypes.c_int
     lib.pe_step_graph_destroy.argtypes = [_vp]
     lib.pe_step_graph_destroy.restype = None
+    _i64 = ctypes.c_int64
+    for name, args in (
+            ("pe_linear_w4", [_i32] * 4 + [_vp, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+            ("pe_assign_pages", [_i32] + [_vp] * 5 + [_i32] * 2 + [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp]),
+            ("pe_release_pages", [_i32] + [_vp] * 4 + [_i32] * 2 + [_vp, _i32] + [_vp] * 4),
+            ("pe_kv8_append", [_i32] * 4 + [_vp, _i64, _vp, _i64] + [_vp] * 3 + [_i32] * 2 + [_vp] * 6),
+            ("pe_attention_kv8_scratch", [_i32] * 6 + [ctypes.POINTER(_i64)]),
+            ("pe_attention_kv8", [_i32] * 5 + [_vp, _i64, _vp, _vp, _vp, _i32, _i32] + [_vp] * 4 +
+             [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ctypes.c_int
     _LIB = lib
     return lib
 
@@ -535,3 +548,206 @@ def verify_rebuild_refeed(drafts, target_tokens, page_table, num_pages, n_real, 
                                         _p(o["bonus"]), _p(o["emitted"]), _p(o["slot_mapping"]),
                                         _p(o["rollback_slots"]), _p(o["status"]), _stream_ptr(stream)))
     return o
+
+
+# ---------------------------------------------------------------- low-bit weights and cache
+#
+# The calls below run where their tensors live, on that device's current
+# stream unless `stream` is given; all tensors of a call are on one device.
+
+_INT, _BYTE, _FLOAT, _BF16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+
+
+def _ints(dev, shape, **tensors):
+    """int32 tensors of one shape, contiguous on `dev`."""
+    for name, t in tensors.items():
+        if t.dtype is not _INT or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {shape} on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _run(fn, dev, stream, *args):
+    """Call an entry point with `dev` current, on `stream` or the device's current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    index = dev.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != PE_OK:
+        raise PeError(rc, _LIB.pe_last_error().decode())
+
+
+def _row_stride(t, name):
+    """Elements between the rows of t [..., heads, hd] (or [N, Kd]): its last dimensions are dense, its leading
+    ones one run of rows."""
+    lead = t.dim() - (2 if t.dim() > 2 else 1)
+    sizes, strides = t.shape, t.stride()
+    dense = 1
+    for d in range(t.dim() - 1, lead - 1, -1):
+        if sizes[d] != 1 and strides[d] != dense:
+            raise ValueError(f"{name}: the last dimensions must be contiguous")
+        dense *= sizes[d]
+    step, rows = None, 1
+    for d in range(lead - 1, -1, -1):
+        if sizes[d] != 1:
+            if step is None:
+                step = strides[d]
+            elif strides[d] != step * rows:
+                raise ValueError(f"{name}: rows must be evenly spaced")
+        rows *= sizes[d]
+    return dense if step is None else step
+
+
+def linear_w4(w_codes, w_scale, x, group, zeros=None, y=None, stream=None):
+    """y = x @ W.T in fp32 with W[m, k] = (c[m, k] - z[m, k // group]) * s[m, k // group].
+
+    w_codes [M, Kd/2] uint8 (column 2i in the low half of byte i), w_scale
+    [M, ceil(Kd/group)] bf16 or fp32, zeros uint8 of the same shape (None: 8
+    everywhere), x [N, Kd] bf16 (rows may be strided), group 32, 64 or 128."""
+    lib = load()
+    dev = w_codes.device
+    M, half = w_codes.shape
+    N, Kd = x.shape
+    if w_codes.dtype is not _BYTE or not w_codes.is_contiguous() or Kd != 2 * half:
+        raise ValueError("w_codes must be contiguous uint8 [M, Kd/2]")
+    if x.dtype is not _BF16 or x.device != dev:
+        raise ValueError(f"x must be bfloat16 on {dev}")
+    shape = (M, -(-Kd // group) if group > 0 else 0)
+    kind = {_BF16: PE_DTYPE_BF16, _FLOAT: PE_DTYPE_FP32}.get(w_scale.dtype)
+    if kind is None or w_scale.device != dev or tuple(w_scale.shape) != shape or not w_scale.is_contiguous():
+        raise ValueError(f"w_scale must be contiguous bfloat16 or float32 {shape} on {dev}")
+    if zeros is not None and (zeros.dtype is not _BYTE or zeros.device != dev or tuple(zeros.shape) != shape or
+                              not zeros.is_contiguous()):
+        raise ValueError(f"zeros must be contiguous uint8 {shape} on {dev}")
+    if y is None:
+        y = torch.empty((N, M), dtype=_FLOAT, device=dev)
+    elif y.dtype is not _FLOAT or y.device != dev or tuple(y.shape) != (N, M):
+        raise ValueError(f"y must be float32 {(N, M)} on {dev}")
+    _run(lib.pe_linear_w4, dev, stream, M, N, Kd, group, w_codes.data_ptr(), kind, w_scale.data_ptr(),
+         None if zeros is None else zeros.data_ptr(), x.data_ptr(), _row_stride(x, "x"), y.data_ptr(),
+         _row_stride(y, "y"))
+    return y
+
+
+def assign_pages(seq_lens, new_lens, page_counts, page_table, free_pages, free_count, num_pages, n_max, stream=None):
+    """Take pages for new_lens [B] more entries per request from the stack free_pages[:free_count].
+
+    page_table [B, max_pages] is extended in place. Returns int32 tensors:
+    slot_mapping [B, n_max], page_counts [B], free_count [1], status [B]."""
+    lib = load()
+    dev = seq_lens.device
+    B = seq_lens.shape[0]
+    _ints(dev, (B,), seq_lens=seq_lens, new_lens=new_lens, page_counts=page_counts)
+    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
+    _ints(dev, (free_pages.numel(),), free_pages=free_pages)
+    _ints(dev, (1,), free_count=free_count)
+    o = dict(slot_mapping=torch.empty((B, n_max), dtype=_INT, device=dev),
+             page_counts=torch.empty(B, dtype=_INT, device=dev), free_count=torch.empty(1, dtype=_INT, device=dev),
+             status=torch.empty(B, dtype=_INT, device=dev))
+    _run(lib.pe_assign_pages, dev, stream, B, seq_lens.data_ptr(), new_lens.data_ptr(), page_counts.data_ptr(),
+         o["page_counts"].data_ptr(), page_table.data_ptr(), page_table.shape[1], num_pages, free_pages.data_ptr(),
+         free_pages.shape[0], free_count.data_ptr(), o["free_count"].data_ptr(), n_max, o["slot_mapping"].data_ptr(),
+         o["status"].data_ptr())
+    return o
+
+
+def release_pages(keep_lens, page_counts, page_table, free_pages, free_count, num_pages, stream=None):
+    """Give back the pages behind each request's first keep_lens [B] entries.
+
+    page_table, free_pages, page_counts and free_count are updated in place;
+    returns status [B]."""
+    lib = load()
+    dev = keep_lens.device
+    B = keep_lens.shape[0]
+    _ints(dev, (B,), keep_lens=keep_lens, page_counts=page_counts)
+    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
+    _ints(dev, (free_pages.numel(),), free_pages=free_pages)
+    _ints(dev, (1,), free_count=free_count)
+    status = torch.empty(B, dtype=_INT, device=dev)
+    _run(lib.pe_release_pages, dev, stream, B, keep_lens.data_ptr(), page_counts.data_ptr(), page_counts.data_ptr(),
+         page_table.data_ptr(), page_table.shape[1], num_pages, free_pages.data_ptr(), free_pages.shape[0],
+         free_count.data_ptr(), free_count.data_ptr(), status.data_ptr())
+    return status
+
+
+def _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale):
+    """The paged 8-bit cache of a call; returns its number of pages."""
+    _ints(dev, (B,), seq_lens=seq_lens)
+    if rows is not None:
+        _ints(dev, (B,), rows=rows)
+    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
+    pages = k_codes.shape[0]
+    for name, t, dtype, shape in (("k_codes", k_codes, _BYTE, (pages, nkv, 16, hd)),
+                                  ("v_codes", v_codes, _BYTE, (pages, nkv, 16, hd)),
+                                  ("k_scale", k_scale, _FLOAT, (pages, nkv)),
+                                  ("v_scale", v_scale, _FLOAT, (pages, nkv))):
+        if t.dtype is not dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {dev}")
+    return pages
+
+
+def kv8_append(k, v, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, rows=None, status=None, stream=None):
+    """Store new rows k, v [B, n, nkv, hd] bf16 in the 8-bit paged cache at entries seq_lens[b] ...
+
+    Rows may be strided (columns of a fused projection). rows [B] int32: new
+    rows of each request (None: n). Codes uint8 [pages, nkv, 16, hd], scales
+    fp32 [pages, nkv], updated in place. Returns status [B]."""
+    lib = load()
+    dev = k.device
+    B, n, nkv, hd = k.shape
+    if k.dtype is not _BF16 or v.dtype is not _BF16 or v.device != dev or v.shape != k.shape:
+        raise ValueError(f"k and v must be bfloat16 [B, n, nkv, hd] on {dev}")
+    pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
+    if status is None:
+        status = torch.empty(B, dtype=_INT, device=dev)
+    else:
+        _ints(dev, (B,), status=status)
+    _run(lib.pe_kv8_append, dev, stream, B, n, nkv, hd, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
+         _row_stride(v, "v"), seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(),
+         page_table.shape[1], pages, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+         status.data_ptr())
+    return status
+
+
+def _kv8_scratch(B, K, nq, nkv, hd, max_pages):
+    n = ctypes.c_int64(0)
+    _check(load().pe_attention_kv8_scratch(B, K, nq, nkv, hd, max_pages, ctypes.byref(n)))
+    return n.value
+
+
+def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, scale=None, rows=None, out=None,
+                  status=None, stream=None):
+    """Attention of q [B, K, nq, hd] bf16 over the 8-bit paged cache: row j of request b sees entries
+    0 .. seq_lens[b] + j (append its own row first). Returns (out like q, status [B]).
+
+    scale: softmax scale (None: hd ** -0.5). rows [B] int32: live rows of each
+    request (None: K); the others are zero."""
+    lib = load()
+    dev = q.device
+    B, K, nq, hd = q.shape
+    if q.dtype is not _BF16:
+        raise ValueError("q must be bfloat16 [B, K, nq, hd]")
+    nkv = k_codes.shape[1] if k_codes.dim() == 4 else 0
+    pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
+    if out is None:
+        out = torch.empty((B, K, nq, hd), dtype=_BF16, device=dev)
+    elif out.dtype is not _BF16 or out.device != dev or out.shape != q.shape:
+        raise ValueError(f"out must be bfloat16 {tuple(q.shape)} on {dev}")
+    if status is None:
+        status = torch.empty(B, dtype=_INT, device=dev)
+    else:
+        _ints(dev, (B,), status=status)
+    max_pages = page_table.shape[1]
+    with torch.cuda.device(dev):
+        need = _kv8_scratch(B, K, nq, nkv, hd, max_pages)
+    ws = torch.empty(need, dtype=_FLOAT, device=dev)
+    _run(lib.pe_attention_kv8, dev, stream, B, K, nq, nkv, hd, q.data_ptr(), _row_stride(q, "q"),
+         seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(), max_pages, pages,
+         k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+         hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out, "out"), ws.data_ptr(), need,
+         status.data_ptr())
+    return out, status

@@ -1,0 +1,227 @@
+// The write side of the 8-bit paged KV cache (pe_kv8_append): new key and
+// value rows become E4M3 codes with one scale for each (page, kv head).
+//
+// For the 16 entries of a page and one head, with x the new rows' values,
+//   s = 2^ceil(log2(max|x| / 448)),   code = rn_e4m3(x / s),
+// the smallest power of two under which nothing saturates. A power of two
+// makes x / s exact, so a code is one rounding away from its value, and moving
+// a stored code to a larger scale loses nothing but what falls below E4M3's
+// smallest step: a page that fills up over many calls is not rounded anew each
+// time. A page with committed entries keeps max(s_old, s), and where that is
+// larger than s_old its committed codes move along.
+//
+// One warp owns one (request, page, head, K or V): it reads the page's new
+// rows once (8 bytes a lane), keeps them in registers, takes the maximum by
+// shuffles and stores the codes (4 bytes a lane), so no two warps write one
+// page and nothing is read twice. Bound by DRAM for prompts, by latency for
+// the rows of a draft pass.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pe {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kWarps = 4;
+
+struct AppendParams {
+    int B, n_max, nkv, P, max_pages, num_pages;   // P: pages that n_max new rows can touch
+    const __nv_bfloat16* x[2];                    // k, v
+    long long ld[2];
+    const int32_t* seq_lens;
+    const int32_t* rows;
+    const int32_t* page_table;
+    uint8_t* codes[2];
+    float* scale[2];
+    int32_t* status;
+};
+
+// the exponent of the smallest power of two s >= 2^-126 with amax <= 448 s
+__device__ __forceinline__ float scale_for(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    // amax = 2^(E-127) * 1.m; 448 = 1.75 * 2^8
+    int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    e = max(e, 1);
+    return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"(static_cast<uint16_t>(w)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(static_cast<uint16_t>(w >> 16)));
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    v[0] = f0.x;
+    v[1] = f0.y;
+    v[2] = f1.x;
+    v[3] = f1.y;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const AppendParams p) {
+    constexpr int kLanes = HD / 4;          // lanes that hold one row, four values each
+    constexpr int kPer = 32 / kLanes;       // rows that one load of the warp covers
+    constexpr int kSteps = kPage / kPer;
+    const int lane = threadIdx.x & 31;
+    long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (unit >= 2ll * p.B * p.P * p.nkv) return;
+    const int kv = static_cast<int>(unit & 1);
+    unit >>= 1;
+    const int head = static_cast<int>(unit % p.nkv);
+    unit /= p.nkv;
+    const int pi = static_cast<int>(unit % p.P);
+    const int b = static_cast<int>(unit / p.P);
+
+    const int S = p.seq_lens[b];
+    const int n = p.rows != nullptr ? p.rows[b] : p.n_max;
+    const int32_t* row = p.page_table + static_cast<size_t>(b) * p.max_pages;
+    int st = PE_REQ_OK;
+    int p0 = 0, p1 = 0;
+    if (S < 0 || n < 0 || n > p.n_max) st = PE_REQ_BAD_INPUT;
+    else if (static_cast<long long>(S) + n > static_cast<long long>(p.max_pages) * kPage) st = PE_REQ_CAPACITY;
+    else if (n > 0) {
+        p0 = S / kPage;
+        p1 = (S + n + kPage - 1) / kPage;
+        int bad = 0;
+        for (int i = p0 + lane; i < p1; i += 32) bad |= row[i] < 0 || row[i] >= p.num_pages;
+        if (__any_sync(0xffffffffu, bad)) st = PE_REQ_BAD_PAGE;
+    }
+    if (pi == 0 && head == 0 && kv == 0 && lane == 0) p.status[b] = st;
+    if (st != PE_REQ_OK || p0 + pi >= p1) return;
+
+    const int page = row[p0 + pi];
+    const int first = (p0 + pi) * kPage - S;      // the new row at the page's entry 0 (negative: committed)
+    const int sub = lane / kLanes, d = (lane % kLanes) * 4;
+    const long long ld = kv == 0 ? p.ld[0] : p.ld[1];
+    const __nv_bfloat16* x = (kv == 0 ? p.x[0] : p.x[1]) + static_cast<long long>(b) * p.n_max * ld + head * HD + d;
+    uint2 v[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int r = first + i * kPer + sub;
+        v[i] = make_uint2(0u, 0u);
+        if (r >= 0 && r < n) v[i] = *reinterpret_cast<const uint2*>(x + r * ld);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const uint32_t w[2] = {v[i].x, v[i].y};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // |x| of bf16 pairs; a value that is not finite has no say in the scale
+            const float lo = __uint_as_float((w[h] << 16) & 0x7FFF0000u), hi = __uint_as_float(w[h] & 0x7FFF0000u);
+            if (lo < INFINITY) amax = fmaxf(amax, lo);
+            if (hi < INFINITY) amax = fmaxf(amax, hi);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    float s = scale_for(amax);
+    const size_t tile = static_cast<size_t>(page) * p.nkv + head;
+    uint8_t* dst = (kv == 0 ? p.codes[0] : p.codes[1]) + tile * kPage * HD + d;
+    float* scale = kv == 0 ? p.scale[0] : p.scale[1];
+    if (first < 0) {
+        const float had = scale[tile];
+        if (had < s) {
+            const float f = had / s;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int e = i * kPer + sub;
+                if (first + e < 0) {
+                    float q[4];
+                    uint32_t* at = reinterpret_cast<uint32_t*>(dst + e * HD);
+                    decode4(*at, q);
+                    *at = e4m3x4(q[0] * f, q[1] * f, q[2] * f, q[3] * f);
+                }
+            }
+        } else {
+            s = had;
+        }
+        __syncwarp();   // every lane has read the old scale
+    }
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int e = i * kPer + sub, r = first + e;
+        if (r >= 0 && r < n) {
+            const float a0 = __uint_as_float(v[i].x << 16), a1 = __uint_as_float(v[i].x & 0xFFFF0000u);
+            const float a2 = __uint_as_float(v[i].y << 16), a3 = __uint_as_float(v[i].y & 0xFFFF0000u);
+            *reinterpret_cast<uint32_t*>(dst + e * HD) = e4m3x4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+        }
+    }
+    if (lane == 0) scale[tile] = s;
+}
+
+}  // namespace
+
+int launch_kv8_append(int B, int n_max, int nkv, int hd, const void* k, const void* v, int64_t ld_k, int64_t ld_v,
+                      const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table, int max_pages,
+                      int num_pages, uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale,
+                      int32_t* status, cudaStream_t s, bool pdl) {
+    AppendParams p{};
+    p.B = B;
+    p.n_max = n_max;
+    p.nkv = nkv;
+    p.P = (n_max + kPage - 2) / kPage + 1;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.x[0] = static_cast<const __nv_bfloat16*>(k);
+    p.x[1] = static_cast<const __nv_bfloat16*>(v);
+    p.ld[0] = ld_k;
+    p.ld[1] = ld_v;
+    p.seq_lens = seq_lens;
+    p.rows = rows;
+    p.page_table = page_table;
+    p.codes[0] = k_codes;
+    p.codes[1] = v_codes;
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.status = status;
+    const long long units = 2ll * B * p.P * nkv;
+    const long long blocks = (units + kWarps - 1) / kWarps;
+    if (blocks > 0x7FFFFFFFll) { set_error("pe_kv8_append: too many rows for one call"); return PE_ERR_ARG; }
+    auto kern = hd == 128 ? k_kv8_append<128> : k_kv8_append<64>;
+    PE_CUDA_TRY(launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, s, pdl, p));
+    return PE_OK;
+}
+
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void* k, int64_t ld_k,
+                             const void* v, int64_t ld_v, const int32_t* seq_lens, const int32_t* rows,
+                             const int32_t* page_table, int32_t max_pages, int32_t num_pages, uint8_t* k_codes,
+                             uint8_t* v_codes, float* k_scale, float* v_scale, int32_t* status, void* stream) {
+    if (B < 1 || n_max < 1 || nkv < 1) { set_error("B, n_max and nkv must be >= 1"); return PE_ERR_ARG; }
+    if (hd != 64 && hd != 128) { set_error("head_dim must be 64 or 128"); return PE_ERR_UNSUPPORTED; }
+    if (max_pages < 1 || num_pages < 1) { set_error("max_pages and num_pages must be >= 1"); return PE_ERR_ARG; }
+    if (max_pages > 0x7FFFFFFF / kPage - 2 || n_max > 0x7FFFFFFF / kPage) {
+        set_error("max_pages * 16 and n_max must fit a signed 32-bit entry index");
+        return PE_ERR_ARG;
+    }
+    if (!k || !v || !seq_lens || !page_table || !k_codes || !v_codes || !k_scale || !v_scale || !status) {
+        set_error("null tensor argument");
+        return PE_ERR_ARG;
+    }
+    if (ld_k < static_cast<int64_t>(nkv) * hd || ld_v < static_cast<int64_t>(nkv) * hd || ld_k % 4 != 0 ||
+        ld_v % 4 != 0) {
+        set_error("row strides must be multiples of 4 and at least nkv * head_dim");
+        return PE_ERR_ARG;
+    }
+    if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 7u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(k_codes) | reinterpret_cast<uintptr_t>(v_codes)) & 15u) != 0) {
+        set_error("k and v must be 8-byte aligned, the code arrays 16-byte aligned");
+        return PE_ERR_ARG;
+    }
+    return launch_kv8_append(B, n_max, nkv, hd, k, v, ld_k, ld_v, seq_lens, rows, page_table, max_pages, num_pages,
+                             k_codes, v_codes, k_scale, v_scale, status, static_cast<cudaStream_t>(stream), false);
+}

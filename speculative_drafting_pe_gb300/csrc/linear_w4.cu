@@ -1,0 +1,376 @@
+// y = x W^T for few token rows and 4-bit weights (pe_linear_w4): codes two to
+// a byte, a scale and optionally a zero point for each group of 32, 64 or 128
+// columns.
+//
+//   y[n, m] = sum_g s[m, g] * (sum_{k in g} c[m, k] x[n, k]  -  z[m, g] * sum_{k in g} x[n, k])
+//
+// The inner sum runs on the tensor cores over the bare codes 0..15; the zero
+// point comes off the group's sum of x, once per group, in fp32, where the
+// scale is applied too, so no weight is ever rounded.
+//
+// Bound by the weight bytes, so a code has to cost few instructions. As the
+// low four bits of an fp16 a nibble IS the number c * 2^-24 (a subnormal,
+// exact in the MMA), as the next four bits c * 2^-20: one AND widens two
+// codes, four ANDs and one shift a word of eight. The factor 16 goes into x,
+// which is laid out once per CTA in shared memory as fp16, shifted by a power
+// of two per row so that its largest value lies in [2^14, 2^15) (bf16 values
+// down to 2^-28 of it stay exact), in the order in which the ANDs deliver the
+// codes.
+//
+// A warp owns 16 weight rows (the MMA's M; the token rows are N) and walks
+// their columns 256 at a time through a ring that its lane 0 fills by TMA
+// (128-byte rows, swizzled: the word reads are free of bank conflicts), so
+// the warps never wait for each other while they stream. Where there are few
+// rows, `ks` warps of a CTA share one set of 16, block by block, and their
+// sums are added in order at the end.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pe {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;
+constexpr int kRows = 16;                    // weight rows of a warp
+constexpr int kCols = 256;                   // columns of a stage
+constexpr int kStageBytes = kRows * kCols / 2;
+
+struct W4Params {
+    int M, N, Kd;
+    int ng;            // groups of a weight row
+    int ks;            // warps that share 16 rows (1, 2, 4, 8)
+    int nb;            // 256-column blocks
+    int cb;            // blocks of x in shared memory at a time (a multiple of ks)
+    const void* scale;
+    const uint8_t* zero;
+    const __nv_bfloat16* x;
+    long long ld_x;
+    float* y;
+    long long ld_y;
+};
+
+__device__ __forceinline__ float load_scale(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load_scale(const float* p) { return *p; }
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int GROUP, int NT>
+struct W4Smem {
+    static constexpr int kN = NT * 8;
+    // x row pitch: consecutive rows half the banks apart
+    __host__ __device__ static constexpr int pitch(int cb) { return cb * kCols * 2 + 64; }
+    static constexpr int kX = kWarps * kStages * kStageBytes;
+    __host__ __device__ static constexpr int sums(int cb) { return kX + kN * pitch(cb); }
+    __host__ __device__ static constexpr int up(int cb) { return sums(cb) + cb * (kCols / GROUP) * kN * 4; }
+    __host__ __device__ static constexpr int red(int cb) { return up(cb) + kN * 4; }
+    __host__ __device__ static constexpr int bars(int cb) { return red(cb) + kWarps * kRows * kN * 4; }
+    __host__ __device__ static constexpr int bytes(int cb) { return bars(cb) + kWarps * kStages * 8 + 1024; }
+};
+
+// Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
+// order, the groups' sums * 2^-10, and the factor that undoes the row's shift.
+template <int GROUP, int NT>
+__device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
+    using L = W4Smem<GROUP, NT>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* s_sum = reinterpret_cast<float*>(sm + L::sums(p.cb));
+    float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb));
+    const int blocks = min(p.cb, p.nb - b0);
+    for (int r = warp; r < L::kN; r += kWarps) {
+        const int n = n0 + r;
+        const __nv_bfloat16* src = p.x + static_cast<long long>(n) * p.ld_x;
+        auto get = [&](int blk) {
+            const int k = (b0 + blk) * kCols + lane * 8;
+            return n < p.N && k < p.Kd ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint32_t top = 0;
+        for (int blk = 0; blk < blocks; ++blk) {
+            const uint4 v = get(blk);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int E = min(max(static_cast<int>(top >> 23), 14), 254);
+        const float down = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);   // 2^(141 - E)
+        if (lane == 0) s_up[r] = __uint_as_float(static_cast<uint32_t>(E) << 23);     // 2^(E - 127)
+        uint8_t* dst = sm + L::kX + r * L::pitch(p.cb);
+        for (int blk = 0; blk < blocks; ++blk) {
+            const uint4 v = get(blk);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float f[8], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum += f[i];
+                f[i] *= (i & 1) ? down * 0.0625f : down;
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 h = __floats2half2_rn(f[i], f[i + 4]);
+                o[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(dst + (blk * kCols + lane * 8) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+            for (int d = 1; d < GROUP / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane % (GROUP / 8) == 0)
+                s_sum[(blk * (kCols / GROUP) + lane / (GROUP / 8)) * L::kN + r] = sum * 0.0009765625f;
+        }
+    }
+}
+
+template <int GROUP, int NT, typename S>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_w4(const __grid_constant__ CUtensorMap tmW, const W4Params p) {
+    using L = W4Smem<GROUP, NT>;
+    constexpr int kGroups = kCols / GROUP;   // groups of a block
+    constexpr int kSub = GROUP / 32;         // 32-column steps of a group
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int ks = p.ks, wk = warp % ks, wt = warp / ks, per = kWarps / ks;
+    const int n0 = blockIdx.y * L::kN;
+    uint8_t* ring = sm + warp * kStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bars(p.cb)) + warp * kStages;
+    const float* s_sum = reinterpret_cast<const float*>(sm + L::sums(p.cb));
+    const float* s_up = reinterpret_cast<const float*>(sm + L::up(p.cb));
+    float* s_red = reinterpret_cast<float*>(sm + L::red(p.cb));
+    const int tiles = (p.M + kRows - 1) / kRows;
+    const int iters = (tiles + per - 1) / per;
+
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+    __syncwarp();
+
+    // this warp's blocks in order: (row tile, wk), (row tile, wk + ks), ...,
+    // then the next row tile; the ring runs ahead of the sums
+    const uint64_t policy = l2_policy_evict_first();
+    int f_it = blockIdx.x, f_kb = wk, f_st = 0;
+    auto fetch = [&]() {   // lane 0: the next block of the list into the next stage
+        while (f_it < iters && (f_kb >= p.nb || f_it * per + wt >= tiles)) {
+            f_it += gridDim.x;
+            f_kb = wk;
+        }
+        if (f_it >= iters) return;
+        mbar_arrive_expect_tx(&full[f_st], kStageBytes);
+        tma_load_2d(ring + f_st * kStageBytes, &tmW, &full[f_st], f_kb * (kCols / 2), (f_it * per + wt) * kRows, policy);
+        f_kb += ks;
+        f_st = f_st + 1 == kStages ? 0 : f_st + 1;
+    };
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) fetch();
+
+    int st = 0;
+    uint32_t parity = 0;
+    bool dead = false;
+    const int chunks = (p.nb + p.cb - 1) / p.cb;
+    for (int it = blockIdx.x; it < iters; it += gridDim.x) {
+        const int tile = it * per + wt;
+        const bool mine = tile < tiles;
+        const int m[2] = {tile * kRows + g, tile * kRows + g + 8};
+        float acc[NT][4];
+#pragma unroll
+        for (int a = 0; a < NT; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+            if (chunks > 1 || it == static_cast<int>(blockIdx.x)) {
+                __syncthreads();
+                load_x<GROUP, NT>(p, sm, c * p.cb, n0);
+                __syncthreads();
+            }
+            if (!mine || dead) continue;
+            float up[NT][2];
+#pragma unroll
+            for (int a = 0; a < NT; ++a) {
+                up[a][0] = s_up[a * 8 + 2 * t];
+                up[a][1] = s_up[a * 8 + 2 * t + 1];
+            }
+            const int end = min(p.nb, (c + 1) * p.cb);
+            for (int kb = c * p.cb + wk; kb < end; kb += ks) {
+                // the block's scales and zero points; groups past the row's end count nothing
+                float sc[2][kGroups], zp[2][kGroups];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < kGroups; ++q) {
+                        const int gi = kb * kGroups + q;
+                        const bool in = gi < p.ng && m[h] < p.M;
+                        const size_t at = static_cast<size_t>(m[h]) * p.ng + gi;
+                        sc[h][q] = in ? load_scale(static_cast<const S*>(p.scale) + at) * 1024.f : 0.f;
+                        zp[h][q] = in && p.zero != nullptr ? static_cast<float>(p.zero[at]) : 8.f;
+                    }
+                const bool ok = mbar_wait(&full[st], (parity >> st) & 1u, nullptr, 0u);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    dead = true;
+                    break;
+                }
+                parity ^= 1u << st;
+                const uint8_t* wr = ring + st * kStageBytes + g * 128 + t * 4;
+                const uint8_t* xr = sm + L::kX + g * L::pitch(p.cb) + ((kb - c * p.cb) * kCols + t * 8) * 2;
+                const int g0 = (kb - c * p.cb) * kGroups;
+#pragma unroll
+                for (int q = 0; q < kGroups; ++q) {
+                    float part[NT][4];
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) part[a][0] = part[a][1] = part[a][2] = part[a][3] = 0.f;
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+                        const int i = q * kSub + u;
+                        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wr + ((i ^ g) << 4));
+                        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wr + 8 * 128 + ((i ^ g) << 4));
+                        const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+                        const uint32_t lo[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u};
+                        const uint32_t hi[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
+#pragma unroll
+                        for (int a = 0; a < NT; ++a) {
+                            const uint4 xv = *reinterpret_cast<const uint4*>(xr + a * 8 * L::pitch(p.cb) + i * 64);
+                            mma_f16(part[a], lo, xv.x, xv.y);
+                            mma_f16(part[a], hi, xv.z, xv.w);
+                        }
+                    }
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        const float2 xs = *reinterpret_cast<const float2*>(&s_sum[(g0 + q) * L::kN + a * 8 + 2 * t]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            acc[a][2 * h] += sc[h][q] * (part[a][2 * h] * up[a][0] - zp[h][q] * xs.x);
+                            acc[a][2 * h + 1] += sc[h][q] * (part[a][2 * h + 1] * up[a][1] - zp[h][q] * xs.y);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) fetch();
+                st = st + 1 == kStages ? 0 : st + 1;
+            }
+        }
+        if (dead)
+#pragma unroll
+            for (int a = 0; a < NT; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = NAN;   // never a wrong number
+        if (ks > 1) {
+            __syncthreads();   // the last tile's sums have been read
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+                *reinterpret_cast<float4*>(s_red + ((warp * NT + a) * 32 + lane) * 4) =
+                    make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+            __syncthreads();
+            if (wk == 0) {
+                for (int w = 1; w < ks; ++w)
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        const float4 v = *reinterpret_cast<const float4*>(s_red + (((warp + w) * NT + a) * 32 + lane) * 4);
+                        acc[a][0] += v.x;
+                        acc[a][1] += v.y;
+                        acc[a][2] += v.z;
+                        acc[a][3] += v.w;
+                    }
+            }
+        }
+        if (wk == 0 && mine) {
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = n0 + a * 8 + 2 * t + (j & 1), mm = m[j >> 1];
+                    if (n < p.N && mm < p.M) p.y[static_cast<long long>(n) * p.ld_y + mm] = acc[a][j];
+                }
+        }
+    }
+    if (dead) __nanosleep(100000);   // a wait gave up: let copies still in flight land
+}
+
+constexpr int kXBytes = 100 * 1024;   // shared memory for x at most
+
+template <int GROUP, int NT, typename S>
+int launch(const CUtensorMap& tm, W4Params p, int sms, cudaStream_t s) {
+    using L = W4Smem<GROUP, NT>;
+    const int tiles = (p.M + kRows - 1) / kRows;
+    p.nb = (p.Kd + kCols - 1) / kCols;
+    // warps to a row tile: enough that every SM has its eight, as far as there
+    // are blocks to share
+    p.ks = 1;
+    while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps)
+        p.ks *= 2;
+    int fit = kXBytes / (L::kN * (kCols * 2 + kCols / GROUP * 4));
+    fit = fit / kWarps * kWarps;
+    p.cb = p.nb <= fit ? (p.nb + p.ks - 1) / p.ks * p.ks : fit;
+    const int iters = (tiles * p.ks + kWarps - 1) / kWarps;
+    auto kern = k_linear_w4<GROUP, NT, S>;
+    const int smem = L::bytes(p.cb);
+    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const int per_sm = smem <= 110 * 1024 ? 2 : 1;
+    const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
+    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, tm, p));
+    return PE_OK;
+}
+
+template <int GROUP, typename S>
+int launch_nt(const CUtensorMap& tm, const W4Params& p, int sms, cudaStream_t s) {
+    return p.N <= 8 ? launch<GROUP, 1, S>(tm, p, sms, s) : launch<GROUP, 2, S>(tm, p, sms, s);
+}
+
+template <typename S>
+int launch_group(int group, const CUtensorMap& tm, const W4Params& p, int sms, cudaStream_t s) {
+    if (group == 32) return launch_nt<32, S>(tm, p, sms, s);
+    if (group == 64) return launch_nt<64, S>(tm, p, sms, s);
+    return launch_nt<128, S>(tm, p, sms, s);
+}
+
+}  // namespace
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,
+                            const void* w_scale, const uint8_t* w_zero, const void* x, int64_t ld_x, float* y,
+                            int64_t ld_y, void* stream) {
+    if (!w || !w_scale || !x || !y) { set_error("null tensor argument"); return PE_ERR_ARG; }
+    if (M < 1 || N < 1 || Kd < 32 || Kd % 32 != 0) {
+        set_error("need M, N >= 1 and Kd a positive multiple of 32");
+        return PE_ERR_ARG;
+    }
+    if (group != 32 && group != 64 && group != 128) { set_error("group must be 32, 64 or 128"); return PE_ERR_UNSUPPORTED; }
+    if (scale_dtype != PE_DTYPE_BF16 && scale_dtype != PE_DTYPE_FP32) { set_error("scales are bf16 or fp32"); return PE_ERR_ARG; }
+    if (ld_x < Kd || ld_x % 8 != 0 || ld_y < M) {
+        set_error("ld_x must be a multiple of 8 and at least Kd, ld_y at least M");
+        return PE_ERR_ARG;
+    }
+    if (((reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(x)) & 15u) != 0) {
+        set_error("w and x must be 16-byte aligned");
+        return PE_ERR_ARG;
+    }
+    if (M > 0x7FFFFFFF - 256 || N > 16 * 65535) { set_error("M or N too large"); return PE_ERR_ARG; }
+    int dev = 0, sms = 0;
+    PE_CUDA_TRY(cudaGetDevice(&dev));
+    PE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    CUtensorMap tm;
+    int rc = encode_tmap_2d_u8(&tm, w, static_cast<uint64_t>(Kd) / 2, static_cast<uint64_t>(M), kRows);
+    if (rc != PE_OK) return rc;
+    W4Params p{};
+    p.M = M;
+    p.N = N;
+    p.Kd = Kd;
+    p.ng = (Kd + group - 1) / group;
+    p.scale = w_scale;
+    p.zero = w_zero;
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.ld_x = ld_x;
+    p.y = y;
+    p.ld_y = ld_y;
+    return scale_dtype == PE_DTYPE_BF16 ? launch_group<__nv_bfloat16>(group, tm, p, sms, static_cast<cudaStream_t>(stream))
+                                        : launch_group<float>(group, tm, p, sms, static_cast<cudaStream_t>(stream));
+}
