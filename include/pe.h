@@ -347,8 +347,8 @@ int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const voi
  *  x       [N, Kd] bf16, rows ld_x elements apart; y [N, M] fp32 OUT, rows ld_y apart
  * group is 32, 64 or 128 (the last group of a row may be short); Kd a
  * multiple of 32; w and x 16-byte aligned, ld_x a multiple of 8. Products and
- * sums in fp32; the weights are not rounded. The inputs are finite: a row of
- * x that holds an infinity or NaN gives NaN in its row of y. No scratch; the
+ * sums in fp32; the weights are not rounded. A row of x that holds an infinity
+ * or NaN gives infinities or NaN in its row of y, and in no other. No scratch; the
  * device that holds the tensors must be current. Rows of x go 16 at a time, and
  * each 16 read the weights again. */
 int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,

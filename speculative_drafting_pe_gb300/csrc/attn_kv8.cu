@@ -25,82 +25,21 @@
 // byte permutes. Queries enter as fp16 after an exact shift by a power of two
 // per row, scores and sums are fp32, weights go to fp16 (2^-11) relative to
 // the row's running maximum and the largest V scale seen.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "internal.h"
+#include "attn_kv8.cuh"
 
 namespace pe {
 namespace {
 
-constexpr int kPage = 16;
+using namespace kv8;
+
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 4;         // units in flight per warp
 constexpr int kTileRows = 16;      // query rows of a unit (the MMA's M)
 constexpr int kMaxUnits = 1024;    // units of one CTA
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
-constexpr float kRescale = 8.f;    // running maximum (log2) moves only by more than this
 constexpr float kLog2e = 1.4426950408889634f;
-// marks in the place of a row's sum: the request's outputs are zero
-constexpr float kMarkBadPage = -1.f, kMarkTimeout = -2.f;
 
-struct Kv8Params {
-    int B, K, nq, nkv, max_pages, num_pages;
-    const __nv_bfloat16* q;
-    long long ld_q;
-    const int32_t* seq_lens;
-    const int32_t* rows;
-    const int32_t* page_table;
-    const float* k_scale;
-    const float* v_scale;
-    float scale_log2;
-    __nv_bfloat16* out;
-    long long ld_out;
-    int32_t* status;
-    int32_t* first;    // [B + 1] OUT: first unit of each request, [B + 1]: units of a CTA
-    float* part;       // [2 * grid] partial tiles (kv8_part_floats each)
-};
-
-__host__ __device__ constexpr int kv8_part_floats(int hd) { return kTileRows * hd + 2 * kTileRows; }
-
-// What request b asks for: its live rows, or a status.
-struct Req {
-    int st, S, rows, pages, tiles, units;
-};
-__device__ __forceinline__ Req request_of(const Kv8Params& p, int b) {
-    Req r{PE_REQ_OK, p.seq_lens[b], p.rows != nullptr ? p.rows[b] : p.K, 0, 0, 0};
-    if (r.S < 0 || r.rows < 0 || r.rows > p.K) r.st = PE_REQ_BAD_INPUT;
-    else if (static_cast<long long>(r.S) + r.rows > static_cast<long long>(p.max_pages) * kPage)
-        r.st = PE_REQ_CAPACITY;
-    if (r.st != PE_REQ_OK) r.rows = 0;
-    if (r.rows > 0) {
-        r.pages = (r.S + r.rows + kPage - 1) / kPage;
-        r.tiles = (r.rows * (p.nq / p.nkv) + kTileRows - 1) / kTileRows;
-        r.units = r.pages * r.tiles * p.nkv;
-    }
-    return r;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -109,14 +48,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 }
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
-// bytes of w that are E4M3's NaN become 0; `any` collects whether there were some
-__device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
-    const uint32_t other = ((w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu;   // bit 7 of a byte: not NaN
-    const uint32_t nan = ~other & 0x80808080u;
-    any |= nan != 0;
-    return w & ~((nan >> 7) * 0xFFu);
-}
-
 template <int HD>
 struct Smem {
     static constexpr int kTile = kPage * HD;                 // a page's K or V of one head
@@ -128,99 +59,6 @@ struct Smem {
     static constexpr int kUnit = kInfo + kMaxUnits * 16;     // tile, ks, vs
     static constexpr int kBytes = kUnit + kMaxUnits * 12 + 1024;
 };
-
-// The rows that no unit covers: rows past a request's own, and requests that
-// have none or are refused. A warp per (request, row).
-__device__ __forceinline__ void zero_idle_rows(const Kv8Params& p, int hd) {
-    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    for (int i = warp; i < p.B * p.K; i += gridDim.x * kWarps) {
-        const int b = i / p.K, j = i - b * p.K;
-        const Req r = request_of(p, b);
-        if (j == 0 && lane == 0 && r.units == 0) p.status[b] = r.st;
-        if (j < r.rows) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(i) * p.ld_out);
-        for (int c = lane; c < p.nq * hd / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
-    }
-}
-
-// This CTA's share of the line of units, and the units' pages in shared
-// memory: s_info of a unit that begins a segment (a run of one head and row
-// tile) = {request, head * tiles + row tile, first page, pages}.
-template <int HD>
-__device__ int gather_units(const Kv8Params& p, uint8_t* sm, long long& lo) {
-    __shared__ int s_scan[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int4* s_info = reinterpret_cast<int4*>(sm + Smem<HD>::kInfo);
-    int* s_tile = reinterpret_cast<int*>(sm + Smem<HD>::kUnit);
-    float* s_ks = reinterpret_cast<float*>(s_tile + kMaxUnits);
-    float* s_vs = s_ks + kMaxUnits;
-    int total = 0;
-    for (int b = tid; b < p.B; b += kThreads) total += request_of(p, b).units;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_scan[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += s_scan[i];
-    const int grid = static_cast<int>(gridDim.x);
-    const int per = max(kMinUnits, (total + grid - 1) / grid);
-    lo = static_cast<long long>(blockIdx.x) * per;
-    const int hi = static_cast<int>(min(static_cast<long long>(total), lo + per));
-    int base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        const Req r = b < p.B ? request_of(p, b) : Req{};
-        int incl = r.units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = incl;
-        __syncthreads();
-        int below = base;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) below += s_scan[i];
-            base += s_scan[i];
-        }
-        const int u0 = below + incl - r.units;
-        if (blockIdx.x == 0 && b < p.B) p.first[b] = u0;
-        const bool mine = r.units > 0 && u0 < hi && u0 + r.units > lo;
-        for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
-            const int src = __ffs(todo) - 1;
-            const int rb = b0 + warp * 32 + src;
-            const int ru = __shfl_sync(0xffffffffu, u0, src), rn = __shfl_sync(0xffffffffu, r.units, src);
-            const int rp = __shfl_sync(0xffffffffu, r.pages, src), rt = __shfl_sync(0xffffffffu, r.tiles, src);
-            const int32_t* row = p.page_table + static_cast<size_t>(rb) * p.max_pages;
-            const int end = min(hi, ru + rn);
-            for (int u = max(static_cast<int>(lo), ru) + lane; u < end; u += 32) {
-                const int i = u - static_cast<int>(lo);
-                const int pair = (u - ru) / rp, page = (u - ru) - pair * rp;
-                const int id = row[page];
-                int tile = -1;
-                float ks = 0.f, vs = 0.f;
-                if (id >= 0 && id < p.num_pages) {
-                    tile = id * p.nkv + pair / rt;
-                    ks = p.k_scale[tile];
-                    vs = p.v_scale[tile];
-                }
-                s_tile[i] = tile;
-                s_ks[i] = ks;
-                s_vs[i] = vs;
-                if (i == 0 || page == 0) s_info[i] = make_int4(rb, pair, page, rp);
-            }
-        }
-    }
-    if (blockIdx.x == 0 && tid == 0) {
-        p.first[p.B] = base;
-        p.first[p.B + 1] = per;
-    }
-    __syncthreads();
-    return hi > lo ? hi - static_cast<int>(lo) : 0;
-}
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -237,18 +75,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar) + warp * kStages;
     float* s_o = reinterpret_cast<float*>(sm + L::kO);
     float2* s_ml = reinterpret_cast<float2*>(sm + L::kMl);
-    const int4* s_info = reinterpret_cast<const int4*>(sm + L::kInfo);
-    const int* s_tile = reinterpret_cast<const int*>(sm + L::kUnit);
-    const float* s_ks = reinterpret_cast<const float*>(s_tile + kMaxUnits);
-    const float* s_vs = s_ks + kMaxUnits;
+    int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
+    int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
+    float* s_ks = reinterpret_cast<float*>(s_tile + kMaxUnits);
+    float* s_vs = s_ks + kMaxUnits;
 
     pdl_launch_dependents();
     if (lane == 0)
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
-    long long lo;
-    const int n = gather_units<HD>(p, sm, lo);
-    zero_idle_rows(p, HD);
+    int lo;
+    const int n = gather_units<kThreads, 1, kTileRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs, lo);
+    zero_idle_rows_by<1, kTileRows>(p, HD, warp, kWarps);
 
     const uint64_t policy = l2_policy_evict_first();
     auto fetch = [&](int i) {   // lane 0: unit i into its stage
@@ -529,9 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             bad < 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
                 }
                 if (info.y == 0 && tid == 0)
-                    p.status[b] = bad == 0.f ? PE_REQ_OK : (bad == kMarkBadPage ? PE_REQ_BAD_PAGE : PE_REQ_TIMEOUT);
+                    p.status[b] = status_of(bad);
             } else {
-                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * kv8_part_floats(HD);
+                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kTileRows, HD);
 #pragma unroll
                 for (int d = 0; d < kOut; ++d) dst[r * HD + d0 + d] = acc[d];
                 if ((tid & 15) == 0) {
@@ -546,30 +384,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of every (head, row tile) that several CTAs share, in unit
-// order. The part that CTA c left of a run of units [u0, u1) is its first one
-// where the run begins at or before c's share, its second one otherwise.
+// order; a block per 16 rows. The part that CTA c left of a run of units
+// [u0, u1) is its first one where the run begins at or before c's share, its
+// second one otherwise.
 template <int HD>
-__global__ void __launch_bounds__(kThreads) k_kv8_merge(const Kv8Params p, int tiles_max) {
+__global__ void __launch_bounds__(kThreads) k_kv8_merge(const Kv8Params p, int tiles_max, int tr, int ppu) {
     pdl_wait();
-    const int tile = static_cast<int>(blockIdx.x) % tiles_max;
-    const int bh = static_cast<int>(blockIdx.x) / tiles_max;
-    const int head = bh % p.nkv, b = bh / p.nkv;
+    const int b = blockIdx.z, head = blockIdx.y;
     const int u_b = p.first[b], units = p.first[b + 1] - u_b, per = p.first[p.B + 1];
     if (units == 0) return;
+    const int r16 = blockIdx.x * 16;                  // first of the block's rows
     const int G = p.nq / p.nkv;
     const int S = p.seq_lens[b], rows = p.rows != nullptr ? p.rows[b] : p.K;
-    const int tiles = (rows * G + kTileRows - 1) / kTileRows;
-    if (tile >= tiles) return;
-    const int pages = (S + rows + kPage - 1) / kPage;
-    const int u0 = u_b + (head * tiles + tile) * pages, u1 = u0 + pages;
+    if (r16 >= rows * G) return;
+    const int tiles = (rows * G + tr - 1) / tr, tile = r16 / tr;
+    const int run = ((S + rows + kPage - 1) / kPage + ppu - 1) / ppu;
+    const int u0 = u_b + (head * tiles + tile) * run, u1 = u0 + run;
     const int c0 = u0 / per, c1 = (u1 - 1) / per;
     if (c0 == c1) return;   // written by its CTA
     constexpr int kOut = HD / 16;
-    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kOut;
+    const int rr = r16 + (threadIdx.x >> 4), r = rr - tile * tr, d0 = (threadIdx.x & 15) * kOut;
+    if (rr >= rows * G) return;
     float M = -INFINITY, bad = 0.f;
     for (int c = c0; c <= c1; ++c) {
-        const float* src = p.part + static_cast<size_t>(2 * c + (u0 <= c * per ? 0 : 1)) * kv8_part_floats(HD) + kTileRows * HD;
-        const float sum = src[kTileRows + r];
+        const float* src = p.part + static_cast<size_t>(2 * c + (u0 <= c * per ? 0 : 1)) * part_floats(tr, HD) + tr * HD;
+        const float sum = src[tr + r];
         if (sum < 0.f) bad = fminf(bad, sum);
         else M = fmaxf(M, src[r]);
     }
@@ -577,10 +416,10 @@ __global__ void __launch_bounds__(kThreads) k_kv8_merge(const Kv8Params p, int t
 #pragma unroll
     for (int d = 0; d < kOut; ++d) acc[d] = 0.f;
     for (int c = c0; c <= c1; ++c) {
-        const float* src = p.part + static_cast<size_t>(2 * c + (u0 <= c * per ? 0 : 1)) * kv8_part_floats(HD);
-        const float sum = src[kTileRows * HD + kTileRows + r];
+        const float* src = p.part + static_cast<size_t>(2 * c + (u0 <= c * per ? 0 : 1)) * part_floats(tr, HD);
+        const float sum = src[tr * HD + tr + r];
         if (sum <= 0.f) continue;
-        const float f = ex2(src[kTileRows * HD + r] - M);
+        const float f = ex2(src[tr * HD + r] - M);
         total += sum * f;
 #pragma unroll
         for (int d = 0; d < kOut; d += 4) {
@@ -591,10 +430,7 @@ __global__ void __launch_bounds__(kThreads) k_kv8_merge(const Kv8Params p, int t
             acc[d + 3] += v.w * f;
         }
     }
-    if (head == 0 && tile == 0 && threadIdx.x == 0)
-        p.status[b] = bad == 0.f ? PE_REQ_OK : (bad == kMarkBadPage ? PE_REQ_BAD_PAGE : PE_REQ_TIMEOUT);
-    const int rr = tile * kTileRows + r;
-    if (rr >= rows * G) return;
+    if (head == 0 && rr == 0 && threadIdx.x == 0) p.status[b] = status_of(bad);
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const int j = rr / G;
     __nv_bfloat16* dst = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
@@ -605,42 +441,43 @@ __global__ void __launch_bounds__(kThreads) k_kv8_merge(const Kv8Params p, int t
             bad < 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
 }
 
-struct Kv8Plan {
-    int grid, tiles_max;
-    bool merge;
-    size_t first_floats, ws_floats;
-};
+// Query rows of a head from which the tensor-memory kernel is taken: up to 16
+// rows one tile of the register kernel covers them; above, it would read the
+// cache once per 16 rows.
+constexpr int kUmmaFrom = 17;
 
-int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Kv8Plan* out) {
+int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     int dev = 0, sms = 0;
     PE_CUDA_TRY(cudaGetDevice(&dev));
     PE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    Kv8Plan a{};
-    a.tiles_max = (K * (nq / nkv) + kTileRows - 1) / kTileRows;
-    const long long most = static_cast<long long>(B) * nkv * a.tiles_max * max_pages;
-    if (most > 0x3FFFFFFFll) {
+    Plan a{};
+    const int rows = K * (nq / nkv);
+    const bool umma = rows >= kUmmaFrom;
+    a.ppu = umma ? kUmmaPages : 1;
+    a.tr = umma ? kUmmaRows : kTileRows;
+    const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? 1 : kMinUnits;
+    a.tiles_max = (rows + a.tr - 1) / a.tr;
+    const long long most = static_cast<long long>(B) * nkv * a.tiles_max * ((max_pages + a.ppu - 1) / a.ppu);
+    if (most > 0x3FFFFFFFll || B > 65535 || nkv > 65535) {
         set_error("attention: batch * heads * pages is too large for one call");
         return PE_ERR_UNSUPPORTED;
     }
     // one CTA per SM, and as many rounds as keep a CTA's share in its tables
-    const long long rounds = (most + static_cast<long long>(sms) * kMaxUnits - 1) / (static_cast<long long>(sms) * kMaxUnits);
-    const long long want = (most + kMinUnits - 1) / kMinUnits;
-    a.grid = static_cast<int>(want < sms * rounds ? want : sms * rounds);
-    a.merge = a.grid > 1;
+    const long long round = static_cast<long long>(sms) * max_units;
+    const long long slots = static_cast<long long>(sms) * ((most + round - 1) / round);
+    const long long want = (most + least - 1) / least;
+    a.grid = static_cast<int>(want < slots ? want : slots);
     a.first_floats = (static_cast<size_t>(B) + 2 + 3) / 4 * 4;
-    a.ws_floats = a.first_floats + 2 * static_cast<size_t>(a.grid) * kv8_part_floats(hd);
+    a.ws_floats = a.first_floats + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
     *out = a;
     return PE_OK;
 }
 
 template <int HD>
-int launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Kv8Plan& a, cudaStream_t s) {
+int launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, cudaStream_t s) {
     auto kern = k_attn_kv8<HD>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<HD>::kBytes));
     PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Smem<HD>::kBytes, s, false, tk, tv, p));
-    if (a.merge)
-        PE_CUDA_TRY(launch_ex(k_kv8_merge<HD>, dim3(p.B * p.nkv * a.tiles_max), dim3(kThreads), 0, s, true, p,
-                              a.tiles_max));
     return PE_OK;
 }
 
@@ -664,6 +501,15 @@ int check_shape(int B, int K, int nq, int nkv, int hd, int max_pages) {
 }
 
 }  // namespace
+
+namespace kv8 {
+int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
+    const dim3 grid((p.K * (p.nq / p.nkv) + 15) / 16, p.nkv, p.B);
+    auto kern = hd == 128 ? k_kv8_merge<128> : k_kv8_merge<64>;
+    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), 0, s, true, p, a.tiles_max, a.tr, a.ppu));
+    return PE_OK;
+}
+}  // namespace kv8
 }  // namespace pe
 
 using namespace pe;
@@ -673,7 +519,7 @@ extern "C" int pe_attention_kv8_scratch(int32_t B, int32_t K, int32_t n_q_heads,
     if (ws_floats == nullptr) { set_error("null argument"); return PE_ERR_ARG; }
     int rc = check_shape(B, K, n_q_heads, n_kv_heads, head_dim, max_pages);
     if (rc != PE_OK) return rc;
-    Kv8Plan a;
+    Plan a;
     if ((rc = plan_kv8(B, K, n_q_heads, n_kv_heads, head_dim, max_pages, &a)) != PE_OK) return rc;
     *ws_floats = static_cast<int64_t>(a.ws_floats);
     return PE_OK;
@@ -704,7 +550,7 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
                            reinterpret_cast<uintptr_t>(k_codes) | reinterpret_cast<uintptr_t>(v_codes) |
                            reinterpret_cast<uintptr_t>(ws);
     if ((bits & 15u) != 0) { set_error("q, out, ws and the code arrays must be 16-byte aligned"); return PE_ERR_ARG; }
-    Kv8Plan a;
+    Plan a;
     if ((rc = plan_kv8(B, K, n_q_heads, n_kv_heads, head_dim, max_pages, &a)) != PE_OK) return rc;
     if (ws_floats < static_cast<int64_t>(a.ws_floats)) {
         set_error("attention scratch too small: " + std::to_string(a.ws_floats) + " floats needed");
@@ -734,6 +580,9 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.status = status;
     p.first = reinterpret_cast<int32_t*>(ws);
     p.part = ws + a.first_floats;
-    return head_dim == 128 ? launch_hd<128>(tk, tv, p, a, static_cast<cudaStream_t>(stream))
-                           : launch_hd<64>(tk, tv, p, a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.tr == kUmmaRows) rc = launch_umma(tk, tv, p, a, head_dim, s);
+    else rc = head_dim == 128 ? launch_hd<128>(tk, tv, p, a, s) : launch_hd<64>(tk, tv, p, a, s);
+    // a grid of one covers every head whole
+    return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
 }

@@ -1,0 +1,208 @@
+// Shared by the two kernels of the attention over the 8-bit KV cache: the
+// parameters, the line of units that the CTAs divide, and the partial sums
+// that k_kv8_merge joins.
+//
+// A unit is PPU pages of one (kv head, tile of TR query rows). All units of
+// the batch stand in one line (request, kv head, row tile, page) and every CTA
+// takes the same number of them, so ragged lengths, many requests and a single
+// long one are split alike; the lengths stay on the device. A run of units of
+// one head and row tile within a CTA is a segment. A CTA writes the heads that
+// it covers whole; a head that several CTAs share leaves one partial tile per
+// CTA in scratch, at places that follow from the unit numbers, and k_kv8_merge
+// joins them in order.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pe {
+namespace kv8 {
+
+constexpr int kPage = 16;
+constexpr float kRescale = 8.f;    // running maximum (log2) moves only by more than this
+// marks in the place of a row's sum: the request's outputs are zero
+constexpr float kMarkBadPage = -1.f, kMarkTimeout = -2.f;
+
+struct Kv8Params {
+    int B, K, nq, nkv, max_pages, num_pages;
+    const __nv_bfloat16* q;
+    long long ld_q;
+    const int32_t* seq_lens;
+    const int32_t* rows;
+    const int32_t* page_table;
+    const float* k_scale;
+    const float* v_scale;
+    float scale_log2;
+    __nv_bfloat16* out;
+    long long ld_out;
+    int32_t* status;
+    int32_t* first;    // [B + 1] OUT: first unit of each request, [B + 1]: units of a CTA
+    float* part;       // [2 * grid] partial tiles (part_floats each)
+};
+
+// a partial tile: O [tr][hd], the running maxima (log2) [tr], the sums [tr]
+__host__ __device__ constexpr int part_floats(int tr, int hd) { return tr * hd + 2 * tr; }
+
+// What request b asks for: its live rows, or a status.
+struct Req {
+    int st, S, rows, pages, tiles, run, units;   // run: units of one head and row tile
+};
+template <int PPU, int TR>
+__device__ __forceinline__ Req request_of(const Kv8Params& p, int b) {
+    Req r{PE_REQ_OK, p.seq_lens[b], p.rows != nullptr ? p.rows[b] : p.K, 0, 0, 0, 0};
+    if (r.S < 0 || r.rows < 0 || r.rows > p.K) r.st = PE_REQ_BAD_INPUT;
+    else if (static_cast<long long>(r.S) + r.rows > static_cast<long long>(p.max_pages) * kPage)
+        r.st = PE_REQ_CAPACITY;
+    if (r.st != PE_REQ_OK) r.rows = 0;
+    if (r.rows > 0) {
+        r.pages = (r.S + r.rows + kPage - 1) / kPage;
+        r.tiles = (r.rows * (p.nq / p.nkv) + TR - 1) / TR;
+        r.run = (r.pages + PPU - 1) / PPU;
+        r.units = r.run * r.tiles * p.nkv;
+    }
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// bytes of w that are E4M3's NaN become 0; `any` collects whether there were some
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
+    const uint32_t other = ((w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu;   // bit 7 of a byte: not NaN
+    const uint32_t nan = ~other & 0x80808080u;
+    any |= nan != 0;
+    return w & ~((nan >> 7) * 0xFFu);
+}
+
+// The rows that no unit covers: rows past a request's own, and requests that
+// have none or are refused. A warp per (request, row), by warp my_warp
+// of the CTA's `warps` first ones.
+template <int PPU, int TR>
+__device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int my_warp, int warps) {
+    const int warp = blockIdx.x * warps + my_warp, lane = threadIdx.x & 31;
+    for (int i = warp; i < p.B * p.K; i += gridDim.x * warps) {
+        const int b = i / p.K, j = i - b * p.K;
+        const Req r = request_of<PPU, TR>(p, b);
+        if (j == 0 && lane == 0 && r.units == 0) p.status[b] = r.st;
+        if (j < r.rows) continue;
+        uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(i) * p.ld_out);
+        for (int c = lane; c < p.nq * hd / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// This CTA's share of the line, and its units' pages in shared memory:
+// info[i] of a unit that begins a segment = {request, head * tiles + row tile,
+// unit within its run, units of the run}; of page q of unit i, entry
+// i * PPU + q of tile (page * nkv + head, -1: outside the pool, -2: behind the
+// request's last page), ks and vs. Returns the number of units; lo is the
+// first one. All NT threads of the CTA; every CTA's share is at least
+// `least` and at most max_units (the planner's grid sees to that).
+template <int NT, int PPU, int TR>
+__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, float* ks, float* vs, int& lo) {
+    constexpr int kWarps = NT / 32;
+    __shared__ int s_scan[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int total = 0;
+    for (int b = tid; b < p.B; b += NT) total += request_of<PPU, TR>(p, b).units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_scan[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) total += s_scan[i];
+    const int grid = static_cast<int>(gridDim.x);
+    const int per = max(least, (total + grid - 1) / grid);
+    const long long at = static_cast<long long>(blockIdx.x) * per;
+    lo = static_cast<int>(min(at, static_cast<long long>(total)));
+    const int hi = static_cast<int>(min(static_cast<long long>(total), at + per));
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
+        const int b = b0 + tid;
+        const Req r = b < p.B ? request_of<PPU, TR>(p, b) : Req{};
+        int incl = r.units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int below = base;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) below += s_scan[i];
+            base += s_scan[i];
+        }
+        const int u0 = below + incl - r.units;
+        if (blockIdx.x == 0 && b < p.B) p.first[b] = u0;
+        const bool mine = r.units > 0 && u0 < hi && u0 + r.units > lo;
+        for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const int rb = b0 + warp * 32 + src;
+            const int ru = __shfl_sync(0xffffffffu, u0, src), rn = __shfl_sync(0xffffffffu, r.units, src);
+            const int rp = __shfl_sync(0xffffffffu, r.pages, src), rt = __shfl_sync(0xffffffffu, r.tiles, src);
+            const int run = __shfl_sync(0xffffffffu, r.run, src);
+            const int32_t* row = p.page_table + static_cast<size_t>(rb) * p.max_pages;
+            const int from = max(lo, ru), count = (min(hi, ru + rn) - from) * PPU;
+            for (int x = lane; x < count; x += 32) {
+                const int u = from + x / PPU, i = u - lo;
+                const int pair = (u - ru) / run, at_run = (u - ru) - pair * run;
+                const int page = at_run * PPU + x % PPU;
+                int id = -2;
+                if (page < rp) {
+                    id = row[page];
+                    id = id >= 0 && id < p.num_pages ? id * p.nkv + pair / rt : -1;
+                }
+                tile[i * PPU + x % PPU] = id;
+                ks[i * PPU + x % PPU] = id >= 0 ? p.k_scale[id] : 0.f;
+                vs[i * PPU + x % PPU] = id >= 0 ? p.v_scale[id] : 0.f;
+                if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(rb, pair, at_run, run);
+            }
+        }
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        p.first[p.B] = base;
+        p.first[p.B + 1] = per;
+    }
+    __syncthreads();
+    return hi > lo ? hi - lo : 0;
+}
+
+__device__ __forceinline__ int status_of(float mark) {
+    return mark == 0.f ? PE_REQ_OK : (mark == kMarkBadPage ? PE_REQ_BAD_PAGE : PE_REQ_TIMEOUT);
+}
+
+struct Plan {
+    int ppu, tr;             // pages of a unit, rows of its tile
+    int grid, tiles_max;
+    size_t first_floats, ws_floats;
+};
+
+int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
+// rows past which the tensor-memory kernel takes over, and its launch
+int launch_umma(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, int hd,
+                cudaStream_t s);
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 192;
+
+}  // namespace kv8
+}  // namespace pe

@@ -2,20 +2,22 @@
 // a byte, a scale and optionally a zero point for each group of 32, 64 or 128
 // columns.
 //
-//   y[n, m] = sum_g s[m, g] * (sum_{k in g} c[m, k] x[n, k]  -  z[m, g] * sum_{k in g} x[n, k])
+//   y[n, m] = sum_g s[m, g] * sum_{k in g} (c[m, k] - z[m, g]) x[n, k]
 //
-// The inner sum runs on the tensor cores over the bare codes 0..15; the zero
-// point comes off the group's sum of x, once per group, in fp32, where the
-// scale is applied too, so no weight is ever rounded.
+// The inner sum runs on the tensor cores over the whole numbers c - z, which
+// fp16 holds exactly; the scale multiplies the group's fp32 sum, so no weight
+// is ever rounded.
 //
-// Bound by the weight bytes, so a code has to cost few instructions. As the
-// low four bits of an fp16 a nibble IS the number c * 2^-24 (a subnormal,
-// exact in the MMA), as the next four bits c * 2^-20: one AND widens two
-// codes, four ANDs and one shift a word of eight. The factor 16 goes into x,
-// which is laid out once per CTA in shared memory as fp16, shifted by a power
-// of two per row so that its largest value lies in [2^14, 2^15) (bf16 values
-// down to 2^-28 of it stay exact), in the order in which the ANDs deliver the
-// codes.
+// Bound by the weight bytes, so a code has to cost few instructions. Under
+// fp16's exponent of 1024 a nibble in the low four bits is 1024 + c, in the
+// next four 1024 + 16 c: one AND-OR sets two of them apart, one subtraction or
+// fused multiply-add makes them c - z, five or so instructions for four codes.
+// (Bare nibbles as fp16 subnormals need no arithmetic at all, but the tensor
+// cores align the products by the operands' exponents, so beside a large x
+// the other products lost up to ten bits.) x is laid out once per CTA in
+// shared memory in the order in which the nibbles come out, as fp16 shifted by
+// a power of two per row so that its largest value lies in [2^14, 2^15): bf16
+// values down to 2^-28 of that stay exact.
 //
 // A warp owns 16 weight rows (the MMA's M; the token rows are N) and walks
 // their columns 256 at a time through a ring that its lane 0 fills by TMA
@@ -55,6 +57,9 @@ struct W4Params {
 __device__ __forceinline__ float load_scale(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_scale(const float* p) { return *p; }
 
+__device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -68,20 +73,18 @@ struct W4Smem {
     // x row pitch: consecutive rows half the banks apart
     __host__ __device__ static constexpr int pitch(int cb) { return cb * kCols * 2 + 64; }
     static constexpr int kX = kWarps * kStages * kStageBytes;
-    __host__ __device__ static constexpr int sums(int cb) { return kX + kN * pitch(cb); }
-    __host__ __device__ static constexpr int up(int cb) { return sums(cb) + cb * (kCols / GROUP) * kN * 4; }
+    __host__ __device__ static constexpr int up(int cb) { return kX + kN * pitch(cb); }
     __host__ __device__ static constexpr int red(int cb) { return up(cb) + kN * 4; }
     __host__ __device__ static constexpr int bars(int cb) { return red(cb) + kWarps * kRows * kN * 4; }
     __host__ __device__ static constexpr int bytes(int cb) { return bars(cb) + kWarps * kStages * 8 + 1024; }
 };
 
 // Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
-// order, the groups' sums * 2^-10, and the factor that undoes the row's shift.
+// order, and the factor that undoes the row's shift.
 template <int GROUP, int NT>
 __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
     using L = W4Smem<GROUP, NT>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* s_sum = reinterpret_cast<float*>(sm + L::sums(p.cb));
     float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb));
     const int blocks = min(p.cb, p.nb - b0);
     for (int r = warp; r < L::kN; r += kWarps) {
@@ -107,16 +110,11 @@ __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
         for (int blk = 0; blk < blocks; ++blk) {
             const uint4 v = get(blk);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float f[8], sum = 0.f;
+            float f[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sum += f[i];
-                f[i] *= (i & 1) ? down * 0.0625f : down;
+                f[2 * i] = __uint_as_float(w[i] << 16) * down;
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * down;
             }
             uint32_t o[4];
 #pragma unroll
@@ -125,19 +123,24 @@ __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
                 o[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
             *reinterpret_cast<uint4*>(dst + (blk * kCols + lane * 8) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
-#pragma unroll
-            for (int d = 1; d < GROUP / 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane % (GROUP / 8) == 0)
-                s_sum[(blk * (kCols / GROUP) + lane / (GROUP / 8)) * L::kN + r] = sum * 0.0009765625f;
         }
     }
 }
 
-template <int GROUP, int NT, typename S>
-__global__ void __launch_bounds__(kThreads, 1)
+// Scales and zero points of one block for rows g and g + 8.
+template <int GROUP>
+struct Groups {
+    static constexpr int kN = kCols / GROUP;
+    float scale[2][kN];
+    uint32_t zero[2][kN];
+};
+
+// MB: CTAs that share an SM
+template <int GROUP, int NT, typename S, int MB>
+__global__ void __launch_bounds__(kThreads, MB)
     k_linear_w4(const __grid_constant__ CUtensorMap tmW, const W4Params p) {
     using L = W4Smem<GROUP, NT>;
-    constexpr int kGroups = kCols / GROUP;   // groups of a block
+    using GR = Groups<GROUP>;
     constexpr int kSub = GROUP / 32;         // 32-column steps of a group
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -147,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n0 = blockIdx.y * L::kN;
     uint8_t* ring = sm + warp * kStages * kStageBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bars(p.cb)) + warp * kStages;
-    const float* s_sum = reinterpret_cast<const float*>(sm + L::sums(p.cb));
     const float* s_up = reinterpret_cast<const float*>(sm + L::up(p.cb));
     float* s_red = reinterpret_cast<float*>(sm + L::red(p.cb));
     const int tiles = (p.M + kRows - 1) / kRows;
@@ -176,10 +178,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0)
         for (int s = 0; s < kStages; ++s) fetch();
 
+    // groups past the row's end count nothing
+    auto load_groups = [&](GR& o, int it, int kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = (it * per + wt) * kRows + g + 8 * h;
+            const size_t at = static_cast<size_t>(row) * p.ng + kb * GR::kN;
+#pragma unroll
+            for (int q = 0; q < GR::kN; ++q) {
+                const bool in = row < p.M && kb * GR::kN + q < p.ng;
+                o.scale[h][q] = in ? load_scale(static_cast<const S*>(p.scale) + at + q) : 0.f;
+                o.zero[h][q] = 8u;
+                if (p.zero != nullptr) o.zero[h][q] = in ? p.zero[at + q] : 0u;
+            }
+        }
+    };
+
     int st = 0;
     uint32_t parity = 0;
     bool dead = false;
     const int chunks = (p.nb + p.cb - 1) / p.cb;
+    GR next;
+    if (wk < p.nb) load_groups(next, blockIdx.x, wk);
     for (int it = blockIdx.x; it < iters; it += gridDim.x) {
         const int tile = it * per + wt;
         const bool mine = tile < tiles;
@@ -194,26 +214,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncthreads();
             }
             if (!mine || dead) continue;
-            float up[NT][2];
+            float sum[NT][4];
 #pragma unroll
-            for (int a = 0; a < NT; ++a) {
-                up[a][0] = s_up[a * 8 + 2 * t];
-                up[a][1] = s_up[a * 8 + 2 * t + 1];
-            }
+            for (int a = 0; a < NT; ++a) sum[a][0] = sum[a][1] = sum[a][2] = sum[a][3] = 0.f;
             const int end = min(p.nb, (c + 1) * p.cb);
             for (int kb = c * p.cb + wk; kb < end; kb += ks) {
-                // the block's scales and zero points; groups past the row's end count nothing
-                float sc[2][kGroups], zp[2][kGroups];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int q = 0; q < kGroups; ++q) {
-                        const int gi = kb * kGroups + q;
-                        const bool in = gi < p.ng && m[h] < p.M;
-                        const size_t at = static_cast<size_t>(m[h]) * p.ng + gi;
-                        sc[h][q] = in ? load_scale(static_cast<const S*>(p.scale) + at) * 1024.f : 0.f;
-                        zp[h][q] = in && p.zero != nullptr ? static_cast<float>(p.zero[at]) : 8.f;
-                    }
+                const GR now = next;
+                // the next block's scales are on their way during this one
+                if (kb + ks < p.nb) load_groups(next, it, kb + ks);
+                else if (it + static_cast<int>(gridDim.x) < iters) load_groups(next, it + gridDim.x, wk);
                 const bool ok = mbar_wait(&full[st], (parity >> st) & 1u, nullptr, 0u);
                 if (!__all_sync(0xffffffffu, ok)) {
                     dead = true;
@@ -222,20 +231,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 parity ^= 1u << st;
                 const uint8_t* wr = ring + st * kStageBytes + g * 128 + t * 4;
                 const uint8_t* xr = sm + L::kX + g * L::pitch(p.cb) + ((kb - c * p.cb) * kCols + t * 8) * 2;
-                const int g0 = (kb - c * p.cb) * kGroups;
 #pragma unroll
-                for (int q = 0; q < kGroups; ++q) {
+                for (int q = 0; q < GR::kN; ++q) {
+                    __half2 z1[2], z16[2];   // 1024 + z, and -(64 + z)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        z1[h] = h2(0x64006400u + now.zero[h][q] * 0x00010001u);
+                        z16[h] = __hsub2(h2(0x63806380u), z1[h]);   // 960 - (1024 + z)
+                    }
                     float part[NT][4];
 #pragma unroll
                     for (int a = 0; a < NT; ++a) part[a][0] = part[a][1] = part[a][2] = part[a][3] = 0.f;
 #pragma unroll
                     for (int u = 0; u < kSub; ++u) {
                         const int i = q * kSub + u;
-                        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wr + ((i ^ g) << 4));
-                        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wr + 8 * 128 + ((i ^ g) << 4));
-                        const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-                        const uint32_t lo[4] = {w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u};
-                        const uint32_t hi[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
+                        uint32_t lo[4], hi[4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(wr + h * 8 * 128 + ((i ^ g) << 4));
+                            const uint32_t v = w >> 8;
+                            lo[h] = u32(__hsub2(h2((w & 0x000F000Fu) | 0x64006400u), z1[h]));
+                            lo[2 + h] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), h2(0x2C002C00u), z16[h]));
+                            hi[h] = u32(__hsub2(h2((v & 0x000F000Fu) | 0x64006400u), z1[h]));
+                            hi[2 + h] = u32(__hfma2(h2((v & 0x00F000F0u) | 0x64006400u), h2(0x2C002C00u), z16[h]));
+                        }
 #pragma unroll
                         for (int a = 0; a < NT; ++a) {
                             const uint4 xv = *reinterpret_cast<const uint4*>(xr + a * 8 * L::pitch(p.cb) + i * 64);
@@ -244,19 +263,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
 #pragma unroll
-                    for (int a = 0; a < NT; ++a) {
-                        const float2 xs = *reinterpret_cast<const float2*>(&s_sum[(g0 + q) * L::kN + a * 8 + 2 * t]);
+                    for (int a = 0; a < NT; ++a)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            acc[a][2 * h] += sc[h][q] * (part[a][2 * h] * up[a][0] - zp[h][q] * xs.x);
-                            acc[a][2 * h + 1] += sc[h][q] * (part[a][2 * h + 1] * up[a][1] - zp[h][q] * xs.y);
-                        }
-                    }
+                        for (int j = 0; j < 4; ++j) sum[a][j] = fmaf(now.scale[j >> 1][q], part[a][j], sum[a][j]);
                 }
                 __syncwarp();
                 if (lane == 0) fetch();
                 st = st + 1 == kStages ? 0 : st + 1;
             }
+            // back from the rows' shift by 2^14 and their own powers of two
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[a][j] += sum[a][j] * 6.103515625e-05f * s_up[a * 8 + 2 * t + (j & 1)];
         }
         if (dead)
 #pragma unroll
@@ -305,14 +325,13 @@ int launch(const CUtensorMap& tm, W4Params p, int sms, cudaStream_t s) {
     p.ks = 1;
     while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps)
         p.ks *= 2;
-    int fit = kXBytes / (L::kN * (kCols * 2 + kCols / GROUP * 4));
-    fit = fit / kWarps * kWarps;
+    const int fit = kXBytes / (L::kN * kCols * 2) / kWarps * kWarps;
     p.cb = p.nb <= fit ? (p.nb + p.ks - 1) / p.ks * p.ks : fit;
     const int iters = (tiles * p.ks + kWarps - 1) / kWarps;
-    auto kern = k_linear_w4<GROUP, NT, S>;
     const int smem = L::bytes(p.cb);
+    const int per_sm = NT == 1 && smem <= 112 * 1024 ? 2 : 1;
+    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, NT == 1 ? 2 : 1> : k_linear_w4<GROUP, NT, S, 1>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const int per_sm = smem <= 110 * 1024 ? 2 : 1;
     const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, tm, p));
     return PE_OK;
