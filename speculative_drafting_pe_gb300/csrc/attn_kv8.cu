@@ -8,23 +8,23 @@
 // one pass with a running maximum (base 2). The page scales never touch the
 // codes: ks multiplies the page's scores, vs its weights, both in fp32.
 //
-// Work. A unit is one page of one (kv head, tile of 16 query rows): 16 entries
-// of K and of V. All units of the batch stand in one line (request, kv head,
-// row tile, page) and every CTA takes the same number of them, so ragged
-// lengths, many requests and a single long one are split alike; the lengths
-// stay on the device. A CTA writes the heads that it covers whole; a head that
-// several CTAs share leaves partial sums in scratch, at places that follow
-// from the unit numbers, and k_kv8_merge joins them in order.
+// This file: the kernel for up to 16 query rows of a head (single tokens),
+// whose unit is one page, the merge and the entry point; the line of units
+// that both kernels divide is described in attn_kv8.cuh.
 //
-// A warp takes every eighth unit of its CTA through a ring of its own: lane 0
+// A warp takes every twelfth unit of its CTA through a ring of its own: lane 0
 // fetches the page's K and V by TMA (swizzled, so that both read patterns
-// below are free of bank conflicts) kStages units ahead. The codes are widened
-// to fp16, which holds every E4M3 value, in registers, in the layout of
-// mma.m16n8k16: the dimension order of a K word is permuted, and Q's with it,
-// so a lane reads whole 16-byte chunks; pairs of V rows are interleaved by
-// byte permutes. Queries enter as fp16 after an exact shift by a power of two
-// per row, scores and sums are fp32, weights go to fp16 (2^-11) relative to
-// the row's running maximum and the largest V scale seen.
+// below are free of bank conflicts) kStages units ahead. Both products are
+// transposed, S^T = K Q^T and O^T = V^T P^T, so that the entries and the
+// dimensions fill the 16 rows of mma.m16n8k16 and 8 query rows its columns: a
+// head with few rows leaves no part of the MMA idle. The codes are widened to
+// fp16, which holds every E4M3 value, in registers and where they land: the
+// dimension order of a K word is permuted, and Q's with it, so a lane reads
+// whole 16-byte chunks; pairs of V rows are interleaved by byte permutes; P^T
+// comes out of S^T's layout by two 8x8 transposes. Queries enter as fp16 after
+// an exact shift by a power of two per row, scores and sums are fp32, weights
+// go to fp16 (2^-11) relative to the row's running maximum and the largest V
+// scale seen.
 #include <algorithm>
 
 #include "attn_kv8.cuh"
@@ -34,10 +34,9 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;         // units in flight per warp
-constexpr int kTileRows = 16;      // query rows of a unit (the MMA's M)
+constexpr int kStages = 3;         // units in flight per warp
 constexpr int kMaxUnits = 1024;    // units of one CTA
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,27 +47,44 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
-template <int HD>
+
+// NT: tiles of 8 query rows
+template <int HD, int NT>
 struct Smem {
+    static constexpr int kRows = 8 * NT;
     static constexpr int kTile = kPage * HD;                 // a page's K or V of one head
+    static constexpr int kSlots = kWarps / 2;                // two warps share a slot of sums
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kO = kRing;                         // [kWarps][16][HD] fp32
-    static constexpr int kMl = kO + kWarps * kTileRows * HD * 4;
-    static constexpr int kBar = kMl + kWarps * kTileRows * 8;
-    static constexpr int kInfo = kBar + kWarps * kStages * 8;
+    static constexpr int kO = kRing;                         // [kSlots][kRows][HD] fp32
+    static constexpr int kMl = kO + kSlots * kRows * HD * 4; // [2][kWarps][kRows] (max, sum)
+    static constexpr int kBar = kMl + 2 * kWarps * kRows * 8;
+    static constexpr int kInfo = (kBar + kWarps * kStages * 8 + 15) / 16 * 16;
     static constexpr int kUnit = kInfo + kMaxUnits * 16;     // tile, ks, vs
     static constexpr int kBytes = kUnit + kMaxUnits * 12 + 1024;
+    // 16-byte chunk c of row r of a slot stands at c ^ swizzle(r): the lanes
+    // of a quarter warp (four row pairs, two runs of dimensions) meet no bank twice
+    __device__ static __forceinline__ int swizzle(int r) {
+        const int t = (r >> 1) & 3;
+        return HD == 128 ? t : (t & 1) | ((t >> 1) << 2);
+    }
 };
+static_assert(Smem<128, 2>::kBytes <= 232448 - 128, "shared memory of a block");
 
-template <int HD>
+template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv8(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Kv8Params p) {
-    using L = Smem<HD>;
-    constexpr int kSteps = HD / 16;       // MMA steps over the head dimension
-    constexpr int kWords = HD / 16;       // 32-bit words of a lane's quarter of a K row
-    constexpr int kCols = HD / 8;         // output column tiles = bytes of a lane's part of a V row
+    using L = Smem<HD, NT>;
+    constexpr int kRows = L::kRows;
+    constexpr int kSteps = HD / 16;       // MMA steps over the head dimension = words of a lane's quarter of a K row
+    constexpr int kCols = HD / 8;         // dimensions of a lane's part of a V row
+    constexpr int kMt = kCols / 2;        // 16-dimension tiles of the output
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -76,7 +92,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* ring = sm + warp * kStages * 2 * L::kTile;
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar) + warp * kStages;
     float* s_o = reinterpret_cast<float*>(sm + L::kO);
-    float2* s_ml = reinterpret_cast<float2*>(sm + L::kMl);
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
     float* s_ks = reinterpret_cast<float*>(s_tile + kMaxUnits);
@@ -87,51 +102,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
     int lo;
-    const int n = gather_units<kThreads, 1, kTileRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs, lo);
-    zero_idle_rows_by<1, kTileRows>(p, HD, warp, kWarps);
+    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs, lo);
 
     const uint64_t policy = l2_policy_evict_first();
-    auto fetch = [&](int i) {   // lane 0: unit i into its stage
+    auto fetch = [&](int i, int st) {   // lane 0: unit i into stage st
         const int tile = i < n ? s_tile[i] : -1;
         if (tile < 0) return;
-        const int st = (i / kWarps) % kStages;
         uint8_t* at = ring + st * 2 * L::kTile;
         mbar_arrive_expect_tx(&full[st], 2 * L::kTile);
         tma_load_2d(at, &tmK, &full[st], 0, tile * kPage, policy);
         tma_load_2d(at + L::kTile, &tmV, &full[st], 0, tile * kPage, policy);
     };
     if (lane == 0)
-        for (int s = 0; s < kStages; ++s) fetch(warp + s * kWarps);
+        for (int s = 0; s < kStages; ++s) fetch(warp + s * kWarps, s);
+    zero_idle_rows_by<1, kRows>(p, HD, warp, kWarps);
     uint32_t parity = 0;   // bit s: the phase that stage s completes next
+    int st = 0;            // the stage of this warp's next unit
 
     const int G = p.nq / p.nkv;
     int i = warp;          // this warp's next unit
+    int turn = 0;
     bool dead = false;
-    for (int seg = 0; seg < n;) {
+    for (int seg = 0; seg < n; turn ^= 1) {
         const int4 info = s_info[seg];
         const int b = info.x, page0 = info.z;
         const int len = min(info.w - page0, n - seg);
         const int S = p.seq_lens[b];
         const int rows = p.rows != nullptr ? p.rows[b] : p.K;
-        const int tiles = (rows * G + kTileRows - 1) / kTileRows;
-        const int head = info.y / tiles, r0 = (info.y - head * tiles) * kTileRows;
-        const int live = min(kTileRows, rows * G - r0);   // rows of this tile
+        const int tiles = (rows * G + kRows - 1) / kRows;
+        const int head = info.y / tiles, r0 = (info.y - head * tiles) * kRows;
+        const int live = min(kRows, rows * G - r0);       // rows of this tile
         const int last = S + rows - 1;                    // last entry that any row sees
         float mark = 0.f;
-        float o[kCols][4];
+        // of rows a * 8 + 2t + x: o[j][a][2y + x] is dimension g * kCols + 2j + y
+        float o[kMt][NT][4];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f;
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+            for (int a = 0; a < NT; ++a) o[j][a][0] = o[j][a][1] = o[j][a][2] = o[j][a][3] = 0.f;
+        float m[NT][2], l[NT][2], vref = 0.f, vinv = 0.f;
+#pragma unroll
+        for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
 
         if (i < seg + len && !dead) {
-            // queries: rows g and g + 8, this lane's quarter of the dimensions
-            uint32_t qa[kSteps][4];
-            float cs[2];
-            int lim[2];
+            // queries: row a * 8 + g, this lane's quarter of the dimensions
+            uint32_t qb[NT][kSteps][2];
+            float cs[NT][2];   // of rows a * 8 + 2t + x
+            int lim[NT][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = g + 8 * h;
-                const int j = (r0 + r) / G;
+            for (int a = 0; a < NT; ++a) {
+                const int r = a * 8 + g, j = (r0 + r) / G;
                 const __nv_bfloat16* src =
                     p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                     static_cast<long long>(head * G + (r0 + r) - j * G) * HD + t * (HD / 4);
@@ -150,19 +170,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the row times 2^(127 - E): its largest value lies in [1, 2)
                 const int E = min(max(static_cast<int>(top >> 23), 1), 253);
                 const float down = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);
-                cs[h] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E) << 23);
-                lim[h] = r < live ? S + j : -1;
+                const float up = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E) << 23);
 #pragma unroll
-                for (int c = 0; c < HD / 8; ++c) {
-                    const float x0 = __uint_as_float(w[c] << 16) * down, x1 = __uint_as_float(w[c] & 0xFFFF0000u) * down;
-                    qa[c >> 1][(c & 1) * 2 + h] = pack_f16(x0, x1);
+                for (int x = 0; x < 2; ++x) {
+                    cs[a][x] = __shfl_sync(0xffffffffu, up, (2 * t + x) * 4);
+                    const int rx = a * 8 + 2 * t + x;
+                    lim[a][x] = rx < live ? S + (r0 + rx) / G : -1;
                 }
+#pragma unroll
+                for (int c = 0; c < HD / 8; ++c)
+                    qb[a][c >> 1][c & 1] = pack_f16(__uint_as_float(w[c] << 16) * down,
+                                                    __uint_as_float(w[c] & 0xFFFF0000u) * down);
             }
             for (; i < seg + len; i += kWarps) {
-                const int st = (i / kWarps) % kStages;
                 if (s_tile[i] < 0) {
                     mark = kMarkBadPage;
-                    if (lane == 0) fetch(i + kStages * kWarps);
+                    if (lane == 0) fetch(i + kStages * kWarps, st);
+                    st = st + 1 == kStages ? 0 : st + 1;
                     continue;
                 }
                 const bool ok = mbar_wait(&full[st], (parity >> st) & 1u, nullptr, 0u);
@@ -177,26 +201,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int e0 = (page0 + i - seg) * kPage;   // the page's first entry
                 const bool inner = e0 + kPage - 1 <= S;     // every row sees all of it
 
-                // scores of entries g (columns 0-7) and g + 8 (columns 8-15)
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                // S^T: entries g and g + 8 of the page
+                uint32_t kw[2][kSteps];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = g + 8 * h;
-                    uint32_t w[kWords];
                     if constexpr (HD == 128) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const uint4 x = lds128(kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4));
-                            w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+                            kw[h][4 * c] = x.x; kw[h][4 * c + 1] = x.y; kw[h][4 * c + 2] = x.z; kw[h][4 * c + 3] = x.w;
                         }
                     } else {
                         const uint4 x = lds128(kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
-                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+                        kw[h][0] = x.x; kw[h][1] = x.y; kw[h][2] = x.z; kw[h][3] = x.w;
                     }
-#pragma unroll
-                    for (int c = 0; c < kSteps; ++c) mma_f16(s[h], qa[c], widen_lo(w[c]), widen_hi(w[c]));
                 }
-                // V rows 2t, 2t+1, 2t+8, 2t+9: this lane's HD/8 columns
+                // V rows 2t, 2t+1, 2t+8, 2t+9: this lane's kCols dimensions
                 uint32_t vw[4][kCols / 4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -210,13 +231,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) fetch(i + kStages * kWarps);
+                if (lane == 0) fetch(i + kStages * kWarps, st);
+                st = st + 1 == kStages ? 0 : st + 1;
 
-                const float f0 = cs[0] * ks, f1 = cs[1] * ks;
+                float s[NT][4], s2[NT][4];   // two chains of MMAs
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s[h][0] *= f0; s[h][1] *= f0; s[h][2] *= f1; s[h][3] *= f1;
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[a][x] = s2[a][x] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kSteps; ++c) {
+                    const uint32_t ka[4] = {widen_lo(kw[0][c]), widen_lo(kw[1][c]), widen_hi(kw[0][c]), widen_hi(kw[1][c])};
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) mma_f16((c & 1) ? s2[a] : s[a], ka, qb[a][c][0], qb[a][c][1]);
                 }
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[a][x] = (s[a][x] + s2[a][x]) * (cs[a][x & 1] * ks);
                 if (!inner) {
                     // Entries that some row does not see. What stands behind
                     // the last one is no one's: its V is dropped. A NaN in a
@@ -236,147 +268,166 @@ __global__ void __launch_bounds__(kThreads, 1)
                     nan |= __shfl_xor_sync(0xffffffffu, nan, 4);
                     nan |= __shfl_xor_sync(0xffffffffu, nan, 8);
                     nan |= __shfl_xor_sync(0xffffffffu, nan, 16);
+                    nan = __shfl_sync(0xffffffffu, nan, g >> 1) >> (g & 1);   // bit 0: entry g, bit 2: entry g + 8
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int e = e0 + 2 * t + (x & 1) + 8 * (x >> 1);
+                    for (int a = 0; a < NT; ++a)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float& v = s[x >> 1][2 * h + (x & 1)];
-                            if ((nan >> x) & 1) v = NAN;
-                            if (e > lim[h]) v = -INFINITY;
+                        for (int x = 0; x < 4; ++x) {
+                            if ((nan >> (x & 2)) & 1) s[a][x] = NAN;
+                            if (e0 + g + 4 * (x & 2) > lim[a][x & 1]) s[a][x] = -INFINITY;
                         }
-                    }
                 }
-                float top[2];
+                float top[NT][2];
+                bool up = false;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-                }
-                const bool up = top[0] > m[0] + kRescale || top[1] > m[1] + kRescale;
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        top[a][x] = fmaxf(s[a][x], s[a][2 + x]);
+                        top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 4));
+                        top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 8));
+                        top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 16));
+                        up |= top[a][x] > m[a][x] + kRescale;
+                    }
                 const float av = fabsf(vs);
                 const bool grow = av > 16.f * vref;
                 if (__any_sync(0xffffffffu, up) || grow) {
-                    float f[2];
+                    float fv = 1.f;
+                    if (grow) {
+                        fv = vref / av;
+                        vref = av;
+                        vinv = 1.f / av;
+                    }
+#pragma unroll
+                    for (int a = 0; a < NT; ++a)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float f = 1.f;
+                            if (top[a][x] > m[a][x] + kRescale) {
+                                f = m[a][x] == -INFINITY ? 0.f : ex2(m[a][x] - top[a][x]);
+                                m[a][x] = top[a][x];
+                            }
+                            l[a][x] *= f;
+                            f *= fv;
+#pragma unroll
+                            for (int j = 0; j < kMt; ++j) {
+                                o[j][a][x] *= f;
+                                o[j][a][2 + x] *= f;
+                            }
+                        }
+                }
+                const float vr = vs * vinv;
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    const float m0 = m[a][0] == -INFINITY ? 0.f : m[a][0], m1 = m[a][1] == -INFINITY ? 0.f : m[a][1];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        f[h] = 1.f;
-                        if (top[h] > m[h] + kRescale) {
-                            f[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - top[h]);
-                            m[h] = top[h];
-                        }
-                        l[h] *= f[h];
-                    }
-                    if (grow) {
-                        const float fv = vref / av;
-                        vref = av;
-                        f[0] *= fv;
-                        f[1] *= fv;
-                    }
-#pragma unroll
-                    for (int c = 0; c < kCols; ++c) {
-                        o[c][0] *= f[0]; o[c][1] *= f[0]; o[c][2] *= f[1]; o[c][3] *= f[1];
-                    }
-                }
-                const float vr = vref > 0.f ? vs / vref : 0.f;
-                uint32_t pa[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float mm = m[h] == -INFINITY ? 0.f : m[h];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float w0 = ex2(s[x][2 * h] - mm), w1 = ex2(s[x][2 * h + 1] - mm);
-                        l[h] += w0 + w1;
-                        pa[2 * x + h] = pack_f16(w0 * vr, w1 * vr);
+                        const float w0 = ex2(s[a][2 * h] - m0), w1 = ex2(s[a][2 * h + 1] - m1);
+                        l[a][0] += w0;
+                        l[a][1] += w1;
+                        pb[a][h] = transpose8x8(pack_f16(w0 * vr, w1 * vr));
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < kCols / 4; ++c) {
-                    const uint32_t a0 = __byte_perm(vw[0][c], vw[1][c], 0x5140), a1 = __byte_perm(vw[0][c], vw[1][c], 0x7362);
-                    const uint32_t b0 = __byte_perm(vw[2][c], vw[3][c], 0x5140), b1 = __byte_perm(vw[2][c], vw[3][c], 0x7362);
-                    mma_f16(o[4 * c], pa, widen_lo(a0), widen_lo(b0));
-                    mma_f16(o[4 * c + 1], pa, widen_hi(a0), widen_hi(b0));
-                    mma_f16(o[4 * c + 2], pa, widen_lo(a1), widen_lo(b1));
-                    mma_f16(o[4 * c + 3], pa, widen_hi(a1), widen_hi(b1));
-                }
+                for (int c = 0; c < kCols / 4; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t lo2 = __byte_perm(vw[0][c], vw[1][c], h == 0 ? 0x5140 : 0x7362);
+                        const uint32_t hi2 = __byte_perm(vw[2][c], vw[3][c], h == 0 ? 0x5140 : 0x7362);
+                        const uint32_t va[4] = {widen_lo(lo2), widen_hi(lo2), widen_lo(hi2), widen_hi(hi2)};
+#pragma unroll
+                        for (int a = 0; a < NT; ++a) mma_f16(o[2 * c + h][a], va, pb[a][0], pb[a][1]);
+                    }
             }
         }
         if (dead) mark = kMarkTimeout;
 
-        // Join the warps. A lane holds, of rows g and g + 8, the 2 * kCols
-        // columns from t * 2 * kCols on; row r's 16-byte chunk c of that
-        // quarter goes to chunk c ^ (2t + (r & 1)) of it (banks).
-        __syncthreads();   // the last segment's sums have been read
-        constexpr int kChunks = kCols / 2;   // 16-byte chunks of a quarter row
+        // Join the warps: maxima and sums through a table that two segments
+        // take in turn, then every warp's output relative to the common
+        // maximum, two warps to a slot.
+        float2* s_ml = reinterpret_cast<float2*>(sm + L::kMl) + turn * kWarps * kRows;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = g + 8 * h;
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (t == 0) s_ml[warp * kTileRows + r] = make_float2(m[h], mark != 0.f ? mark : l[h]);
-            float* dst = s_o + (warp * kTileRows + r) * HD + t * (HD / 4);
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                // column 2t of the tile stands for dimensions 2t * kCols + tile, column 2t + 1 for the next kCols
-                const int x = c * 4 / kCols, y = c * 4 - x * kCols;
-                const float4 v = make_float4(o[y][2 * h + x] * vref, o[y + 1][2 * h + x] * vref,
-                                             o[y + 2][2 * h + x] * vref, o[y + 3][2 * h + x] * vref);
-                *reinterpret_cast<float4*>(dst + ((c ^ ((2 * t + (r & 1)) & (kChunks - 1))) << 2)) = v;
+            for (int x = 0; x < 2; ++x) {
+                l[a][x] += __shfl_xor_sync(0xffffffffu, l[a][x], 4);
+                l[a][x] += __shfl_xor_sync(0xffffffffu, l[a][x], 8);
+                l[a][x] += __shfl_xor_sync(0xffffffffu, l[a][x], 16);
+                if (g == 0)
+                    s_ml[warp * kRows + a * 8 + 2 * t + x] = make_float2(m[a][x], mark != 0.f ? mark : l[a][x]);
             }
-        }
         __syncthreads();
-        {
-            constexpr int kOut = HD / 16;    // columns of a thread
-            const int r = tid >> 4, d0 = (tid & 15) * kOut;
-            float M = -INFINITY, bad = 0.f;
-            float2 ml[kWarps];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                ml[w] = s_ml[w * kTileRows + r];
-                if (ml[w].y < 0.f) bad = fminf(bad, ml[w].y);
-                else M = fmaxf(M, ml[w].x);
-            }
-            float acc[kOut], sum = 0.f;
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int d = 0; d < kOut; ++d) acc[d] = 0.f;
-            const int quarter = d0 / (HD / 4), c0 = (d0 - quarter * (HD / 4)) / 4;
+            for (int x = 0; x < 2; ++x) {
+                const int r = a * 8 + 2 * t + x;
+                float M = -INFINITY;
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
+                const float f = m[a][x] == -INFINITY ? vref : vref * ex2(m[a][x] - M);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (ml[w].y <= 0.f) continue;   // saw nothing (a NaN sum goes on)
-                const float f = ex2(ml[w].x - M);
-                sum += ml[w].y * f;
-                const float* src = s_o + (w * kTileRows + r) * HD + quarter * (HD / 4);
-#pragma unroll
-                for (int c = 0; c < kOut / 4; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(
-                        src + (((c0 + c) ^ ((2 * quarter + (r & 1)) & (kChunks - 1))) << 2));
-                    acc[4 * c] += v.x * f;
-                    acc[4 * c + 1] += v.y * f;
-                    acc[4 * c + 2] += v.z * f;
-                    acc[4 * c + 3] += v.w * f;
+                for (int j = 0; j < kMt; ++j) {
+                    o[j][a][x] *= f;
+                    o[j][a][2 + x] *= f;
                 }
+            }
+#pragma unroll
+        for (int round = 0; round < 2; ++round) {
+            if ((warp >= L::kSlots) == (round == 1)) {
+                float* slot = s_o + (warp - round * L::kSlots) * kRows * HD;
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = a * 8 + 2 * t + x;
+#pragma unroll
+                        for (int c = 0; c < kCols / 4; ++c) {
+                            float4* at = reinterpret_cast<float4*>(slot + r * HD) + ((g * (kCols / 4) + c) ^ L::swizzle(r));
+                            float4 v = make_float4(o[2 * c][a][x], o[2 * c][a][2 + x], o[2 * c + 1][a][x], o[2 * c + 1][a][2 + x]);
+                            if (round == 1) {
+                                const float4 u = *at;
+                                v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                            }
+                            *at = v;
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        for (int item = tid; item < kRows * (HD / 4); item += kThreads) {
+            const int r = item / (HD / 4), q = item - r * (HD / 4);
+            float M = -INFINITY, bad = 0.f, sum = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = s_ml[w * kRows + r];
+                if (ml.y < 0.f) bad = fminf(bad, ml.y);
+                else if (ml.y != 0.f) sum += ml.y * (ml.x == -INFINITY ? 1.f : ex2(ml.x - M));   // a NaN sum stays one
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < L::kSlots; ++w) {
+                const float4 v = *(reinterpret_cast<const float4*>(s_o + (w * kRows + r) * HD) + (q ^ L::swizzle(r)));
+                acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
             }
             if (len == info.w) {   // the whole head: write the output
-                const float inv = bad < 0.f || sum == 0.f ? 0.f : 1.f / sum;
                 if (r < live) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    if (bad < 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    else acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
                     const int j = (r0 + r) / G;
-                    __nv_bfloat16* dst = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
-                                         static_cast<long long>(head * G + (r0 + r) - j * G) * HD + d0;
-#pragma unroll
-                    for (int d = 0; d < kOut; d += 2)
-                        *reinterpret_cast<__nv_bfloat162*>(dst + d) =
-                            bad < 0.f ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(acc[d] * inv, acc[d + 1] * inv);
+                    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+                        p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
+                        static_cast<long long>(head * G + (r0 + r) - j * G) * HD + q * 4);
+                    dst[0] = __floats2bfloat162_rn(acc.x, acc.y);
+                    dst[1] = __floats2bfloat162_rn(acc.z, acc.w);
                 }
-                if (info.y == 0 && tid == 0)
-                    p.status[b] = status_of(bad);
+                if (info.y == 0 && item == 0) p.status[b] = status_of(bad);
             } else {
-                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kTileRows, HD);
-#pragma unroll
-                for (int d = 0; d < kOut; ++d) dst[r * HD + d0 + d] = acc[d];
-                if ((tid & 15) == 0) {
-                    dst[kTileRows * HD + r] = M;
-                    dst[kTileRows * HD + kTileRows + r] = bad < 0.f ? bad : sum;
+                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kRows, HD);
+                *reinterpret_cast<float4*>(dst + r * HD + q * 4) = acc;
+                if (q == 0) {
+                    dst[kRows * HD + r] = M;
+                    dst[kRows * HD + kRows + r] = bad < 0.f ? bad : sum;
                 }
             }
         }
@@ -475,7 +526,7 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const int rows = K * (nq / nkv);
     const bool umma = rows >= kUmmaFrom;
     a.ppu = umma ? kUmmaPages : 1;
-    a.tr = umma ? kUmmaRows : kTileRows;
+    a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
     const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? 1 : kMinUnits;
     a.tiles_max = (rows + a.tr - 1) / a.tr;
     const long long most = static_cast<long long>(B) * nkv * a.tiles_max * ((max_pages + a.ppu - 1) / a.ppu);
@@ -494,11 +545,12 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     return PE_OK;
 }
 
-template <int HD>
-int launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, cudaStream_t s) {
-    auto kern = k_attn_kv8<HD>;
-    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<HD>::kBytes));
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Smem<HD>::kBytes, s, false, tk, tv, p));
+template <int HD, int NT>
+int launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, cudaStream_t s) {
+    auto kern = k_attn_kv8<HD, NT>;
+    constexpr int smem = Smem<HD, NT>::kBytes;
+    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), smem, s, false, tk, tv, p));
     return PE_OK;
 }
 
@@ -608,7 +660,8 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.part = ws + a.first_floats;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tr == kUmmaRows) rc = launch_umma(tk, tv, p, a, head_dim, s);
-    else rc = head_dim == 128 ? launch_hd<128>(tk, tv, p, a, s) : launch_hd<64>(tk, tv, p, a, s);
+    else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(tk, tv, p, a, s) : launch_rows<64, 1>(tk, tv, p, a, s);
+    else rc = head_dim == 128 ? launch_rows<128, 2>(tk, tv, p, a, s) : launch_rows<64, 2>(tk, tv, p, a, s);
     // a grid of one covers every head whole
     return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
 }

@@ -34,6 +34,13 @@ constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpConv = 10;
 
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 template <int HD>
 struct Layout {
     static constexpr int kSub = HD / 64;                     // 128-byte sub-tiles of an fp16 row
@@ -138,31 +145,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
-        if (lane == 0 && n > 0) {
+        // The whole warp walks the units and one elected lane issues: in
+        // warp-uniform control flow the descriptors stay in uniform registers.
+        // Issued by a branch on the lane number, each MMA took about 125
+        // cycles to issue and the kernel 2000 cycles a unit.
+        if (n > 0) {
             const uint32_t idesc_s = umma_idesc(0, kRows, kTile);
             const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
+            const uint32_t q_base = smem_u32(sm + L::kQ), cv_base = smem_u32(sm + L::kConv);
             // S and P.V walk the segments each for itself
-            int s_seg = 0, s_end = min(s_info[0].w - s_info[0].z, n), s_no = 0;
+            int s_end = min(s_info[0].w - s_info[0].z, n), s_no = 0;
             auto issue_s = [&](int i) -> bool {
                 if (i == s_end) {
-                    s_seg = i;
                     s_end = i + min(s_info[i].w - s_info[i].z, n - i);
                     ++s_no;
                 }
                 const int c = i % L::kCv;
                 if (!mbar_wait_ab(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1), nullptr, 0u, abort)) return false;
                 tc_fence_after_sync();
-                const uint32_t q_addr = smem_u32(sm + L::kQ + (s_no & 1) * L::kQTile);
-                const uint32_t k_addr = smem_u32(sm + L::kConv + c * 2 * L::kCvTile);
+                const uint32_t q_addr = q_base + (s_no & 1) * L::kQTile, k_addr = cv_base + c * 2 * L::kCvTile;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t sub = static_cast<uint32_t>(kk >> 2), within = static_cast<uint32_t>((kk & 3) * 32);
-                    UmmaKind<__nv_bfloat16>::mma(tmem + static_cast<uint32_t>((i & 1) * kTile),
-                                                 umma_desc_sw128(q_addr + sub * kRows * 128 + within),
-                                                 umma_desc_sw128(k_addr + sub * kTile * 128 + within), idesc_s,
-                                                 kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t sub = static_cast<uint32_t>(kk >> 2), within = static_cast<uint32_t>((kk & 3) * 32);
+                        UmmaKind<__nv_bfloat16>::mma(tmem + static_cast<uint32_t>((i & 1) * kTile),
+                                                     umma_desc_sw128(q_addr + sub * kRows * 128 + within),
+                                                     umma_desc_sw128(k_addr + sub * kTile * 128 + within), idesc_s,
+                                                     kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&s_full[i & 1]);
                 }
-                umma_commit(&s_full[i & 1]);
+                __syncwarp();
                 return true;
             };
             ok = issue_s(0) && (n < 2 || issue_s(1));
@@ -172,21 +185,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o_seg = i;
                     o_end = i + min(s_info[i].w - s_info[i].z, n - i);
                 }
-                if (!mbar_wait_ab(&p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), nullptr, 0u, abort)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait_ab(&p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), nullptr, 0u, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t p_tmem = tmem + static_cast<uint32_t>((i & 1) * kTile);
-                const uint32_t v_addr = smem_u32(sm + L::kConv + (i % L::kCv) * 2 * L::kCvTile + L::kCvTile);
+                const uint32_t v_addr = cv_base + (i % L::kCv) * 2 * L::kCvTile + L::kCvTile;
+                const uint32_t more = i - o_seg > 1 ? 1u : 0u;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    umma_bf16_a_tmem(t_o + static_cast<uint32_t>((i & 1) * HD), p_tmem + static_cast<uint32_t>(kk * 8),
-                                     umma_desc_sw128_mn(v_addr + kk * 16 * 128, kTile * 128), idesc_o,
-                                     (i - o_seg > 1 || kk > 0) ? 1u : 0u);
-                umma_commit(&o_done[i & 1]);
-                umma_commit(&cv_empty[i % L::kCv]);
-                if (i + 2 < n) ok = issue_s(i + 2);
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        umma_bf16_a_tmem(t_o + static_cast<uint32_t>((i & 1) * HD), p_tmem + static_cast<uint32_t>(kk * 8),
+                                         umma_desc_sw128_mn(v_addr + kk * 16 * 128, kTile * 128), idesc_o,
+                                         kk > 0 ? 1u : more);
+                    umma_commit(&o_done[i & 1]);
+                    umma_commit(&cv_empty[i % L::kCv]);
+                }
+                __syncwarp();
+                if (i + 2 < n) {
+                    ok = issue_s(i + 2);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
             }
         }
         __syncwarp();
@@ -196,13 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
         for (int i = 0; i < n; ++i) {
             const int c = i % L::kCv, st = i % L::kRaw;
-            if (i >= L::kCv) ok = mbar_wait_ab(&cv_empty[c], static_cast<uint32_t>((i / L::kCv) & 1) ^ 1u, nullptr, 0u, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (i == end) {
-                // A new segment: its query rows. The tile two segments back
-                // ended at unit i - 2 at the latest; with kCv >= 3 slots that
-                // unit's slot may still be in use, so wait for its products.
+            const bool fresh = i == end;      // a segment begins: its query rows, all loads in flight at once
+            uint4 q[HD / 8];
+            if (fresh) {
                 const int4 info = s_info[i];
                 seg = i;
                 end = i + min(info.w - info.z, n - i);
@@ -211,20 +226,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 S = p.seq_lens[b];
                 const int rows = p.rows != nullptr ? p.rows[b] : p.K;
                 last = S + rows - 1;
-                if (i >= 2) ok = mbar_wait_ab(&o_done[i & 1], static_cast<uint32_t>(((i - 2) >> 1) & 1), nullptr, 0u, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
                 const int j = ct / G;
-                const bool live = ct < rows * G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
+#pragma unroll
+                for (int x = 0; x < HD / 8; ++x) {
+                    q[x] = make_uint4(0u, 0u, 0u, 0u);
+                    if (ct < rows * G) q[x] = *reinterpret_cast<const uint4*>(src + x * 8);
+                }
+            }
+            if (i >= L::kCv) ok = mbar_wait_ab(&cv_empty[c], static_cast<uint32_t>((i / L::kCv) & 1) ^ 1u, nullptr, 0u, abort);
+            // The query tile was last read by the segment two back, which
+            // ended at unit i - 2 at the latest: wait for that unit's products.
+            if (ok && fresh && i >= 2) ok = mbar_wait_ab(&o_done[i & 1], static_cast<uint32_t>(((i - 2) >> 1) & 1), nullptr, 0u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (fresh) {
                 uint8_t* dst = sm + L::kQ + (no & 1) * L::kQTile + ct * 128;
                 uint32_t top = 0;
 #pragma unroll
                 for (int x = 0; x < HD / 8; ++x) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live) v = *reinterpret_cast<const uint4*>(src + x * 8);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
                 }
@@ -233,9 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float down = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);
 #pragma unroll
                 for (int x = 0; x < HD / 8; ++x) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (live) v = *reinterpret_cast<const uint4*>(src + x * 8);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
                     uint32_t o[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
