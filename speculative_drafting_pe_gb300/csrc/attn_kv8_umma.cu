@@ -2,25 +2,31 @@
 // of every head of a group): the tensor-memory kernel behind pe_attention_kv8.
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
-// (at most 128, the MMA's M) share every entry, so the cache is read once. The
-// codes are widened to fp16, which holds every E4M3 value, once per tile, in
-// shared memory, by warps of their own; the products run as tcgen05.mma on
-// fp16 with fp32 sums in tensor memory. Roles (448 threads):
-//   warp 8      TMA: the tile's K and V pages into a ring of raw stages
-//   warps 10-13 converters: raw codes to fp16 K and V tiles (128-byte swizzle;
-//               V stays entry-major and is read as an MN-major operand), V of
-//               entries that no row sees to zero, and at the start of a
-//               segment the query rows, as fp16 after an exact shift by a
-//               power of two per row, into one of two query tiles
-//   warp 9      lane 0 issues S_t = Q K_t^T (M=128, N=64) and O += P_t V_t
-//               (A = P_t from tensor memory)
+// (at most 128, the MMA's M) share every entry, so the cache is read once.
+// Roles (448 threads):
+//   warp 8      TMA: the unit's K pages and V pages into a ring each
+//   warps 10-13 converters. V codes to an fp16 tile (fp16 holds every E4M3
+//               value; 128-byte swizzle, entry-major, read as an MN-major
+//               operand), V of entries that no row sees to zero. At the start
+//               of a segment the query rows: shifted by a power of two per row
+//               so that the largest value lies in [128, 256) and split into
+//               two E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16
+//               value exactly down to 1/1024 of the row's largest and to 2^-18
+//               of that below.
+//   warp 9      one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
+//               N=64, E4M3 operands: the K codes are read where TMA put them)
+//               and O += P_t V_t (fp16, A = P_t from tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
-//               x takes the tiles t = x (mod 2), with a running maximum, sum
+//               x takes the units t = x (mod 2), with a running maximum, sum
 //               and output accumulator of its own, so that neither waits for
 //               the other; they meet at the end of a segment.
-// One S_t buffer per group: P_t (fp16 pairs) overwrites the columns of S_t,
-// and S_{t+2} is issued after P_t V_t. The MMAs of a CTA complete in order, so
-// a complete S_{t+2} also says that the accumulator is at rest.
+// Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
+// kAhead units ahead of P.V, so a group finds its next scores ready when it is
+// done with the last. The MMAs of a CTA complete in issue order.
+//
+// K codes as MMA operands leave only V to be widened: with K widened too the
+// shared memory carried 128 KB a unit, a quarter more than now, at 128 bytes a
+// cycle the first limit of the kernel.
 #include "attn_kv8.cuh"
 
 namespace pe {
@@ -33,6 +39,8 @@ constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpConv = 10;
+constexpr int kAhead = 3;                   // units by which S runs ahead of P.V
+constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -41,29 +49,95 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
+// E4M3 x E4M3, K = 32
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// K-major operand of HD-byte rows under the swizzle of that width
+template <int HD>
+__device__ __forceinline__ uint64_t desc_codes(uint32_t smem_addr) {
+    if constexpr (HD == 128) return umma_desc_sw128(smem_addr);
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(512 >> 4) << 32;   // 8 rows of 64 bytes
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(4) << 61;          // 64-byte swizzle
+    return d;
+}
+
+// 32 consecutive columns of the lane's TMEM row
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// two floats in one instruction
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <int HD>
 struct Layout {
     static constexpr int kSub = HD / 64;                     // 128-byte sub-tiles of an fp16 row
-    static constexpr int kRaw = HD == 128 ? 3 : 6;           // raw stages
-    static constexpr int kCv = HD == 128 ? 3 : 4;            // fp16 tiles
-    static constexpr int kRawTile = kTile * HD;              // codes of K or V of a tile
+    static constexpr int kK = HD == 128 ? 5 : 8;             // stages of K codes
+    static constexpr int kV = HD == 128 ? 4 : 8;             // stages of V codes
+    static constexpr int kCv = HD == 128 ? 4 : 5;            // fp16 V tiles
+    static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
-    static constexpr int kQTile = kRows * HD * 2;
-    static constexpr int kQ = 0;                             // [2]
-    static constexpr int kConv = kQ + 2 * kQTile;            // [kCv][K, V]
-    static constexpr int kRing = kConv + kCv * 2 * kCvTile;  // [kRaw][K, V]
-    static constexpr int kInfo = kRing + kRaw * 2 * kRawTile;
+    static constexpr int kQTerm = kRows * HD;                // hi or lo
+    static constexpr int kQ = 0;                             // [2][hi, lo]
+    static constexpr int kConv = kQ + 4 * kQTerm;
+    static constexpr int kKRing = kConv + kCv * kCvTile;
+    static constexpr int kVRing = kKRing + kK * kCodes;
+    static constexpr int kInfo = kVRing + kV * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
-    static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 12;   // [2][kRows]
-    static constexpr int kEx = kCs + 2 * kRows * 4;          // [2][kRows] float4
+    static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 12;   // [kCsTurns][kRows]
+    static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
     static constexpr int kNan = kEx + 2 * kRows * 16;        // [kCv][kTile] bytes
     static constexpr int kBar = kNan + kCv * kTile;
-    // raw_full, raw_empty [kRaw], cv_full, cv_empty [kCv], s_full, p_full, o_done [2]
-    static constexpr int kBars = 2 * kRaw + 2 * kCv + 6;
+    // k_full, k_empty, v_full, v_empty, cv_full, cv_empty, q_full[2], q_empty[2], s_full[4], p_full[4], o_done[2]
+    static constexpr int kBars = 2 * (kK + kV + kCv) + 14;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448 - 128 && Layout<64>::kBytes <= 232448 - 128, "shared memory of a block");
+// a V slot is free again once P.V of the unit kCv back is done, and S waits for
+// the queries of a unit kAhead ahead, which the converters bring in unit order
+static_assert(kAhead <= 3 && Layout<128>::kCv >= kAhead && Layout<64>::kCv >= kAhead, "S must not wait for itself");
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -81,13 +155,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_cs = reinterpret_cast<float*>(sm + L::kCs);
     float4* s_ex = reinterpret_cast<float4*>(sm + L::kEx);
     uint8_t* s_nan = sm + L::kNan;
-    uint64_t* raw_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t* raw_empty = raw_full + L::kRaw;
-    uint64_t* cv_full = raw_empty + L::kRaw;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t* k_empty = k_full + L::kK;
+    uint64_t* v_full = k_empty + L::kK;
+    uint64_t* v_empty = v_full + L::kV;
+    uint64_t* cv_full = v_empty + L::kV;
     uint64_t* cv_empty = cv_full + L::kCv;
-    uint64_t* s_full = cv_empty + L::kCv;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_done = p_full + 2;
+    uint64_t* q_full = cv_empty + L::kCv;
+    uint64_t* q_empty = q_full + 2;
+    uint64_t* s_full = q_empty + 2;
+    uint64_t* p_full = s_full + 4;
+    uint64_t* o_done = p_full + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.nq / p.nkv;
@@ -95,18 +173,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) {
         s_abort = 0;
-        for (int s = 0; s < L::kRaw; ++s) {
-            mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], 4);
+        for (int s = 0; s < L::kK; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < L::kV; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 4);
         }
         for (int s = 0; s < L::kCv; ++s) {
             mbar_init(&cv_full[s], 4);
             mbar_init(&cv_empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 4);
+            mbar_init(&q_empty[s], 1);
+            mbar_init(&o_done[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 128);
-            mbar_init(&o_done[s], 1);
         }
         fence_mbar_init();
     }
@@ -119,78 +205,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile, s_ks, s_vs, lo);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t t_o = tmem + 128;     // group x's output: columns 128 + x * HD ..
+    const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
     bool ok = true;
+    // parity of use u of a barrier of a ring of `size`, for who waits until it is full / empty again
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
     if (warp == kWarpTma) {
         if (lane == 0) {
             const uint64_t policy = l2_policy_evict_first();
-            for (int i = 0; i < n; ++i) {
-                const int st = i % L::kRaw;
-                if (i >= L::kRaw && !mbar_wait_ab(&raw_empty[st], static_cast<uint32_t>((i / L::kRaw) & 1) ^ 1u, nullptr, 0u, abort)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* kt = sm + L::kRing + st * 2 * L::kRawTile;
-                int pages = 0;
-                for (int q = 0; q < kUmmaPages; ++q) pages += s_tile[i * kUmmaPages + q] >= 0;
-                mbar_arrive_expect_tx(&raw_full[st], static_cast<uint32_t>(pages * 2 * kPage * HD));
-                for (int q = 0; q < kUmmaPages; ++q) {
-                    const int tile = s_tile[i * kUmmaPages + q];
-                    if (tile < 0) continue;
-                    tma_load_2d(kt + q * kPage * HD, &tmK, &raw_full[st], 0, tile * kPage, policy);
-                    tma_load_2d(kt + L::kRawTile + q * kPage * HD, &tmV, &raw_full[st], 0, tile * kPage, policy);
-                }
+            for (int i = 0; i < n && ok; ++i) {
+                const int ki = i % L::kK, vi = i % L::kV;
+                const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
+                const int tile[4] = {tl.x, tl.y, tl.z, tl.w};
+                const int pages = (tile[0] >= 0) + (tile[1] >= 0) + (tile[2] >= 0) + (tile[3] >= 0);
+                if (i >= L::kK) ok = wait(&k_empty[ki], static_cast<uint32_t>((i / L::kK) & 1) ^ 1u);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&k_full[ki], static_cast<uint32_t>(pages * kPage * HD));
+#pragma unroll
+                for (int q = 0; q < kUmmaPages; ++q)
+                    if (tile[q] >= 0)
+                        tma_load_2d(sm + L::kKRing + ki * L::kCodes + q * kPage * HD, &tmK, &k_full[ki], 0, tile[q] * kPage, policy);
+                if (i >= L::kV) ok = wait(&v_empty[vi], static_cast<uint32_t>((i / L::kV) & 1) ^ 1u);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&v_full[vi], static_cast<uint32_t>(pages * kPage * HD));
+#pragma unroll
+                for (int q = 0; q < kUmmaPages; ++q)
+                    if (tile[q] >= 0)
+                        tma_load_2d(sm + L::kVRing + vi * L::kCodes + q * kPage * HD, &tmV, &v_full[vi], 0, tile[q] * kPage, policy);
             }
         }
         __syncwarp();
     } else if (warp == kWarpMma) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
-        // Issued by a branch on the lane number, each MMA took about 125
-        // cycles to issue and the kernel 2000 cycles a unit.
         if (n > 0) {
-            const uint32_t idesc_s = umma_idesc(0, kRows, kTile);
+            const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
             const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
-            const uint32_t q_base = smem_u32(sm + L::kQ), cv_base = smem_u32(sm + L::kConv);
+            const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
+            const uint32_t cv_base = smem_u32(sm + L::kConv);
             // S and P.V walk the segments each for itself
-            int s_end = min(s_info[0].w - s_info[0].z, n), s_no = 0;
+            int s_end = 0, s_no = -1;
             auto issue_s = [&](int i) -> bool {
+                bool good = true;
                 if (i == s_end) {
                     s_end = i + min(s_info[i].w - s_info[i].z, n - i);
                     ++s_no;
+                    good = wait(&q_full[s_no & 1], static_cast<uint32_t>((s_no >> 1) & 1));
                 }
-                const int c = i % L::kCv;
-                if (!mbar_wait_ab(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1), nullptr, 0u, abort)) return false;
+                const int ki = i % L::kK;
+                good = good && wait(&k_full[ki], static_cast<uint32_t>((i / L::kK) & 1));
+                if (!__all_sync(0xffffffffu, good)) return false;
                 tc_fence_after_sync();
-                const uint32_t q_addr = q_base + (s_no & 1) * L::kQTile, k_addr = cv_base + c * 2 * L::kCvTile;
+                const uint32_t q_addr = q_base + (s_no & 1) * 2 * L::kQTerm, k_addr = k_base + ki * L::kCodes;
+                const uint32_t d = tmem + static_cast<uint32_t>((i & 3) * kTile);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; ++kk) {
-                        const uint32_t sub = static_cast<uint32_t>(kk >> 2), within = static_cast<uint32_t>((kk & 3) * 32);
-                        UmmaKind<__nv_bfloat16>::mma(tmem + static_cast<uint32_t>((i & 1) * kTile),
-                                                     umma_desc_sw128(q_addr + sub * kRows * 128 + within),
-                                                     umma_desc_sw128(k_addr + sub * kTile * 128 + within), idesc_s,
-                                                     kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < HD / 32; ++kk) {
+                        const uint64_t kd = desc_codes<HD>(k_addr + kk * 32);
+                        umma_e4m3(d, desc_codes<HD>(q_addr + kk * 32), kd, idesc_s, kk > 0 ? 1u : 0u);
+                        umma_e4m3(d, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc_s, 1u);
                     }
-                    umma_commit(&s_full[i & 1]);
+                    umma_commit(&s_full[i & 3]);
+                    umma_commit(&k_empty[ki]);
+                    if (i + 1 == s_end) umma_commit(&q_empty[s_no & 1]);
                 }
                 __syncwarp();
                 return true;
             };
-            ok = issue_s(0) && (n < 2 || issue_s(1));
-            int o_seg = 0, o_end = min(s_info[0].w - s_info[0].z, n);
+            for (int i = 0; i < min(n, kAhead) && ok; ++i) ok = issue_s(i);
+            int o_seg = 0, o_end = 0;
             for (int i = 0; i < n && ok; ++i) {
+                if (i + kAhead < n) ok = issue_s(i + kAhead);   // its buffer held P_{i-1}, whose P.V is issued
+                if (!ok) break;
                 if (i == o_end) {
                     o_seg = i;
                     o_end = i + min(s_info[i].w - s_info[i].z, n - i);
                 }
-                ok = mbar_wait_ab(&p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), nullptr, 0u, abort);
+                const int c = i % L::kCv;
+                ok = wait(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1)) &&
+                     wait(&p_full[i & 3], static_cast<uint32_t>((i >> 2) & 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t p_tmem = tmem + static_cast<uint32_t>((i & 1) * kTile);
-                const uint32_t v_addr = cv_base + (i % L::kCv) * 2 * L::kCvTile + L::kCvTile;
+                const uint32_t p_tmem = tmem + static_cast<uint32_t>((i & 3) * kTile);
+                const uint32_t v_addr = cv_base + c * L::kCvTile;
                 const uint32_t more = i - o_seg > 1 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
@@ -199,25 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          umma_desc_sw128_mn(v_addr + kk * 16 * 128, kTile * 128), idesc_o,
                                          kk > 0 ? 1u : more);
                     umma_commit(&o_done[i & 1]);
-                    umma_commit(&cv_empty[i % L::kCv]);
+                    umma_commit(&cv_empty[c]);
                 }
                 __syncwarp();
-                if (i + 2 < n) {
-                    ok = issue_s(i + 2);
-                    ok = __all_sync(0xffffffffu, ok);
-                }
             }
         }
         __syncwarp();
     } else if (warp >= kWarpConv) {
         const int ct = tid - kWarpConv * 32;
-        const int row = ct >> 1, half = ct & 1;    // entry of the tile, half of its dimensions
+        const int row = ct >> 1, half = ct & 1;    // entry of the unit, half of its dimensions
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
         for (int i = 0; i < n; ++i) {
-            const int c = i % L::kCv, st = i % L::kRaw;
-            const bool fresh = i == end;      // a segment begins: its query rows, all loads in flight at once
-            uint4 q[HD / 8];
-            if (fresh) {
+            const int c = i % L::kCv, vi = i % L::kV;
+            if (i == end) {      // a segment begins: its query rows, all loads in flight at once
                 const int4 info = s_info[i];
                 seg = i;
                 end = i + min(info.w - info.z, n - i);
@@ -229,20 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
+                uint4 q[HD / 8];
 #pragma unroll
                 for (int x = 0; x < HD / 8; ++x) {
                     q[x] = make_uint4(0u, 0u, 0u, 0u);
                     if (ct < rows * G) q[x] = *reinterpret_cast<const uint4*>(src + x * 8);
                 }
-            }
-            if (i >= L::kCv) ok = mbar_wait_ab(&cv_empty[c], static_cast<uint32_t>((i / L::kCv) & 1) ^ 1u, nullptr, 0u, abort);
-            // The query tile was last read by the segment two back, which
-            // ended at unit i - 2 at the latest: wait for that unit's products.
-            if (ok && fresh && i >= 2) ok = mbar_wait_ab(&o_done[i & 1], static_cast<uint32_t>(((i - 2) >> 1) & 1), nullptr, 0u, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (fresh) {
-                uint8_t* dst = sm + L::kQ + (no & 1) * L::kQTile + ct * 128;
+                // the tile's last reader: S of the segment two back
+                if (no >= 2) ok = wait(&q_empty[no & 1], static_cast<uint32_t>((no >> 1) & 1) ^ 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 uint32_t top = 0;
 #pragma unroll
                 for (int x = 0; x < HD / 8; ++x) {
@@ -250,67 +338,85 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
                 }
-                // the row times 2^(127 - E): its largest value lies in [1, 2)
-                const int E = min(max(static_cast<int>(top >> 23), 1), 253);
-                const float down = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);
+                // the row times 2^(134 - E): its largest value lies in [128, 256)
+                const int E = min(max(static_cast<int>(top >> 23), 8), 254);
+                const float down = __uint_as_float(static_cast<uint32_t>(261 - E) << 23);
+                uint8_t* dst = sm + L::kQ + (no & 1) * 2 * L::kQTerm + ct * HD;
 #pragma unroll
-                for (int x = 0; x < HD / 8; ++x) {
-                    const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
-                    uint32_t o[4];
+                for (int x = 0; x < HD / 16; ++x) {
+                    const uint32_t w[8] = {q[2 * x].x, q[2 * x].y, q[2 * x].z, q[2 * x].w,
+                                           q[2 * x + 1].x, q[2 * x + 1].y, q[2 * x + 1].z, q[2 * x + 1].w};
+                    uint32_t hi[4], rest[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        o[y] = pack_f16(__uint_as_float(w[y] << 16) * down, __uint_as_float(w[y] & 0xFFFF0000u) * down);
-                    *reinterpret_cast<uint4*>(dst + (x >> 3) * kRows * 128 + (((x & 7) ^ (ct & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int y = 0; y < 4; ++y) {
+                        const float v0 = __uint_as_float(w[2 * y] << 16) * down, v1 = __uint_as_float(w[2 * y] & 0xFFFF0000u) * down;
+                        const float v2 = __uint_as_float(w[2 * y + 1] << 16) * down, v3 = __uint_as_float(w[2 * y + 1] & 0xFFFF0000u) * down;
+                        hi[y] = e4m3x4(v0, v1, v2, v3);
+                        const uint32_t a = widen_lo(hi[y]), d = widen_hi(hi[y]);
+                        const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+                        const float2 fd = __half22float2(*reinterpret_cast<const __half2*>(&d));
+                        rest[y] = e4m3x4(v0 - fa.x, v1 - fa.y, v2 - fd.x, v3 - fd.y);
+                    }
+                    const int at = (HD == 128 ? x ^ (ct & 7) : x ^ ((ct >> 1) & 3)) << 4;
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + L::kQTerm + at) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                 }
-                s_cs[(no & 1) * kRows + ct] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E) << 23);
+                // E4M3 has no infinity: a row that holds one (or a NaN) is NaN
+                s_cs[(no & (kCsTurns - 1)) * kRows + ct] =
+                    top >= 0x7F800000u ? NAN : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E - 7) << 23);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
-            ok = mbar_wait_ab(&raw_full[st], static_cast<uint32_t>((i / L::kRaw) & 1), nullptr, 0u, abort);
+            if (i >= L::kCv) ok = wait(&cv_empty[c], static_cast<uint32_t>((i / L::kCv) & 1) ^ 1u);
+            ok = ok && wait(&v_full[vi], static_cast<uint32_t>((i / L::kV) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int e0 = (s_info[seg].z + i - seg) * kTile;
             const int e = e0 + row;
             const bool inner = e0 + kTile - 1 <= S;
-            int nan = 0;
+            const uint8_t* src = sm + L::kVRing + vi * L::kCodes + row * HD;
+            uint8_t* dst = sm + L::kConv + c * L::kCvTile + row * 128;
+            uint4 v[HD / 32];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint8_t* src = sm + L::kRing + (st * 2 + kv) * L::kRawTile + row * HD;
-                uint8_t* dst = sm + L::kConv + (c * 2 + kv) * L::kCvTile + row * 128;
-#pragma unroll
-                for (int x = 0; x < HD / 32; ++x) {
-                    const int ch = half * (HD / 32) + x;
-                    const int at = HD == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + (at << 4));
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    if (kv == 1 && !inner) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) w[y] = e > last ? 0u : without_nan(w[y], nan);
-                    }
-                    uint8_t* d = dst + (ch >> 2) * kTile * 128;
-                    const int j0 = 2 * (ch & 3);
-                    *reinterpret_cast<uint4*>(d + ((j0 ^ (row & 7)) << 4)) =
-                        make_uint4(widen_lo(w[0]), widen_hi(w[0]), widen_lo(w[1]), widen_hi(w[1]));
-                    *reinterpret_cast<uint4*>(d + (((j0 + 1) ^ (row & 7)) << 4)) =
-                        make_uint4(widen_lo(w[2]), widen_hi(w[2]), widen_lo(w[3]), widen_hi(w[3]));
-                }
+            for (int x = 0; x < HD / 32; ++x) {
+                const int ch = half * (HD / 32) + x;
+                v[x] = *reinterpret_cast<const uint4*>(src + ((HD == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4));
             }
             if (!inner) {
+                int nan = 0;
+#pragma unroll
+                for (int x = 0; x < HD / 32; ++x) {
+                    v[x].x = e > last ? 0u : without_nan(v[x].x, nan);
+                    v[x].y = e > last ? 0u : without_nan(v[x].y, nan);
+                    v[x].z = e > last ? 0u : without_nan(v[x].z, nan);
+                    v[x].w = e > last ? 0u : without_nan(v[x].w, nan);
+                }
                 nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
                 if (half == 0) s_nan[c * kTile + row] = static_cast<uint8_t>(nan);
+            }
+#pragma unroll
+            for (int x = 0; x < HD / 32; ++x) {
+                const int ch = half * (HD / 32) + x, j0 = 2 * (ch & 3);
+                uint8_t* d = dst + (ch >> 2) * kTile * 128;
+                *reinterpret_cast<uint4*>(d + ((j0 ^ (row & 7)) << 4)) =
+                    make_uint4(widen_lo(v[x].x), widen_hi(v[x].x), widen_lo(v[x].y), widen_hi(v[x].y));
+                *reinterpret_cast<uint4*>(d + (((j0 + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(widen_lo(v[x].z), widen_hi(v[x].z), widen_lo(v[x].w), widen_hi(v[x].w));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&cv_full[c]);
-                mbar_arrive(&raw_empty[st]);
+                mbar_arrive(&v_empty[vi]);
             }
         }
     } else {
         // ------------------------------------------------ softmax: thread = query row
         const int grp = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>(grp * kTile);
         const uint32_t t_mine = t_o + lane_off + static_cast<uint32_t>(grp * HD);
+        const bool flip = p.scale_log2 < 0.f;
         int no = 0;
         for (int seg = 0; seg < n; ++no) {
             const int4 info = s_info[seg];
@@ -321,40 +427,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int R = rows * G;
             const bool busy = (warp & 3) * 32 < R;      // some row of this warp is live
             const int j = row / G, lim = S + j;
-            const int first = seg + ((seg ^ grp) & 1);  // this group's first tile of the segment
+            const int first = seg + ((seg ^ grp) & 1);  // this group's first unit of the segment
             const int count = first < seg + len ? (seg + len - first + 1) / 2 : 0;
             float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f, mark = 0.f, cs = 0.f;
             for (int i = first; i < seg + len; i += 2) {
-                if (ok) ok = mbar_wait_ab(&s_full[grp], static_cast<uint32_t>((i >> 1) & 1), nullptr, 0u, abort);
+                const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i & 3) * kTile);
+                if (ok) ok = wait(&s_full[i & 3], static_cast<uint32_t>((i >> 2) & 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after_sync();
                 if (busy) {
-                    if (i == first) cs = s_cs[(no & 1) * kRows + row];
-                    float s[kTile];
-                    tmem_ld64(t_s, s);
+                    if (i == first) cs = s_cs[(no & (kCsTurns - 1)) * kRows + row];
                     const float4 ks = *reinterpret_cast<const float4*>(s_ks + i * kUmmaPages);
                     const float4 vs = *reinterpret_cast<const float4*>(s_vs + i * kUmmaPages);
                     const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
+                    float s[kTile];
+                    tmem_ld64(t_s, s);
                     if (tl.x == -1 || tl.y == -1 || tl.z == -1 || tl.w == -1) mark = kMarkBadPage;
-                    const float kf[4] = {cs * ks.x, cs * ks.y, cs * ks.z, cs * ks.w};
-#pragma unroll
-                    for (int x = 0; x < kTile; ++x) s[x] *= kf[x >> 4];
+                    float kf[4] = {cs * ks.x, cs * ks.y, cs * ks.z, cs * ks.w};
                     const int e0 = (info.z + i - seg) * kTile;
-                    if (e0 + kTile - 1 > S) {
-                        // Some row does not see all of it. A NaN in a V that
-                        // only some rows see enters through the score (the
-                        // converters cleared it).
-                        const uint8_t* nan = s_nan + (i % L::kCv) * kTile;
+                    const bool inner = e0 + kTile - 1 <= S;
+                    if (!inner || flip || ks.x < 0.f || ks.y < 0.f || ks.z < 0.f || ks.w < 0.f) {
+                        // the page factors first: a masked score must not meet
+                        // a factor of 0, nor a maximum a negative one
 #pragma unroll
-                        for (int x = 0; x < kTile; ++x) {
-                            if (nan[x]) s[x] = NAN;
-                            if (e0 + x > lim) s[x] = -INFINITY;
+                        for (int x = 0; x < kTile; ++x) s[x] *= kf[x >> 4];
+                        kf[0] = kf[1] = kf[2] = kf[3] = 1.f;
+                        if (!inner) {
+                            // Some row does not see all of it. A NaN in a V
+                            // that only some rows see enters through the score
+                            // (the converters cleared it, before V.P needs it).
+                            const int c = i % L::kCv;
+                            ok = wait(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1));
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) continue;
+                            const uint8_t* nan = s_nan + c * kTile;
+#pragma unroll
+                            for (int x = 0; x < kTile; ++x) {
+                                if (nan[x]) s[x] = NAN;
+                                if (e0 + x > lim) s[x] = -INFINITY;
+                            }
                         }
                     }
-                    float top = s[0];
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int x = 1; x < kTile; ++x) top = fmaxf(top, s[x]);
+                    for (int q = 0; q < 4; ++q) {
+                        const float* sq = s + q * 16;
+                        float t4[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) t4[x] = fmaxf(fmaxf(sq[x], sq[x + 4]), fmaxf(sq[x + 8], sq[x + 12]));
+                        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q]);
+                    }
                     float f = 1.f;
                     if (top > m + kRescale) {
                         f = m == -INFINITY ? 0.f : ex2(m - top);
@@ -368,7 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vinv = 1.f / av;
                     }
                     if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
+                        // this group's last P.V has to be done
+                        ok = wait(&o_done[grp], static_cast<uint32_t>(((i - 2) >> 1) & 1));
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) continue;
+                        tc_fence_after_sync();
+#pragma unroll 1
                         for (int c = 0; c < HD / 16; ++c) {
                             float o[16];
                             tmem_ld16(t_mine + static_cast<uint32_t>(c * 16), o);
@@ -377,26 +505,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st16(t_mine + static_cast<uint32_t>(c * 16), o);
                         }
                     }
-                    const float mm = m == -INFINITY ? 0.f : m;
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    const uint64_t m2 = f2(mm, mm);
                     const float vr[4] = {vs.x * vinv, vs.y * vinv, vs.z * vinv, vs.w * vinv};
+                    uint64_t sum[2] = {0ull, 0ull};
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float pk[16];
+                    for (int q = 0; q < 4; ++q) {
+                        const uint64_t k2 = f2(kf[q], kf[q]), r2 = f2(vr[q], vr[q]);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float w0 = ex2(s[h * 32 + 2 * x] - mm), w1 = ex2(s[h * 32 + 2 * x + 1] - mm);
-                            l += w0 + w1;
-                            const float r = vr[h * 2 + (x >> 3)];
-                            pk[x] = __uint_as_float(pack_f16(w0 * r, w1 * r));
+                        for (int x = 0; x < 8; ++x) {
+                            const float2 a = unf2(fma2(f2(s[q * 16 + 2 * x], s[q * 16 + 2 * x + 1]), k2, m2));
+                            const uint64_t w = f2(ex2(a.x), ex2(a.y));
+                            sum[x & 1] = add2(sum[x & 1], w);
+                            const float2 r = unf2(mul2(w, r2));
+                            pk[q * 8 + x] = pack_f16(r.x, r.y);
                         }
-                        tmem_st16(t_s + static_cast<uint32_t>(h * 16), pk);
                     }
+                    const float2 sa = unf2(add2(sum[0], sum[1]));
+                    l += sa.x + sa.y;
+                    tmem_st32(t_s, pk);
                 }
                 tc_fence_before_sync();
-                mbar_arrive(&p_full[grp]);
+                mbar_arrive(&p_full[i & 3]);
             }
-            if (ok && count > 0)
-                ok = mbar_wait_ab(&o_done[grp], static_cast<uint32_t>(((first + 2 * (count - 1)) >> 1) & 1), nullptr, 0u, abort);
+            if (ok && count > 0) ok = wait(&o_done[grp], static_cast<uint32_t>(((first + 2 * (count - 1)) >> 1) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) mark = kMarkTimeout;
             tc_fence_after_sync();
