@@ -3,7 +3,7 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (448 threads):
+// Roles (480 threads):
 //   warp 8      TMA: the unit's K pages and V pages into a ring each
 //   warps 10-13 converters. V codes to an fp16 tile (fp16 holds every E4M3
 //               value; 128-byte swizzle, entry-major, read as an MN-major
@@ -15,14 +15,19 @@
 //               of that below.
 //   warp 9      one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
 //               N=64, E4M3 operands: the K codes are read where TMA put them)
-//               and O += P_t V_t (fp16, A = P_t from tensor memory)
+//   warp 14     one elected lane issues O += P_t V_t (fp16, A = P_t from
+//               tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
 //               and output accumulator of its own, so that neither waits for
 //               the other; they meet at the end of a segment.
 // Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
-// kAhead units ahead of P.V, so a group finds its next scores ready when it is
-// done with the last. The MMAs of a CTA complete in issue order.
+// up to four units ahead of P.V, so a group finds its next scores ready when it
+// is done with the last. K codes, V tiles and S_t have four places each, so
+// "S_t is complete" also frees K_t's place and "P_t V_t is complete" V_t's and
+// S_t's: one commit for each product. Waits, MMAs and commits cost their warp
+// about 100, 40 and 100 cycles each; with both products and six commits in one
+// warp that, 1550 cycles a unit, was what bounded the kernel.
 //
 // K codes as MMA operands leave only V to be widened: with K widened too the
 // shared memory carried 128 KB a unit, a quarter more than now, at 128 bytes a
@@ -34,12 +39,12 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpConv = 10;
-constexpr int kAhead = 3;                   // units by which S runs ahead of P.V
+constexpr int kWarpTma = 8, kWarpS = 9, kWarpConv = 10, kWarpPv = 14;
+constexpr int kTurns = 4;                   // places of K codes, fp16 V tiles and scores
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 // true in one lane of a converged warp
@@ -113,32 +118,26 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 template <int HD>
 struct Layout {
     static constexpr int kSub = HD / 64;                     // 128-byte sub-tiles of an fp16 row
-    static constexpr int kK = HD == 128 ? 5 : 8;             // stages of K codes
-    static constexpr int kV = HD == 128 ? 4 : 8;             // stages of V codes
-    static constexpr int kCv = HD == 128 ? 4 : 5;            // fp16 V tiles
+    static constexpr int kV = HD == 128 ? 5 : 8;             // stages of V codes
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
     static constexpr int kQTerm = kRows * HD;                // hi or lo
     static constexpr int kQ = 0;                             // [2][hi, lo]
     static constexpr int kConv = kQ + 4 * kQTerm;
-    static constexpr int kKRing = kConv + kCv * kCvTile;
-    static constexpr int kVRing = kKRing + kK * kCodes;
+    static constexpr int kKRing = kConv + kTurns * kCvTile;
+    static constexpr int kVRing = kKRing + kTurns * kCodes;
     static constexpr int kInfo = kVRing + kV * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
     static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 12;   // [kCsTurns][kRows]
     static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
-    static constexpr int kNan = kEx + 2 * kRows * 16;        // [kCv][kTile] bytes
-    static constexpr int kBar = kNan + kCv * kTile;
-    // k_full, k_empty, v_full, v_empty, cv_full, cv_empty, q_full[2], q_empty[2], s_full[4], p_full[4], o_done[2]
-    static constexpr int kBars = 2 * (kK + kV + kCv) + 14;
+    static constexpr int kNan = kEx + 2 * kRows * 16;        // [kTurns][kTile] bytes
+    static constexpr int kBar = kNan + kTurns * kTile;
+    // k_full, cv_full, s_full, p_full, pv_done [kTurns], v_full, v_empty [kV], q_full, q_empty [2]
+    static constexpr int kBars = 5 * kTurns + 2 * kV + 4;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448 - 128 && Layout<64>::kBytes <= 232448 - 128, "shared memory of a block");
-// a V slot is free again once P.V of the unit kCv back is done, and S waits for
-// the queries of a unit kAhead ahead, which the converters bring in unit order
-static_assert(kAhead <= 3 && Layout<128>::kCv >= kAhead && Layout<64>::kCv >= kAhead, "S must not wait for itself");
-
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -156,16 +155,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* s_ex = reinterpret_cast<float4*>(sm + L::kEx);
     uint8_t* s_nan = sm + L::kNan;
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t* k_empty = k_full + L::kK;
-    uint64_t* v_full = k_empty + L::kK;
+    uint64_t* cv_full = k_full + kTurns;
+    uint64_t* s_full = cv_full + kTurns;
+    uint64_t* p_full = s_full + kTurns;
+    uint64_t* pv_done = p_full + kTurns;
+    uint64_t* v_full = pv_done + kTurns;
     uint64_t* v_empty = v_full + L::kV;
-    uint64_t* cv_full = v_empty + L::kV;
-    uint64_t* cv_empty = cv_full + L::kCv;
-    uint64_t* q_full = cv_empty + L::kCv;
+    uint64_t* q_full = v_empty + L::kV;
     uint64_t* q_empty = q_full + 2;
-    uint64_t* s_full = q_empty + 2;
-    uint64_t* p_full = s_full + 4;
-    uint64_t* o_done = p_full + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.nq / p.nkv;
@@ -173,30 +170,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) {
         s_abort = 0;
-        for (int s = 0; s < L::kK; ++s) {
+        for (int s = 0; s < kTurns; ++s) {
             mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
+            mbar_init(&cv_full[s], 4);
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 128);
+            mbar_init(&pv_done[s], 1);
         }
         for (int s = 0; s < L::kV; ++s) {
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 4);
         }
-        for (int s = 0; s < L::kCv; ++s) {
-            mbar_init(&cv_full[s], 4);
-            mbar_init(&cv_empty[s], 1);
-        }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 4);
             mbar_init(&q_empty[s], 1);
-            mbar_init(&o_done[s], 1);
-        }
-        for (int s = 0; s < 4; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 128);
         }
         fence_mbar_init();
     }
-    if (warp == kWarpMma) {
+    if (warp == kWarpS) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -207,18 +198,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
     bool ok = true;
-    // parity of use u of a barrier of a ring of `size`, for who waits until it is full / empty again
+    auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
     if (warp == kWarpTma) {
         if (lane == 0) {
             const uint64_t policy = l2_policy_evict_first();
             for (int i = 0; i < n && ok; ++i) {
-                const int ki = i % L::kK, vi = i % L::kV;
+                const int ki = i % kTurns, vi = i % L::kV;
                 const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
                 const int tile[4] = {tl.x, tl.y, tl.z, tl.w};
                 const int pages = (tile[0] >= 0) + (tile[1] >= 0) + (tile[2] >= 0) + (tile[3] >= 0);
-                if (i >= L::kK) ok = wait(&k_empty[ki], static_cast<uint32_t>((i / L::kK) & 1) ^ 1u);
+                if (i >= kTurns) ok = wait(&s_full[ki], turn(i) ^ 1u);   // S of the unit before it in this place
                 if (!ok) break;
                 mbar_arrive_expect_tx(&k_full[ki], static_cast<uint32_t>(pages * kPage * HD));
 #pragma unroll
@@ -235,72 +226,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpS || warp == kWarpPv) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
-        if (n > 0) {
-            const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
-            const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
-            const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
-            const uint32_t cv_base = smem_u32(sm + L::kConv);
-            // S and P.V walk the segments each for itself
-            int s_end = 0, s_no = -1;
-            auto issue_s = [&](int i) -> bool {
-                bool good = true;
-                if (i == s_end) {
-                    s_end = i + min(s_info[i].w - s_info[i].z, n - i);
-                    ++s_no;
-                    good = wait(&q_full[s_no & 1], static_cast<uint32_t>((s_no >> 1) & 1));
-                }
-                const int ki = i % L::kK;
-                good = good && wait(&k_full[ki], static_cast<uint32_t>((i / L::kK) & 1));
-                if (!__all_sync(0xffffffffu, good)) return false;
-                tc_fence_after_sync();
-                const uint32_t q_addr = q_base + (s_no & 1) * 2 * L::kQTerm, k_addr = k_base + ki * L::kCodes;
-                const uint32_t d = tmem + static_cast<uint32_t>((i & 3) * kTile);
+        const bool scores = warp == kWarpS;
+        const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
+        const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
+        const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
+        const uint32_t cv_base = smem_u32(sm + L::kConv);
+        int seg = 0, end = 0, no = -1;
+        for (int i = 0; i < n; ++i) {
+            const int x = i % kTurns;
+            if (i == end) {
+                seg = i;
+                end = i + min(s_info[i].w - s_info[i].z, n - i);
+                ++no;
+                if (scores) ok = wait(&q_full[no & 1], static_cast<uint32_t>((no >> 1) & 1));
+            }
+            if (scores) ok = ok && wait(&k_full[x], turn(i)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
+            else ok = ok && wait(&cv_full[x], turn(i)) && wait(&p_full[x], turn(i));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t t_s = tmem + static_cast<uint32_t>(x * kTile);
+            if (scores) {
+                const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + x * L::kCodes;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 32; ++kk) {
                         const uint64_t kd = desc_codes<HD>(k_addr + kk * 32);
-                        umma_e4m3(d, desc_codes<HD>(q_addr + kk * 32), kd, idesc_s, kk > 0 ? 1u : 0u);
-                        umma_e4m3(d, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc_s, 1u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + kk * 32), kd, idesc_s, kk > 0 ? 1u : 0u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc_s, 1u);
                     }
-                    umma_commit(&s_full[i & 3]);
-                    umma_commit(&k_empty[ki]);
-                    if (i + 1 == s_end) umma_commit(&q_empty[s_no & 1]);
+                    umma_commit(&s_full[x]);
+                    if (i + 1 == end) umma_commit(&q_empty[no & 1]);
                 }
-                __syncwarp();
-                return true;
-            };
-            for (int i = 0; i < min(n, kAhead) && ok; ++i) ok = issue_s(i);
-            int o_seg = 0, o_end = 0;
-            for (int i = 0; i < n && ok; ++i) {
-                if (i + kAhead < n) ok = issue_s(i + kAhead);   // its buffer held P_{i-1}, whose P.V is issued
-                if (!ok) break;
-                if (i == o_end) {
-                    o_seg = i;
-                    o_end = i + min(s_info[i].w - s_info[i].z, n - i);
-                }
-                const int c = i % L::kCv;
-                ok = wait(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1)) &&
-                     wait(&p_full[i & 3], static_cast<uint32_t>((i >> 2) & 1));
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t p_tmem = tmem + static_cast<uint32_t>((i & 3) * kTile);
-                const uint32_t v_addr = cv_base + c * L::kCvTile;
-                const uint32_t more = i - o_seg > 1 ? 1u : 0u;
+            } else {
+                const uint32_t v_addr = cv_base + x * L::kCvTile;
+                const uint32_t more = i - seg > 1 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_bf16_a_tmem(t_o + static_cast<uint32_t>((i & 1) * HD), p_tmem + static_cast<uint32_t>(kk * 8),
+                        umma_bf16_a_tmem(t_o + static_cast<uint32_t>((i & 1) * HD), t_s + static_cast<uint32_t>(kk * 8),
                                          umma_desc_sw128_mn(v_addr + kk * 16 * 128, kTile * 128), idesc_o,
                                          kk > 0 ? 1u : more);
-                    umma_commit(&o_done[i & 1]);
-                    umma_commit(&cv_empty[c]);
+                    umma_commit(&pv_done[x]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
         }
         __syncwarp();
     } else if (warp >= kWarpConv) {
@@ -308,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = ct >> 1, half = ct & 1;    // entry of the unit, half of its dimensions
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
         for (int i = 0; i < n; ++i) {
-            const int c = i % L::kCv, vi = i % L::kV;
+            const int c = i % kTurns, vi = i % L::kV;
             if (i == end) {      // a segment begins: its query rows, all loads in flight at once
                 const int4 info = s_info[i];
                 seg = i;
@@ -368,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
-            if (i >= L::kCv) ok = wait(&cv_empty[c], static_cast<uint32_t>((i / L::kCv) & 1) ^ 1u);
+            if (i >= kTurns) ok = wait(&pv_done[c], turn(i) ^ 1u);
             ok = ok && wait(&v_full[vi], static_cast<uint32_t>((i / L::kV) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -431,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int count = first < seg + len ? (seg + len - first + 1) / 2 : 0;
             float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f, mark = 0.f, cs = 0.f;
             for (int i = first; i < seg + len; i += 2) {
-                const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i & 3) * kTile);
-                if (ok) ok = wait(&s_full[i & 3], static_cast<uint32_t>((i >> 2) & 1));
+                const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i % kTurns) * kTile);
+                if (ok) ok = wait(&s_full[i % kTurns], turn(i));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after_sync();
@@ -457,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // Some row does not see all of it. A NaN in a V
                             // that only some rows see enters through the score
                             // (the converters cleared it, before V.P needs it).
-                            const int c = i % L::kCv;
-                            ok = wait(&cv_full[c], static_cast<uint32_t>((i / L::kCv) & 1));
+                            const int c = i % kTurns;
+                            ok = wait(&cv_full[c], turn(i));
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) continue;
                             const uint8_t* nan = s_nan + c * kTile;
@@ -492,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
                         // this group's last P.V has to be done
-                        ok = wait(&o_done[grp], static_cast<uint32_t>(((i - 2) >> 1) & 1));
+                        ok = wait(&pv_done[(i - 2) % kTurns], turn(i - 2));
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) continue;
                         tc_fence_after_sync();
@@ -527,9 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(t_s, pk);
                 }
                 tc_fence_before_sync();
-                mbar_arrive(&p_full[i & 3]);
+                mbar_arrive(&p_full[i % kTurns]);
             }
-            if (ok && count > 0) ok = wait(&o_done[grp], static_cast<uint32_t>(((first + 2 * (count - 1)) >> 1) & 1));
+            const int final = first + 2 * (count - 1);
+            if (ok && count > 0) ok = wait(&pv_done[final % kTurns], turn(final));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) mark = kMarkTimeout;
             tc_fence_after_sync();
@@ -608,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == kWarpS) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
