@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
     int lo;
-    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs, lo);
+    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs,
+                                                    reinterpret_cast<int2*>(sm), lo);   // the list in the ring's place
 
     const uint64_t policy = l2_policy_evict_first();
     auto fetch = [&](int i, int st) {   // lane 0: unit i into stage st

@@ -121,77 +121,97 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 // request's last page), ks and vs. Returns the number of units; lo is the
 // first one. All NT threads of the CTA; every CTA's share is at least
 // `least` and at most max_units (the planner's grid sees to that).
+// `list` is scratch for two ints per unit of the share, whose memory a TMA
+// copy may take afterwards. The requests of the share are listed first and
+// then all threads look their pages up, so the dependent loads (page, scales)
+// of all pages are in flight together.
 template <int NT, int PPU, int TR>
-__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, float* ks, float* vs, int& lo) {
+__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, float* ks, float* vs, int2* list,
+                            int& lo) {
     constexpr int kWarps = NT / 32;
-    __shared__ int s_scan[kWarps];
+    __shared__ int s_scan[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int total = 0;
-    for (int b = tid; b < p.B; b += NT) total += request_of<PPU, TR>(p, b).units;
+    const Req mine0 = tid < p.B ? request_of<PPU, TR>(p, tid) : Req{};   // most batches fit the CTA's threads
+    int total = mine0.units;
+    for (int b = tid + NT; b < p.B; b += NT) total += request_of<PPU, TR>(p, b).units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_scan[warp] = total;
+    if (lane == 0) s_scan[0][warp] = total;
     __syncthreads();
     total = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += s_scan[i];
+    for (int i = 0; i < kWarps; ++i) total += s_scan[0][i];
     const int grid = static_cast<int>(gridDim.x);
     const int per = max(least, (total + grid - 1) / grid);
     const long long at = static_cast<long long>(blockIdx.x) * per;
     lo = static_cast<int>(min(at, static_cast<long long>(total)));
     const int hi = static_cast<int>(min(static_cast<long long>(total), at + per));
-    int base = 0;
+    const int n = hi - lo;
+    // the requests that the share touches, in order: {request, its first unit}
+    int base = 0, listed = 0;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
-        const Req r = b < p.B ? request_of<PPU, TR>(p, b) : Req{};
+        const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, TR>(p, b) : Req{});
         int incl = r.units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = incl;
+        if (b0 > 0) __syncthreads();   // the last round's sums have been read
+        if (lane == 31) s_scan[1][warp] = incl;
         __syncthreads();
         int below = base;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) below += s_scan[i];
-            base += s_scan[i];
+            if (i < warp) below += s_scan[1][i];
+            base += s_scan[1][i];
         }
         const int u0 = below + incl - r.units;
         if (blockIdx.x == 0 && b < p.B) p.first[b] = u0;
         const bool mine = r.units > 0 && u0 < hi && u0 + r.units > lo;
-        for (unsigned todo = __ballot_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
-            const int src = __ffs(todo) - 1;
-            const int rb = b0 + warp * 32 + src;
-            const int ru = __shfl_sync(0xffffffffu, u0, src), rn = __shfl_sync(0xffffffffu, r.units, src);
-            const int rp = __shfl_sync(0xffffffffu, r.pages, src), rt = __shfl_sync(0xffffffffu, r.tiles, src);
-            const int run = __shfl_sync(0xffffffffu, r.run, src);
-            const int32_t* row = p.page_table + static_cast<size_t>(rb) * p.max_pages;
-            const int from = max(lo, ru), count = (min(hi, ru + rn) - from) * PPU;
-            for (int x = lane; x < count; x += 32) {
-                const int u = from + x / PPU, i = u - lo;
-                const int pair = (u - ru) / run, at_run = (u - ru) - pair * run;
-                const int page = at_run * PPU + x % PPU;
-                int id = -2;
-                if (page < rp) {
-                    id = row[page];
-                    id = id >= 0 && id < p.num_pages ? id * p.nkv + pair / rt : -1;
-                }
-                tile[i * PPU + x % PPU] = id;
-                ks[i * PPU + x % PPU] = id >= 0 ? p.k_scale[id] : 0.f;
-                vs[i * PPU + x % PPU] = id >= 0 ? p.v_scale[id] : 0.f;
-                if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(rb, pair, at_run, run);
-            }
+        const unsigned vote = __ballot_sync(0xffffffffu, mine);
+        __syncthreads();
+        if (lane == 0) s_scan[1][warp] = __popc(vote);
+        __syncthreads();
+        int rank = listed + __popc(vote & ((1u << lane) - 1u));
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) rank += s_scan[1][i];
+            listed += s_scan[1][i];
         }
+        if (mine) list[rank] = make_int2(b, u0);
     }
     if (blockIdx.x == 0 && tid == 0) {
         p.first[p.B] = base;
         p.first[p.B + 1] = per;
     }
     __syncthreads();
-    return hi > lo ? hi - lo : 0;
+    for (int x = tid; x < n * PPU; x += NT) {
+        const int i = x / PPU, u = lo + i;
+        int at_list = 0;   // the last listed request that begins at or before u
+        for (int step = listed; step > 1;) {
+            step = (step + 1) / 2;
+            if (at_list + step < listed && list[at_list + step].y <= u) at_list += step;
+        }
+        while (at_list + 1 < listed && list[at_list + 1].y <= u) ++at_list;
+        const int b = list[at_list].x, u0 = list[at_list].y;
+        const Req r = request_of<PPU, TR>(p, b);
+        const int pair = (u - u0) / r.run, at_run = (u - u0) - pair * r.run;
+        const int page = at_run * PPU + x % PPU;
+        int id = -2;
+        if (page < r.pages) {
+            id = p.page_table[static_cast<size_t>(b) * p.max_pages + page];
+            id = id >= 0 && id < p.num_pages ? id * p.nkv + pair / r.tiles : -1;
+        }
+        tile[x] = id;
+        ks[x] = id >= 0 ? p.k_scale[id] : 0.f;
+        vs[x] = id >= 0 ? p.v_scale[id] : 0.f;
+        if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(b, pair, at_run, r.run);
+    }
+    fence_proxy_async_smem();   // the list, before TMA writes over it
+    __syncthreads();
+    return n;
 }
 
 __device__ __forceinline__ int status_of(float mark) {

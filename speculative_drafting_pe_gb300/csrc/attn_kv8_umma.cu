@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before_sync();
     int lo;
-    const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile, s_ks, s_vs, lo);
+    const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile, s_ks, s_vs,
+                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
@@ -202,28 +203,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
     if (warp == kWarpTma) {
-        if (lane == 0) {
-            const uint64_t policy = l2_policy_evict_first();
-            for (int i = 0; i < n && ok; ++i) {
-                const int ki = i % kTurns, vi = i % L::kV;
-                const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
-                const int tile[4] = {tl.x, tl.y, tl.z, tl.w};
-                const int pages = (tile[0] >= 0) + (tile[1] >= 0) + (tile[2] >= 0) + (tile[3] >= 0);
-                if (i >= kTurns) ok = wait(&s_full[ki], turn(i) ^ 1u);   // S of the unit before it in this place
-                if (!ok) break;
-                mbar_arrive_expect_tx(&k_full[ki], static_cast<uint32_t>(pages * kPage * HD));
-#pragma unroll
-                for (int q = 0; q < kUmmaPages; ++q)
-                    if (tile[q] >= 0)
-                        tma_load_2d(sm + L::kKRing + ki * L::kCodes + q * kPage * HD, &tmK, &k_full[ki], 0, tile[q] * kPage, policy);
-                if (i >= L::kV) ok = wait(&v_empty[vi], static_cast<uint32_t>((i / L::kV) & 1) ^ 1u);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&v_full[vi], static_cast<uint32_t>(pages * kPage * HD));
-#pragma unroll
-                for (int q = 0; q < kUmmaPages; ++q)
-                    if (tile[q] >= 0)
-                        tma_load_2d(sm + L::kVRing + vi * L::kCodes + q * kPage * HD, &tmV, &v_full[vi], 0, tile[q] * kPage, policy);
-            }
+        // a lane per page: one after the other from one lane, a unit's eight
+        // copies took 1200 cycles to issue
+        const uint64_t policy = l2_policy_evict_first();
+        for (int i = 0; i < n; ++i) {
+            const int ki = i % kTurns, vi = i % L::kV;
+            const int tile = lane < kUmmaPages ? s_tile[i * kUmmaPages + lane] : -1;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) * kPage * HD);
+            if (i >= kTurns) ok = wait(&s_full[ki], turn(i) ^ 1u);   // S of the unit before it in this place
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[ki], bytes);
+            __syncwarp();
+            if (tile >= 0)
+                tma_load_2d(sm + L::kKRing + ki * L::kCodes + lane * kPage * HD, &tmK, &k_full[ki], 0, tile * kPage, policy);
+            if (i >= L::kV) ok = wait(&v_empty[vi], static_cast<uint32_t>((i / L::kV) & 1) ^ 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[vi], bytes);
+            __syncwarp();
+            if (tile >= 0)
+                tma_load_2d(sm + L::kVRing + vi * L::kCodes + lane * kPage * HD, &tmV, &v_full[vi], 0, tile * kPage, policy);
         }
         __syncwarp();
     } else if (warp == kWarpS || warp == kWarpPv) {
