@@ -12,14 +12,16 @@
 // whose unit is one page, the merge and the entry point; the line of units
 // that both kernels divide is described in attn_kv8.cuh.
 //
-// A warp takes every twelfth unit of its CTA through a ring of its own: lane 0
-// fetches the page's K and V by TMA (swizzled, so that both read patterns
-// below are free of bank conflicts) kStages units ahead. Both products are
+// A warp takes every twelfth unit of its CTA, kStages units ahead, through
+// asynchronous copies of its own lanes: each lane fetches the very chunks that
+// it will read, to a place of its own, so there is no barrier to wait at and
+// no bank conflict. (TMA boxes of one page, 16 rows, took about 150 cycles
+// each and held the kernel at 28 bytes/ns per SM.) Both products are
 // transposed, S^T = K Q^T and O^T = V^T P^T, so that the entries and the
 // dimensions fill the 16 rows of mma.m16n8k16 and 8 query rows its columns: a
 // head with few rows leaves no part of the MMA idle. The codes are widened to
 // fp16, which holds every E4M3 value, in registers and where they land: the
-// dimension order of a K word is permuted, and Q's with it, so a lane reads
+// dimension order of a K word is permuted, and Q's with it, so a lane takes
 // whole 16-byte chunks; pairs of V rows are interleaved by byte permutes; P^T
 // comes out of S^T's layout by two 8x8 transposes. Queries enter as fp16 after
 // an exact shift by a power of two per row, scores and sums are fp32, weights
@@ -36,7 +38,8 @@ using namespace kv8;
 
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;         // units in flight per warp
+constexpr int kStages = 2;         // units in flight per warp: 96 KB per SM. More only lengthens the queue
+                                   // in front of every other load
 constexpr int kMaxUnits = 1024;    // units of one CTA
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
 constexpr float kLog2e = 1.4426950408889634f;
@@ -52,20 +55,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 
 // NT: tiles of 8 query rows
 template <int HD, int NT>
 struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kTile = kPage * HD;                 // a page's K or V of one head
+    // a stage of a warp: K chunks [HD / 32][lane] of 16 bytes, V chunks [4][lane] of HD / 8
     static constexpr int kSlots = kWarps / 2;                // two warps share a slot of sums
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
     static constexpr int kO = kRing;                         // [kSlots][kRows][HD] fp32
     static constexpr int kMl = kO + kSlots * kRows * HD * 4; // [2][kWarps][kRows] (max, sum)
-    static constexpr int kBar = kMl + 2 * kWarps * kRows * 8;
-    static constexpr int kInfo = (kBar + kWarps * kStages * 8 + 15) / 16 * 16;
+    static constexpr int kInfo = (kMl + 2 * kWarps * kRows * 8 + 15) / 16 * 16;
     static constexpr int kUnit = kInfo + kMaxUnits * 16;     // tile, ks, vs
     static constexpr int kBytes = kUnit + kMaxUnits * 12 + 1024;
     // 16-byte chunk c of row r of a slot stands at c ^ swizzle(r): the lanes
@@ -79,7 +80,7 @@ static_assert(Smem<128, 2>::kBytes <= 232448 - 128, "shared memory of a block");
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_kv8(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Kv8Params p) {
+    k_attn_kv8(const Kv8Params p) {
     using L = Smem<HD, NT>;
     constexpr int kRows = L::kRows;
     constexpr int kSteps = HD / 16;       // MMA steps over the head dimension = words of a lane's quarter of a K row
@@ -90,7 +91,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * kStages * 2 * L::kTile;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar) + warp * kStages;
     float* s_o = reinterpret_cast<float*>(sm + L::kO);
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
@@ -98,32 +98,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_vs = s_ks + kMaxUnits;
 
     pdl_launch_dependents();
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
-    fence_mbar_init();
     int lo;
+    bool idle;
     const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs,
-                                                    reinterpret_cast<int2*>(sm), lo);   // the list in the ring's place
+                                                    reinterpret_cast<int2*>(sm), lo, idle);   // the list in the ring's place
 
     const uint64_t policy = l2_policy_evict_first();
-    auto fetch = [&](int i, int st) {   // lane 0: unit i into stage st
+    const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kTile + lane * kCols;
+    auto fetch = [&](int i, int st) {   // unit i into stage st; a group even where there is nothing to copy
         const int tile = i < n ? s_tile[i] : -1;
-        if (tile < 0) return;
-        uint8_t* at = ring + st * 2 * L::kTile;
-        mbar_arrive_expect_tx(&full[st], 2 * L::kTile);
-        tma_load_2d(at, &tmK, &full[st], 0, tile * kPage, policy);
-        tma_load_2d(at + L::kTile, &tmV, &full[st], 0, tile * kPage, policy);
+        if (tile >= 0) {
+            // K rows g and g + 8, chunks t and t + 4 (of 64-wide rows: t); V rows 2t, 2t+1, 2t+8, 2t+9, part g
+            const uint8_t* k = p.k_codes + static_cast<size_t>(tile) * L::kTile + g * HD + t * 16;
+            const uint8_t* v = p.v_codes + static_cast<size_t>(tile) * L::kTile + 2 * t * HD + g * kCols;
+            const uint32_t at = ring_at + st * 2 * L::kTile, at_v = ring_v + st * 2 * L::kTile;
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c)
+                copy_async<16>(at + c * 512, k + (HD == 128 ? (c >> 1) * 8 * HD + (c & 1) * 64 : c * 8 * HD), policy);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) copy_async<kCols>(at_v + x * 32 * kCols, v + ((x & 1) + 8 * (x >> 1)) * HD, policy);
+        }
+        copies_commit();
     };
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) fetch(warp + s * kWarps, s);
-    zero_idle_rows_by<1, kRows>(p, HD, warp, kWarps);
-    uint32_t parity = 0;   // bit s: the phase that stage s completes next
+    for (int s = 0; s < kStages; ++s) fetch(warp + s * kWarps, s);
     int st = 0;            // the stage of this warp's next unit
 
     const int G = p.nq / p.nkv;
     int i = warp;          // this warp's next unit
     int turn = 0;
-    bool dead = false;
     for (int seg = 0; seg < n; turn ^= 1) {
         const int4 info = s_info[seg];
         const int b = info.x, page0 = info.z;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
 
-        if (i < seg + len && !dead) {
+        if (i < seg + len) {
             // queries: row a * 8 + g, this lane's quarter of the dimensions
             uint32_t qb[NT][kSteps][2];
             float cs[NT][2];   // of rows a * 8 + 2t + x
@@ -155,12 +157,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = a * 8 + g, j = (r0 + r) / G;
                 const __nv_bfloat16* src =
                     p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
-                    static_cast<long long>(head * G + (r0 + r) - j * G) * HD + t * (HD / 4);
+                    static_cast<long long>(head * G + (r0 + r) - j * G) * HD + t * 16;
                 uint4 raw[HD / 32];
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
                     raw[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < live) raw[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                    if (r < live) raw[c] = *reinterpret_cast<const uint4*>(src + (c >> 1) * 64 + (c & 1) * 8);
                 }
                 uint32_t top = 0;
                 const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
@@ -184,20 +186,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __uint_as_float(w[c] & 0xFFFF0000u) * down);
             }
             for (; i < seg + len; i += kWarps) {
+                copies_wait<kStages - 1>();
                 if (s_tile[i] < 0) {
                     mark = kMarkBadPage;
-                    if (lane == 0) fetch(i + kStages * kWarps, st);
+                    fetch(i + kStages * kWarps, st);
                     st = st + 1 == kStages ? 0 : st + 1;
                     continue;
                 }
-                const bool ok = mbar_wait(&full[st], (parity >> st) & 1u, nullptr, 0u);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    dead = true;
-                    break;
-                }
-                parity ^= 1u << st;
-                const uint8_t* kt = ring + st * 2 * L::kTile;
-                const uint8_t* vt = kt + L::kTile;
+                const uint8_t* kt = ring + st * 2 * L::kTile + lane * 16;
+                const uint8_t* vt = ring + st * 2 * L::kTile + L::kTile + lane * kCols;
                 const float ks = s_ks[i], vs = s_vs[i];
                 const int e0 = (page0 + i - seg) * kPage;   // the page's first entry
                 const bool inner = e0 + kPage - 1 <= S;     // every row sees all of it
@@ -205,34 +202,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // S^T: entries g and g + 8 of the page
                 uint32_t kw[2][kSteps];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = g + 8 * h;
-                    if constexpr (HD == 128) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint4 x = lds128(kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4));
-                            kw[h][4 * c] = x.x; kw[h][4 * c + 1] = x.y; kw[h][4 * c + 2] = x.z; kw[h][4 * c + 3] = x.w;
-                        }
-                    } else {
-                        const uint4 x = lds128(kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
-                        kw[h][0] = x.x; kw[h][1] = x.y; kw[h][2] = x.z; kw[h][3] = x.w;
-                    }
+                for (int c = 0; c < HD / 32; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(kt + c * 512);
+                    uint32_t* w = HD == 128 ? &kw[c >> 1][(c & 1) * 4] : &kw[c][0];
+                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
                 }
                 // V rows 2t, 2t+1, 2t+8, 2t+9: this lane's kCols dimensions
                 uint32_t vw[4][kCols / 4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int r = 2 * t + (x & 1) + 8 * (x >> 1);
                     if constexpr (HD == 128) {
-                        const uint4 y = lds128(vt + r * 128 + ((g ^ (r & 7)) << 4));
+                        const uint4 y = *reinterpret_cast<const uint4*>(vt + x * 512);
                         vw[x][0] = y.x; vw[x][1] = y.y; vw[x][2] = y.z; vw[x][3] = y.w;
                     } else {
-                        const uint2 y = lds64(vt + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+                        const uint2 y = *reinterpret_cast<const uint2*>(vt + x * 256);
                         vw[x][0] = y.x; vw[x][1] = y.y;
                     }
                 }
-                __syncwarp();
-                if (lane == 0) fetch(i + kStages * kWarps, st);
+                fetch(i + kStages * kWarps, st);
                 st = st + 1 == kStages ? 0 : st + 1;
 
                 float s[NT][4], s2[NT][4];   // two chains of MMAs
@@ -342,7 +329,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
             }
         }
-        if (dead) mark = kMarkTimeout;
 
         // Join the warps: maxima and sums through a table that two segments
         // take in turn, then every warp's output relative to the common
@@ -365,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x) {
                 const int r = a * 8 + 2 * t + x;
                 float M = -INFINITY;
+#pragma unroll
                 for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
                 const float f = m[a][x] == -INFINITY ? vref : vref * ex2(m[a][x] - M);
 #pragma unroll
@@ -399,13 +386,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int item = tid; item < kRows * (HD / 4); item += kThreads) {
             const int r = item / (HD / 4), q = item - r * (HD / 4);
             float M = -INFINITY, bad = 0.f, sum = 0.f;
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
+            float2 ml[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) ml[w] = s_ml[w * kRows + r];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w].x);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = s_ml[w * kRows + r];
-                if (ml.y < 0.f) bad = fminf(bad, ml.y);
-                else if (ml.y != 0.f) sum += ml.y * (ml.x == -INFINITY ? 1.f : ex2(ml.x - M));   // a NaN sum stays one
+                bad = fminf(bad, ml[w].y < 0.f ? ml[w].y : 0.f);
+                // a warp that saw nothing adds 0, a NaN sum stays one
+                sum += ml[w].y == 0.f ? 0.f : ml[w].y * (ml[w].x == -INFINITY ? 1.f : ex2(ml[w].x - M));
             }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
             for (int w = 0; w < L::kSlots; ++w) {
                 const float4 v = *(reinterpret_cast<const float4*>(s_o + (w * kRows + r) * HD) + (q ^ L::swizzle(r)));
                 acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
@@ -434,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         seg += len;
     }
-    if (dead) __nanosleep(100000);   // a wait gave up: let copies still in flight land
+    copies_wait<0>();
+    if (idle) zero_idle_rows_by<1, kRows>(p, HD, warp, kWarps);
 }
 
 // Joins the parts of every (head, row tile) that several CTAs share, in unit
@@ -547,11 +541,11 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
 }
 
 template <int HD, int NT>
-int launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, cudaStream_t s) {
+int launch_rows(const Kv8Params& p, const Plan& a, cudaStream_t s) {
     auto kern = k_attn_kv8<HD, NT>;
     constexpr int smem = Smem<HD, NT>::kBytes;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), smem, s, false, tk, tv, p));
+    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), smem, s, false, p));
     return PE_OK;
 }
 
@@ -635,10 +629,6 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
         set_error("attention scratch too small: " + std::to_string(a.ws_floats) + " floats needed");
         return PE_ERR_ARG;
     }
-    CUtensorMap tk, tv;
-    const uint64_t lines = static_cast<uint64_t>(num_pages) * n_kv_heads * kPage;
-    if ((rc = encode_tmap_codes(&tk, k_codes, head_dim, lines)) != PE_OK) return rc;
-    if ((rc = encode_tmap_codes(&tv, v_codes, head_dim, lines)) != PE_OK) return rc;
     Kv8Params p{};
     p.B = B;
     p.K = K;
@@ -651,6 +641,8 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.seq_lens = seq_lens;
     p.rows = rows;
     p.page_table = page_table;
+    p.k_codes = k_codes;
+    p.v_codes = v_codes;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.scale_log2 = scale * kLog2e;
@@ -660,9 +652,9 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.first = reinterpret_cast<int32_t*>(ws);
     p.part = ws + a.first_floats;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a.tr == kUmmaRows) rc = launch_umma(tk, tv, p, a, head_dim, s);
-    else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(tk, tv, p, a, s) : launch_rows<64, 1>(tk, tv, p, a, s);
-    else rc = head_dim == 128 ? launch_rows<128, 2>(tk, tv, p, a, s) : launch_rows<64, 2>(tk, tv, p, a, s);
+    if (a.tr == kUmmaRows) rc = launch_umma(p, a, head_dim, s);
+    else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
+    else rc = head_dim == 128 ? launch_rows<128, 2>(p, a, s) : launch_rows<64, 2>(p, a, s);
     // a grid of one covers every head whole
     return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
 }

@@ -32,6 +32,8 @@ struct Kv8Params {
     const int32_t* seq_lens;
     const int32_t* rows;
     const int32_t* page_table;
+    const uint8_t* k_codes;
+    const uint8_t* v_codes;
     const float* k_scale;
     const float* v_scale;
     float scale_log2;
@@ -90,6 +92,18 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
+// asynchronous copies of this thread (16 or 8 bytes), in groups
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t smem, const void* src, uint64_t policy) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "l"(policy) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2;" ::"r"(smem), "l"(src), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // bytes of w that are E4M3's NaN become 0; `any` collects whether there were some
 __device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
     const uint32_t other = ((w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu) + 0x7F7F7F7Fu;   // bit 7 of a byte: not NaN
@@ -99,18 +113,19 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
 }
 
 // The rows that no unit covers: rows past a request's own, and requests that
-// have none or are refused. A warp per (request, row), by warp my_warp
-// of the CTA's `warps` first ones.
+// have none or are refused; the requests b = blockIdx.x (mod gridDim.x) are
+// this CTA's to look after. gather_units says whether there are any, so that a
+// batch without them pays nothing. By warp my_warp of the CTA's `warps` first.
 template <int PPU, int TR>
 __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int my_warp, int warps) {
-    const int warp = blockIdx.x * warps + my_warp, lane = threadIdx.x & 31;
-    for (int i = warp; i < p.B * p.K; i += gridDim.x * warps) {
-        const int b = i / p.K, j = i - b * p.K;
+    const int lane = threadIdx.x & 31;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const Req r = request_of<PPU, TR>(p, b);
-        if (j == 0 && lane == 0 && r.units == 0) p.status[b] = r.st;
-        if (j < r.rows) continue;
-        uint4* o = reinterpret_cast<uint4*>(p.out + static_cast<long long>(i) * p.ld_out);
-        for (int c = lane; c < p.nq * hd / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (my_warp == 0 && lane == 0 && r.units == 0) p.status[b] = r.st;
+        for (int j = r.rows + my_warp; j < p.K; j += warps) {
+            uint4* o = reinterpret_cast<uint4*>(p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out);
+            for (int c = lane; c < p.nq * hd / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
 }
 
@@ -119,15 +134,14 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 // unit within its run, units of the run}; of page q of unit i, entry
 // i * PPU + q of tile (page * nkv + head, -1: outside the pool, -2: behind the
 // request's last page), ks and vs. Returns the number of units; lo is the
-// first one. All NT threads of the CTA; every CTA's share is at least
+// first one, and idle whether zero_idle_rows_by has work. All NT threads of the CTA; every CTA's share is at least
 // `least` and at most max_units (the planner's grid sees to that).
-// `list` is scratch for two ints per unit of the share, whose memory a TMA
-// copy may take afterwards. The requests of the share are listed first and
+// `list` is scratch for two ints per unit of the share. The requests of the share are listed first and
 // then all threads look their pages up, so the dependent loads (page, scales)
 // of all pages are in flight together.
 template <int NT, int PPU, int TR>
 __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, float* ks, float* vs, int2* list,
-                            int& lo) {
+                            int& lo, bool& idle) {
     constexpr int kWarps = NT / 32;
     __shared__ int s_scan[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,10 +162,11 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
     const int hi = static_cast<int>(min(static_cast<long long>(total), at + per));
     const int n = hi - lo;
     // the requests that the share touches, in order: {request, its first unit}
-    int base = 0, listed = 0;
+    int base = 0, listed = 0, rest = 0;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
         const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, TR>(p, b) : Req{});
+        rest |= b < p.B && r.rows < p.K && b % grid == static_cast<int>(blockIdx.x);
         int incl = r.units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -186,7 +201,7 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         p.first[p.B] = base;
         p.first[p.B + 1] = per;
     }
-    __syncthreads();
+    idle = __syncthreads_or(rest) != 0;
     for (int x = tid; x < n * PPU; x += NT) {
         const int i = x / PPU, u = lo + i;
         int at_list = 0;   // the last listed request that begins at or before u
@@ -209,7 +224,6 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         vs[x] = id >= 0 ? p.v_scale[id] : 0.f;
         if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(b, pair, at_run, r.run);
     }
-    fence_proxy_async_smem();   // the list, before TMA writes over it
     __syncthreads();
     return n;
 }
@@ -226,8 +240,7 @@ struct Plan {
 
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
-int launch_umma(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, int hd,
-                cudaStream_t s);
+int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 192;
 
 }  // namespace kv8

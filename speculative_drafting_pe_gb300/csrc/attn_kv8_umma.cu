@@ -3,19 +3,21 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (480 threads):
-//   warp 8      TMA: the unit's K pages and V pages into a ring each
-//   warps 10-13 converters. V codes to an fp16 tile (fp16 holds every E4M3
-//               value; 128-byte swizzle, entry-major, read as an MN-major
-//               operand), V of entries that no row sees to zero. At the start
-//               of a segment the query rows: shifted by a power of two per row
-//               so that the largest value lies in [128, 256) and split into
-//               two E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16
-//               value exactly down to 1/1024 of the row's largest and to 2^-18
-//               of that below.
-//   warp 9      one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
-//               N=64, E4M3 operands: the K codes are read where TMA put them)
-//   warp 14     one elected lane issues O += P_t V_t (fp16, A = P_t from
+// Roles (448 threads):
+//   warps 10-13 loaders and converters. Each thread fetches 16-byte chunks of
+//               K and V, kDepth units ahead, by asynchronous copies: K to
+//               where the MMA reads it (the swizzle of a K-major operand), V
+//               to a place of the thread's own. V codes then become an fp16
+//               tile (fp16 holds every E4M3 value; 128-byte swizzle,
+//               entry-major, read as an MN-major operand), V of entries that
+//               no row sees zero. At the start of a segment the query rows:
+//               shifted by a power of two per row so that the largest value
+//               lies in [128, 256) and split into two E4M3 terms, q = hi + lo,
+//               which hold the 8 bits of a bf16 value exactly down to 1/1024
+//               of the row's largest and to 2^-18 of that below.
+//   warp 8      one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
+//               N=64, E4M3 operands: the codes themselves)
+//   warp 9      one elected lane issues O += P_t V_t (fp16, A = P_t from
 //               tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
@@ -23,13 +25,15 @@
 //               the other; they meet at the end of a segment.
 // Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
 // up to four units ahead of P.V, so a group finds its next scores ready when it
-// is done with the last. K codes, V tiles and S_t have four places each, so
-// "S_t is complete" also frees K_t's place and "P_t V_t is complete" V_t's and
-// S_t's: one commit for each product. Waits, MMAs and commits cost their warp
+// is done with the last. V tiles and S_t have four places each and "P_t V_t is
+// complete" frees both, as "S_t is complete" frees K_t's place: one commit for
+// each product. Waits, MMAs and commits cost their warp
 // about 100, 40 and 100 cycles each; with both products and six commits in one
 // warp that, 1550 cycles a unit, was what bounded the kernel.
 //
-// K codes as MMA operands leave only V to be widened: with K widened too the
+// TMA boxes of one page (16 rows) took about 150 cycles each, whoever issued
+// them, 1300 cycles a unit; the copies of 128 threads take none of a unit's
+// time. K codes as MMA operands leave only V to be widened: with K widened too the
 // shared memory carried 128 KB a unit, a quarter more than now, at 128 bytes a
 // cycle the first limit of the kernel.
 #include "attn_kv8.cuh"
@@ -39,12 +43,14 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 480;
+constexpr int kThreads = 448;
 constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpTma = 8, kWarpS = 9, kWarpConv = 10, kWarpPv = 14;
-constexpr int kTurns = 4;                   // places of K codes, fp16 V tiles and scores
+constexpr int kWarpS = 8, kWarpPv = 9, kWarpConv = 10;
+constexpr int kTurns = 4;                   // places of fp16 V tiles and scores
+constexpr int kDepth = 4;                   // units whose copies are in flight
+constexpr int kPlacesK = kDepth + 1;
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 // true in one lane of a converged warp
@@ -118,30 +124,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 template <int HD>
 struct Layout {
     static constexpr int kSub = HD / 64;                     // 128-byte sub-tiles of an fp16 row
-    static constexpr int kV = HD == 128 ? 5 : 8;             // stages of V codes
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
     static constexpr int kQTerm = kRows * HD;                // hi or lo
     static constexpr int kQ = 0;                             // [2][hi, lo]
     static constexpr int kConv = kQ + 4 * kQTerm;
     static constexpr int kKRing = kConv + kTurns * kCvTile;
-    static constexpr int kVRing = kKRing + kTurns * kCodes;
-    static constexpr int kInfo = kVRing + kV * kCodes;
+    static constexpr int kVRing = kKRing + kPlacesK * kCodes;
+    static constexpr int kInfo = kVRing + kDepth * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
     static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 12;   // [kCsTurns][kRows]
     static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
     static constexpr int kNan = kEx + 2 * kRows * 16;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
-    // k_full, cv_full, s_full, p_full, pv_done [kTurns], v_full, v_empty [kV], q_full, q_empty [2]
-    static constexpr int kBars = 5 * kTurns + 2 * kV + 4;
+    // k_full [kPlacesK], cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
+    static constexpr int kBars = kPlacesK + 4 * kTurns + 4;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448 - 128 && Layout<64>::kBytes <= 232448 - 128, "shared memory of a block");
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const Kv8Params p) {
+    k_attn_kv8_umma(const Kv8Params p) {
     using L = Layout<HD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -155,13 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* s_ex = reinterpret_cast<float4*>(sm + L::kEx);
     uint8_t* s_nan = sm + L::kNan;
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t* cv_full = k_full + kTurns;
+    uint64_t* cv_full = k_full + kPlacesK;
     uint64_t* s_full = cv_full + kTurns;
     uint64_t* p_full = s_full + kTurns;
     uint64_t* pv_done = p_full + kTurns;
-    uint64_t* v_full = pv_done + kTurns;
-    uint64_t* v_empty = v_full + L::kV;
-    uint64_t* q_full = v_empty + L::kV;
+    uint64_t* q_full = pv_done + kTurns;
     uint64_t* q_empty = q_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -170,16 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) {
         s_abort = 0;
+        for (int s = 0; s < kPlacesK; ++s) mbar_init(&k_full[s], 4);
         for (int s = 0; s < kTurns; ++s) {
-            mbar_init(&k_full[s], 1);
             mbar_init(&cv_full[s], 4);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 128);
             mbar_init(&pv_done[s], 1);
-        }
-        for (int s = 0; s < L::kV; ++s) {
-            mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 4);
@@ -193,8 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before_sync();
     int lo;
+    bool idle;
     const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile, s_ks, s_vs,
-                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo);
+                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo,
+                                                               idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
@@ -202,31 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
-    if (warp == kWarpTma) {
-        // a lane per page: one after the other from one lane, a unit's eight
-        // copies took 1200 cycles to issue
-        const uint64_t policy = l2_policy_evict_first();
-        for (int i = 0; i < n; ++i) {
-            const int ki = i % kTurns, vi = i % L::kV;
-            const int tile = lane < kUmmaPages ? s_tile[i * kUmmaPages + lane] : -1;
-            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) * kPage * HD);
-            if (i >= kTurns) ok = wait(&s_full[ki], turn(i) ^ 1u);   // S of the unit before it in this place
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&k_full[ki], bytes);
-            __syncwarp();
-            if (tile >= 0)
-                tma_load_2d(sm + L::kKRing + ki * L::kCodes + lane * kPage * HD, &tmK, &k_full[ki], 0, tile * kPage, policy);
-            if (i >= L::kV) ok = wait(&v_empty[vi], static_cast<uint32_t>((i / L::kV) & 1) ^ 1u);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&v_full[vi], bytes);
-            __syncwarp();
-            if (tile >= 0)
-                tma_load_2d(sm + L::kVRing + vi * L::kCodes + lane * kPage * HD, &tmV, &v_full[vi], 0, tile * kPage, policy);
-        }
-        __syncwarp();
-    } else if (warp == kWarpS || warp == kWarpPv) {
+    if (warp == kWarpS || warp == kWarpPv) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
         const bool scores = warp == kWarpS;
@@ -236,21 +212,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t cv_base = smem_u32(sm + L::kConv);
         int seg = 0, end = 0, no = -1;
         for (int i = 0; i < n; ++i) {
-            const int x = i % kTurns;
+            const int x = i % kTurns, ki = i % kPlacesK;
             if (i == end) {
                 seg = i;
                 end = i + min(s_info[i].w - s_info[i].z, n - i);
                 ++no;
                 if (scores) ok = wait(&q_full[no & 1], static_cast<uint32_t>((no >> 1) & 1));
             }
-            if (scores) ok = ok && wait(&k_full[x], turn(i)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
+            if (scores) ok = ok && wait(&k_full[ki], static_cast<uint32_t>((i / kPlacesK) & 1)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
             else ok = ok && wait(&cv_full[x], turn(i)) && wait(&p_full[x], turn(i));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t t_s = tmem + static_cast<uint32_t>(x * kTile);
             if (scores) {
-                const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + x * L::kCodes;
+                const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + ki * L::kCodes;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 32; ++kk) {
@@ -278,10 +254,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kWarpConv) {
         const int ct = tid - kWarpConv * 32;
-        const int row = ct >> 1, half = ct & 1;    // entry of the unit, half of its dimensions
+        // chunk `ch` of the unit's entries row0, row0 + kPass, ...
+        constexpr int kChunks = HD / 16, kPass = 128 / kChunks, kPasses = kTile / kPass;
+        const int ch = ct % kChunks, row0 = ct / kChunks;
+        const uint64_t policy = l2_policy_evict_first();
+        const uint32_t v_at = smem_u32(sm + L::kVRing) + ct * 16;
+        auto fetch = [&](int i) {   // a group even where there is nothing to copy
+            if (i < n) {
+                const uint32_t k_at = smem_u32(sm + L::kKRing) + (i % kPlacesK) * L::kCodes;
+#pragma unroll
+                for (int x = 0; x < kPasses; ++x) {
+                    const int r = row0 + x * kPass;
+                    const int tile = s_tile[i * kUmmaPages + r / kPage];
+                    if (tile < 0) continue;
+                    const size_t from = (static_cast<size_t>(tile) * kPage + r % kPage) * HD + ch * 16;
+                    const int at = HD == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
+                    copy_async<16>(k_at + r * HD + (at << 4), p.k_codes + from, policy);
+                    copy_async<16>(v_at + (i % kDepth) * L::kCodes + x * 2048, p.v_codes + from, policy);
+                }
+            }
+            copies_commit();
+        };
+        for (int i = 0; i < kDepth; ++i) fetch(i);
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
         for (int i = 0; i < n; ++i) {
-            const int c = i % kTurns, vi = i % L::kV;
+            const int c = i % kTurns;
             if (i == end) {      // a segment begins: its query rows, all loads in flight at once
                 const int4 info = s_info[i];
                 seg = i;
@@ -341,49 +338,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
+            copies_wait<kDepth - 1>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[i % kPlacesK]);
+            uint4 v[kPasses];
+#pragma unroll
+            for (int x = 0; x < kPasses; ++x)
+                v[x] = *reinterpret_cast<const uint4*>(sm + L::kVRing + (i % kDepth) * L::kCodes + x * 2048 + ct * 16);
             if (i >= kTurns) ok = wait(&pv_done[c], turn(i) ^ 1u);
-            ok = ok && wait(&v_full[vi], static_cast<uint32_t>((i / L::kV) & 1));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int e0 = (s_info[seg].z + i - seg) * kTile;
-            const int e = e0 + row;
             const bool inner = e0 + kTile - 1 <= S;
-            const uint8_t* src = sm + L::kVRing + vi * L::kCodes + row * HD;
-            uint8_t* dst = sm + L::kConv + c * L::kCvTile + row * 128;
-            uint4 v[HD / 32];
-#pragma unroll
-            for (int x = 0; x < HD / 32; ++x) {
-                const int ch = half * (HD / 32) + x;
-                v[x] = *reinterpret_cast<const uint4*>(src + ((HD == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4));
-            }
             if (!inner) {
-                int nan = 0;
 #pragma unroll
-                for (int x = 0; x < HD / 32; ++x) {
-                    v[x].x = e > last ? 0u : without_nan(v[x].x, nan);
-                    v[x].y = e > last ? 0u : without_nan(v[x].y, nan);
-                    v[x].z = e > last ? 0u : without_nan(v[x].z, nan);
-                    v[x].w = e > last ? 0u : without_nan(v[x].w, nan);
+                for (int x = 0; x < kPasses; ++x) {
+                    const int r = row0 + x * kPass;
+                    const bool out = e0 + r > last;
+                    int nan = 0;
+                    v[x].x = out ? 0u : without_nan(v[x].x, nan);
+                    v[x].y = out ? 0u : without_nan(v[x].y, nan);
+                    v[x].z = out ? 0u : without_nan(v[x].z, nan);
+                    v[x].w = out ? 0u : without_nan(v[x].w, nan);
+#pragma unroll
+                    for (int d = 1; d < kChunks; d <<= 1) nan |= __shfl_xor_sync(0xffffffffu, nan, d);
+                    if (ch == 0) s_nan[c * kTile + r] = static_cast<uint8_t>(nan);
                 }
-                nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
-                if (half == 0) s_nan[c * kTile + row] = static_cast<uint8_t>(nan);
             }
+            // 32 bytes of fp16 a chunk; which half goes first keeps the banks apart
+            uint8_t* dst = sm + L::kConv + c * L::kCvTile + (ch >> 2) * kTile * 128;
+            const int j0 = 2 * (ch & 3), odd = (ch >> 2) & 1;
 #pragma unroll
-            for (int x = 0; x < HD / 32; ++x) {
-                const int ch = half * (HD / 32) + x, j0 = 2 * (ch & 3);
-                uint8_t* d = dst + (ch >> 2) * kTile * 128;
-                *reinterpret_cast<uint4*>(d + ((j0 ^ (row & 7)) << 4)) =
-                    make_uint4(widen_lo(v[x].x), widen_hi(v[x].x), widen_lo(v[x].y), widen_hi(v[x].y));
-                *reinterpret_cast<uint4*>(d + (((j0 + 1) ^ (row & 7)) << 4)) =
-                    make_uint4(widen_lo(v[x].z), widen_hi(v[x].z), widen_lo(v[x].w), widen_hi(v[x].w));
+            for (int x = 0; x < kPasses; ++x) {
+                const int r = row0 + x * kPass;
+                const uint4 a = make_uint4(widen_lo(v[x].x), widen_hi(v[x].x), widen_lo(v[x].y), widen_hi(v[x].y));
+                const uint4 b = make_uint4(widen_lo(v[x].z), widen_hi(v[x].z), widen_lo(v[x].w), widen_hi(v[x].w));
+                *reinterpret_cast<uint4*>(dst + r * 128 + (((j0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+                *reinterpret_cast<uint4*>(dst + r * 128 + (((j0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&cv_full[c]);
-                mbar_arrive(&v_empty[vi]);
-            }
+            if (lane == 0) mbar_arrive(&cv_full[c]);
+            // the next unit's copies: K's place is free once S of the unit before this one is complete
+            if (i >= 1) ok = wait(&s_full[(i - 1) % kTurns], turn(i - 1));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            fetch(i + kDepth);
         }
+        copies_wait<0>();
     } else {
         // ------------------------------------------------ softmax: thread = query row
         const int grp = warp >> 2, row = tid & 127;
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             seg += len;
         }
-        zero_idle_rows_by<kUmmaPages, kRows>(p, HD, warp, kSoft / 32);
+        if (idle) zero_idle_rows_by<kUmmaPages, kRows>(p, HD, warp, kSoft / 32);
     }
     if (!ok) {
         s_abort = 1;              // the other roles' waits end too
@@ -589,19 +592,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HD>
-int launch_hd(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, cudaStream_t s) {
+int launch_hd(const Kv8Params& p, const Plan& a, cudaStream_t s) {
     auto kern = k_attn_kv8_umma<HD>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::kBytes));
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, tk, tv, p));
+    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, p));
     return PE_OK;
 }
 
 }  // namespace
 
 namespace kv8 {
-int launch_umma(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, const Plan& a, int hd,
-                cudaStream_t s) {
-    return hd == 128 ? launch_hd<128>(tk, tv, p, a, s) : launch_hd<64>(tk, tv, p, a, s);
+int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
+    return hd == 128 ? launch_hd<128>(p, a, s) : launch_hd<64>(p, a, s);
 }
 }  // namespace kv8
 }  // namespace pe
