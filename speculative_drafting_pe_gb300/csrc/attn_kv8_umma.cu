@@ -3,21 +3,23 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (448 threads):
-//   warps 10-13 loaders and converters. Each thread fetches 16-byte chunks of
-//               K and V, kDepth units ahead, by asynchronous copies: K to
+// Roles (640 threads; the registers move to the softmax):
+//   warps 8-11, 12-15  two groups of loaders and converters, which take the
+//               units in turn. Each thread fetches 16-byte chunks of K and V,
+//               two of its group's units ahead, by asynchronous copies: K to
 //               where the MMA reads it (the swizzle of a K-major operand), V
 //               to a place of the thread's own. V codes then become an fp16
 //               tile (fp16 holds every E4M3 value; 128-byte swizzle,
 //               entry-major, read as an MN-major operand), V of entries that
-//               no row sees zero. At the start of a segment the query rows:
-//               shifted by a power of two per row so that the largest value
-//               lies in [128, 256) and split into two E4M3 terms, q = hi + lo,
-//               which hold the 8 bits of a bf16 value exactly down to 1/1024
-//               of the row's largest and to 2^-18 of that below.
-//   warp 8      one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
+//               no row sees zero. The group of a segment's first unit also
+//               brings its query rows: shifted by a power of two per row so
+//               that the largest value lies in [128, 256) and split into two
+//               E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16 value
+//               exactly down to 1/1024 of the row's largest and to 2^-18 of
+//               that below.
+//   warp 16     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
 //               N=64, E4M3 operands: the codes themselves)
-//   warp 9      one elected lane issues O += P_t V_t (fp16, A = P_t from
+//   warp 17     one elected lane issues O += P_t V_t (fp16, A = P_t from
 //               tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
@@ -32,10 +34,10 @@
 // warp that, 1550 cycles a unit, was what bounded the kernel.
 //
 // TMA boxes of one page (16 rows) took about 150 cycles each, whoever issued
-// them, 1300 cycles a unit; the copies of 128 threads take none of a unit's
-// time. K codes as MMA operands leave only V to be widened: with K widened too the
-// shared memory carried 128 KB a unit, a quarter more than now, at 128 bytes a
-// cycle the first limit of the kernel.
+// them, 1300 cycles a unit; one group of loaders 1800 (100 to 500 cycles for
+// each of its waits, its copies and the conversion). K codes as MMA operands
+// leave only V to be widened: with K widened too the shared memory carried
+// 128 KB a unit, a quarter more than now, at 128 bytes a cycle.
 #include "attn_kv8.cuh"
 
 namespace pe {
@@ -43,15 +45,21 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 640;
 constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpS = 8, kWarpPv = 9, kWarpConv = 10;
+constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17;
 constexpr int kTurns = 4;                   // places of fp16 V tiles and scores
-constexpr int kDepth = 4;                   // units whose copies are in flight
+constexpr int kDepth = 4;                   // units whose copies are in flight, half of them each group's
 constexpr int kPlacesK = kDepth + 1;
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
+
+// Registers of a thread: at launch, and in the softmax, loader and issuing
+// warpgroups afterwards. What the one side gains the others give: setmaxnreg
+// waits for registers that the launch did not bring.
+constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsConv = 80, kRegsIssue = 64;
+static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegsLaunch, "registers of a block");
 
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -123,7 +131,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 template <int HD>
 struct Layout {
-    static constexpr int kSub = HD / 64;                     // 128-byte sub-tiles of an fp16 row
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
     static constexpr int kQTerm = kRows * HD;                // hi or lo
@@ -202,7 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
-    if (warp == kWarpS || warp == kWarpPv) {
+    if (warp >= kWarpS) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+      if (warp <= kWarpPv) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
         const bool scores = warp == kWarpS;
@@ -252,84 +261,108 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         __syncwarp();
+      }
     } else if (warp >= kWarpConv) {
-        const int ct = tid - kWarpConv * 32;
-        // chunk `ch` of the unit's entries row0, row0 + kPass, ...
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        const int grp = (warp - kWarpConv) >> 2, ct = tid & 127;
+        // this thread's chunk of row `row` of pages page0 (+ 1 pass by pass of
+        // 128-wide rows, + 2 of 64-wide ones)
         constexpr int kChunks = HD / 16, kPass = 128 / kChunks, kPasses = kTile / kPass;
-        const int ch = ct % kChunks, row0 = ct / kChunks;
+        const int ch = ct % kChunks, row0 = ct / kChunks, row = row0 % kPage, page_step = kPass / kPage;
         const uint64_t policy = l2_policy_evict_first();
+        const uint8_t* k_from = p.k_codes + row * HD + ch * 16;
+        const uint8_t* v_from = p.v_codes + row * HD + ch * 16;
+        const int at = HD == 128 ? ch ^ (row0 & 7) : ch ^ ((row0 >> 1) & 3);
+        const uint32_t k_at = smem_u32(sm + L::kKRing) + row0 * HD + (at << 4);
         const uint32_t v_at = smem_u32(sm + L::kVRing) + ct * 16;
-        auto fetch = [&](int i) {   // a group even where there is nothing to copy
+        auto fetch = [&](int i) {   // a group of copies even where there is nothing to copy
             if (i < n) {
-                const uint32_t k_at = smem_u32(sm + L::kKRing) + (i % kPlacesK) * L::kCodes;
+                const int* tiles = s_tile + i * kUmmaPages + row0 / kPage;
+                const uint32_t k_to = k_at + (i % kPlacesK) * L::kCodes, v_to = v_at + (i % kDepth) * L::kCodes;
 #pragma unroll
                 for (int x = 0; x < kPasses; ++x) {
-                    const int r = row0 + x * kPass;
-                    const int tile = s_tile[i * kUmmaPages + r / kPage];
+                    const int tile = tiles[x * page_step];
                     if (tile < 0) continue;
-                    const size_t from = (static_cast<size_t>(tile) * kPage + r % kPage) * HD + ch * 16;
-                    const int at = HD == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3);
-                    copy_async<16>(k_at + r * HD + (at << 4), p.k_codes + from, policy);
-                    copy_async<16>(v_at + (i % kDepth) * L::kCodes + x * 2048, p.v_codes + from, policy);
+                    const long long off = static_cast<long long>(tile) * (kPage * HD);
+                    copy_async<16>(k_to + x * 2048, k_from + off, policy);
+                    copy_async<16>(v_to + x * 2048, v_from + off, policy);
                 }
             }
             copies_commit();
         };
-        for (int i = 0; i < kDepth; ++i) fetch(i);
+        fetch(grp);
+        fetch(grp + 2);
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
-        for (int i = 0; i < n; ++i) {
+        for (int i = grp; i < n; i += 2) {
             const int c = i % kTurns;
-            if (i == end) {      // a segment begins: its query rows, all loads in flight at once
-                const int4 info = s_info[i];
-                seg = i;
-                end = i + min(info.w - info.z, n - i);
+            // segments that begin with this unit, or with the other group's before it
+            while (end <= i && ok) {
+                const int4 info = s_info[end];
+                seg = end;
+                end += min(info.w - info.z, n - end);
                 ++no;
                 const int b = info.x;
                 S = p.seq_lens[b];
                 const int rows = p.rows != nullptr ? p.rows[b] : p.K;
                 last = S + rows - 1;
+                if ((seg & 1) != grp) continue;      // the other group brings the queries
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
-                uint4 q[HD / 8];
+                // twice over the row, eight loads in flight at a time: its
+                // largest value, then its terms
+                const bool live = ct < rows * G;
+                constexpr int kHalf = HD / 16;
+                auto load = [&](uint4 (&q)[kHalf], int half) {
 #pragma unroll
-                for (int x = 0; x < HD / 8; ++x) {
-                    q[x] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ct < rows * G) q[x] = *reinterpret_cast<const uint4*>(src + x * 8);
+                    for (int x = 0; x < kHalf; ++x) {
+                        q[x] = make_uint4(0u, 0u, 0u, 0u);
+                        if (live) q[x] = *reinterpret_cast<const uint4*>(src + (half * kHalf + x) * 8);
+                    }
+                };
+                uint32_t top = 0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint4 q[kHalf];
+                    load(q, half);
+#pragma unroll
+                    for (int x = 0; x < kHalf; ++x) {
+                        const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
+                    }
                 }
                 // the tile's last reader: S of the segment two back
                 if (no >= 2) ok = wait(&q_empty[no & 1], static_cast<uint32_t>((no >> 1) & 1) ^ 1u);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                uint32_t top = 0;
-#pragma unroll
-                for (int x = 0; x < HD / 8; ++x) {
-                    const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
-                }
                 // the row times 2^(134 - E): its largest value lies in [128, 256)
                 const int E = min(max(static_cast<int>(top >> 23), 8), 254);
                 const float down = __uint_as_float(static_cast<uint32_t>(261 - E) << 23);
                 uint8_t* dst = sm + L::kQ + (no & 1) * 2 * L::kQTerm + ct * HD;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint4 q[kHalf];
+                    load(q, half);
 #pragma unroll
-                for (int x = 0; x < HD / 16; ++x) {
-                    const uint32_t w[8] = {q[2 * x].x, q[2 * x].y, q[2 * x].z, q[2 * x].w,
-                                           q[2 * x + 1].x, q[2 * x + 1].y, q[2 * x + 1].z, q[2 * x + 1].w};
-                    uint32_t hi[4], rest[4];
+                    for (int x = 0; x < kHalf / 2; ++x) {
+                        const uint32_t w[8] = {q[2 * x].x, q[2 * x].y, q[2 * x].z, q[2 * x].w,
+                                               q[2 * x + 1].x, q[2 * x + 1].y, q[2 * x + 1].z, q[2 * x + 1].w};
+                        uint32_t hi[4], rest[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float v0 = __uint_as_float(w[2 * y] << 16) * down, v1 = __uint_as_float(w[2 * y] & 0xFFFF0000u) * down;
-                        const float v2 = __uint_as_float(w[2 * y + 1] << 16) * down, v3 = __uint_as_float(w[2 * y + 1] & 0xFFFF0000u) * down;
-                        hi[y] = e4m3x4(v0, v1, v2, v3);
-                        const uint32_t a = widen_lo(hi[y]), d = widen_hi(hi[y]);
-                        const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
-                        const float2 fd = __half22float2(*reinterpret_cast<const __half2*>(&d));
-                        rest[y] = e4m3x4(v0 - fa.x, v1 - fa.y, v2 - fd.x, v3 - fd.y);
+                        for (int y = 0; y < 4; ++y) {
+                            const float v0 = __uint_as_float(w[2 * y] << 16) * down, v1 = __uint_as_float(w[2 * y] & 0xFFFF0000u) * down;
+                            const float v2 = __uint_as_float(w[2 * y + 1] << 16) * down, v3 = __uint_as_float(w[2 * y + 1] & 0xFFFF0000u) * down;
+                            hi[y] = e4m3x4(v0, v1, v2, v3);
+                            const uint32_t a = widen_lo(hi[y]), d = widen_hi(hi[y]);
+                            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+                            const float2 fd = __half22float2(*reinterpret_cast<const __half2*>(&d));
+                            rest[y] = e4m3x4(v0 - fa.x, v1 - fa.y, v2 - fd.x, v3 - fd.y);
+                        }
+                        const int part = half * (kHalf / 2) + x;   // 16 dimensions
+                        const int to = (HD == 128 ? part ^ (ct & 7) : part ^ ((ct >> 1) & 3)) << 4;
+                        *reinterpret_cast<uint4*>(dst + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(dst + L::kQTerm + to) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                     }
-                    const int at = (HD == 128 ? x ^ (ct & 7) : x ^ ((ct >> 1) & 3)) << 4;
-                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + L::kQTerm + at) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                 }
                 // E4M3 has no infinity: a row that holds one (or a NaN) is NaN
                 s_cs[(no & (kCsTurns - 1)) * kRows + ct] =
@@ -338,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
-            copies_wait<kDepth - 1>();
+            if (!ok) break;
+            copies_wait<kDepth / 2 - 1>();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_full[i % kPlacesK]);
@@ -389,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         copies_wait<0>();
     } else {
         // ------------------------------------------------ softmax: thread = query row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int grp = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_mine = t_o + lane_off + static_cast<uint32_t>(grp * HD);
@@ -594,6 +629,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 int launch_hd(const Kv8Params& p, const Plan& a, cudaStream_t s) {
     auto kern = k_attn_kv8_umma<HD>;
+    // the register split needs what it was reckoned with
+    static const int regs = [&] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != kRegsLaunch) {
+        set_error("attention: the kernel was built with " + std::to_string(regs) + " registers a thread, not " +
+                  std::to_string(kRegsLaunch));
+        return PE_ERR_UNSUPPORTED;
+    }
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::kBytes));
     PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, p));
     return PE_OK;
