@@ -7,6 +7,7 @@ there is no fallback path.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -554,23 +555,24 @@ def verify_rebuild_refeed(drafts, target_tokens, page_table, num_pages, n_real, 
 #
 # The calls below run where their tensors live, on that device's current
 # stream unless `stream` is given; all tensors of a call are on one device.
+# They stand in the loop of a server, where a call of a few microseconds on the
+# GPU waits for the host, so their checks are plain comparisons.
 
 _INT, _BYTE, _FLOAT, _BF16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
 
 
-def _ints(dev, shape, **tensors):
-    """int32 tensors of one shape, contiguous on `dev`."""
-    for name, t in tensors.items():
-        if t.dtype is not _INT or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {shape} on {dev}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _need_is(name, t, dtype, dev, shape):
+    """t is a contiguous tensor of this type and shape on dev."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _run(fn, dev, stream, *args):
     """Call an entry point with `dev` current, on `stream` or the device's current stream."""
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got {dev}")
     index = dev.index
+    if index is None or dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
         rc = fn(*args, raw)
@@ -584,10 +586,13 @@ def _run(fn, dev, stream, *args):
 def _row_stride(t, name):
     """Elements between the rows of t [..., heads, hd] (or [N, Kd]): its last dimensions are dense, its leading
     ones one run of rows."""
-    lead = t.dim() - (2 if t.dim() > 2 else 1)
-    sizes, strides = t.shape, t.stride()
-    dense = 1
-    for d in range(t.dim() - 1, lead - 1, -1):
+    sizes = t.shape
+    inner = 2 if len(sizes) > 2 else 1
+    if t.is_contiguous():
+        return sizes[-1] * sizes[-2] if inner == 2 else sizes[-1]
+    strides = t.stride()
+    lead, dense = len(sizes) - inner, 1
+    for d in range(len(sizes) - 1, lead - 1, -1):
         if sizes[d] != 1 and strides[d] != dense:
             raise ValueError(f"{name}: the last dimensions must be contiguous")
         dense *= sizes[d]
@@ -616,18 +621,21 @@ def linear_w4(w_codes, w_scale, x, group, zeros=None, y=None, stream=None):
         raise ValueError("w_codes must be contiguous uint8 [M, Kd/2]")
     if x.dtype is not _BF16 or x.device != dev:
         raise ValueError(f"x must be bfloat16 on {dev}")
-    shape = (M, -(-Kd // group) if group > 0 else 0)
-    kind = {_BF16: PE_DTYPE_BF16, _FLOAT: PE_DTYPE_FP32}.get(w_scale.dtype)
-    if kind is None or w_scale.device != dev or tuple(w_scale.shape) != shape or not w_scale.is_contiguous():
-        raise ValueError(f"w_scale must be contiguous bfloat16 or float32 {shape} on {dev}")
-    if zeros is not None and (zeros.dtype is not _BYTE or zeros.device != dev or tuple(zeros.shape) != shape or
-                              not zeros.is_contiguous()):
-        raise ValueError(f"zeros must be contiguous uint8 {shape} on {dev}")
+    if group < 1:
+        raise ValueError("group must be 32, 64 or 128")
+    shape = (M, -(-Kd // group))
+    kind = w_scale.dtype
+    if kind is not _BF16 and kind is not _FLOAT:
+        raise ValueError("w_scale must be bfloat16 or float32")
+    _need_is("w_scale", w_scale, kind, dev, shape)
+    if zeros is not None:
+        _need_is("zeros", zeros, _BYTE, dev, shape)
     if y is None:
         y = torch.empty((N, M), dtype=_FLOAT, device=dev)
-    elif y.dtype is not _FLOAT or y.device != dev or tuple(y.shape) != (N, M):
+    elif y.dtype is not _FLOAT or y.device != dev or y.shape != (N, M):
         raise ValueError(f"y must be float32 {(N, M)} on {dev}")
-    _run(lib.pe_linear_w4, dev, stream, M, N, Kd, group, w_codes.data_ptr(), kind, w_scale.data_ptr(),
+    _run(lib.pe_linear_w4, dev, stream, M, N, Kd, group, w_codes.data_ptr(),
+         PE_DTYPE_BF16 if kind is _BF16 else PE_DTYPE_FP32, w_scale.data_ptr(),
          None if zeros is None else zeros.data_ptr(), x.data_ptr(), _row_stride(x, "x"), y.data_ptr(),
          _row_stride(y, "y"))
     return y
@@ -640,19 +648,21 @@ def assign_pages(seq_lens, new_lens, page_counts, page_table, free_pages, free_c
     slot_mapping [B, n_max], page_counts [B], free_count [1], status [B]."""
     lib = load()
     dev = seq_lens.device
-    B = seq_lens.shape[0]
-    _ints(dev, (B,), seq_lens=seq_lens, new_lens=new_lens, page_counts=page_counts)
-    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
-    _ints(dev, (free_pages.numel(),), free_pages=free_pages)
-    _ints(dev, (1,), free_count=free_count)
-    o = dict(slot_mapping=torch.empty((B, n_max), dtype=_INT, device=dev),
-             page_counts=torch.empty(B, dtype=_INT, device=dev), free_count=torch.empty(1, dtype=_INT, device=dev),
-             status=torch.empty(B, dtype=_INT, device=dev))
+    shape = seq_lens.shape
+    _need_is("seq_lens", seq_lens, _INT, dev, (shape[0],))
+    _need_is("new_lens", new_lens, _INT, dev, shape)
+    _need_is("page_counts", page_counts, _INT, dev, shape)
+    B, max_pages = shape[0], page_table.shape[-1]
+    _need_is("page_table", page_table, _INT, dev, (B, max_pages))
+    cap = free_pages.shape[0]
+    _need_is("free_pages", free_pages, _INT, dev, (cap,))
+    _need_is("free_count", free_count, _INT, dev, (1,))
+    slots = torch.empty((B, n_max), dtype=_INT, device=dev)
+    counts, left, status = torch.empty_like(seq_lens), torch.empty_like(free_count), torch.empty_like(seq_lens)
     _run(lib.pe_assign_pages, dev, stream, B, seq_lens.data_ptr(), new_lens.data_ptr(), page_counts.data_ptr(),
-         o["page_counts"].data_ptr(), page_table.data_ptr(), page_table.shape[1], num_pages, free_pages.data_ptr(),
-         free_pages.shape[0], free_count.data_ptr(), o["free_count"].data_ptr(), n_max, o["slot_mapping"].data_ptr(),
-         o["status"].data_ptr())
-    return o
+         counts.data_ptr(), page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap,
+         free_count.data_ptr(), left.data_ptr(), n_max, slots.data_ptr(), status.data_ptr())
+    return dict(slot_mapping=slots, page_counts=counts, free_count=left, status=status)
 
 
 def release_pages(keep_lens, page_counts, page_table, free_pages, free_count, num_pages, stream=None):
@@ -662,31 +672,33 @@ def release_pages(keep_lens, page_counts, page_table, free_pages, free_count, nu
     returns status [B]."""
     lib = load()
     dev = keep_lens.device
-    B = keep_lens.shape[0]
-    _ints(dev, (B,), keep_lens=keep_lens, page_counts=page_counts)
-    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
-    _ints(dev, (free_pages.numel(),), free_pages=free_pages)
-    _ints(dev, (1,), free_count=free_count)
-    status = torch.empty(B, dtype=_INT, device=dev)
+    shape = keep_lens.shape
+    _need_is("keep_lens", keep_lens, _INT, dev, (shape[0],))
+    _need_is("page_counts", page_counts, _INT, dev, shape)
+    B, max_pages = shape[0], page_table.shape[-1]
+    _need_is("page_table", page_table, _INT, dev, (B, max_pages))
+    cap = free_pages.shape[0]
+    _need_is("free_pages", free_pages, _INT, dev, (cap,))
+    _need_is("free_count", free_count, _INT, dev, (1,))
+    status = torch.empty_like(keep_lens)
     _run(lib.pe_release_pages, dev, stream, B, keep_lens.data_ptr(), page_counts.data_ptr(), page_counts.data_ptr(),
-         page_table.data_ptr(), page_table.shape[1], num_pages, free_pages.data_ptr(), free_pages.shape[0],
-         free_count.data_ptr(), free_count.data_ptr(), status.data_ptr())
+         page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap, free_count.data_ptr(),
+         free_count.data_ptr(), status.data_ptr())
     return status
 
 
 def _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale):
     """The paged 8-bit cache of a call; returns its number of pages."""
-    _ints(dev, (B,), seq_lens=seq_lens)
+    _need_is("seq_lens", seq_lens, _INT, dev, (B,))
     if rows is not None:
-        _ints(dev, (B,), rows=rows)
-    _ints(dev, (B, page_table.shape[-1]), page_table=page_table)
+        _need_is("rows", rows, _INT, dev, (B,))
+    _need_is("page_table", page_table, _INT, dev, (B, page_table.shape[-1]))
     pages = k_codes.shape[0]
-    for name, t, dtype, shape in (("k_codes", k_codes, _BYTE, (pages, nkv, 16, hd)),
-                                  ("v_codes", v_codes, _BYTE, (pages, nkv, 16, hd)),
-                                  ("k_scale", k_scale, _FLOAT, (pages, nkv)),
-                                  ("v_scale", v_scale, _FLOAT, (pages, nkv))):
-        if t.dtype is not dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {dev}")
+    codes, scales = (pages, nkv, 16, hd), (pages, nkv)
+    _need_is("k_codes", k_codes, _BYTE, dev, codes)
+    _need_is("v_codes", v_codes, _BYTE, dev, codes)
+    _need_is("k_scale", k_scale, _FLOAT, dev, scales)
+    _need_is("v_scale", v_scale, _FLOAT, dev, scales)
     return pages
 
 
@@ -703,9 +715,9 @@ def kv8_append(k, v, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, r
         raise ValueError(f"k and v must be bfloat16 [B, n, nkv, hd] on {dev}")
     pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
     if status is None:
-        status = torch.empty(B, dtype=_INT, device=dev)
+        status = torch.empty_like(seq_lens)
     else:
-        _ints(dev, (B,), status=status)
+        _need_is("status", status, _INT, dev, (B,))
     _run(lib.pe_kv8_append, dev, stream, B, n, nkv, hd, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
          _row_stride(v, "v"), seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(),
          page_table.shape[1], pages, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -713,9 +725,12 @@ def kv8_append(k, v, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, r
     return status
 
 
-def _kv8_scratch(B, K, nq, nkv, hd, max_pages):
+@functools.lru_cache(maxsize=4096)
+def _kv8_scratch(index, B, K, nq, nkv, hd, max_pages):
+    """Floats of scratch of an attention call on device `index`."""
     n = ctypes.c_int64(0)
-    _check(load().pe_attention_kv8_scratch(B, K, nq, nkv, hd, max_pages, ctypes.byref(n)))
+    with torch.cuda.device(index):
+        _check(load().pe_attention_kv8_scratch(B, K, nq, nkv, hd, max_pages, ctypes.byref(n)))
     return n.value
 
 
@@ -738,12 +753,13 @@ def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, s
     elif out.dtype is not _BF16 or out.device != dev or out.shape != q.shape:
         raise ValueError(f"out must be bfloat16 {tuple(q.shape)} on {dev}")
     if status is None:
-        status = torch.empty(B, dtype=_INT, device=dev)
+        status = torch.empty_like(seq_lens)
     else:
-        _ints(dev, (B,), status=status)
+        _need_is("status", status, _INT, dev, (B,))
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
     max_pages = page_table.shape[1]
-    with torch.cuda.device(dev):
-        need = _kv8_scratch(B, K, nq, nkv, hd, max_pages)
+    need = _kv8_scratch(dev.index, B, K, nq, nkv, hd, max_pages)
     ws = torch.empty(need, dtype=_FLOAT, device=dev)
     _run(lib.pe_attention_kv8, dev, stream, B, K, nq, nkv, hd, q.data_ptr(), _row_stride(q, "q"),
          seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(), max_pages, pages,
