@@ -66,9 +66,10 @@ struct Smem {
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
     static constexpr int kO = kRing;                         // [kSlots][kRows][HD] fp32
     static constexpr int kMl = kO + kSlots * kRows * HD * 4; // [2][kWarps][kRows] (max, sum)
-    static constexpr int kInfo = (kMl + 2 * kWarps * kRows * 8 + 15) / 16 * 16;
-    static constexpr int kUnit = kInfo + kMaxUnits * 16;     // tile, ks, vs
-    static constexpr int kBytes = kUnit + kMaxUnits * 12 + 1024;
+    static constexpr int kScale = kMl + 2 * kWarps * kRows * 8;   // [kWarps][kStages] (ks, vs)
+    static constexpr int kInfo = (kScale + kWarps * kStages * 8 + 15) / 16 * 16;
+    static constexpr int kUnit = kInfo + kMaxUnits * 16;     // tile
+    static constexpr int kBytes = kUnit + kMaxUnits * 4 + 1024;
     // 16-byte chunk c of row r of a slot stands at c ^ swizzle(r): the lanes
     // of a quarter warp (four row pairs, two runs of dimensions) meet no bank twice
     __device__ static __forceinline__ int swizzle(int r) {
@@ -94,20 +95,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_o = reinterpret_cast<float*>(sm + L::kO);
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
-    float* s_ks = reinterpret_cast<float*>(s_tile + kMaxUnits);
-    float* s_vs = s_ks + kMaxUnits;
 
     pdl_launch_dependents();
     int lo;
     bool idle;
-    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, s_ks, s_vs,
-                                                    reinterpret_cast<int2*>(sm), lo, idle);   // the list in the ring's place
+    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, reinterpret_cast<int2*>(sm), lo, idle);   // the list in the ring's place
 
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kTile + lane * kCols;
+    float2* scales = reinterpret_cast<float2*>(sm + L::kScale) + warp * kStages;
+    const uint32_t scales_at = smem_u32(scales) + lane * 4;
+    const float* scale_from = lane == 0 ? p.k_scale : p.v_scale;
     auto fetch = [&](int i, int st) {   // unit i into stage st; a group even where there is nothing to copy
         const int tile = i < n ? s_tile[i] : -1;
         if (tile >= 0) {
+            if (lane < 2) copy_async<4>(scales_at + st * 8, scale_from + tile, policy);
             // K rows g and g + 8, chunks t and t + 4 (of 64-wide rows: t); V rows 2t, 2t+1, 2t+8, 2t+9, part g
             const uint8_t* k = p.k_codes + static_cast<size_t>(tile) * L::kTile + g * HD + t * 16;
             const uint8_t* v = p.v_codes + static_cast<size_t>(tile) * L::kTile + 2 * t * HD + g * kCols;
@@ -195,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint8_t* kt = ring + st * 2 * L::kTile + lane * 16;
                 const uint8_t* vt = ring + st * 2 * L::kTile + L::kTile + lane * kCols;
-                const float ks = s_ks[i], vs = s_vs[i];
+                __syncwarp();   // the scales come by two lanes
+                const float ks = scales[st].x, vs = scales[st].y;
                 const int e0 = (page0 + i - seg) * kPage;   // the page's first entry
                 const bool inner = e0 + kPage - 1 <= S;     // every row sees all of it
 
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vw[x][0] = y.x; vw[x][1] = y.y;
                     }
                 }
+                __syncwarp();
                 fetch(i + kStages * kWarps, st);
                 st = st + 1 == kStages ? 0 : st + 1;
 
@@ -435,37 +439,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 // order. The part that CTA c left of a run of units [u0, u1) is its first one
 // where the run begins at or before c's share, its second one otherwise. A
 // thread per row and four dimensions; the parts are read eight at a time, all
-// loads of a batch in flight, and folded with a running maximum: with one part
-// at a time the loads' latency alone was 0.7 us a part.
+// loads of a batch in flight, and folded with a running maximum. Where rows
+// are few and parts many (one long request), SHARE warps take a row together,
+// each a run of its parts, and their sums meet in shared memory.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeBatch = 8;
 
-template <int HD>
+struct Joined {
+    float M = -INFINITY, bad = 0.f, total = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void raise(float top) {   // to a larger maximum
+        if (top > M) {
+            const float f = M == -INFINITY ? 0.f : ex2(M - top);
+            total *= f;
+            acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+            M = top;
+        }
+    }
+    // nothing seen, or a mark, adds nothing; a NaN sum goes on
+    __device__ __forceinline__ void add(float m, float l, const float4& o) {
+        if (l <= 0.f) return;
+        const float f = ex2(m - M);
+        total = fmaf(l, f, total);
+        acc.x = fmaf(o.x, f, acc.x);
+        acc.y = fmaf(o.y, f, acc.y);
+        acc.z = fmaf(o.z, f, acc.z);
+        acc.w = fmaf(o.w, f, acc.w);
+    }
+};
+
+template <int HD, int SHARE>
 __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, int tr, int ppu) {
-    constexpr int kPerRow = HD / 4, kBlockRows = kMergeThreads / kPerRow;
+    constexpr int kPerRow = HD / 4, kTeam = kPerRow * SHARE, kBlockRows = kMergeThreads / kTeam;
+    __shared__ float4 s_acc[SHARE > 1 ? kMergeThreads : 1];
+    __shared__ float3 s_sum[SHARE > 1 ? kMergeThreads : 1];
     pdl_wait();
     const int b = blockIdx.z, head = blockIdx.y;
     const int u_b = p.first[b], units = p.first[b + 1] - u_b, per = p.first[p.B + 1];
     const int G = p.nq / p.nkv;
     const int S = p.seq_lens[b], rows = p.rows != nullptr ? p.rows[b] : p.K;
-    if (units == 0) return;
+    const int rr = blockIdx.x * kBlockRows + threadIdx.x / kTeam;
+    const int piece = threadIdx.x % kTeam / kPerRow, d = (threadIdx.x % kPerRow) * 4;
+    if (units == 0 || blockIdx.x * kBlockRows >= rows * G) return;
     const int tiles = (rows * G + tr - 1) / tr;
     const int run = ((S + rows + kPage - 1) / kPage + ppu - 1) / ppu;
-    const int d = (threadIdx.x % kPerRow) * 4;
-    for (int rr = blockIdx.x * kBlockRows + threadIdx.x / kPerRow; rr < rows * G; rr += gridDim.x * kBlockRows) {
-        const int tile = rr / tr, r = rr - tile * tr;
-        const int u0 = u_b + (head * tiles + tile) * run, u1 = u0 + run;
-        const int c0 = u0 / per, c1 = (u1 - 1) / per;
-        if (c0 == c1) continue;   // written by its CTA
-        float M = -INFINITY, bad = 0.f, total = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; c += kMergeBatch) {
+    const int tile = rr / tr, r = rr - tile * tr;
+    const int u0 = u_b + (head * tiles + tile) * run, u1 = u0 + run;
+    const int c0 = u0 / per, c1 = (u1 - 1) / per;
+    const bool mine = rr < rows * G && c0 != c1;   // one part alone was written by its CTA
+    Joined j;
+    if (mine) {
+        const int each = (c1 - c0 + SHARE) / SHARE;
+        const int from = c0 + piece * each, to = min(c1, from + each - 1);
+        for (int c = from; c <= to; c += kMergeBatch) {
             float mv[kMergeBatch], lv[kMergeBatch];
             float4 ov[kMergeBatch];
 #pragma unroll
             for (int x = 0; x < kMergeBatch; ++x) {
-                lv[x] = 0.f;
-                if (c + x <= c1) {
+                mv[x] = lv[x] = 0.f;
+                if (c + x <= to) {
                     const int part = 2 * (c + x) + (u0 <= (c + x) * per ? 0 : 1);
                     const float* src = p.part + static_cast<size_t>(part) * part_floats(tr, HD);
                     mv[x] = src[tr * HD + r];
@@ -473,39 +505,39 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, 
                     ov[x] = *reinterpret_cast<const float4*>(src + r * HD + d);
                 }
             }
-            float top = M;
+            float top = j.M;
 #pragma unroll
             for (int x = 0; x < kMergeBatch; ++x) {
-                if (lv[x] < 0.f) bad = fminf(bad, lv[x]);
+                if (lv[x] < 0.f) j.bad = fminf(j.bad, lv[x]);
                 else if (lv[x] != 0.f) top = fmaxf(top, mv[x]);
             }
-            if (top > M) {
-                const float f = M == -INFINITY ? 0.f : ex2(M - top);
-                total *= f;
-                acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-                M = top;
-            }
+            j.raise(top);
 #pragma unroll
-            for (int x = 0; x < kMergeBatch; ++x) {
-                if (lv[x] <= 0.f) continue;   // nothing seen, or a mark; a NaN sum goes on
-                if (c + x > c1) continue;
-                const float f = ex2(mv[x] - M);
-                total = fmaf(lv[x], f, total);
-                acc.x = fmaf(ov[x].x, f, acc.x);
-                acc.y = fmaf(ov[x].y, f, acc.y);
-                acc.z = fmaf(ov[x].z, f, acc.z);
-                acc.w = fmaf(ov[x].w, f, acc.w);
-            }
+            for (int x = 0; x < kMergeBatch; ++x)
+                if (c + x <= to) j.add(mv[x], lv[x], ov[x]);
         }
-        if (head == 0 && rr == 0 && d == 0) p.status[b] = status_of(bad);
-        const float inv = total == 0.f || bad < 0.f ? 0.f : 1.f / total;
-        const int j = rr / G;
-        __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
-            p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out + static_cast<long long>(head * G + rr - j * G) * HD + d);
-        if (bad < 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        dst[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        dst[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     }
+    if constexpr (SHARE > 1) {
+        s_acc[threadIdx.x] = j.acc;
+        s_sum[threadIdx.x] = make_float3(j.M, j.total, j.bad);
+        __syncthreads();
+        if (piece != 0) return;
+        for (int x = 1; x < SHARE; ++x) {
+            const float3 o = s_sum[threadIdx.x + x * kPerRow];
+            j.bad = fminf(j.bad, o.z);
+            j.raise(o.y != 0.f ? fmaxf(j.M, o.x) : j.M);
+            j.add(o.x, o.y, s_acc[threadIdx.x + x * kPerRow]);
+        }
+    }
+    if (!mine) return;
+    if (head == 0 && rr == 0 && d == 0) p.status[b] = status_of(j.bad);
+    const float inv = j.total == 0.f || j.bad < 0.f ? 0.f : 1.f / j.total;
+    if (j.bad < 0.f) j.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int row = rr / G;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+        p.out + (static_cast<long long>(b) * p.K + row) * p.ld_out + static_cast<long long>(head * G + rr - row * G) * HD + d);
+    dst[0] = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
+    dst[1] = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
 }
 
 // Query rows of a head from which the tensor-memory kernel is taken: up to 16
@@ -572,13 +604,12 @@ int check_shape(int B, int K, int nq, int nkv, int hd, int max_pages) {
 
 namespace kv8 {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
-    // blocks for every row while the heads are few, a block for several rows
-    // where there are enough of them
-    const int block_rows = kMergeThreads / (hd / 4);
-    const int all = (p.K * (p.nq / p.nkv) + block_rows - 1) / block_rows;
-    const int some = std::max(1, 2048 / (p.B * p.nkv));
-    const dim3 grid(all < some ? all : some, p.nkv, p.B);
-    auto kern = hd == 128 ? k_kv8_merge<128> : k_kv8_merge<64>;
+    // four warps to a row where that leaves at most some waves of blocks
+    const int rows = p.K * (p.nq / p.nkv);
+    const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;
+    const int block_rows = kMergeThreads / (hd / 4) / (share ? 4 : 1);
+    const dim3 grid((rows + std::max(1, block_rows) - 1) / std::max(1, block_rows), p.nkv, p.B);
+    auto kern = hd == 128 ? (share ? k_kv8_merge<128, 4> : k_kv8_merge<128, 1>) : (share ? k_kv8_merge<64, 4> : k_kv8_merge<64, 1>);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kMergeThreads), 0, s, true, p, a.tr, a.ppu));
     return PE_OK;
 }

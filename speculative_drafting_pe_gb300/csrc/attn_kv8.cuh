@@ -92,13 +92,13 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
-// asynchronous copies of this thread (16 or 8 bytes), in groups
+// asynchronous copies of this thread (4, 8 or 16 bytes), in groups
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t smem, const void* src, uint64_t policy) {
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "l"(policy) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2;" ::"r"(smem), "l"(src), "l"(policy) : "memory");
+        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %3, %2;" ::"r"(smem), "l"(src), "l"(policy), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -133,15 +133,14 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 // info[i] of a unit that begins a segment = {request, head * tiles + row tile,
 // unit within its run, units of the run}; of page q of unit i, entry
 // i * PPU + q of tile (page * nkv + head, -1: outside the pool, -2: behind the
-// request's last page), ks and vs. Returns the number of units; lo is the
+// request's last page). Returns the number of units; lo is the
 // first one, and idle whether zero_idle_rows_by has work. All NT threads of the CTA; every CTA's share is at least
 // `least` and at most max_units (the planner's grid sees to that).
 // `list` is scratch for two ints per unit of the share. The requests of the share are listed first and
 // then all threads look their pages up, so the dependent loads (page, scales)
 // of all pages are in flight together.
 template <int NT, int PPU, int TR>
-__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, float* ks, float* vs, int2* list,
-                            int& lo, bool& idle) {
+__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int2* list, int& lo, bool& idle) {
     constexpr int kWarps = NT / 32;
     __shared__ int s_scan[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,8 +219,6 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
             id = id >= 0 && id < p.num_pages ? id * p.nkv + pair / r.tiles : -1;
         }
         tile[x] = id;
-        ks[x] = id >= 0 ? p.k_scale[id] : 0.f;
-        vs[x] = id >= 0 ? p.v_scale[id] : 0.f;
         if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(b, pair, at_run, r.run);
     }
     __syncthreads();
@@ -241,7 +238,7 @@ struct Plan {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
-constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 192;
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 432;
 
 }  // namespace kv8
 }  // namespace pe

@@ -53,10 +53,11 @@ constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17;
 constexpr int kTurns = 4;                   // places of fp16 V tiles and scores
 constexpr int kDepth = 4;                   // units whose copies are in flight, half of them each group's
 constexpr int kPlacesK = kDepth + 1;
+constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 // Registers of a thread: at launch, and in the softmax, loader and issuing
-// warpgroups afterwards. What the one side gains the others give: setmaxnreg
+// warpgroups afterwards. What the softmax gains the others give: setmaxnreg
 // waits for registers that the launch did not bring.
 constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsConv = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegsLaunch, "registers of a block");
@@ -140,9 +141,10 @@ struct Layout {
     static constexpr int kVRing = kKRing + kPlacesK * kCodes;
     static constexpr int kInfo = kVRing + kDepth * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
-    static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 12;   // [kCsTurns][kRows]
+    static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 4;   // [kCsTurns][kRows]
     static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
-    static constexpr int kNan = kEx + 2 * kRows * 16;        // [kTurns][kTile] bytes
+    static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages]
+    static constexpr int kNan = kScale + kScales * 32;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
     // k_full [kPlacesK], cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
     static constexpr int kBars = kPlacesK + 4 * kTurns + 4;
@@ -160,10 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const volatile int* abort = &s_abort;
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
-    float* s_ks = reinterpret_cast<float*>(s_tile + kUmmaUnits * kUmmaPages);
-    float* s_vs = s_ks + kUmmaUnits * kUmmaPages;
     float* s_cs = reinterpret_cast<float*>(sm + L::kCs);
     float4* s_ex = reinterpret_cast<float4*>(sm + L::kEx);
+    float* s_scale = reinterpret_cast<float*>(sm + L::kScale);
     uint8_t* s_nan = sm + L::kNan;
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t* cv_full = k_full + kPlacesK;
@@ -199,9 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     int lo;
     bool idle;
-    const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile, s_ks, s_vs,
-                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo,
-                                                               idle);
+    const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile,
+                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo, idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
@@ -287,6 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     copy_async<16>(k_to + x * 2048, k_from + off, policy);
                     copy_async<16>(v_to + x * 2048, v_from + off, policy);
                 }
+                if (ct < 2 * kUmmaPages) {   // a page's K or V scale each
+                    const int tile = s_tile[i * kUmmaPages + ct % kUmmaPages];
+                    float* to = s_scale + (i % kScales) * 8 + ct;
+                    if (tile >= 0) copy_async<4>(smem_u32(to), (ct < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
+                    else *to = 0.f;
+                }
             }
             copies_commit();
         };
@@ -309,10 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
-                // twice over the row, eight loads in flight at a time: its
+                // twice over the row, half of it at a time (registers): its
                 // largest value, then its terms
                 const bool live = ct < rows * G;
                 constexpr int kHalf = HD / 16;
+                if (live) {
+#pragma unroll
+                    for (int x = 0; x < HD / 64; ++x)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(src + x * 64));
+                }
                 auto load = [&](uint4 (&q)[kHalf], int half) {
 #pragma unroll
                     for (int x = 0; x < kHalf; ++x) {
@@ -449,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 if (busy) {
                     if (i == first) cs = s_cs[(no & (kCsTurns - 1)) * kRows + row];
-                    const float4 ks = *reinterpret_cast<const float4*>(s_ks + i * kUmmaPages);
-                    const float4 vs = *reinterpret_cast<const float4*>(s_vs + i * kUmmaPages);
+                    const float4 ks = *reinterpret_cast<const float4*>(s_scale + (i % kScales) * 8);
+                    const float4 vs = *reinterpret_cast<const float4*>(s_scale + (i % kScales) * 8 + 4);
                     const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
                     float s[kTile];
                     tmem_ld64(t_s, s);
