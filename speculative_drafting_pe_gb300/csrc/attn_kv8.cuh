@@ -238,7 +238,7 @@ struct Plan {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
-constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 432;
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448;
 
 }  // namespace kv8
 }  // namespace pe

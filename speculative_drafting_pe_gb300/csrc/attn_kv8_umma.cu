@@ -27,8 +27,8 @@
 //               the other; they meet at the end of a segment.
 // Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
 // up to four units ahead of P.V, so a group finds its next scores ready when it
-// is done with the last. V tiles and S_t have four places each and "P_t V_t is
-// complete" frees both, as "S_t is complete" frees K_t's place: one commit for
+// is done with the last. "P_t V_t is complete" frees the
+// places of V_t and S_t, as "S_t is complete" frees K_t's place: one commit for
 // each product. Waits, MMAs and commits cost their warp
 // about 100, 40 and 100 cycles each; with both products and six commits in one
 // warp that, 1550 cycles a unit, was what bounded the kernel.
@@ -50,9 +50,10 @@ constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17;
-constexpr int kTurns = 4;                   // places of fp16 V tiles and scores
+constexpr int kTurns = 4;                   // places of scores
 constexpr int kDepth = 4;                   // units whose copies are in flight, half of them each group's
-constexpr int kPlacesK = kDepth + 1;
+constexpr int kPlacesK = 6;                 // K codes: even, so that a pair of units stands side by side
+constexpr int kPlacesV = 3;                 // fp16 V tiles
 constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
@@ -137,7 +138,7 @@ struct Layout {
     static constexpr int kQTerm = kRows * HD;                // hi or lo
     static constexpr int kQ = 0;                             // [2][hi, lo]
     static constexpr int kConv = kQ + 4 * kQTerm;
-    static constexpr int kKRing = kConv + kTurns * kCvTile;
+    static constexpr int kKRing = kConv + kPlacesV * kCvTile;
     static constexpr int kVRing = kKRing + kPlacesK * kCodes;
     static constexpr int kInfo = kVRing + kDepth * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
@@ -146,8 +147,8 @@ struct Layout {
     static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages]
     static constexpr int kNan = kScale + kScales * 32;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
-    // k_full [kPlacesK], cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
-    static constexpr int kBars = kPlacesK + 4 * kTurns + 4;
+    // k_full [kPlacesK], cv_full [kPlacesV], s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
+    static constexpr int kBars = kPlacesK + kPlacesV + 3 * kTurns + 4;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* s_nan = sm + L::kNan;
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t* cv_full = k_full + kPlacesK;
-    uint64_t* s_full = cv_full + kTurns;
+    uint64_t* s_full = cv_full + kPlacesV;
     uint64_t* p_full = s_full + kTurns;
     uint64_t* pv_done = p_full + kTurns;
     uint64_t* q_full = pv_done + kTurns;
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         s_abort = 0;
         for (int s = 0; s < kPlacesK; ++s) mbar_init(&k_full[s], 4);
+        for (int s = 0; s < kPlacesV; ++s) mbar_init(&cv_full[s], 4);
         for (int s = 0; s < kTurns; ++s) {
-            mbar_init(&cv_full[s], 4);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 128);
             mbar_init(&pv_done[s], 1);
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
         const bool scores = warp == kWarpS;
-        const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
+        // formats 0: E4M3 here, fp16 below
+        const uint32_t idesc_s = umma_idesc(0, kRows, kTile), idesc_pair = umma_idesc(0, kRows, 2 * kTile);
         const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
         const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
         const uint32_t cv_base = smem_u32(sm + L::kConv);
@@ -228,26 +230,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++no;
                 if (scores) ok = wait(&q_full[no & 1], static_cast<uint32_t>((no >> 1) & 1));
             }
-            if (scores) ok = ok && wait(&k_full[ki], static_cast<uint32_t>((i / kPlacesK) & 1)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
-            else ok = ok && wait(&cv_full[x], turn(i)) && wait(&p_full[x], turn(i));
+            // Two units of a segment that stand side by side make one product
+            // of 128 columns: the queries, which the MMA reads from shared
+            // memory, are read once for both.
+            const bool pair = scores && (i & 1) == 0 && i + 1 < end;
+            if (scores) {
+                for (int u = i; u <= i + (pair ? 1 : 0); ++u)
+                    ok = ok && wait(&k_full[u % kPlacesK], static_cast<uint32_t>((u / kPlacesK) & 1)) &&
+                         (u < kTurns || wait(&pv_done[u % kTurns], turn(u) ^ 1u));
+            } else {
+                ok = ok && wait(&cv_full[i % kPlacesV], static_cast<uint32_t>((i / kPlacesV) & 1)) && wait(&p_full[x], turn(i));
+            }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t t_s = tmem + static_cast<uint32_t>(x * kTile);
             if (scores) {
                 const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + ki * L::kCodes;
+                const uint32_t idesc = pair ? idesc_pair : idesc_s;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 32; ++kk) {
                         const uint64_t kd = desc_codes<HD>(k_addr + kk * 32);
-                        umma_e4m3(t_s, desc_codes<HD>(q_addr + kk * 32), kd, idesc_s, kk > 0 ? 1u : 0u);
-                        umma_e4m3(t_s, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc_s, 1u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + kk * 32), kd, idesc, kk > 0 ? 1u : 0u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc, 1u);
                     }
                     umma_commit(&s_full[x]);
-                    if (i + 1 == end) umma_commit(&q_empty[no & 1]);
+                    if (pair) umma_commit(&s_full[x + 1]);
+                    if (i + (pair ? 2 : 1) == end) umma_commit(&q_empty[no & 1]);
                 }
+                if (pair) ++i;
             } else {
-                const uint32_t v_addr = cv_base + x * L::kCvTile;
+                const uint32_t v_addr = cv_base + (i % kPlacesV) * L::kCvTile;
                 const uint32_t more = i - seg > 1 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch(grp + 2);
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
         for (int i = grp; i < n; i += 2) {
-            const int c = i % kTurns;
+            const int c = i % kPlacesV;
             // segments that begin with this unit, or with the other group's before it
             while (end <= i && ok) {
                 const int4 info = s_info[end];
@@ -391,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < kPasses; ++x)
                 v[x] = *reinterpret_cast<const uint4*>(sm + L::kVRing + (i % kDepth) * L::kCodes + x * 2048 + ct * 16);
-            if (i >= kTurns) ok = wait(&pv_done[c], turn(i) ^ 1u);
+            if (i >= kPlacesV) ok = wait(&pv_done[(i - kPlacesV) % kTurns], turn(i - kPlacesV));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int e0 = (s_info[seg].z + i - seg) * kTile;
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[x].w = out ? 0u : without_nan(v[x].w, nan);
 #pragma unroll
                     for (int d = 1; d < kChunks; d <<= 1) nan |= __shfl_xor_sync(0xffffffffu, nan, d);
-                    if (ch == 0) s_nan[c * kTile + r] = static_cast<uint8_t>(nan);
+                    if (ch == 0) s_nan[(i % kTurns) * kTile + r] = static_cast<uint8_t>(nan);
                 }
             }
             // 32 bytes of fp16 a chunk; which half goes first keeps the banks apart
@@ -425,8 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cv_full[c]);
-            // the next unit's copies: K's place is free once S of the unit before this one is complete
-            if (i >= 1) ok = wait(&s_full[(i - 1) % kTurns], turn(i - 1));
+            // the next unit's copies: K's place is free once S of the unit that held it is complete
+            constexpr int kBack = kPlacesK - kDepth;
+            if (i >= kBack) ok = wait(&s_full[(i - kBack) % kTurns], turn(i - kBack));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fetch(i + kDepth);
@@ -479,11 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // Some row does not see all of it. A NaN in a V
                             // that only some rows see enters through the score
                             // (the converters cleared it, before V.P needs it).
-                            const int c = i % kTurns;
-                            ok = wait(&cv_full[c], turn(i));
+                            ok = wait(&cv_full[i % kPlacesV], static_cast<uint32_t>((i / kPlacesV) & 1));
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) continue;
-                            const uint8_t* nan = s_nan + c * kTile;
+                            const uint8_t* nan = s_nan + (i % kTurns) * kTile;
 #pragma unroll
                             for (int x = 0; x < kTile; ++x) {
                                 if (nan[x]) s[x] = NAN;
