@@ -3,23 +3,23 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (640 threads; the registers move to the softmax):
-//   warps 8-11, 12-15  two groups of loaders and converters, which take the
-//               units in turn. Each thread fetches 16-byte chunks of K and V,
-//               two of its group's units ahead, by asynchronous copies: K to
-//               where the MMA reads it (the swizzle of a K-major operand), V
-//               to a place of the thread's own. V codes then become an fp16
-//               tile (fp16 holds every E4M3 value; 128-byte swizzle,
-//               entry-major, read as an MN-major operand), V of entries that
-//               no row sees zero. The group of a segment's first unit also
-//               brings its query rows: shifted by a power of two per row so
-//               that the largest value lies in [128, 256) and split into two
-//               E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16 value
+// Roles (480 threads):
+//   warp 12     TMA: the unit's K pages, a lane per page, to where the MMA
+//               reads them (the swizzle of a K-major operand), and the page
+//               scales by asynchronous copies of eight lanes
+//   warps 8-11  converters. Each thread fetches 16-byte chunks of V, kDepth
+//               units ahead, by asynchronous copies to a place of its own, and
+//               turns them into an fp16 tile (fp16 holds every E4M3 value;
+//               128-byte swizzle, entry-major, read as an MN-major operand),
+//               V of entries that no row sees zero. At the start of a segment
+//               the query rows: shifted by a power of two per row so that the
+//               largest value lies in [128, 256) and split into two E4M3
+//               terms, q = hi + lo, which hold the 8 bits of a bf16 value
 //               exactly down to 1/1024 of the row's largest and to 2^-18 of
 //               that below.
-//   warp 16     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
+//   warp 13     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
 //               N=64, E4M3 operands: the codes themselves)
-//   warp 17     one elected lane issues O += P_t V_t (fp16, A = P_t from
+//   warp 14     one elected lane issues O += P_t V_t (fp16, A = P_t from
 //               tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
@@ -27,15 +27,15 @@
 //               the other; they meet at the end of a segment.
 // Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
 // up to four units ahead of P.V, so a group finds its next scores ready when it
-// is done with the last. "P_t V_t is complete" frees the
-// places of V_t and S_t, as "S_t is complete" frees K_t's place: one commit for
+// is done with the last. V tiles and S_t have four places each and "P_t V_t is
+// complete" frees both, as "S_t is complete" frees K_t's place: one commit for
 // each product. Waits, MMAs and commits cost their warp
 // about 100, 40 and 100 cycles each; with both products and six commits in one
 // warp that, 1550 cycles a unit, was what bounded the kernel.
 //
-// TMA boxes of one page (16 rows) took about 150 cycles each, whoever issued
-// them, 1300 cycles a unit; one group of loaders 1800 (100 to 500 cycles for
-// each of its waits, its copies and the conversion). K codes as MMA operands
+// A TMA box of one page (16 rows) takes about 150 cycles, whoever issues it:
+// K and V both by TMA took 1300 cycles a unit, both by the converters' copies
+// 1800; half of it each way, neither holds the kernel. K codes as MMA operands
 // leave only V to be widened: with K widened too the shared memory carried
 // 128 KB a unit, a quarter more than now, at 128 bytes a cycle.
 #include "attn_kv8.cuh"
@@ -45,23 +45,15 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 480;
 constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17;
-constexpr int kTurns = 4;                   // places of scores
-constexpr int kDepth = 4;                   // units whose copies are in flight, half of them each group's
-constexpr int kPlacesK = 6;                 // K codes: even, so that a pair of units stands side by side
-constexpr int kPlacesV = 3;                 // fp16 V tiles
+constexpr int kWarpConv = 8, kWarpTma = 12, kWarpS = 13, kWarpPv = 14;
+constexpr int kTurns = 4;                   // places of K codes, fp16 V tiles and scores
+constexpr int kDepth = 4;                   // units whose V copies are in flight
 constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
-
-// Registers of a thread: at launch, and in the softmax, loader and issuing
-// warpgroups afterwards. What the softmax gains the others give: setmaxnreg
-// waits for registers that the launch did not bring.
-constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsConv = 80, kRegsIssue = 64;
-static_assert(2 * kRegsSoft + 2 * kRegsConv + kRegsIssue <= 5 * kRegsLaunch, "registers of a block");
 
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -138,8 +130,8 @@ struct Layout {
     static constexpr int kQTerm = kRows * HD;                // hi or lo
     static constexpr int kQ = 0;                             // [2][hi, lo]
     static constexpr int kConv = kQ + 4 * kQTerm;
-    static constexpr int kKRing = kConv + kPlacesV * kCvTile;
-    static constexpr int kVRing = kKRing + kPlacesK * kCodes;
+    static constexpr int kKRing = kConv + kTurns * kCvTile;
+    static constexpr int kVRing = kKRing + kTurns * kCodes;
     static constexpr int kInfo = kVRing + kDepth * kCodes;
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
     static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 4;   // [kCsTurns][kRows]
@@ -147,15 +139,15 @@ struct Layout {
     static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages]
     static constexpr int kNan = kScale + kScales * 32;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
-    // k_full [kPlacesK], cv_full [kPlacesV], s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
-    static constexpr int kBars = kPlacesK + kPlacesV + 3 * kTurns + 4;
+    // k_full, cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
+    static constexpr int kBars = 5 * kTurns + 4;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448 - 128 && Layout<64>::kBytes <= 232448 - 128, "shared memory of a block");
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_kv8_umma(const Kv8Params p) {
+    k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const Kv8Params p) {
     using L = Layout<HD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -168,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_scale = reinterpret_cast<float*>(sm + L::kScale);
     uint8_t* s_nan = sm + L::kNan;
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t* cv_full = k_full + kPlacesK;
-    uint64_t* s_full = cv_full + kPlacesV;
+    uint64_t* cv_full = k_full + kTurns;
+    uint64_t* s_full = cv_full + kTurns;
     uint64_t* p_full = s_full + kTurns;
     uint64_t* pv_done = p_full + kTurns;
     uint64_t* q_full = pv_done + kTurns;
@@ -181,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) {
         s_abort = 0;
-        for (int s = 0; s < kPlacesK; ++s) mbar_init(&k_full[s], 4);
-        for (int s = 0; s < kPlacesV; ++s) mbar_init(&cv_full[s], 4);
         for (int s = 0; s < kTurns; ++s) {
+            mbar_init(&k_full[s], 1 + 2 * kUmmaPages);
+            mbar_init(&cv_full[s], 4);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 128);
             mbar_init(&pv_done[s], 1);
@@ -202,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lo;
     bool idle;
     const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile,
-                                                               reinterpret_cast<int2*>(sm + L::kKRing), lo, idle);
+                                                               reinterpret_cast<int2*>(sm + L::kVRing), lo, idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
@@ -210,58 +202,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
-    if (warp >= kWarpS) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-      if (warp <= kWarpPv) {
+    if (warp == kWarpTma) {
+        const uint64_t policy = l2_policy_evict_first();
+        for (int i = 0; i < n; ++i) {
+            const int x = i % kTurns;
+            const int tile = lane < 2 * kUmmaPages ? s_tile[i * kUmmaPages + lane % kUmmaPages] : -1;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) / 2 * kPage * HD);
+            if (i >= kTurns) ok = wait(&s_full[x], turn(i) ^ 1u);   // S of the unit before it in this place
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[x], bytes);
+            __syncwarp();
+            if (lane < kUmmaPages && tile >= 0)
+                tma_load_2d(sm + L::kKRing + x * L::kCodes + lane * kPage * HD, &tmK, &k_full[x], 0, tile * kPage, policy);
+            if (lane < 2 * kUmmaPages) {   // a page's K or V scale each
+                float* to = s_scale + (i % kScales) * 8 + lane;
+                if (tile >= 0) {
+                    copy_async<4>(smem_u32(to), (lane < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
+                    copies_arrive(&k_full[x]);
+                } else {
+                    *to = 0.f;
+                    mbar_arrive(&k_full[x]);
+                }
+            }
+        }
+        copies_commit();
+        copies_wait<0>();
+        __syncwarp();
+    } else if (warp >= kWarpS) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
         const bool scores = warp == kWarpS;
-        // formats 0: E4M3 here, fp16 below
-        const uint32_t idesc_s = umma_idesc(0, kRows, kTile), idesc_pair = umma_idesc(0, kRows, 2 * kTile);
+        const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
         const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
         const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
         const uint32_t cv_base = smem_u32(sm + L::kConv);
         int seg = 0, end = 0, no = -1;
         for (int i = 0; i < n; ++i) {
-            const int x = i % kTurns, ki = i % kPlacesK;
+            const int x = i % kTurns;
             if (i == end) {
                 seg = i;
                 end = i + min(s_info[i].w - s_info[i].z, n - i);
                 ++no;
                 if (scores) ok = wait(&q_full[no & 1], static_cast<uint32_t>((no >> 1) & 1));
             }
-            // Two units of a segment that stand side by side make one product
-            // of 128 columns: the queries, which the MMA reads from shared
-            // memory, are read once for both.
-            const bool pair = scores && (i & 1) == 0 && i + 1 < end;
-            if (scores) {
-                for (int u = i; u <= i + (pair ? 1 : 0); ++u)
-                    ok = ok && wait(&k_full[u % kPlacesK], static_cast<uint32_t>((u / kPlacesK) & 1)) &&
-                         (u < kTurns || wait(&pv_done[u % kTurns], turn(u) ^ 1u));
-            } else {
-                ok = ok && wait(&cv_full[i % kPlacesV], static_cast<uint32_t>((i / kPlacesV) & 1)) && wait(&p_full[x], turn(i));
-            }
+            if (scores) ok = ok && wait(&k_full[x], turn(i)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
+            else ok = ok && wait(&cv_full[x], turn(i)) && wait(&p_full[x], turn(i));
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t t_s = tmem + static_cast<uint32_t>(x * kTile);
             if (scores) {
-                const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + ki * L::kCodes;
-                const uint32_t idesc = pair ? idesc_pair : idesc_s;
+                const uint32_t q_addr = q_base + (no & 1) * 2 * L::kQTerm, k_addr = k_base + x * L::kCodes;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 32; ++kk) {
                         const uint64_t kd = desc_codes<HD>(k_addr + kk * 32);
-                        umma_e4m3(t_s, desc_codes<HD>(q_addr + kk * 32), kd, idesc, kk > 0 ? 1u : 0u);
-                        umma_e4m3(t_s, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc, 1u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + kk * 32), kd, idesc_s, kk > 0 ? 1u : 0u);
+                        umma_e4m3(t_s, desc_codes<HD>(q_addr + L::kQTerm + kk * 32), kd, idesc_s, 1u);
                     }
                     umma_commit(&s_full[x]);
-                    if (pair) umma_commit(&s_full[x + 1]);
-                    if (i + (pair ? 2 : 1) == end) umma_commit(&q_empty[no & 1]);
+                    if (i + 1 == end) umma_commit(&q_empty[no & 1]);
                 }
-                if (pair) ++i;
             } else {
-                const uint32_t v_addr = cv_base + (i % kPlacesV) * L::kCvTile;
+                const uint32_t v_addr = cv_base + x * L::kCvTile;
                 const uint32_t more = i - seg > 1 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
@@ -275,57 +279,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         __syncwarp();
-      }
     } else if (warp >= kWarpConv) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-        const int grp = (warp - kWarpConv) >> 2, ct = tid & 127;
+        const int ct = tid & 127;
         // this thread's chunk of row `row` of pages page0 (+ 1 pass by pass of
         // 128-wide rows, + 2 of 64-wide ones)
         constexpr int kChunks = HD / 16, kPass = 128 / kChunks, kPasses = kTile / kPass;
         const int ch = ct % kChunks, row0 = ct / kChunks, row = row0 % kPage, page_step = kPass / kPage;
         const uint64_t policy = l2_policy_evict_first();
-        const uint8_t* k_from = p.k_codes + row * HD + ch * 16;
-        const uint8_t* v_from = p.v_codes + row * HD + ch * 16;
-        const int at = HD == 128 ? ch ^ (row0 & 7) : ch ^ ((row0 >> 1) & 3);
-        const uint32_t k_at = smem_u32(sm + L::kKRing) + row0 * HD + (at << 4);
+        const uint8_t* from = p.v_codes + row * HD + ch * 16;
         const uint32_t v_at = smem_u32(sm + L::kVRing) + ct * 16;
         auto fetch = [&](int i) {   // a group of copies even where there is nothing to copy
             if (i < n) {
                 const int* tiles = s_tile + i * kUmmaPages + row0 / kPage;
-                const uint32_t k_to = k_at + (i % kPlacesK) * L::kCodes, v_to = v_at + (i % kDepth) * L::kCodes;
 #pragma unroll
                 for (int x = 0; x < kPasses; ++x) {
                     const int tile = tiles[x * page_step];
-                    if (tile < 0) continue;
-                    const long long off = static_cast<long long>(tile) * (kPage * HD);
-                    copy_async<16>(k_to + x * 2048, k_from + off, policy);
-                    copy_async<16>(v_to + x * 2048, v_from + off, policy);
-                }
-                if (ct < 2 * kUmmaPages) {   // a page's K or V scale each
-                    const int tile = s_tile[i * kUmmaPages + ct % kUmmaPages];
-                    float* to = s_scale + (i % kScales) * 8 + ct;
-                    if (tile >= 0) copy_async<4>(smem_u32(to), (ct < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
-                    else *to = 0.f;
+                    if (tile >= 0)
+                        copy_async<16>(v_at + (i % kDepth) * L::kCodes + x * 2048,
+                                       from + static_cast<long long>(tile) * (kPage * HD), policy);
                 }
             }
             copies_commit();
         };
-        fetch(grp);
-        fetch(grp + 2);
+        for (int i = 0; i < kDepth; ++i) fetch(i);
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
-        for (int i = grp; i < n; i += 2) {
-            const int c = i % kPlacesV;
-            // segments that begin with this unit, or with the other group's before it
-            while (end <= i && ok) {
-                const int4 info = s_info[end];
-                seg = end;
-                end += min(info.w - info.z, n - end);
+        for (int i = 0; i < n; ++i) {
+            const int c = i % kTurns;
+            if (i == end) {      // a segment begins: its query rows
+                const int4 info = s_info[i];
+                seg = i;
+                end = i + min(info.w - info.z, n - i);
                 ++no;
                 const int b = info.x;
                 S = p.seq_lens[b];
                 const int rows = p.rows != nullptr ? p.rows[b] : p.K;
                 last = S + rows - 1;
-                if ((seg & 1) != grp) continue;      // the other group brings the queries
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
@@ -396,16 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
-            if (!ok) break;
-            copies_wait<kDepth / 2 - 1>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_full[i % kPlacesK]);
+            copies_wait<kDepth - 1>();
             uint4 v[kPasses];
 #pragma unroll
             for (int x = 0; x < kPasses; ++x)
                 v[x] = *reinterpret_cast<const uint4*>(sm + L::kVRing + (i % kDepth) * L::kCodes + x * 2048 + ct * 16);
-            if (i >= kPlacesV) ok = wait(&pv_done[(i - kPlacesV) % kTurns], turn(i - kPlacesV));
+            fetch(i + kDepth);
+            if (i >= kTurns) ok = ok && wait(&pv_done[c], turn(i) ^ 1u);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const int e0 = (s_info[seg].z + i - seg) * kTile;
@@ -422,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[x].w = out ? 0u : without_nan(v[x].w, nan);
 #pragma unroll
                     for (int d = 1; d < kChunks; d <<= 1) nan |= __shfl_xor_sync(0xffffffffu, nan, d);
-                    if (ch == 0) s_nan[(i % kTurns) * kTile + r] = static_cast<uint8_t>(nan);
+                    if (ch == 0) s_nan[c * kTile + r] = static_cast<uint8_t>(nan);
                 }
             }
             // 32 bytes of fp16 a chunk; which half goes first keeps the banks apart
@@ -439,17 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&cv_full[c]);
-            // the next unit's copies: K's place is free once S of the unit that held it is complete
-            constexpr int kBack = kPlacesK - kDepth;
-            if (i >= kBack) ok = wait(&s_full[(i - kBack) % kTurns], turn(i - kBack));
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            fetch(i + kDepth);
         }
         copies_wait<0>();
     } else {
         // ------------------------------------------------ softmax: thread = query row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         const int grp = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_mine = t_o + lane_off + static_cast<uint32_t>(grp * HD);
@@ -494,15 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // Some row does not see all of it. A NaN in a V
                             // that only some rows see enters through the score
                             // (the converters cleared it, before V.P needs it).
-                            ok = wait(&cv_full[i % kPlacesV], static_cast<uint32_t>((i / kPlacesV) & 1));
+                            ok = wait(&cv_full[i % kTurns], turn(i));
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) continue;
-                            const uint8_t* nan = s_nan + (i % kTurns) * kTile;
+                            const uint4* nan = reinterpret_cast<const uint4*>(s_nan + (i % kTurns) * kTile);
+#pragma unroll 1
+                            for (int q = 0; q < kTile / 16; ++q) {
+                                const uint4 f = nan[q];
+                                if ((f.x | f.y | f.z | f.w) == 0u) continue;   // as good as always
 #pragma unroll
-                            for (int x = 0; x < kTile; ++x) {
-                                if (nan[x]) s[x] = NAN;
-                                if (e0 + x > lim) s[x] = -INFINITY;
+                                for (int x = 0; x < kTile; ++x) {
+                                    const uint32_t w = (x & 12) == 0 ? f.x : (x & 12) == 4 ? f.y : (x & 12) == 8 ? f.z : f.w;
+                                    if ((x >> 4) == q && ((w >> (8 * (x & 3))) & 0xFFu)) s[x] = NAN;
+                                }
                             }
+#pragma unroll
+                            for (int x = 0; x < kTile; ++x)
+                                if (e0 + x > lim) s[x] = -INFINITY;
                         }
                     }
                     float top = -INFINITY;
@@ -581,8 +567,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const float ga = fa * xa.z * inv, gb = fb * xb.z * inv;
-            __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
-                                 static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
+            // four lanes of a row's neighbourhood trade their 16-byte parts, so
+            // that a store fills whole sectors: rows `near` + k, columns 4 (lane mod 4) ..
+            const int near = row & ~3, four = (lane & 3) * 4;
+            long long at[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int jj = (near + k) / G;
+                at[k] = (static_cast<long long>(b) * p.K + jj) * p.ld_out +
+                        static_cast<long long>(head * G + near + k - jj * G) * HD + grp * (HD / 2) + four;
+            }
             float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kRows, HD);
             const bool all_ok = __all_sync(0xffffffffu, !(bad < 0.f));
             // which groups had a tile: the same for the whole segment
@@ -608,21 +602,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 16; ++x) v[x] = fmaf(o[x], gb, v[x]);
                     }
-                    if (row < R) {
+#pragma unroll
+                    for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            if ((x >> 2) & bit) continue;
+                            const bool hi = (lane & bit) != 0;
+                            const float got = __shfl_xor_sync(0xffffffffu, hi ? v[x] : v[x + 4 * bit], bit);
+                            if (hi) v[x] = got;
+                            else v[x + 4 * bit] = got;
+                        }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (near + k >= R) continue;
                         if (whole) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
-                                w[x] = *reinterpret_cast<const uint32_t*>(&h);
-                            }
-                            *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[4 * k], v[4 * k + 1]);
+                            const __nv_bfloat162 h1 = __floats2bfloat162_rn(v[4 * k + 2], v[4 * k + 3]);
+                            *reinterpret_cast<uint2*>(p.out + at[k] + c * 16) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
                         } else {
-#pragma unroll
-                            for (int x = 0; x < 16; x += 4)
-                                *reinterpret_cast<float4*>(part + row * HD + grp * (HD / 2) + c * 16 + x) =
-                                    make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+                            *reinterpret_cast<float4*>(part + (near + k) * HD + grp * (HD / 2) + c * 16 + four) =
+                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                         }
                     }
                 }
@@ -652,20 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HD>
-int launch_hd(const Kv8Params& p, const Plan& a, cudaStream_t s) {
+int launch_hd(const CUtensorMap& tk, const Kv8Params& p, const Plan& a, cudaStream_t s) {
     auto kern = k_attn_kv8_umma<HD>;
-    // the register split needs what it was reckoned with
-    static const int regs = [&] {
-        cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs != kRegsLaunch) {
-        set_error("attention: the kernel was built with " + std::to_string(regs) + " registers a thread, not " +
-                  std::to_string(kRegsLaunch));
-        return PE_ERR_UNSUPPORTED;
-    }
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::kBytes));
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, p));
+    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, tk, p));
     return PE_OK;
 }
 
@@ -673,7 +663,10 @@ int launch_hd(const Kv8Params& p, const Plan& a, cudaStream_t s) {
 
 namespace kv8 {
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
-    return hd == 128 ? launch_hd<128>(p, a, s) : launch_hd<64>(p, a, s);
+    CUtensorMap tk;
+    const int rc = encode_tmap_codes(&tk, p.k_codes, hd, static_cast<uint64_t>(p.num_pages) * p.nkv * kPage);
+    if (rc != PE_OK) return rc;
+    return hd == 128 ? launch_hd<128>(tk, p, a, s) : launch_hd<64>(tk, p, a, s);
 }
 }  // namespace kv8
 }  // namespace pe

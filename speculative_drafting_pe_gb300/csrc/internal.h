@@ -30,6 +30,10 @@ int encode_tmap_2d(CUtensorMap* map, const void* base, int dtype, uint64_t inner
 // the same over one-byte elements (FP8 weight codes)
 int encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
 
+// 8-bit KV cache codes as [lines][hd] bytes (16 lines per page and head); box =
+// one page of one head, swizzled over the row's hd bytes
+int encode_tmap_codes(CUtensorMap* map, const void* codes, int hd, uint64_t lines);
+
 // ---------------------------------------------------------------- GEMM
 
 enum Epi : int { EPI_STORE = 0, EPI_QKV = 1, EPI_RESID = 2, EPI_SWIGLU = 3, EPI_ARGMAX = 4 };
