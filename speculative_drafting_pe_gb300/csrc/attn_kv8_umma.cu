@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kWarpS) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
-        const bool scores = warp == kWarpS;
+        const bool scores = warp != kWarpPv;
         const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // formats 0: E4M3 here, fp16 below
         const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
         const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);

@@ -20,11 +20,13 @@
 // values down to 2^-28 of that stay exact.
 //
 // A warp owns 16 weight rows (the MMA's M; the token rows are N) and walks
-// their columns 256 at a time through a ring that its lane 0 fills by TMA
-// (128-byte rows, swizzled: the word reads are free of bank conflicts), so
-// the warps never wait for each other while they stream. Where there are few
-// rows, `ks` warps of a CTA share one set of 16, block by block, and their
-// sums are added in order at the end.
+// their columns 256 at a time, kStages blocks ahead, through asynchronous
+// copies of its own lanes (128-byte rows, the 16-byte chunks swizzled: the word
+// reads are free of bank conflicts), so the warps never wait for each other
+// while they stream. (TMA boxes of these 16 rows took some 150 cycles each,
+// 26 bytes/ns per SM: the LM head took 48 us.) Where there are few rows, `ks`
+// warps of a CTA share one set of 16, block by block, and their sums are added
+// in order at the end.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -46,6 +48,8 @@ struct W4Params {
     int ks;            // warps that share 16 rows (1, 2, 4, 8)
     int nb;            // 256-column blocks
     int cb;            // blocks of x in shared memory at a time (a multiple of ks)
+    int whole;         // a block's scales and zero points are whole aligned words
+    const uint8_t* w;
     const void* scale;
     const uint8_t* zero;
     const __nv_bfloat16* x;
@@ -53,9 +57,6 @@ struct W4Params {
     float* y;
     long long ld_y;
 };
-
-__device__ __forceinline__ float load_scale(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load_scale(const float* p) { return *p; }
 
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
@@ -75,8 +76,7 @@ struct W4Smem {
     static constexpr int kX = kWarps * kStages * kStageBytes;
     __host__ __device__ static constexpr int up(int cb) { return kX + kN * pitch(cb); }
     __host__ __device__ static constexpr int red(int cb) { return up(cb) + kN * 4; }
-    __host__ __device__ static constexpr int bars(int cb) { return red(cb) + kWarps * kRows * kN * 4; }
-    __host__ __device__ static constexpr int bytes(int cb) { return bars(cb) + kWarps * kStages * 8 + 1024; }
+    __host__ __device__ static constexpr int bytes(int cb) { return red(cb) + kWarps * kRows * kN * 4 + 1024; }
 };
 
 // Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
@@ -127,20 +127,68 @@ __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
     }
 }
 
-// Scales and zero points of one block for rows g and g + 8.
-template <int GROUP>
+// Scales and zero points of one block of a weight row.
+template <int GROUP, typename S>
 struct Groups {
     static constexpr int kN = kCols / GROUP;
-    float scale[2][kN];
-    uint32_t zero[2][kN];
+    static constexpr int kWords = kN * static_cast<int>(sizeof(S)) / 4;   // 1, 2, 4 or 8
+    uint32_t scale[kWords];
+    uint32_t zero[kN > 4 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const W4Params& p, int row, int kb) {
+        const size_t at = static_cast<size_t>(row) * p.ng + kb * kN;
+        const S* from = static_cast<const S*>(p.scale) + at;
+        const uint8_t* z = p.zero + at;
+        if (p.whole) {
+            if constexpr (kWords == 1) {
+                scale[0] = *reinterpret_cast<const uint32_t*>(from);
+            } else if constexpr (kWords == 2) {
+                const uint2 v = *reinterpret_cast<const uint2*>(from);
+                scale[0] = v.x; scale[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords / 4; ++i) {
+                    const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+                    scale[4 * i] = v.x; scale[4 * i + 1] = v.y; scale[4 * i + 2] = v.z; scale[4 * i + 3] = v.w;
+                }
+            }
+            if (p.zero != nullptr) {
+                if constexpr (kN == 2) zero[0] = *reinterpret_cast<const uint16_t*>(z);
+                else if constexpr (kN == 4) zero[0] = *reinterpret_cast<const uint32_t*>(z);
+                else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(z);
+                    zero[0] = v.x; zero[kN > 4 ? 1 : 0] = v.y;
+                }
+                return;
+            }
+        } else {   // one by one; groups past the row's end count nothing
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) scale[i] = 0u;
+            zero[0] = zero[kN > 4 ? 1 : 0] = 0u;
+#pragma unroll
+            for (int q = 0; q < kN; ++q) {
+                if (kb * kN + q >= p.ng) break;
+                if constexpr (sizeof(S) == 4) scale[q] = *reinterpret_cast<const uint32_t*>(from + q);
+                else scale[q / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(from + q)) << (16 * (q & 1));
+                if (p.zero != nullptr) zero[q / 4] |= static_cast<uint32_t>(z[q]) << (8 * (q & 3));
+            }
+            if (p.zero != nullptr) return;
+        }
+        zero[0] = zero[kN > 4 ? 1 : 0] = 0x08080808u;
+    }
+    __device__ __forceinline__ float s(int q) const {
+        if constexpr (sizeof(S) == 4) return __uint_as_float(scale[q]);
+        else return __uint_as_float((q & 1) ? scale[q / 2] & 0xFFFF0000u : scale[q / 2] << 16);
+    }
+    __device__ __forceinline__ uint32_t z(int q) const { return (zero[q / 4] >> (8 * (q & 3))) & 0xFFu; }
 };
 
 // MB: CTAs that share an SM
 template <int GROUP, int NT, typename S, int MB>
 __global__ void __launch_bounds__(kThreads, MB)
-    k_linear_w4(const __grid_constant__ CUtensorMap tmW, const W4Params p) {
+    k_linear_w4(const W4Params p) {
     using L = W4Smem<GROUP, NT>;
-    using GR = Groups<GROUP>;
+    using GR = Groups<GROUP, S>;
     constexpr int kSub = GROUP / 32;         // 32-column steps of a group
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -149,56 +197,49 @@ __global__ void __launch_bounds__(kThreads, MB)
     const int ks = p.ks, wk = warp % ks, wt = warp / ks, per = kWarps / ks;
     const int n0 = blockIdx.y * L::kN;
     uint8_t* ring = sm + warp * kStages * kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bars(p.cb)) + warp * kStages;
     const float* s_up = reinterpret_cast<const float*>(sm + L::up(p.cb));
     float* s_red = reinterpret_cast<float*>(sm + L::red(p.cb));
     const int tiles = (p.M + kRows - 1) / kRows;
     const int iters = (tiles + per - 1) / per;
 
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
-    fence_mbar_init();
-    __syncwarp();
-
     // this warp's blocks in order: (row tile, wk), (row tile, wk + ks), ...,
-    // then the next row tile; the ring runs ahead of the sums
+    // then the next row tile; the copies run ahead of the sums. Rows past the
+    // last one are copies of it that are never stored; what stands in columns
+    // past the row's end meets an x of 0.
     const uint64_t policy = l2_policy_evict_first();
-    int f_it = blockIdx.x, f_kb = wk, f_st = 0;
-    auto fetch = [&]() {   // lane 0: the next block of the list into the next stage
-        while (f_it < iters && (f_kb >= p.nb || f_it * per + wt >= tiles)) {
+    const int half = p.Kd / 2, c8 = lane & 7, r4 = lane >> 3;   // row bytes; this lane's chunk, and its first row of four
+    const uint32_t ring_at = smem_u32(ring) + r4 * 128;
+    int f_it = blockIdx.x, f_kb = wk;
+    auto fetch = [&](int st) {   // the next block of the list; a group of copies even at its end
+        if (f_kb >= p.nb) {
             f_it += gridDim.x;
             f_kb = wk;
         }
-        if (f_it >= iters) return;
-        mbar_arrive_expect_tx(&full[f_st], kStageBytes);
-        tma_load_2d(ring + f_st * kStageBytes, &tmW, &full[f_st], f_kb * (kCols / 2), (f_it * per + wt) * kRows, policy);
-        f_kb += ks;
-        f_st = f_st + 1 == kStages ? 0 : f_st + 1;
-    };
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s) fetch();
-
-    // groups past the row's end count nothing
-    auto load_groups = [&](GR& o, int it, int kb) {
+        if (f_it < iters && f_kb < p.nb) {
+            const int col = f_kb * (kCols / 2) + c8 * 16, row = (f_it * per + wt) * kRows + r4;
+            if (col < half) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = (it * per + wt) * kRows + g + 8 * h;
-            const size_t at = static_cast<size_t>(row) * p.ng + kb * GR::kN;
-#pragma unroll
-            for (int q = 0; q < GR::kN; ++q) {
-                const bool in = row < p.M && kb * GR::kN + q < p.ng;
-                o.scale[h][q] = in ? load_scale(static_cast<const S*>(p.scale) + at + q) : 0.f;
-                o.zero[h][q] = 8u;
-                if (p.zero != nullptr) o.zero[h][q] = in ? p.zero[at + q] : 0u;
+                for (int j = 0; j < 4; ++j) {
+                    const uint8_t* from = p.w + static_cast<size_t>(min(row + 4 * j, p.M - 1)) * half + col;
+                    const uint32_t to = ring_at + st * kStageBytes + j * 512 + ((c8 ^ ((r4 + 4 * j) & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
+                }
             }
+            f_kb += ks;
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) fetch(s);
+
+    auto load_groups = [&](GR (&o)[2], int it, int kb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) o[h].load(p, min((it * per + wt) * kRows + g + 8 * h, p.M - 1), kb);
     };
 
     int st = 0;
-    uint32_t parity = 0;
-    bool dead = false;
     const int chunks = (p.nb + p.cb - 1) / p.cb;
-    GR next;
+    GR next[2];   // of rows g and g + 8
     if (wk < p.nb) load_groups(next, blockIdx.x, wk);
     for (int it = blockIdx.x; it < iters; it += gridDim.x) {
         const int tile = it * per + wt;
@@ -213,22 +254,18 @@ __global__ void __launch_bounds__(kThreads, MB)
                 load_x<GROUP, NT>(p, sm, c * p.cb, n0);
                 __syncthreads();
             }
-            if (!mine || dead) continue;
+            if (!mine) continue;
             float sum[NT][4];
 #pragma unroll
             for (int a = 0; a < NT; ++a) sum[a][0] = sum[a][1] = sum[a][2] = sum[a][3] = 0.f;
             const int end = min(p.nb, (c + 1) * p.cb);
             for (int kb = c * p.cb + wk; kb < end; kb += ks) {
-                const GR now = next;
+                const GR now[2] = {next[0], next[1]};
                 // the next block's scales are on their way during this one
                 if (kb + ks < p.nb) load_groups(next, it, kb + ks);
                 else if (it + static_cast<int>(gridDim.x) < iters) load_groups(next, it + gridDim.x, wk);
-                const bool ok = mbar_wait(&full[st], (parity >> st) & 1u, nullptr, 0u);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    dead = true;
-                    break;
-                }
-                parity ^= 1u << st;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+                __syncwarp();
                 const uint8_t* wr = ring + st * kStageBytes + g * 128 + t * 4;
                 const uint8_t* xr = sm + L::kX + g * L::pitch(p.cb) + ((kb - c * p.cb) * kCols + t * 8) * 2;
 #pragma unroll
@@ -236,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, MB)
                     __half2 z1[2], z16[2];   // 1024 + z, and -(64 + z)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        z1[h] = h2(0x64006400u + now.zero[h][q] * 0x00010001u);
+                        z1[h] = h2(0x64006400u + now[h].z(q) * 0x00010001u);
                         z16[h] = __hsub2(h2(0x63806380u), z1[h]);   // 960 - (1024 + z)
                     }
                     float part[NT][4];
@@ -265,10 +302,10 @@ __global__ void __launch_bounds__(kThreads, MB)
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sum[a][j] = fmaf(now.scale[j >> 1][q], part[a][j], sum[a][j]);
+                        for (int j = 0; j < 4; ++j) sum[a][j] = fmaf(now[j >> 1].s(q), part[a][j], sum[a][j]);
                 }
                 __syncwarp();
-                if (lane == 0) fetch();
+                fetch(st);
                 st = st + 1 == kStages ? 0 : st + 1;
             }
             // back from the rows' shift by 2^14 and their own powers of two
@@ -278,9 +315,6 @@ __global__ void __launch_bounds__(kThreads, MB)
                 for (int j = 0; j < 4; ++j)
                     acc[a][j] += sum[a][j] * 6.103515625e-05f * s_up[a * 8 + 2 * t + (j & 1)];
         }
-        if (dead)
-#pragma unroll
-            for (int a = 0; a < NT; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = NAN;   // never a wrong number
         if (ks > 1) {
             __syncthreads();   // the last tile's sums have been read
 #pragma unroll
@@ -310,16 +344,18 @@ __global__ void __launch_bounds__(kThreads, MB)
                 }
         }
     }
-    if (dead) __nanosleep(100000);   // a wait gave up: let copies still in flight land
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 constexpr int kXBytes = 100 * 1024;   // shared memory for x at most
 
 template <int GROUP, int NT, typename S>
-int launch(const CUtensorMap& tm, W4Params p, int sms, cudaStream_t s) {
+int launch(W4Params p, int sms, cudaStream_t s) {
     using L = W4Smem<GROUP, NT>;
     const int tiles = (p.M + kRows - 1) / kRows;
     p.nb = (p.Kd + kCols - 1) / kCols;
+    p.whole = p.ng % (kCols / GROUP) == 0 &&
+              ((reinterpret_cast<uintptr_t>(p.scale) | reinterpret_cast<uintptr_t>(p.zero)) & 15u) == 0;
     // warps to a row tile: enough that every SM has its eight, as far as there
     // are blocks to share
     p.ks = 1;
@@ -333,20 +369,20 @@ int launch(const CUtensorMap& tm, W4Params p, int sms, cudaStream_t s) {
     auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, NT == 1 ? 2 : 1> : k_linear_w4<GROUP, NT, S, 1>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
-    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, tm, p));
+    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, p));
     return PE_OK;
 }
 
 template <int GROUP, typename S>
-int launch_nt(const CUtensorMap& tm, const W4Params& p, int sms, cudaStream_t s) {
-    return p.N <= 8 ? launch<GROUP, 1, S>(tm, p, sms, s) : launch<GROUP, 2, S>(tm, p, sms, s);
+int launch_nt(const W4Params& p, int sms, cudaStream_t s) {
+    return p.N <= 8 ? launch<GROUP, 1, S>(p, sms, s) : launch<GROUP, 2, S>(p, sms, s);
 }
 
 template <typename S>
-int launch_group(int group, const CUtensorMap& tm, const W4Params& p, int sms, cudaStream_t s) {
-    if (group == 32) return launch_nt<32, S>(tm, p, sms, s);
-    if (group == 64) return launch_nt<64, S>(tm, p, sms, s);
-    return launch_nt<128, S>(tm, p, sms, s);
+int launch_group(int group, const W4Params& p, int sms, cudaStream_t s) {
+    if (group == 32) return launch_nt<32, S>(p, sms, s);
+    if (group == 64) return launch_nt<64, S>(p, sms, s);
+    return launch_nt<128, S>(p, sms, s);
 }
 
 }  // namespace
@@ -376,20 +412,18 @@ extern "C" int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, con
     int dev = 0, sms = 0;
     PE_CUDA_TRY(cudaGetDevice(&dev));
     PE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    CUtensorMap tm;
-    int rc = encode_tmap_2d_u8(&tm, w, static_cast<uint64_t>(Kd) / 2, static_cast<uint64_t>(M), kRows);
-    if (rc != PE_OK) return rc;
     W4Params p{};
     p.M = M;
     p.N = N;
     p.Kd = Kd;
     p.ng = (Kd + group - 1) / group;
+    p.w = w;
     p.scale = w_scale;
     p.zero = w_zero;
     p.x = static_cast<const __nv_bfloat16*>(x);
     p.ld_x = ld_x;
     p.y = y;
     p.ld_y = ld_y;
-    return scale_dtype == PE_DTYPE_BF16 ? launch_group<__nv_bfloat16>(group, tm, p, sms, static_cast<cudaStream_t>(stream))
-                                        : launch_group<float>(group, tm, p, sms, static_cast<cudaStream_t>(stream));
+    return scale_dtype == PE_DTYPE_BF16 ? launch_group<__nv_bfloat16>(group, p, sms, static_cast<cudaStream_t>(stream))
+                                        : launch_group<float>(group, p, sms, static_cast<cudaStream_t>(stream));
 }
