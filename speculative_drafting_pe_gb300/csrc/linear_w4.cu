@@ -58,6 +58,23 @@ struct W4Params {
     long long ld_y;
 };
 
+// (a & mask) | magic in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+    return r;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(r) : "r"(at), "n"(OFF));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
+    return r;
+}
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 __device__ __forceinline__ uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
@@ -128,7 +145,7 @@ __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
 }
 
 // Scales and zero points of one block of a weight row.
-template <int GROUP, typename S>
+template <int GROUP, typename S, bool ZERO>
 struct Groups {
     static constexpr int kN = kCols / GROUP;
     static constexpr int kWords = kN * static_cast<int>(sizeof(S)) / 4;   // 1, 2, 4 or 8
@@ -152,14 +169,13 @@ struct Groups {
                     scale[4 * i] = v.x; scale[4 * i + 1] = v.y; scale[4 * i + 2] = v.z; scale[4 * i + 3] = v.w;
                 }
             }
-            if (p.zero != nullptr) {
+            if constexpr (ZERO) {
                 if constexpr (kN == 2) zero[0] = *reinterpret_cast<const uint16_t*>(z);
                 else if constexpr (kN == 4) zero[0] = *reinterpret_cast<const uint32_t*>(z);
                 else {
                     const uint2 v = *reinterpret_cast<const uint2*>(z);
                     zero[0] = v.x; zero[kN > 4 ? 1 : 0] = v.y;
                 }
-                return;
             }
         } else {   // one by one; groups past the row's end count nothing
 #pragma unroll
@@ -170,25 +186,23 @@ struct Groups {
                 if (kb * kN + q >= p.ng) break;
                 if constexpr (sizeof(S) == 4) scale[q] = *reinterpret_cast<const uint32_t*>(from + q);
                 else scale[q / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(from + q)) << (16 * (q & 1));
-                if (p.zero != nullptr) zero[q / 4] |= static_cast<uint32_t>(z[q]) << (8 * (q & 3));
+                if constexpr (ZERO) zero[q / 4] |= static_cast<uint32_t>(z[q]) << (8 * (q & 3));
             }
-            if (p.zero != nullptr) return;
         }
-        zero[0] = zero[kN > 4 ? 1 : 0] = 0x08080808u;
     }
     __device__ __forceinline__ float s(int q) const {
         if constexpr (sizeof(S) == 4) return __uint_as_float(scale[q]);
         else return __uint_as_float((q & 1) ? scale[q / 2] & 0xFFFF0000u : scale[q / 2] << 16);
     }
-    __device__ __forceinline__ uint32_t z(int q) const { return (zero[q / 4] >> (8 * (q & 3))) & 0xFFu; }
+    __device__ __forceinline__ uint32_t z(int q) const { return ZERO ? (zero[q / 4] >> (8 * (q & 3))) & 0xFFu : 8u; }
 };
 
-// MB: CTAs that share an SM
-template <int GROUP, int NT, typename S, int MB>
+// MB: CTAs that share an SM; ZERO: zero points are given (8 otherwise)
+template <int GROUP, int NT, typename S, bool ZERO, int MB>
 __global__ void __launch_bounds__(kThreads, MB)
     k_linear_w4(const W4Params p) {
     using L = W4Smem<GROUP, NT>;
-    using GR = Groups<GROUP, S>;
+    using GR = Groups<GROUP, S, ZERO>;
     constexpr int kSub = GROUP / 32;         // 32-column steps of a group
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -210,23 +224,29 @@ __global__ void __launch_bounds__(kThreads, MB)
     const int half = p.Kd / 2, c8 = lane & 7, r4 = lane >> 3;   // row bytes; this lane's chunk, and its first row of four
     const uint32_t ring_at = smem_u32(ring) + r4 * 128;
     int f_it = blockIdx.x, f_kb = wk;
+    const uint8_t* rows[4];   // of the tile being fetched
+    auto turn_to = [&](int it) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            rows[j] = p.w + static_cast<size_t>(min((it * per + wt) * kRows + r4 + 4 * j, p.M - 1)) * half + c8 * 16;
+    };
+    turn_to(f_it);
+    const uint32_t to0 = ring_at + ((c8 ^ r4) << 4), to1 = ring_at + ((c8 ^ (r4 + 4)) << 4);
     auto fetch = [&](int st) {   // the next block of the list; a group of copies even at its end
         if (f_kb >= p.nb) {
             f_it += gridDim.x;
             f_kb = wk;
+            if (f_it < iters) turn_to(f_it);
         }
-        if (f_it < iters && f_kb < p.nb) {
-            const int col = f_kb * (kCols / 2) + c8 * 16, row = (f_it * per + wt) * kRows + r4;
-            if (col < half) {
+        const int col = f_kb * (kCols / 2);
+        if (f_it < iters && col + c8 * 16 < half) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint8_t* from = p.w + static_cast<size_t>(min(row + 4 * j, p.M - 1)) * half + col;
-                    const uint32_t to = ring_at + st * kStageBytes + j * 512 + ((c8 ^ ((r4 + 4 * j) & 7)) << 4);
-                    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy) : "memory");
-                }
-            }
-            f_kb += ks;
+            for (int j = 0; j < 4; ++j)
+                asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(((j & 1) ? to1 : to0) + st * kStageBytes + j * 512),
+                             "l"(rows[j] + col), "l"(policy)
+                             : "memory");
         }
+        f_kb += ks;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -237,6 +257,9 @@ __global__ void __launch_bounds__(kThreads, MB)
         for (int h = 0; h < 2; ++h) o[h].load(p, min((it * per + wt) * kRows + g + 8 * h, p.M - 1), kb);
     };
 
+    const uint32_t wr0 = smem_u32(ring) + g * 128 + t * 4 + (g << 4);
+    const uint32_t xr0 = smem_u32(sm + L::kX) + g * L::pitch(p.cb) + t * 16;
+    const uint32_t low = 0x000F000Fu, high = 0x00F000F0u, magic = 0x64006400u;
     int st = 0;
     const int chunks = (p.nb + p.cb - 1) / p.cb;
     GR next[2];   // of rows g and g + 8
@@ -266,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, MB)
                 else if (it + static_cast<int>(gridDim.x) < iters) load_groups(next, it + gridDim.x, wk);
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
                 __syncwarp();
-                const uint8_t* wr = ring + st * kStageBytes + g * 128 + t * 4;
-                const uint8_t* xr = sm + L::kX + g * L::pitch(p.cb) + ((kb - c * p.cb) * kCols + t * 8) * 2;
+                // word t of chunk i of row g stands at chunk i ^ g
+                const uint32_t wr = wr0 + st * kStageBytes, xr = xr0 + (kb - c * p.cb) * (kCols * 2);
 #pragma unroll
                 for (int q = 0; q < GR::kN; ++q) {
                     __half2 z1[2], z16[2];   // 1024 + z, and -(64 + z)
@@ -283,18 +306,19 @@ __global__ void __launch_bounds__(kThreads, MB)
                     for (int u = 0; u < kSub; ++u) {
                         const int i = q * kSub + u;
                         uint32_t lo[4], hi[4];
+                        const uint32_t at = wr ^ (i << 4);
+                        const uint32_t word[2] = {lds32<0>(at), lds32<8 * 128>(at)};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(wr + h * 8 * 128 + ((i ^ g) << 4));
-                            const uint32_t v = w >> 8;
-                            lo[h] = u32(__hsub2(h2((w & 0x000F000Fu) | 0x64006400u), z1[h]));
-                            lo[2 + h] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), h2(0x2C002C00u), z16[h]));
-                            hi[h] = u32(__hsub2(h2((v & 0x000F000Fu) | 0x64006400u), z1[h]));
-                            hi[2 + h] = u32(__hfma2(h2((v & 0x00F000F0u) | 0x64006400u), h2(0x2C002C00u), z16[h]));
+                            const uint32_t w = word[h], v = w >> 8;
+                            lo[h] = u32(__hsub2(h2(and_or(w, low, magic)), z1[h]));
+                            lo[2 + h] = u32(__hfma2(h2(and_or(w, high, magic)), h2(0x2C002C00u), z16[h]));
+                            hi[h] = u32(__hsub2(h2(and_or(v, low, magic)), z1[h]));
+                            hi[2 + h] = u32(__hfma2(h2(and_or(v, high, magic)), h2(0x2C002C00u), z16[h]));
                         }
 #pragma unroll
                         for (int a = 0; a < NT; ++a) {
-                            const uint4 xv = *reinterpret_cast<const uint4*>(xr + a * 8 * L::pitch(p.cb) + i * 64);
+                            const uint4 xv = lds128(xr + a * 8 * L::pitch(p.cb) + i * 64);
                             mma_f16(part[a], lo, xv.x, xv.y);
                             mma_f16(part[a], hi, xv.z, xv.w);
                         }
@@ -349,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, MB)
 
 constexpr int kXBytes = 100 * 1024;   // shared memory for x at most
 
-template <int GROUP, int NT, typename S>
+template <int GROUP, int NT, typename S, bool ZERO>
 int launch(W4Params p, int sms, cudaStream_t s) {
     using L = W4Smem<GROUP, NT>;
     const int tiles = (p.M + kRows - 1) / kRows;
@@ -366,7 +390,7 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     const int iters = (tiles * p.ks + kWarps - 1) / kWarps;
     const int smem = L::bytes(p.cb);
     const int per_sm = NT == 1 && smem <= 112 * 1024 ? 2 : 1;
-    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, NT == 1 ? 2 : 1> : k_linear_w4<GROUP, NT, S, 1>;
+    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, ZERO, NT == 1 ? 2 : 1> : k_linear_w4<GROUP, NT, S, ZERO, 1>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, p));
@@ -375,7 +399,8 @@ int launch(W4Params p, int sms, cudaStream_t s) {
 
 template <int GROUP, typename S>
 int launch_nt(const W4Params& p, int sms, cudaStream_t s) {
-    return p.N <= 8 ? launch<GROUP, 1, S>(p, sms, s) : launch<GROUP, 2, S>(p, sms, s);
+    if (p.zero != nullptr) return p.N <= 8 ? launch<GROUP, 1, S, true>(p, sms, s) : launch<GROUP, 2, S, true>(p, sms, s);
+    return p.N <= 8 ? launch<GROUP, 1, S, false>(p, sms, s) : launch<GROUP, 2, S, false>(p, sms, s);
 }
 
 template <typename S>
