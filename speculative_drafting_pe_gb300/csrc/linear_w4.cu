@@ -16,8 +16,8 @@
 // cores align the products by the operands' exponents, so beside a large x
 // the other products lost up to ten bits.) x is laid out once per CTA in
 // shared memory in the order in which the nibbles come out, as fp16 shifted by
-// a power of two per row so that its largest value lies in [2^14, 2^15): bf16
-// values down to 2^-28 of that stay exact.
+// a power of two per row and 256 columns so that the largest value lies in
+// [2^14, 2^15): bf16 values down to 2^-28 of that stay exact.
 //
 // A warp owns 16 weight rows (the MMA's M; the token rows are N) and walks
 // their columns 256 at a time, kStages blocks ahead, through asynchronous
@@ -64,6 +64,8 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t m
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
     return r;
 }
+// In the order of the program, as the MMAs are: left to the compiler, the loads
+// of later steps moved up, and the LM head took 38 instead of 34 us.
 template <int OFF>
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
     uint32_t r;
@@ -92,54 +94,54 @@ struct W4Smem {
     __host__ __device__ static constexpr int pitch(int cb) { return cb * kCols * 2 + 64; }
     static constexpr int kX = kWarps * kStages * kStageBytes;
     __host__ __device__ static constexpr int up(int cb) { return kX + kN * pitch(cb); }
-    __host__ __device__ static constexpr int red(int cb) { return up(cb) + kN * 4; }
+    __host__ __device__ static constexpr int red(int cb) { return up(cb) + cb * kN * 4; }
     __host__ __device__ static constexpr int bytes(int cb) { return red(cb) + kWarps * kRows * kN * 4 + 1024; }
 };
 
 // Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
-// order, and the factor that undoes the row's shift.
+// order, and for each row and block the factor that undoes its shift. A warp
+// per (row, block), four of them in flight.
 template <int GROUP, int NT>
 __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
     using L = W4Smem<GROUP, NT>;
+    constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb));
-    const int blocks = min(p.cb, p.nb - b0);
-    for (int r = warp; r < L::kN; r += kWarps) {
-        const int n = n0 + r;
-        const __nv_bfloat16* src = p.x + static_cast<long long>(n) * p.ld_x;
-        auto get = [&](int blk) {
-            const int k = (b0 + blk) * kCols + lane * 8;
-            return n < p.N && k < p.Kd ? *reinterpret_cast<const uint4*>(src + k) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        uint32_t top = 0;
-        for (int blk = 0; blk < blocks; ++blk) {
-            const uint4 v = get(blk);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // rows past the last one stay as they are: an MMA column of its own each, never stored
+    const int rows = min(L::kN, p.N - n0), items = min(p.cb, p.nb - b0) * rows;
+    for (int i0 = warp; i0 < items; i0 += kWarps * kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kWarps, n = n0 + i % rows, k = (b0 + i / rows) * kCols + lane * 8;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < items && k < p.Kd)
+                v[j] = *reinterpret_cast<const uint4*>(p.x + static_cast<long long>(n) * p.ld_x + k);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int E = min(max(static_cast<int>(top >> 23), 14), 254);
-        const float down = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);   // 2^(141 - E)
-        if (lane == 0) s_up[r] = __uint_as_float(static_cast<uint32_t>(E) << 23);     // 2^(E - 127)
-        uint8_t* dst = sm + L::kX + r * L::pitch(p.cb);
-        for (int blk = 0; blk < blocks; ++blk) {
-            const uint4 v = get(blk);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kWarps;
+            if (i >= items) break;
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = max(top, max((w[q] << 16) & 0x7FFF0000u, w[q] & 0x7FFF0000u));
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int E = min(max(static_cast<int>(top >> 23), 15), 254);
+            const float down = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);   // 2^(141 - E)
+            const int r = i % rows, blk = i / rows;
+            if (lane == 0) s_up[blk * L::kN + r] = __uint_as_float(static_cast<uint32_t>(E - 14) << 23);   // 2^(E - 141)
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16) * down;
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * down;
+            for (int q = 0; q < 4; ++q) {
+                f[2 * q] = __uint_as_float(w[q] << 16) * down;
+                f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u) * down;
             }
             uint32_t o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 h = __floats2half2_rn(f[i], f[i + 4]);
-                o[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(dst + (blk * kCols + lane * 8) * 2) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int q = 0; q < 4; ++q) o[q] = u32(__floats2half2_rn(f[q], f[q + 4]));
+            *reinterpret_cast<uint4*>(sm + L::kX + r * L::pitch(p.cb) + (blk * kCols + lane * 8) * 2) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -278,9 +280,6 @@ __global__ void __launch_bounds__(kThreads, MB)
                 __syncthreads();
             }
             if (!mine) continue;
-            float sum[NT][4];
-#pragma unroll
-            for (int a = 0; a < NT; ++a) sum[a][0] = sum[a][1] = sum[a][2] = sum[a][3] = 0.f;
             const int end = min(p.nb, (c + 1) * p.cb);
             for (int kb = c * p.cb + wk; kb < end; kb += ks) {
                 const GR now[2] = {next[0], next[1]};
@@ -290,6 +289,9 @@ __global__ void __launch_bounds__(kThreads, MB)
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
                 __syncwarp();
                 // word t of chunk i of row g stands at chunk i ^ g
+                float sum[NT][4];   // the block's, relative to x's shift
+#pragma unroll
+                for (int a = 0; a < NT; ++a) sum[a][0] = sum[a][1] = sum[a][2] = sum[a][3] = 0.f;
                 const uint32_t wr = wr0 + st * kStageBytes, xr = xr0 + (kb - c * p.cb) * (kCols * 2);
 #pragma unroll
                 for (int q = 0; q < GR::kN; ++q) {
@@ -328,16 +330,16 @@ __global__ void __launch_bounds__(kThreads, MB)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) sum[a][j] = fmaf(now[j >> 1].s(q), part[a][j], sum[a][j]);
                 }
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    const float2 up = *reinterpret_cast<const float2*>(s_up + (kb - c * p.cb) * L::kN + a * 8 + 2 * t);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[a][j] = fmaf(sum[a][j], (j & 1) ? up.y : up.x, acc[a][j]);
+                }
                 __syncwarp();
                 fetch(st);
                 st = st + 1 == kStages ? 0 : st + 1;
             }
-            // back from the rows' shift by 2^14 and their own powers of two
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[a][j] += sum[a][j] * 6.103515625e-05f * s_up[a * 8 + 2 * t + (j & 1)];
         }
         if (ks > 1) {
             __syncthreads();   // the last tile's sums have been read
@@ -371,7 +373,11 @@ __global__ void __launch_bounds__(kThreads, MB)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-constexpr int kXBytes = 100 * 1024;   // shared memory for x at most
+// Shared memory for x at most. Longer rows come in pieces, once for every tile
+// of weight rows; 16 token rows only as far as they fit whole (otherwise eight
+// at a time, with the weights a second time out of L2).
+constexpr int kXBytes = 144 * 1024;
+constexpr int kWide = kXBytes / (16 * 2);   // columns up to which 16 token rows fit
 
 template <int GROUP, int NT, typename S, bool ZERO>
 int launch(W4Params p, int sms, cudaStream_t s) {
@@ -380,10 +386,10 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     p.nb = (p.Kd + kCols - 1) / kCols;
     p.whole = p.ng % (kCols / GROUP) == 0 &&
               ((reinterpret_cast<uintptr_t>(p.scale) | reinterpret_cast<uintptr_t>(p.zero)) & 15u) == 0;
-    // warps to a row tile: enough that every SM has its eight, as far as there
-    // are blocks to share
+    // warps to a row tile: enough that every SM has sixteen, as far as there
+    // are blocks to share (6144 x 2048, 11 rows: 8.1 us, with eight 8.6)
     p.ks = 1;
-    while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps)
+    while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps * 2)
         p.ks *= 2;
     const int fit = kXBytes / (L::kN * kCols * 2) / kWarps * kWarps;
     p.cb = p.nb <= fit ? (p.nb + p.ks - 1) / p.ks * p.ks : fit;
@@ -399,8 +405,9 @@ int launch(W4Params p, int sms, cudaStream_t s) {
 
 template <int GROUP, typename S>
 int launch_nt(const W4Params& p, int sms, cudaStream_t s) {
-    if (p.zero != nullptr) return p.N <= 8 ? launch<GROUP, 1, S, true>(p, sms, s) : launch<GROUP, 2, S, true>(p, sms, s);
-    return p.N <= 8 ? launch<GROUP, 1, S, false>(p, sms, s) : launch<GROUP, 2, S, false>(p, sms, s);
+    const bool one = p.N <= 8 || p.Kd > kWide - kWarps * kCols;
+    if (p.zero != nullptr) return one ? launch<GROUP, 1, S, true>(p, sms, s) : launch<GROUP, 2, S, true>(p, sms, s);
+    return one ? launch<GROUP, 1, S, false>(p, sms, s) : launch<GROUP, 2, S, false>(p, sms, s);
 }
 
 template <typename S>
