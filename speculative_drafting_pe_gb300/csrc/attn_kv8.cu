@@ -566,8 +566,8 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const long long slots = static_cast<long long>(sms) * ((most + round - 1) / round);
     const long long want = (most + least - 1) / least;
     a.grid = static_cast<int>(want < slots ? want : slots);
-    a.first_floats = (static_cast<size_t>(B) + 2 + 3) / 4 * 4;
-    a.ws_floats = a.first_floats + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
+    a.first_floats = (static_cast<size_t>(B) + 2 + 7) / 8 * 8;
+    a.ws_floats = a.first_floats + 4 + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
     *out = a;
     return PE_OK;
 }
@@ -681,7 +681,8 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.ld_out = ld_out;
     p.status = status;
     p.first = reinterpret_cast<int32_t*>(ws);
-    p.part = ws + a.first_floats;
+    // whole sectors: a 16-byte aligned `ws` may be half of one off
+    p.part = ws + a.first_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tr == kUmmaRows) rc = launch_umma(p, a, head_dim, s);
     else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);

@@ -83,6 +83,22 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t smem_addr) {
 }
 
 // 32 consecutive columns of the lane's TMEM row
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -94,6 +110,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
+}
+
+// 32 bytes in one store: a whole sector of L2
+__device__ __forceinline__ void store_sector(void* to, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // two floats in one instruction
@@ -567,62 +590,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const float ga = fa * xa.z * inv, gb = fb * xb.z * inv;
-            // four lanes of a row's neighbourhood trade their 16-byte parts, so
-            // that a store fills whole sectors: rows `near` + k, columns 4 (lane mod 4) ..
-            const int near = row & ~3, four = (lane & 3) * 4;
-            long long at[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int jj = (near + k) / G;
-                at[k] = (static_cast<long long>(b) * p.K + jj) * p.ld_out +
-                        static_cast<long long>(head * G + near + k - jj * G) * HD + grp * (HD / 2) + four;
-            }
+            __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
+                                 static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
+            const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;
             float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kRows, HD);
             const bool all_ok = __all_sync(0xffffffffu, !(bad < 0.f));
             // which groups had a tile: the same for the whole segment
             const bool has_a = (seg & 1) == 0 || len > 1, has_b = (seg & 1) == 1 || len > 1;
             if (busy) {
 #pragma unroll
-                for (int c = 0; c < HD / 32; ++c) {
-                    float v[16];
+                for (int c = 0; c < HD / 2; c += 32) {
+                    float v[32];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) v[x] = 0.f;
-                    const uint32_t col = t_o + lane_off + static_cast<uint32_t>(grp * (HD / 2) + c * 16);
+                    for (int x = 0; x < 32; ++x) v[x] = 0.f;
+                    const uint32_t col = t_o + lane_off + static_cast<uint32_t>(grp * (HD / 2) + c);
                     if (has_a && all_ok) {
-                        float o[16];
-                        tmem_ld16(col, o);
+                        float o[32];
+                        tmem_ld32(col, o);
                         if (xa.y > 0.f || xa.y != xa.y)
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) v[x] = o[x] * ga;
+                            for (int x = 0; x < 32; ++x) v[x] = o[x] * ga;
                     }
                     if (has_b && all_ok) {
-                        float o[16];
-                        tmem_ld16(col + HD, o);
+                        float o[32];
+                        tmem_ld32(col + HD, o);
                         if (xb.y > 0.f || xb.y != xb.y)
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) v[x] = fmaf(o[x], gb, v[x]);
+                            for (int x = 0; x < 32; ++x) v[x] = fmaf(o[x], gb, v[x]);
                     }
+                    if (row >= R) continue;
+                    if (whole) {
 #pragma unroll
-                    for (int bit = 1; bit <= 2; bit <<= 1)
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t h[8];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            if ((x >> 2) & bit) continue;
-                            const bool hi = (lane & bit) != 0;
-                            const float got = __shfl_xor_sync(0xffffffffu, hi ? v[x] : v[x + 4 * bit], bit);
-                            if (hi) v[x] = got;
-                            else v[x + 4 * bit] = got;
+                            for (int y = 0; y < 8; ++y) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(v[16 * x + 2 * y], v[16 * x + 2 * y + 1]);
+                                h[y] = *reinterpret_cast<const uint32_t*>(&two);
+                            }
+                            if (sectors) {
+                                store_sector(out + c + 16 * x, h);
+                            } else {
+                                reinterpret_cast<uint4*>(out + c + 16 * x)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                                reinterpret_cast<uint4*>(out + c + 16 * x)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                            }
                         }
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (near + k >= R) continue;
-                        if (whole) {
-                            const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[4 * k], v[4 * k + 1]);
-                            const __nv_bfloat162 h1 = __floats2bfloat162_rn(v[4 * k + 2], v[4 * k + 3]);
-                            *reinterpret_cast<uint2*>(p.out + at[k] + c * 16) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-                        } else {
-                            *reinterpret_cast<float4*>(part + (near + k) * HD + grp * (HD / 2) + c * 16 + four) =
-                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(v[8 * x + y]);
+                            store_sector(part + row * HD + grp * (HD / 2) + c + 8 * x, w);
                         }
                     }
                 }
