@@ -42,6 +42,7 @@ constexpr int kStages = 2;         // units in flight per warp: 96 KB per SM. Mo
                                    // in front of every other load
 constexpr int kMaxUnits = 1024;    // units of one CTA
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
+constexpr int kPad = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -97,9 +98,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
 
     pdl_launch_dependents();
-    int lo;
-    bool idle;
-    const int n = gather_units<kThreads, 1, kRows>(p, kMinUnits, s_info, s_tile, reinterpret_cast<int2*>(sm), lo, idle);   // the list in the ring's place
+    int idle;
+    const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, s_info, s_tile, reinterpret_cast<int2*>(sm), idle);   // the list in the ring's place
 
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kTile + lane * kCols;
@@ -134,9 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int len = min(info.w - page0, n - seg);
         const int S = p.seq_lens[b];
         const int rows = p.rows != nullptr ? p.rows[b] : p.K;
-        const int tiles = (rows * G + kRows - 1) / kRows;
-        const int head = info.y / tiles, r0 = (info.y - head * tiles) * kRows;
-        const int live = min(kRows, rows * G - r0);       // rows of this tile
+        const int head = info.y, live = rows * G;
         const int last = S + rows - 1;                    // last entry that any row sees
         float mark = 0.f;
         // of rows a * 8 + 2t + x: o[j][a][2y + x] is dimension g * kCols + 2j + y
@@ -156,10 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int lim[NT][2];
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                const int r = a * 8 + g, j = (r0 + r) / G;
+                const int r = a * 8 + g, j = r / G;
                 const __nv_bfloat16* src =
                     p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
-                    static_cast<long long>(head * G + (r0 + r) - j * G) * HD + t * 16;
+                    static_cast<long long>(head * G + r - j * G) * HD + t * 16;
                 uint4 raw[HD / 32];
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x) {
                     cs[a][x] = __shfl_sync(0xffffffffu, up, (2 * t + x) * 4);
                     const int rx = a * 8 + 2 * t + x;
-                    lim[a][x] = rx < live ? S + (r0 + rx) / G : -1;
+                    lim[a][x] = rx < live ? S + rx / G : -1;
                 }
 #pragma unroll
                 for (int c = 0; c < HD / 8; ++c)
@@ -412,16 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     if (bad < 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     else acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                    const int j = (r0 + r) / G;
+                    const int j = r / G;
                     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
                         p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
-                        static_cast<long long>(head * G + (r0 + r) - j * G) * HD + q * 4);
+                        static_cast<long long>(head * G + r - j * G) * HD + q * 4);
                     dst[0] = __floats2bfloat162_rn(acc.x, acc.y);
                     dst[1] = __floats2bfloat162_rn(acc.z, acc.w);
                 }
                 if (info.y == 0 && item == 0) p.status[b] = status_of(bad);
             } else {
-                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kRows, HD);
+                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (page0 > 0 ? 0 : 1)) * part_floats(kRows, HD);
                 *reinterpret_cast<float4*>(dst + r * HD + q * 4) = acc;
                 if (q == 0) {
                     dst[kRows * HD + r] = M;
@@ -432,18 +430,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         seg += len;
     }
     copies_wait<0>();
-    if (idle) zero_idle_rows_by<1, kRows>(p, HD, warp, kWarps);
+    if (idle) zero_idle_rows_by<1, kPad>(p, HD, idle, warp, kWarps);
 }
 
-// Joins the parts of every (head, row tile) that several CTAs share, in unit
-// order. The part that CTA c left of a run of units [u0, u1) is its first one
-// where the run begins at or before c's share, its second one otherwise. A
+// Joins the parts of every head that several CTAs share, in unit order. The
+// part that a CTA left of such a run is its first one where the run began in
+// an earlier share, its second one otherwise. Every block lists the cut runs
+// and takes its blocks of rows from them (a block for every head and row, most
+// of them with nothing to do, took 18.6 us at B=128 K=11). A
 // thread per row and four dimensions; the parts are read eight at a time, all
 // loads of a batch in flight, and folded with a running maximum. Where rows
 // are few and parts many (one long request), SHARE warps take a row together,
 // each a run of its parts, and their sums meet in shared memory.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeBatch = 8;
+constexpr int kMergeBlocks = 16;   // blocks for an SM at most
 
 struct Joined {
     float M = -INFINITY, bad = 0.f, total = 0.f;
@@ -469,75 +470,113 @@ struct Joined {
 };
 
 template <int HD, int SHARE>
-__global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, int tr, int ppu) {
-    constexpr int kPerRow = HD / 4, kTeam = kPerRow * SHARE, kBlockRows = kMergeThreads / kTeam;
+__global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, int tr, int grid) {
+    constexpr int kPerRow = HD / 4, kTeam = kPerRow * SHARE, kBlockRows = kMergeThreads / kTeam, kWarps = kMergeThreads / 32;
     __shared__ float4 s_acc[SHARE > 1 ? kMergeThreads : 1];
     __shared__ float3 s_sum[SHARE > 1 ? kMergeThreads : 1];
+    __shared__ int4 s_run[kMergeThreads];
+    __shared__ int s_c[kMergeThreads], s_count[kWarps];
     pdl_wait();
-    const int b = blockIdx.z, head = blockIdx.y;
-    const int u_b = p.first[b], units = p.first[b + 1] - u_b, per = p.first[p.B + 1];
-    const int G = p.nq / p.nkv;
-    const int S = p.seq_lens[b], rows = p.rows != nullptr ? p.rows[b] : p.K;
-    const int rr = blockIdx.x * kBlockRows + threadIdx.x / kTeam;
-    const int piece = threadIdx.x % kTeam / kPerRow, d = (threadIdx.x % kPerRow) * 4;
-    if (units == 0 || blockIdx.x * kBlockRows >= rows * G) return;
-    const int tiles = (rows * G + tr - 1) / tr;
-    const int run = ((S + rows + kPage - 1) / kPage + ppu - 1) / ppu;
-    const int tile = rr / tr, r = rr - tile * tr;
-    const int u0 = u_b + (head * tiles + tile) * run, u1 = u0 + run;
-    const int c0 = u0 / per, c1 = (u1 - 1) / per;
-    const bool mine = rr < rows * G && c0 != c1;   // one part alone was written by its CTA
-    Joined j;
-    if (mine) {
-        const int each = (c1 - c0 + SHARE) / SHARE;
-        const int from = c0 + piece * each, to = min(c1, from + each - 1);
-        for (int c = from; c <= to; c += kMergeBatch) {
-            float mv[kMergeBatch], lv[kMergeBatch];
-            float4 ov[kMergeBatch];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = p.cut[grid].x, shares = p.cut[grid].y;
+    const int G = p.nq / p.nkv, blocks = (p.K * G + kBlockRows - 1) / kBlockRows;   // blocks of rows of a run
+    int item = blockIdx.x, late = 0;
+    for (int c = tid; c < shares; c += kMergeThreads) late |= p.cut[c].z < 0;
+    if (__syncthreads_or(late)) {   // a CTA gave up waiting: no result of the call is kept
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            const Req q = request_of<1, 0>(p, b);
+            if (q.rows > 0 && tid == 0) p.status[b] = PE_REQ_TIMEOUT;
+            for (int j = warp; j < q.rows; j += kWarps) {
+                uint4* o = reinterpret_cast<uint4*>(p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out);
+                for (int x = lane; x < p.nq * HD / 8; x += 32) o[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        return;
+    }
+    for (int c0 = 0; c0 < shares; c0 += kMergeThreads) {
+        // the runs whose first cut is one of these
+        const int c = c0 + tid;
+        const int4 cut = c < shares ? p.cut[c] : make_int4(0, 0, 0, 0);
+        const bool here = cut.z > 0 && cut.z <= per;
+        const unsigned vote = __ballot_sync(0xffffffffu, here);
+        __syncthreads();   // the last round's runs have been read
+        if (lane == 0) s_count[warp] = __popc(vote);
+        __syncthreads();
+        int rank = __popc(vote & ((1u << lane) - 1u)), runs = 0;
 #pragma unroll
-            for (int x = 0; x < kMergeBatch; ++x) {
-                mv[x] = lv[x] = 0.f;
-                if (c + x <= to) {
-                    const int part = 2 * (c + x) + (u0 <= (c + x) * per ? 0 : 1);
-                    const float* src = p.part + static_cast<size_t>(part) * part_floats(tr, HD);
-                    mv[x] = src[tr * HD + r];
-                    lv[x] = src[tr * HD + tr + r];
-                    ov[x] = *reinterpret_cast<const float4*>(src + r * HD + d);
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) rank += s_count[i];
+            runs += s_count[i];
+        }
+        if (here) {
+            s_run[rank] = cut;
+            s_c[rank] = c;
+        }
+        __syncthreads();
+        for (; item < runs * blocks; item += gridDim.x) {
+            const int x0 = item / blocks, block = item - x0 * blocks;
+            const int4 of = s_run[x0];
+            const int b = of.x, head = of.y, first = s_c[x0] - 1;
+            const int last = (s_c[x0] * per - of.z + of.w - 1) / per;   // the run's first and last share
+            const int rows = p.rows != nullptr ? p.rows[b] : p.K;
+            const int r = block * kBlockRows + tid / kTeam;
+            const int piece = tid % kTeam / kPerRow, d = (tid % kPerRow) * 4;
+            const bool mine = r < rows * G;
+            Joined j;
+            if (mine) {
+                const int each = (last - first + SHARE) / SHARE;
+                const int from = first + piece * each, to = min(last, from + each - 1);
+                for (int q = from; q <= to; q += kMergeBatch) {
+                    float mv[kMergeBatch], lv[kMergeBatch];
+                    float4 ov[kMergeBatch];
+#pragma unroll
+                    for (int x = 0; x < kMergeBatch; ++x) {
+                        mv[x] = lv[x] = 0.f;
+                        if (q + x <= to) {
+                            const int part = 2 * (q + x) + (q + x == first ? 1 : 0);
+                            const float* src = p.part + static_cast<size_t>(part) * part_floats(tr, HD);
+                            mv[x] = src[tr * HD + r];
+                            lv[x] = src[tr * HD + tr + r];
+                            ov[x] = *reinterpret_cast<const float4*>(src + r * HD + d);
+                        }
+                    }
+                    float top = j.M;
+#pragma unroll
+                    for (int x = 0; x < kMergeBatch; ++x) {
+                        if (lv[x] < 0.f) j.bad = fminf(j.bad, lv[x]);
+                        else if (lv[x] != 0.f) top = fmaxf(top, mv[x]);
+                    }
+                    j.raise(top);
+#pragma unroll
+                    for (int x = 0; x < kMergeBatch; ++x)
+                        if (q + x <= to) j.add(mv[x], lv[x], ov[x]);
                 }
             }
-            float top = j.M;
-#pragma unroll
-            for (int x = 0; x < kMergeBatch; ++x) {
-                if (lv[x] < 0.f) j.bad = fminf(j.bad, lv[x]);
-                else if (lv[x] != 0.f) top = fmaxf(top, mv[x]);
+            if constexpr (SHARE > 1) {
+                s_acc[tid] = j.acc;
+                s_sum[tid] = make_float3(j.M, j.total, j.bad);
+                __syncthreads();
+                if (piece == 0)
+                    for (int x = 1; x < SHARE; ++x) {
+                        const float3 o = s_sum[tid + x * kPerRow];
+                        j.bad = fminf(j.bad, o.z);
+                        j.raise(o.y != 0.f ? fmaxf(j.M, o.x) : j.M);
+                        j.add(o.x, o.y, s_acc[tid + x * kPerRow]);
+                    }
+                __syncthreads();
             }
-            j.raise(top);
-#pragma unroll
-            for (int x = 0; x < kMergeBatch; ++x)
-                if (c + x <= to) j.add(mv[x], lv[x], ov[x]);
+            if (!mine || piece != 0) continue;
+            if (head == 0 && r == 0 && d == 0) p.status[b] = status_of(j.bad);
+            const float inv = j.total == 0.f || j.bad < 0.f ? 0.f : 1.f / j.total;
+            if (j.bad < 0.f) j.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int row = r / G;
+            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+                p.out + (static_cast<long long>(b) * p.K + row) * p.ld_out + static_cast<long long>(head * G + r - row * G) * HD + d);
+            dst[0] = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
+            dst[1] = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
         }
+        item -= runs * blocks;
     }
-    if constexpr (SHARE > 1) {
-        s_acc[threadIdx.x] = j.acc;
-        s_sum[threadIdx.x] = make_float3(j.M, j.total, j.bad);
-        __syncthreads();
-        if (piece != 0) return;
-        for (int x = 1; x < SHARE; ++x) {
-            const float3 o = s_sum[threadIdx.x + x * kPerRow];
-            j.bad = fminf(j.bad, o.z);
-            j.raise(o.y != 0.f ? fmaxf(j.M, o.x) : j.M);
-            j.add(o.x, o.y, s_acc[threadIdx.x + x * kPerRow]);
-        }
-    }
-    if (!mine) return;
-    if (head == 0 && rr == 0 && d == 0) p.status[b] = status_of(j.bad);
-    const float inv = j.total == 0.f || j.bad < 0.f ? 0.f : 1.f / j.total;
-    if (j.bad < 0.f) j.acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int row = rr / G;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
-        p.out + (static_cast<long long>(b) * p.K + row) * p.ld_out + static_cast<long long>(head * G + rr - row * G) * HD + d);
-    dst[0] = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
-    dst[1] = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
 }
 
 // Query rows of a head from which the tensor-memory kernel is taken: up to 16
@@ -552,11 +591,11 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     Plan a{};
     const int rows = K * (nq / nkv);
     const bool umma = rows >= kUmmaFrom;
-    a.ppu = umma ? kUmmaPages : 1;
     a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
+    a.sms = sms;
+    const int pages = umma ? kUmmaPages : 1, pad = umma ? kUmmaPad : kPad;
     const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? 1 : kMinUnits;
-    a.tiles_max = (rows + a.tr - 1) / a.tr;
-    const long long most = static_cast<long long>(B) * nkv * a.tiles_max * ((max_pages + a.ppu - 1) / a.ppu);
+    const long long most = static_cast<long long>(B) * nkv * ((max_pages + pages - 1) / pages + pad);
     if (most > 0x3FFFFFFFll || B > 65535 || nkv > 65535) {
         set_error("attention: batch * heads * pages is too large for one call");
         return PE_ERR_UNSUPPORTED;
@@ -566,8 +605,8 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const long long slots = static_cast<long long>(sms) * ((most + round - 1) / round);
     const long long want = (most + least - 1) / least;
     a.grid = static_cast<int>(want < slots ? want : slots);
-    a.first_floats = (static_cast<size_t>(B) + 2 + 7) / 8 * 8;
-    a.ws_floats = a.first_floats + 4 + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
+    a.cut_floats = (static_cast<size_t>(a.grid) + 2) / 2 * 8;
+    a.ws_floats = a.cut_floats + 4 + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
     *out = a;
     return PE_OK;
 }
@@ -604,13 +643,14 @@ int check_shape(int B, int K, int nq, int nkv, int hd, int max_pages) {
 
 namespace kv8 {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
-    // four warps to a row where that leaves at most some waves of blocks
     const int rows = p.K * (p.nq / p.nkv);
-    const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;
-    const int block_rows = kMergeThreads / (hd / 4) / (share ? 4 : 1);
-    const dim3 grid((rows + std::max(1, block_rows) - 1) / std::max(1, block_rows), p.nkv, p.B);
+    const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;   // four warps to a row
+    const int block_rows = std::max(1, kMergeThreads / (hd / 4) / (share ? 4 : 1));
+    const long long runs = std::min<long long>(a.grid - 1, static_cast<long long>(p.B) * p.nkv);   // cut ones at most
+    const long long blocks = runs * ((rows + block_rows - 1) / block_rows);
+    const dim3 grid(static_cast<unsigned>(std::max(1ll, std::min<long long>(blocks, a.sms * kMergeBlocks))));
     auto kern = hd == 128 ? (share ? k_kv8_merge<128, 4> : k_kv8_merge<128, 1>) : (share ? k_kv8_merge<64, 4> : k_kv8_merge<64, 1>);
-    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kMergeThreads), 0, s, true, p, a.tr, a.ppu));
+    PE_CUDA_TRY(launch_ex(kern, grid, dim3(kMergeThreads), 0, s, true, p, a.tr, a.grid));
     return PE_OK;
 }
 }  // namespace kv8
@@ -680,13 +720,14 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.out = static_cast<__nv_bfloat16*>(out);
     p.ld_out = ld_out;
     p.status = status;
-    p.first = reinterpret_cast<int32_t*>(ws);
+    p.sms = a.sms;
+    p.cut = reinterpret_cast<int4*>(ws);
     // whole sectors: a 16-byte aligned `ws` may be half of one off
-    p.part = ws + a.first_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);
+    p.part = ws + a.cut_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tr == kUmmaRows) rc = launch_umma(p, a, head_dim, s);
     else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
     else rc = head_dim == 128 ? launch_rows<128, 2>(p, a, s) : launch_rows<64, 2>(p, a, s);
-    // a grid of one covers every head whole
+    // a single share covers every head whole
     return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
 }

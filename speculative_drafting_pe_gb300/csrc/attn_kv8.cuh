@@ -22,8 +22,8 @@ namespace kv8 {
 
 constexpr int kPage = 16;
 constexpr float kRescale = 8.f;    // running maximum (log2) moves only by more than this
-// marks in the place of a row's sum: the request's outputs are zero
-constexpr float kMarkBadPage = -1.f, kMarkTimeout = -2.f;
+// mark in the place of a row's sum: the request's outputs are zero
+constexpr float kMarkBadPage = -1.f;
 
 struct Kv8Params {
     int B, K, nq, nkv, max_pages, num_pages;
@@ -40,7 +40,9 @@ struct Kv8Params {
     __nv_bfloat16* out;
     long long ld_out;
     int32_t* status;
-    int32_t* first;    // [B + 1] OUT: first unit of each request, [B + 1]: units of a CTA
+    int sms;           // shares of the line, unless a share's tables were too small
+    int4* cut;         // [grid] OUT: the run that CTA c's share begins inside of: {request, head, unit of the
+                       // run (0: none, -1: this CTA gave up), units of the run}; [grid]: {positions of a share, shares}
     float* part;       // [2 * grid] partial tiles (part_floats each)
 };
 
@@ -49,20 +51,19 @@ __host__ __device__ constexpr int part_floats(int tr, int hd) { return tr * hd +
 
 // What request b asks for: its live rows, or a status.
 struct Req {
-    int st, S, rows, pages, tiles, run, units;   // run: units of one head and row tile
+    int st, S, rows, pages, run, span;   // run: units of one head; span: positions of all heads
 };
-template <int PPU, int TR>
+template <int PPU, int PAD>
 __device__ __forceinline__ Req request_of(const Kv8Params& p, int b) {
-    Req r{PE_REQ_OK, p.seq_lens[b], p.rows != nullptr ? p.rows[b] : p.K, 0, 0, 0, 0};
+    Req r{PE_REQ_OK, p.seq_lens[b], p.rows != nullptr ? p.rows[b] : p.K, 0, 0, 0};
     if (r.S < 0 || r.rows < 0 || r.rows > p.K) r.st = PE_REQ_BAD_INPUT;
     else if (static_cast<long long>(r.S) + r.rows > static_cast<long long>(p.max_pages) * kPage)
         r.st = PE_REQ_CAPACITY;
     if (r.st != PE_REQ_OK) r.rows = 0;
     if (r.rows > 0) {
         r.pages = (r.S + r.rows + kPage - 1) / kPage;
-        r.tiles = (r.rows * (p.nq / p.nkv) + TR - 1) / TR;
         r.run = (r.pages + PPU - 1) / PPU;
-        r.units = r.run * r.tiles * p.nkv;
+        r.span = (r.run + PAD) * p.nkv;
     }
     return r;
 }
@@ -120,12 +121,12 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
 // have none or are refused; the requests b = blockIdx.x (mod gridDim.x) are
 // this CTA's to look after. gather_units says whether there are any, so that a
 // batch without them pays nothing. By warp my_warp of the CTA's `warps` first.
-template <int PPU, int TR>
-__device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int my_warp, int warps) {
+template <int PPU, int PAD>
+__device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int shares, int my_warp, int warps) {
     const int lane = threadIdx.x & 31;
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const Req r = request_of<PPU, TR>(p, b);
-        if (my_warp == 0 && lane == 0 && r.units == 0) p.status[b] = r.st;
+    for (int b = blockIdx.x; b < p.B; b += shares) {
+        const Req r = request_of<PPU, PAD>(p, b);
+        if (my_warp == 0 && lane == 0 && r.span == 0) p.status[b] = r.st;
         for (int j = r.rows + my_warp; j < p.K; j += warps) {
             uint4* o = reinterpret_cast<uint4*>(p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out);
             for (int c = lane; c < p.nq * hd / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -134,23 +135,26 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 }
 
 // This CTA's share of the line, and its units' pages in shared memory:
-// info[i] of a unit that begins a segment = {request, head * tiles + row tile,
-// unit within its run, units of the run}; of page q of unit i, entry
-// i * PPU + q of tile (page * nkv + head, -1: outside the pool, -2: behind the
-// request's last page). Returns the number of units; lo is the
-// first one, and idle whether zero_idle_rows_by has work. All NT threads of the CTA; every CTA's share is at least
-// `least` and at most max_units (the planner's grid sees to that).
-// `list` is scratch for two ints per unit of the share. The requests of the share are listed first and
-// then all threads look their pages up, so the dependent loads (page, scales)
-// of all pages are in flight together.
-template <int NT, int PPU, int TR>
-__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int2* list, int& lo, bool& idle) {
+// info[i] of a unit that begins a segment = {request, head, unit within its
+// run, units of the run}; of page q of unit i, entry i * PPU + q of tile
+// (page * nkv + head, -1: outside the pool, -2: behind the request's last
+// page). Returns the number of units; idle: 0, or where zero_idle_rows_by has
+// work the number of CTAs with a share.
+// All NT threads of the CTA. A share is at least `least` positions, and at most
+// MAX, which is what the tables hold (the planner's grid sees to that).
+// Behind each run of units lie PAD positions without work: what the end of a
+// segment costs, so that the shares' times are even, not their units alone.
+// `list` is scratch for two ints per position of the share. The requests of
+// the share are listed first and then all threads look their pages up, so the
+// dependent loads of all pages are in flight together.
+template <int NT, int PPU, int PAD, int MAX>
+__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int2* list, int& idle) {
     constexpr int kWarps = NT / 32;
     __shared__ int s_scan[2][kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Req mine0 = tid < p.B ? request_of<PPU, TR>(p, tid) : Req{};   // most batches fit the CTA's threads
-    int total = mine0.units;
-    for (int b = tid + NT; b < p.B; b += NT) total += request_of<PPU, TR>(p, b).units;
+    const Req mine0 = tid < p.B ? request_of<PPU, PAD>(p, tid) : Req{};   // most batches fit the CTA's threads
+    int total = mine0.span;
+    for (int b = tid + NT; b < p.B; b += NT) total += request_of<PPU, PAD>(p, b).span;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) s_scan[0][warp] = total;
@@ -159,18 +163,22 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) total += s_scan[0][i];
     const int grid = static_cast<int>(gridDim.x);
-    const int per = max(least, (total + grid - 1) / grid);
+    // a share per SM, whatever the page table has room for; more only where
+    // the tables of a share would not hold it
+    const int rounds = max(1, (total + p.sms * MAX - 1) / (p.sms * MAX)), shares = min(grid, rounds * p.sms);
+    const int per = max(least, (total + shares - 1) / shares);
+    idle = 0;
+    if (static_cast<int>(blockIdx.x) >= shares) return 0;
     const long long at = static_cast<long long>(blockIdx.x) * per;
-    lo = static_cast<int>(min(at, static_cast<long long>(total)));
+    const int lo = static_cast<int>(min(at, static_cast<long long>(total)));
     const int hi = static_cast<int>(min(static_cast<long long>(total), at + per));
-    const int n = hi - lo;
-    // the requests that the share touches, in order: {request, its first unit}
+    // the requests that the share touches, in order: {request, its first position}
     int base = 0, listed = 0, rest = 0;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
-        const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, TR>(p, b) : Req{});
-        rest |= b < p.B && r.rows < p.K && b % grid == static_cast<int>(blockIdx.x);
-        int incl = r.units;
+        const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, PAD>(p, b) : Req{});
+        rest |= b < p.B && r.rows < p.K && b % shares == static_cast<int>(blockIdx.x);
+        int incl = r.span;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -185,9 +193,8 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
             if (i < warp) below += s_scan[1][i];
             base += s_scan[1][i];
         }
-        const int u0 = below + incl - r.units;
-        if (blockIdx.x == 0 && b < p.B) p.first[b] = u0;
-        const bool mine = r.units > 0 && u0 < hi && u0 + r.units > lo;
+        const int u0 = below + incl - r.span;
+        const bool mine = r.span > 0 && u0 < hi && u0 + r.span > lo;
         const unsigned vote = __ballot_sync(0xffffffffu, mine);
         __syncthreads();
         if (lane == 0) s_scan[1][warp] = __popc(vote);
@@ -200,49 +207,67 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         }
         if (mine) list[rank] = make_int2(b, u0);
     }
-    if (blockIdx.x == 0 && tid == 0) {
-        p.first[p.B] = base;
-        p.first[p.B + 1] = per;
+    idle = __syncthreads_or(rest) != 0 ? shares : 0;
+    // Units of the listed requests ahead of position u (in listed request j,
+    // of units r.run a head): the positions less the padding of the runs ahead.
+    auto units_to = [&](int j, int run, int u) {
+        const int off = u - list[j].y, head = off / (run + PAD), in = off - head * (run + PAD);
+        return list[j].y - list[0].y - PAD * p.nkv * j + head * run + min(in, run);
+    };
+    int n = 0, skip = 0;
+    if (listed > 0) {
+        skip = units_to(0, request_of<PPU, PAD>(p, list[0].x).run, lo);
+        n = units_to(listed - 1, request_of<PPU, PAD>(p, list[listed - 1].x).run, hi) - skip;
     }
-    idle = __syncthreads_or(rest) != 0;
-    for (int x = tid; x < n * PPU; x += NT) {
-        const int i = x / PPU, u = lo + i;
-        int at_list = 0;   // the last listed request that begins at or before u
+    if (tid == 0) {
+        int4 cut = make_int4(0, 0, 0, 0);
+        if (listed > 0) {
+            const int run = request_of<PPU, PAD>(p, list[0].x).run, off = lo - list[0].y;
+            const int head = off / (run + PAD), in = off - head * (run + PAD);
+            if (in < run) cut = make_int4(list[0].x, head, in, run);
+        }
+        p.cut[blockIdx.x] = cut;
+        if (blockIdx.x == 0) p.cut[grid] = make_int4(per, shares, 0, 0);
+    }
+    for (int x = tid; x < (hi - lo) * PPU; x += NT) {
+        const int u = lo + x / PPU;
+        int j = 0;   // the last listed request that begins at or before u
         for (int step = listed; step > 1;) {
             step = (step + 1) / 2;
-            if (at_list + step < listed && list[at_list + step].y <= u) at_list += step;
+            if (j + step < listed && list[j + step].y <= u) j += step;
         }
-        while (at_list + 1 < listed && list[at_list + 1].y <= u) ++at_list;
-        const int b = list[at_list].x, u0 = list[at_list].y;
-        const Req r = request_of<PPU, TR>(p, b);
-        const int pair = (u - u0) / r.run, at_run = (u - u0) - pair * r.run;
-        const int page = at_run * PPU + x % PPU;
+        while (j + 1 < listed && list[j + 1].y <= u) ++j;
+        const int b = list[j].x, off = u - list[j].y;
+        const Req r = request_of<PPU, PAD>(p, b);
+        const int head = off / (r.run + PAD), in = off - head * (r.run + PAD);
+        if (in >= r.run) continue;
+        const int i = units_to(j, r.run, u) - skip, q = x % PPU, page = in * PPU + q;
         int id = -2;
         if (page < r.pages) {
             id = p.page_table[static_cast<size_t>(b) * p.max_pages + page];
-            id = id >= 0 && id < p.num_pages ? id * p.nkv + pair / r.tiles : -1;
+            id = id >= 0 && id < p.num_pages ? id * p.nkv + head : -1;
         }
-        tile[x] = id;
-        if (x % PPU == 0 && (i == 0 || at_run == 0)) info[i] = make_int4(b, pair, at_run, r.run);
+        tile[i * PPU + q] = id;
+        if (q == 0 && (i == 0 || in == 0)) info[i] = make_int4(b, head, in, r.run);
     }
     __syncthreads();
     return n;
 }
 
 __device__ __forceinline__ int status_of(float mark) {
-    return mark == 0.f ? PE_REQ_OK : (mark == kMarkBadPage ? PE_REQ_BAD_PAGE : PE_REQ_TIMEOUT);
+    return mark == 0.f ? PE_REQ_OK : PE_REQ_BAD_PAGE;
 }
 
 struct Plan {
-    int ppu, tr;             // pages of a unit, rows of its tile
-    int grid, tiles_max;
-    size_t first_floats, ws_floats;
+    int tr;                  // rows of a tile
+    int grid, sms;
+    size_t cut_floats, ws_floats;
 };
 
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
-constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448;
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448, kUmmaPad = 7;
 
 }  // namespace kv8
 }  // namespace pe

@@ -50,7 +50,6 @@ constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpConv = 8, kWarpTma = 12, kWarpS = 13, kWarpPv = 14;
-constexpr int kTurns = 4;                   // places of K codes, fp16 V tiles and scores
 constexpr int kDepth = 4;                   // units whose V copies are in flight
 constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
@@ -148,6 +147,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 template <int HD>
 struct Layout {
+    static constexpr int kTurns = HD == 64 ? 6 : 4;          // places of K codes, fp16 V tiles and scores
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
     static constexpr int kQTerm = kRows * HD;                // hi or lo
@@ -172,6 +172,7 @@ template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const Kv8Params p) {
     using L = Layout<HD>;
+    constexpr int kTurns = L::kTurns;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&k_full[s], 1 + 2 * kUmmaPages);
             mbar_init(&cv_full[s], 4);
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 128);
+            mbar_init(&p_full[s], 4);
             mbar_init(&pv_done[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -214,13 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before_sync();
-    int lo;
-    bool idle;
-    const int n = gather_units<kThreads, kUmmaPages, kRows>(p, 1, s_info, s_tile,
-                                                               reinterpret_cast<int2*>(sm + L::kVRing), lo, idle);
+    int idle;
+    const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(
+        p, 1, s_info, s_tile, reinterpret_cast<int2*>(sm + L::kVRing), idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t t_o = tmem + 256;     // S_t in columns 64 (t mod 4) ..; group x's output in 256 + x * HD ..
+    const uint32_t t_o = tmem + kTurns * kTile;   // S_t in columns 64 (t mod kTurns) ..; group x's output x * HD behind them
     bool ok = true;
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
@@ -572,12 +572,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st32(t_s, pk);
                 }
                 tc_fence_before_sync();
-                mbar_arrive(&p_full[i % kTurns]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[i % kTurns]);
             }
             const int final = first + 2 * (count - 1);
             if (ok && count > 0) ok = wait(&pv_done[final % kTurns], turn(final));
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) mark = kMarkTimeout;
             tc_fence_after_sync();
             // the two groups' sums of each row; each group writes half of the dimensions
             s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, vref, 0.f);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
                                  static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
             const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;
-            float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (seg == 0 ? 0 : 1)) * part_floats(kRows, HD);
+            float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (info.z > 0 ? 0 : 1)) * part_floats(kRows, HD);
             const bool all_ok = __all_sync(0xffffffffu, !(bad < 0.f));
             // which groups had a tile: the same for the whole segment
             const bool has_a = (seg & 1) == 0 || len > 1, has_b = (seg & 1) == 1 || len > 1;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             seg += len;
         }
-        if (idle) zero_idle_rows_by<kUmmaPages, kRows>(p, HD, warp, kSoft / 32);
+        if (idle) zero_idle_rows_by<kUmmaPages, kUmmaPad>(p, HD, idle, warp, kSoft / 32);
     }
     if (!ok) {
         s_abort = 1;              // the other roles' waits end too
@@ -664,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
+    if (tid == 0 && s_abort) p.cut[blockIdx.x].z = -1;   // the merge refuses the call's results
     if (warp == kWarpS) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
