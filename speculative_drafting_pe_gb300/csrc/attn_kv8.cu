@@ -42,7 +42,7 @@ constexpr int kStages = 2;         // units in flight per warp: 96 KB per SM. Mo
                                    // in front of every other load
 constexpr int kMaxUnits = 1024;    // units of one CTA
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
-constexpr int kPad = 32;
+constexpr int kPad = 32;           // a segment's end in units (B=64, 512..8192 entries: 66 us, with 0 73)
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -478,10 +478,13 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, 
     __shared__ int s_c[kMergeThreads], s_count[kWarps];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = p.cut[grid].x, shares = p.cut[grid].y;
+    // the table's entries are on their way before it is known how many count
+    const int4 plan = p.cut[grid], near = p.cut[min(tid, grid)];
+    const int after = p.cut[min(tid + kMergeThreads, grid)].z;
+    const int per = plan.x, shares = plan.y;
     const int G = p.nq / p.nkv, blocks = (p.K * G + kBlockRows - 1) / kBlockRows;   // blocks of rows of a run
-    int item = blockIdx.x, late = 0;
-    for (int c = tid; c < shares; c += kMergeThreads) late |= p.cut[c].z < 0;
+    int item = blockIdx.x, late = (tid < shares && near.z < 0) || (tid + kMergeThreads < shares && after < 0);
+    for (int c = tid + 2 * kMergeThreads; c < shares; c += kMergeThreads) late |= p.cut[c].z < 0;
     if (__syncthreads_or(late)) {   // a CTA gave up waiting: no result of the call is kept
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             const Req q = request_of<1, 0>(p, b);
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, 
     for (int c0 = 0; c0 < shares; c0 += kMergeThreads) {
         // the runs whose first cut is one of these
         const int c = c0 + tid;
-        const int4 cut = c < shares ? p.cut[c] : make_int4(0, 0, 0, 0);
+        const int4 cut = c >= shares ? make_int4(0, 0, 0, 0) : c0 == 0 ? near : p.cut[c];
         const bool here = cut.z > 0 && cut.z <= per;
         const unsigned vote = __ballot_sync(0xffffffffu, here);
         __syncthreads();   // the last round's runs have been read
@@ -594,7 +597,7 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
     a.sms = sms;
     const int pages = umma ? kUmmaPages : 1, pad = umma ? kUmmaPad : kPad;
-    const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? 1 : kMinUnits;
+    const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? kUmmaLeast : kMinUnits;
     const long long most = static_cast<long long>(B) * nkv * ((max_pages + pages - 1) / pages + pad);
     if (most > 0x3FFFFFFFll || B > 65535 || nkv > 65535) {
         set_error("attention: batch * heads * pages is too large for one call");

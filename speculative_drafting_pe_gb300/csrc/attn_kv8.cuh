@@ -267,7 +267,10 @@ struct Plan {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
-constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448, kUmmaPad = 7;
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448;
+// A share's positions at least (B=1 K=7, 2048 entries: 14.9 us, with 1 15.5, with 6 16.6), and the units' worth of a
+// segment's end (B=128 K=11: 190 us, with 0 208; 64-wide heads 87 and 91)
+constexpr int kUmmaLeast = 3, kUmmaPad = 7;
 
 }  // namespace kv8
 }  // namespace pe

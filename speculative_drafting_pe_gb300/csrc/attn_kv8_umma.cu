@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     int idle;
     const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(
-        p, 1, s_info, s_tile, reinterpret_cast<int2*>(sm + L::kVRing), idle);
+        p, kUmmaLeast, s_info, s_tile, reinterpret_cast<int2*>(sm + L::kVRing), idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + kTurns * kTile;   // S_t in columns 64 (t mod kTurns) ..; group x's output x * HD behind them
