@@ -349,8 +349,8 @@ int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const voi
  * multiple of 32; w and x 16-byte aligned, ld_x a multiple of 8. Products and
  * sums in fp32; the weights are not rounded. A row of x that holds an infinity
  * or NaN gives infinities or NaN in its row of y, and in no other. No scratch; the
- * device that holds the tensors must be current. Rows of x go 16 at a time, and
- * each 16 read the weights again. */
+ * device that holds the tensors must be current. Rows of x go 8 or 16 at a time,
+ * and each of these reads the weights again; N <= 524280. */
 int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,
                  const void* w_scale, const uint8_t* w_zero, const void* x, int64_t ld_x, float* y, int64_t ld_y,
                  void* stream);
@@ -423,7 +423,7 @@ int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void*
  *  status [B] OUT; a page-table entry of a needed page that is outside
  *         [0, num_pages) is PE_REQ_BAD_PAGE
  * K * (nq/nkv) <= 128, hd 64 or 128; q, out and codes 16-byte aligned, ld_q and
- * ld_out multiples of 8; B * nkv * ceil(K*nq/nkv/16) * max_pages < 2^30.
+ * ld_out multiples of 8; B * nkv * (max_pages + 32) < 2^30.
  * Entries that no row sees may hold anything. A NaN among the entries that
  * only some rows of the pass see makes those rows NaN and no others. */
 int pe_attention_kv8_scratch(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -599,7 +599,7 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const int pages = umma ? kUmmaPages : 1, pad = umma ? kUmmaPad : kPad;
     const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? kUmmaLeast : kMinUnits;
     const long long most = static_cast<long long>(B) * nkv * ((max_pages + pages - 1) / pages + pad);
-    if (most > 0x3FFFFFFFll || B > 65535 || nkv > 65535) {
+    if (most > 0x3FFFFFFFll) {
         set_error("attention: batch * heads * pages is too large for one call");
         return PE_ERR_UNSUPPORTED;
     }
