@@ -47,6 +47,7 @@ struct W4Params {
     int ng;            // groups of a weight row
     int ks;            // warps that share 16 rows (1, 2, 4, 8)
     int nb;            // 256-column blocks
+    int xr;            // token rows in shared memory at a time
     int cb;            // blocks of x in shared memory at a time (a multiple of ks)
     int whole;         // a block's scales and zero points are whole aligned words
     const uint8_t* w;
@@ -93,9 +94,9 @@ struct W4Smem {
     // x row pitch: consecutive rows half the banks apart
     __host__ __device__ static constexpr int pitch(int cb) { return cb * kCols * 2 + 64; }
     static constexpr int kX = kWarps * kStages * kStageBytes;
-    __host__ __device__ static constexpr int up(int cb) { return kX + kN * pitch(cb); }
-    __host__ __device__ static constexpr int red(int cb) { return up(cb) + cb * kN * 4; }
-    __host__ __device__ static constexpr int bytes(int cb) { return red(cb) + kWarps * kRows * kN * 4 + 1024; }
+    __host__ __device__ static constexpr int up(int cb, int xr) { return kX + xr * pitch(cb); }   // xr: rows held
+    __host__ __device__ static constexpr int red(int cb, int xr) { return up(cb, xr) + cb * kN * 4; }
+    __host__ __device__ static constexpr int bytes(int cb, int xr) { return red(cb, xr) + kWarps * kRows * kN * 4 + 1024; }
 };
 
 // Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
@@ -106,8 +107,7 @@ __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
     using L = W4Smem<GROUP, NT>;
     constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb));
-    // rows past the last one stay as they are: an MMA column of its own each, never stored
+    float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb, p.xr));
     const int rows = min(L::kN, p.N - n0), items = min(p.cb, p.nb - b0) * rows;
     for (int i0 = warp; i0 < items; i0 += kWarps * kBatch) {
         uint4 v[kBatch];
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, MB)
     const int ks = p.ks, wk = warp % ks, wt = warp / ks, per = kWarps / ks;
     const int n0 = blockIdx.y * L::kN;
     uint8_t* ring = sm + warp * kStages * kStageBytes;
-    const float* s_up = reinterpret_cast<const float*>(sm + L::up(p.cb));
-    float* s_red = reinterpret_cast<float*>(sm + L::red(p.cb));
+    const float* s_up = reinterpret_cast<const float*>(sm + L::up(p.cb, p.xr));
+    float* s_red = reinterpret_cast<float*>(sm + L::red(p.cb, p.xr));
     const int tiles = (p.M + kRows - 1) / kRows;
     const int iters = (tiles + per - 1) / per;
 
@@ -260,7 +260,10 @@ __global__ void __launch_bounds__(kThreads, MB)
     };
 
     const uint32_t wr0 = smem_u32(ring) + g * 128 + t * 4 + (g << 4);
-    const uint32_t xr0 = smem_u32(sm + L::kX) + g * L::pitch(p.cb) + t * 16;
+    // columns of the MMA without a token row read the last one's again
+    uint32_t xr0[NT];
+#pragma unroll
+    for (int a = 0; a < NT; ++a) xr0[a] = smem_u32(sm + L::kX) + min(a * 8 + g, p.xr - 1) * L::pitch(p.cb) + t * 16;
     const uint32_t low = 0x000F000Fu, high = 0x00F000F0u, magic = 0x64006400u;
     int st = 0;
     const int chunks = (p.nb + p.cb - 1) / p.cb;
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, MB)
                 float sum[NT][4];   // the block's, relative to x's shift
 #pragma unroll
                 for (int a = 0; a < NT; ++a) sum[a][0] = sum[a][1] = sum[a][2] = sum[a][3] = 0.f;
-                const uint32_t wr = wr0 + st * kStageBytes, xr = xr0 + (kb - c * p.cb) * (kCols * 2);
+                const uint32_t wr = wr0 + st * kStageBytes, xo = (kb - c * p.cb) * (kCols * 2);
 #pragma unroll
                 for (int q = 0; q < GR::kN; ++q) {
                     __half2 z1[2], z16[2];   // 1024 + z, and -(64 + z)
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, MB)
                         }
 #pragma unroll
                         for (int a = 0; a < NT; ++a) {
-                            const uint4 xv = lds128(xr + a * 8 * L::pitch(p.cb) + i * 64);
+                            const uint4 xv = lds128(xr0[a] + xo + i * 64);
                             mma_f16(part[a], lo, xv.x, xv.y);
                             mma_f16(part[a], hi, xv.z, xv.w);
                         }
@@ -374,10 +377,8 @@ __global__ void __launch_bounds__(kThreads, MB)
 }
 
 // Shared memory for x at most. Longer rows come in pieces, once for every tile
-// of weight rows; 16 token rows only as far as they fit whole (otherwise eight
-// at a time, with the weights a second time out of L2).
+// of weight rows.
 constexpr int kXBytes = 144 * 1024;
-constexpr int kWide = kXBytes / (16 * 2);   // columns up to which 16 token rows fit
 
 template <int GROUP, int NT, typename S, bool ZERO>
 int launch(W4Params p, int sms, cudaStream_t s) {
@@ -391,12 +392,16 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     p.ks = 1;
     while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps * 2)
         p.ks *= 2;
-    const int fit = kXBytes / (L::kN * kCols * 2) / kWarps * kWarps;
+    p.xr = p.N < L::kN ? p.N : L::kN;
+    const int fit = kXBytes / (p.xr * kCols * 2) / kWarps * kWarps;
     p.cb = p.nb <= fit ? (p.nb + p.ks - 1) / p.ks * p.ks : fit;
     const int iters = (tiles * p.ks + kWarps - 1) / kWarps;
-    const int smem = L::bytes(p.cb);
-    const int per_sm = NT == 1 && smem <= 112 * 1024 ? 2 : 1;
-    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, ZERO, NT == 1 ? 2 : 1> : k_linear_w4<GROUP, NT, S, ZERO, 1>;
+    const int smem = L::bytes(p.cb, p.xr);
+    // Two CTAs to an SM where their shared memory allows; with more than eight
+    // token rows only where each of them has several tiles to lay x out for
+    // (151936 x 2048, 11 rows: 44 us, alone 49; 6144 x 2048: 8.7 us, alone 8.0)
+    const int per_sm = smem <= 112 * 1024 && (NT == 1 || iters > 4 * sms) ? 2 : 1;
+    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, ZERO, 2> : k_linear_w4<GROUP, NT, S, ZERO, 1>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, p));
@@ -405,7 +410,10 @@ int launch(W4Params p, int sms, cudaStream_t s) {
 
 template <int GROUP, typename S>
 int launch_nt(const W4Params& p, int sms, cudaStream_t s) {
-    const bool one = p.N <= 8 || p.Kd > kWide - kWarps * kCols;
+    // eight rows at a time where sixteen, or as many as there are, do not fit
+    // whole (2048 x 6144, 11 rows: 10.8 us, in two passes 13.7)
+    constexpr int kWhole = kWarps * kCols;
+    const bool one = p.N <= 8 || (p.N < 16 ? p.N : 16) * ((p.Kd + kWhole - 1) / kWhole) > kXBytes / (kWhole * 2);
     if (p.zero != nullptr) return one ? launch<GROUP, 1, S, true>(p, sms, s) : launch<GROUP, 2, S, true>(p, sms, s);
     return one ? launch<GROUP, 1, S, false>(p, sms, s) : launch<GROUP, 2, S, false>(p, sms, s);
 }
