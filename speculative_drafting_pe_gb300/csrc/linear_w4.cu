@@ -387,20 +387,28 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     p.nb = (p.Kd + kCols - 1) / kCols;
     p.whole = p.ng % (kCols / GROUP) == 0 &&
               ((reinterpret_cast<uintptr_t>(p.scale) | reinterpret_cast<uintptr_t>(p.zero)) & 15u) == 0;
-    // warps to a row tile: enough that every SM has sixteen, as far as there
-    // are blocks to share (6144 x 2048, 11 rows: 8.1 us, with eight 8.6)
-    p.ks = 1;
-    while (p.ks < kWarps && p.ks < p.nb && static_cast<long long>(tiles) * p.ks < static_cast<long long>(sms) * kWarps * 2)
-        p.ks *= 2;
     p.xr = p.N < L::kN ? p.N : L::kN;
     const int fit = kXBytes / (p.xr * kCols * 2) / kWarps * kWarps;
-    p.cb = p.nb <= fit ? (p.nb + p.ks - 1) / p.ks * p.ks : fit;
-    const int iters = (tiles * p.ks + kWarps - 1) / kWarps;
+    p.cb = p.nb <= fit ? (p.nb + kWarps - 1) / kWarps * kWarps : fit;
     const int smem = L::bytes(p.cb, p.xr);
     // Two CTAs to an SM where their shared memory allows; with more than eight
     // token rows only where each of them has several tiles to lay x out for
     // (151936 x 2048, 11 rows: 44 us, alone 49; 6144 x 2048: 8.7 us, alone 8.0)
-    const int per_sm = smem <= 112 * 1024 && (NT == 1 || iters > 4 * sms) ? 2 : 1;
+    const int per_sm = smem <= 112 * 1024 && (NT == 1 || tiles > 4 * kWarps * sms) ? 2 : 1;
+    // warps to a row tile: the rounds that the CTAs take, times a warp's blocks
+    // in one and kRound blocks' worth of joining and starting anew
+    constexpr int kRound = 1;
+    long long least = 0;
+    int iters = 0;
+    for (int ks = 1; ks <= kWarps && (ks == 1 || ks < 2 * p.nb); ks *= 2) {
+        const int n = static_cast<int>((static_cast<long long>(tiles) * ks + kWarps - 1) / kWarps);
+        const long long cost = static_cast<long long>((n + sms * per_sm - 1) / (sms * per_sm)) * ((p.nb + ks - 1) / ks + kRound);
+        if (ks == 1 || cost <= least) {
+            least = cost;
+            p.ks = ks;
+            iters = n;
+        }
+    }
     auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, ZERO, 2> : k_linear_w4<GROUP, NT, S, ZERO, 1>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
