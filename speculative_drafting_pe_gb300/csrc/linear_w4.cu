@@ -35,9 +35,9 @@
 namespace pe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;                  // one CTA to an SM: x is laid out once for all of them
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;                  // LM head 34.3 us, with 4 35.1 (less shared memory leaves more L1)
+constexpr int kStages = 2;                  // LM head 32.4 us; two CTAs of 8 warps with three stages 34.4
 constexpr int kRows = 16;                    // weight rows of a warp
 constexpr int kCols = 256;                   // columns of a stage
 constexpr int kStageBytes = kRows * kCols / 2;
@@ -45,10 +45,10 @@ constexpr int kStageBytes = kRows * kCols / 2;
 struct W4Params {
     int M, N, Kd;
     int ng;            // groups of a weight row
-    int ks;            // warps that share 16 rows (1, 2, 4, 8)
+    int ks;            // warps that share 16 rows (1, 2, 4, 8, 16)
     int nb;            // 256-column blocks
     int xr;            // token rows in shared memory at a time
-    int cb;            // blocks of x in shared memory at a time (a multiple of ks)
+    int cb;            // blocks of x in shared memory at a time: all, or a multiple of ks
     int whole;         // a block's scales and zero points are whole aligned words
     const uint8_t* w;
     const void* scale;
@@ -101,11 +101,11 @@ struct W4Smem {
 
 // Blocks [b0, b0 + cb) of the token rows into shared memory: fp16 in code
 // order, and for each row and block the factor that undoes its shift. A warp
-// per (row, block), four of them in flight.
+// per (row, block), kBatch of them in flight.
 template <int GROUP, int NT>
 __device__ void load_x(const W4Params& p, uint8_t* sm, int b0, int n0) {
     using L = W4Smem<GROUP, NT>;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* s_up = reinterpret_cast<float*>(sm + L::up(p.cb, p.xr));
     const int rows = min(L::kN, p.N - n0), items = min(p.cb, p.nb - b0) * rows;
@@ -199,9 +199,9 @@ struct Groups {
     __device__ __forceinline__ uint32_t z(int q) const { return ZERO ? (zero[q / 4] >> (8 * (q & 3))) & 0xFFu : 8u; }
 };
 
-// MB: CTAs that share an SM; ZERO: zero points are given (8 otherwise)
-template <int GROUP, int NT, typename S, bool ZERO, int MB>
-__global__ void __launch_bounds__(kThreads, MB)
+// ZERO: zero points are given (8 otherwise)
+template <int GROUP, int NT, typename S, bool ZERO>
+__global__ void __launch_bounds__(kThreads, 1)
     k_linear_w4(const W4Params p) {
     using L = W4Smem<GROUP, NT>;
     using GR = Groups<GROUP, S, ZERO>;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, MB)
 
 // Shared memory for x at most. Longer rows come in pieces, once for every tile
 // of weight rows.
-constexpr int kXBytes = 144 * 1024;
+constexpr int kXBytes = 140 * 1024;
 
 template <int GROUP, int NT, typename S, bool ZERO>
 int launch(W4Params p, int sms, cudaStream_t s) {
@@ -388,13 +388,9 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     p.whole = p.ng % (kCols / GROUP) == 0 &&
               ((reinterpret_cast<uintptr_t>(p.scale) | reinterpret_cast<uintptr_t>(p.zero)) & 15u) == 0;
     p.xr = p.N < L::kN ? p.N : L::kN;
-    const int fit = kXBytes / (p.xr * kCols * 2) / kWarps * kWarps;
-    p.cb = p.nb <= fit ? (p.nb + kWarps - 1) / kWarps * kWarps : fit;
+    const int fit = kXBytes / (p.xr * kCols * 2);
+    p.cb = p.nb <= fit ? p.nb : fit / kWarps * kWarps;
     const int smem = L::bytes(p.cb, p.xr);
-    // Two CTAs to an SM where their shared memory allows; with more than eight
-    // token rows only where each of them has several tiles to lay x out for
-    // (151936 x 2048, 11 rows: 44 us, alone 49; 6144 x 2048: 8.7 us, alone 8.0)
-    const int per_sm = smem <= 112 * 1024 && (NT == 1 || tiles > 4 * kWarps * sms) ? 2 : 1;
     // warps to a row tile: the rounds that the CTAs take, times a warp's blocks
     // in one and kRound blocks' worth of joining and starting anew
     constexpr int kRound = 1;
@@ -402,16 +398,16 @@ int launch(W4Params p, int sms, cudaStream_t s) {
     int iters = 0;
     for (int ks = 1; ks <= kWarps && (ks == 1 || ks < 2 * p.nb); ks *= 2) {
         const int n = static_cast<int>((static_cast<long long>(tiles) * ks + kWarps - 1) / kWarps);
-        const long long cost = static_cast<long long>((n + sms * per_sm - 1) / (sms * per_sm)) * ((p.nb + ks - 1) / ks + kRound);
+        const long long cost = static_cast<long long>((n + sms - 1) / sms) * ((p.nb + ks - 1) / ks + kRound);
         if (ks == 1 || cost <= least) {
             least = cost;
             p.ks = ks;
             iters = n;
         }
     }
-    auto kern = per_sm == 2 ? k_linear_w4<GROUP, NT, S, ZERO, 2> : k_linear_w4<GROUP, NT, S, ZERO, 1>;
+    auto kern = k_linear_w4<GROUP, NT, S, ZERO>;
     PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    const dim3 grid(iters < sms * per_sm ? iters : sms * per_sm, (p.N + L::kN - 1) / L::kN);
+    const dim3 grid(iters < sms ? iters : sms, (p.N + L::kN - 1) / L::kN);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, p));
     return PE_OK;
 }
@@ -420,8 +416,7 @@ template <int GROUP, typename S>
 int launch_nt(const W4Params& p, int sms, cudaStream_t s) {
     // eight rows at a time where sixteen, or as many as there are, do not fit
     // whole (2048 x 6144, 11 rows: 10.8 us, in two passes 13.7)
-    constexpr int kWhole = kWarps * kCols;
-    const bool one = p.N <= 8 || (p.N < 16 ? p.N : 16) * ((p.Kd + kWhole - 1) / kWhole) > kXBytes / (kWhole * 2);
+    const bool one = p.N <= 8 || static_cast<long long>(p.N < 16 ? p.N : 16) * ((p.Kd + kCols - 1) / kCols) > kXBytes / (kCols * 2);
     if (p.zero != nullptr) return one ? launch<GROUP, 1, S, true>(p, sms, s) : launch<GROUP, 2, S, true>(p, sms, s);
     return one ? launch<GROUP, 1, S, false>(p, sms, s) : launch<GROUP, 2, S, false>(p, sms, s);
 }
