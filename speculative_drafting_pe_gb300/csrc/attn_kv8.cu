@@ -589,9 +589,10 @@ constexpr int kUmmaFrom = 17;
 
 int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     int dev = 0, sms = 0;
-    PE_CUDA_TRY(cudaGetDevice(&dev));
-    PE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const int rc = current_device(&dev, &sms);
+    if (rc != PE_OK) return rc;
     Plan a{};
+    a.dev = dev;
     const int rows = K * (nq / nkv);
     const bool umma = rows >= kUmmaFrom;
     a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
@@ -616,9 +617,10 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
 
 template <int HD, int NT>
 int launch_rows(const Kv8Params& p, const Plan& a, cudaStream_t s) {
-    auto kern = k_attn_kv8<HD, NT>;
+    constexpr auto kern = k_attn_kv8<HD, NT>;
     constexpr int smem = Smem<HD, NT>::kBytes;
-    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const int rc = allow_smem<kern>(a.dev, smem);
+    if (rc != PE_OK) return rc;
     PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), smem, s, false, p));
     return PE_OK;
 }

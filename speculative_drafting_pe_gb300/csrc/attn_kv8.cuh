@@ -260,7 +260,7 @@ __device__ __forceinline__ int status_of(float mark) {
 
 struct Plan {
     int tr;                  // rows of a tile
-    int grid, sms;
+    int grid, sms, dev;
     size_t cut_floats, ws_floats;
 };
 

@@ -673,8 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int HD>
 int launch_hd(const CUtensorMap& tk, const Kv8Params& p, const Plan& a, cudaStream_t s) {
-    auto kern = k_attn_kv8_umma<HD>;
-    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::kBytes));
+    constexpr auto kern = k_attn_kv8_umma<HD>;
+    const int rc = allow_smem<kern>(a.dev, Layout<HD>::kBytes);
+    if (rc != PE_OK) return rc;
     PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, tk, p));
     return PE_OK;
 }

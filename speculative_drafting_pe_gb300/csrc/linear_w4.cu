@@ -43,7 +43,7 @@ constexpr int kCols = 256;                   // columns of a stage
 constexpr int kStageBytes = kRows * kCols / 2;
 
 struct W4Params {
-    int M, N, Kd;
+    int M, N, Kd, dev;
     int ng;            // groups of a weight row
     int ks;            // warps that share 16 rows (1, 2, 4, 8, 16)
     int nb;            // 256-column blocks
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Shared memory for x at most. Longer rows come in pieces, once for every tile
 // of weight rows.
 constexpr int kXBytes = 140 * 1024;
+constexpr int kMaxSmem = 232448;             // of a block
 
 template <int GROUP, int NT, typename S, bool ZERO>
 int launch(W4Params p, int sms, cudaStream_t s) {
@@ -405,8 +406,9 @@ int launch(W4Params p, int sms, cudaStream_t s) {
             iters = n;
         }
     }
-    auto kern = k_linear_w4<GROUP, NT, S, ZERO>;
-    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    constexpr auto kern = k_linear_w4<GROUP, NT, S, ZERO>;
+    const int rc = allow_smem<kern>(p.dev, kMaxSmem);
+    if (rc != PE_OK) return rc;
     const dim3 grid(iters < sms ? iters : sms, (p.N + L::kN - 1) / L::kN);
     PE_CUDA_TRY(launch_ex(kern, grid, dim3(kThreads), smem, s, false, p));
     return PE_OK;
@@ -453,9 +455,10 @@ extern "C" int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, con
     }
     if (M > 0x7FFFFFFF - 256 || N > 8 * 65535) { set_error("M or N too large"); return PE_ERR_ARG; }
     int dev = 0, sms = 0;
-    PE_CUDA_TRY(cudaGetDevice(&dev));
-    PE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const int rc = current_device(&dev, &sms);
+    if (rc != PE_OK) return rc;
     W4Params p{};
+    p.dev = dev;
     p.M = M;
     p.N = N;
     p.Kd = Kd;
