@@ -63,7 +63,8 @@ struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr int kTile = kPage * HD;                 // a page's K or V of one head
     // a stage of a warp: K chunks [HD / 32][lane] of 16 bytes, V chunks [4][lane] of HD / 8
-    static constexpr int kSlots = kWarps / 2;                // two warps share a slot of sums
+    static constexpr int kRounds = NT;                       // warps that share a slot of sums
+    static constexpr int kSlots = kWarps / kRounds;
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
     static constexpr int kO = kRing;                         // [kSlots][kRows][HD] fp32
     static constexpr int kMl = kO + kSlots * kRows * HD * 4; // [2][kWarps][kRows] (max, sum)
@@ -363,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
 #pragma unroll
-        for (int round = 0; round < 2; ++round) {
-            if ((warp >= L::kSlots) == (round == 1)) {
+        for (int round = 0; round < L::kRounds; ++round) {
+            if (warp / L::kSlots == round) {
                 float* slot = s_o + (warp - round * L::kSlots) * kRows * HD;
 #pragma unroll
                 for (int a = 0; a < NT; ++a)
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < kCols / 4; ++c) {
                             float4* at = reinterpret_cast<float4*>(slot + r * HD) + ((g * (kCols / 4) + c) ^ L::swizzle(r));
                             float4 v = make_float4(o[2 * c][a][x], o[2 * c][a][2 + x], o[2 * c + 1][a][x], o[2 * c + 1][a][2 + x]);
-                            if (round == 1) {
+                            if (round > 0) {
                                 const float4 u = *at;
                                 v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
                             }
