@@ -27,6 +27,13 @@
 // an exact shift by a power of two per row, scores and sums are fp32, weights
 // go to fp16 (2^-11) relative to the row's running maximum and the largest V
 // scale seen.
+//
+// Bound by the cache's bytes while it streams (a CTA's twelve warps take 1900
+// cycles for twelve pages of K and V, 48 KB, the rate of the measured copy);
+// around that stand the launch and the look-up of the share (about 5 us), a
+// join of the warps per segment (2 us) and the merge. 64 requests of 512 to
+// 8192 entries, one row of 8 heads to each of 4 of 128: 66 us, 4.3 TB/s, 65%
+// of the measured copy; one of 131072 entries 38 us, 53%.
 #include <algorithm>
 
 #include "attn_kv8.cuh"

@@ -2,14 +2,13 @@
 // parameters, the line of units that the CTAs divide, and the partial sums
 // that k_kv8_merge joins.
 //
-// A unit is PPU pages of one (kv head, tile of TR query rows). All units of
-// the batch stand in one line (request, kv head, row tile, page) and every CTA
-// takes the same number of them, so ragged lengths, many requests and a single
+// A unit is PPU pages of one kv head, with all the query rows over it. All
+// units of the batch stand in one line (request, kv head, page) and every CTA
+// takes an equal share of it, so ragged lengths, many requests and a single
 // long one are split alike; the lengths stay on the device. A run of units of
-// one head and row tile within a CTA is a segment. A CTA writes the heads that
-// it covers whole; a head that several CTAs share leaves one partial tile per
-// CTA in scratch, at places that follow from the unit numbers, and k_kv8_merge
-// joins them in order.
+// one head within a CTA is a segment. A CTA writes the heads that it covers
+// whole; a head that several CTAs share leaves one partial tile per CTA in
+// scratch, and k_kv8_merge joins them in order.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -43,7 +42,7 @@ struct Kv8Params {
     int sms;           // shares of the line, unless a share's tables were too small
     int4* cut;         // [grid] OUT: the run that CTA c's share begins inside of: {request, head, unit of the
                        // run (0: none, -1: this CTA gave up), units of the run}; [grid]: {positions of a share, shares}
-    float* part;       // [2 * grid] partial tiles (part_floats each)
+    float* part;       // [2 * grid] partial tiles (part_floats each): of a CTA's run that began in an earlier share, and of the other one
 };
 
 // a partial tile: O [tr][hd], the running maxima (log2) [tr], the sums [tr]

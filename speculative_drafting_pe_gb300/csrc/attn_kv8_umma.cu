@@ -25,11 +25,11 @@
 //               x takes the units t = x (mod 2), with a running maximum, sum
 //               and output accumulator of its own, so that neither waits for
 //               the other; they meet at the end of a segment.
-// Four S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S runs
-// up to four units ahead of P.V, so a group finds its next scores ready when it
-// is done with the last. V tiles and S_t have four places each and "P_t V_t is
-// complete" frees both, as "S_t is complete" frees K_t's place: one commit for
-// each product. Waits, MMAs and commits cost their warp
+// kTurns S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t, and S
+// runs up to that many units ahead of P.V, so a group finds its next scores
+// ready when it is done with the last. V tiles and S_t have as many places and
+// "P_t V_t is complete" frees both, as "S_t is complete" frees K_t's place: one
+// commit for each product. Waits, MMAs and commits cost their warp
 // about 100, 40 and 100 cycles each; with both products and six commits in one
 // warp that, 1550 cycles a unit, was what bounded the kernel.
 //
@@ -38,6 +38,16 @@
 // 1800; half of it each way, neither holds the kernel. K codes as MMA operands
 // leave only V to be widened: with K widened too the shared memory carried
 // 128 KB a unit, a quarter more than now, at 128 bytes a cycle.
+//
+// A unit takes some 1170 cycles (64-wide heads: 1100), where its bytes would
+// take 730 (370) and its products 640; no stage by itself is what holds it:
+// without any one of the copies, the exponentials or a product it is no more
+// than a tenth faster. K by a warp's own copies (220 us), units of 128 entries
+// (64-wide heads 93 us, 128-wide ones 250), a third softmax group for 64-wide
+// heads (100) and scores of two units in one product (242, then 235 without)
+// did not help. 128 requests of 512 to 8192 entries, 11 rows of
+// 8 heads to each of 4 of 128: 190 us, 3.1 TB/s, 47% of the measured copy; 64
+// of 1024 to 4096, up to 10 rows of 8 heads to each of 8 of 64: 87 us, 27%.
 #include "attn_kv8.cuh"
 
 namespace pe {

@@ -13,8 +13,10 @@
 // One warp owns one (request, page, head, K or V): it reads the page's new
 // rows once (8 bytes a lane), keeps them in registers, takes the maximum by
 // shuffles and stores the codes (4 bytes a lane), so no two warps write one
-// page and nothing is read twice. Bound by DRAM for prompts, by latency for
-// the rows of a draft pass.
+// page and nothing is read twice. Bound by latency: a warp's loads (length,
+// page, rows, committed codes and scale) depend on one another. 8 rows of 32
+// requests, 4 heads of 128, take 5.0 us; 8 prompts of up to 2048 rows, 8 heads
+// of 64, 7.4 us, 0.94 TB/s.
 #include <cuda_fp16.h>
 
 #include "common.cuh"

@@ -27,6 +27,12 @@
 // 26 bytes/ns per SM: the LM head took 48 us.) Where there are few rows, `ks`
 // warps of a CTA share one set of 16, block by block, and their sums are added
 // in order at the end.
+//
+// 151936 x 2048 (an LM head) with 8 rows: 32.5 us, 5.2 TB/s, 78% of the
+// measured copy, with 11 rows 41 us: the instructions per code, and the MMAs
+// twice, are next. Small matrices are bound by laying out x and by one block's
+// latency after a launch: 2048 x 4096 and one row 4.1 us, 6144 x 2048 and 11
+// rows 7.8 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
