@@ -157,6 +157,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 template <int HD>
 struct Layout {
+    static constexpr int kTeam = HD == 64 ? 1 : 2;           // converter warps to a unit
     static constexpr int kTurns = HD == 64 ? 6 : 4;          // places of K codes, fp16 V tiles and scores
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_abort = 0;
         for (int s = 0; s < kTurns; ++s) {
             mbar_init(&k_full[s], 1 + 2 * kUmmaPages);
-            mbar_init(&cv_full[s], 4);
+            mbar_init(&cv_full[s], L::kTeam);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
             mbar_init(&pv_done[s], 1);
@@ -313,35 +314,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kWarpConv) {
-        const int ct = tid & 127;
-        // this thread's chunk of row `row` of pages page0 (+ 1 pass by pass of
-        // 128-wide rows, + 2 of 64-wide ones)
-        constexpr int kChunks = HD / 16, kPass = 128 / kChunks, kPasses = kTile / kPass;
-        const int ch = ct % kChunks, row0 = ct / kChunks, row = row0 % kPage, page_step = kPass / kPage;
+        constexpr int kTeam = L::kTeam, kTeams = 4 / kTeam, kAhead = kDepth / kTeams;
+        const int ct = tid & 127, team = (warp - kWarpConv) / kTeam, part = (warp - kWarpConv) % kTeam;
+        // a pass of a warp covers kPass rows of its part of the unit; this lane's chunk of them
+        constexpr int kChunks = HD / 16, kPass = 32 / kChunks, kPasses = kTile / kTeam / kPass, kMine = kUmmaPages / kTeam;
+        const int ch = lane % kChunks, row0 = part * (kTile / kTeam) + lane / kChunks;
         const uint64_t policy = l2_policy_evict_first();
-        const uint8_t* from = p.v_codes + row * HD + ch * 16;
-        const uint32_t v_at = smem_u32(sm + L::kVRing) + ct * 16;
-        auto fetch = [&](int i) {   // a group of copies even where there is nothing to copy
+        const uint8_t* from = p.v_codes + lane * 16;
+        uint8_t* ring = sm + L::kVRing + part * kMine * kPage * HD + lane * 16;
+        const uint32_t v_at = smem_u32(ring);
+        auto fetch = [&](int i) {
             if (i < n) {
-                const int* tiles = s_tile + i * kUmmaPages + row0 / kPage;
 #pragma unroll
-                for (int x = 0; x < kPasses; ++x) {
-                    const int tile = tiles[x * page_step];
-                    if (tile >= 0)
-                        copy_async<16>(v_at + (i % kDepth) * L::kCodes + x * 2048,
-                                       from + static_cast<long long>(tile) * (kPage * HD), policy);
+                for (int q = 0; q < kMine; ++q) {
+                    const int tile = s_tile[i * kUmmaPages + part * kMine + q];
+                    if (tile < 0) continue;
+                    const uint8_t* src = from + static_cast<long long>(tile) * (kPage * HD);
+#pragma unroll
+                    for (int x = 0; x < kPage / kPass; ++x)
+                        copy_async<16>(v_at + (i % kDepth) * L::kCodes + q * kPage * HD + x * 512, src + x * 512, policy);
                 }
             }
             copies_commit();
         };
-        for (int i = 0; i < kDepth; ++i) fetch(i);
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) fetch(team + x * kTeams);
         int seg = 0, end = 0, no = -1, S = 0, last = 0;
-        for (int i = 0; i < n; ++i) {
-            const int c = i % kTurns;
-            if (i == end) {      // a segment begins: its query rows
-                const int4 info = s_info[i];
-                seg = i;
-                end = i + min(info.w - info.z, n - i);
+        // the query rows of the segments up to the one of unit `upto`: every
+        // warp has 32 of them
+        auto queries = [&](int upto) {
+            while (ok && end <= upto) {
+                const int4 info = s_info[end];
+                seg = end;
+                end = seg + min(info.w - info.z, n - seg);
                 ++no;
                 const int b = info.x;
                 S = p.seq_lens[b];
@@ -417,11 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no & 1]);
             }
-            copies_wait<kDepth - 1>();
+        };
+        for (int i = team; i < n; i += kTeams) {
+            const int c = i % kTurns;
+            queries(i);
+            copies_wait<kAhead - 1>();
             uint4 v[kPasses];
 #pragma unroll
             for (int x = 0; x < kPasses; ++x)
-                v[x] = *reinterpret_cast<const uint4*>(sm + L::kVRing + (i % kDepth) * L::kCodes + x * 2048 + ct * 16);
+                v[x] = *reinterpret_cast<const uint4*>(ring + (i % kDepth) * L::kCodes + x * 512);
             fetch(i + kDepth);
             if (i >= kTurns) ok = ok && wait(&pv_done[c], turn(i) ^ 1u);
             ok = __all_sync(0xffffffffu, ok);
@@ -458,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&cv_full[c]);
         }
+        queries(n - 1);
         copies_wait<0>();
     } else {
         // ------------------------------------------------ softmax: thread = query row
