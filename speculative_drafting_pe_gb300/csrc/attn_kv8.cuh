@@ -268,7 +268,7 @@ int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448;
 // A share's positions at least (B=1 K=7, 2048 entries: 14.9 us, with 1 15.5, with 6 16.6), and the units' worth of a
-// segment's end (B=128 K=11: 190 us, with 0 208; 64-wide heads 87 and 91)
+// segment's end (B=128 K=11: 190 us, with 0 208; 64-wide heads 87 and 91; as all of these were then)
 constexpr int kUmmaLeast = 3, kUmmaPad = 7;
 
 }  // namespace kv8

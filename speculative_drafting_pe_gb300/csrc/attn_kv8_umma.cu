@@ -3,23 +3,29 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (480 threads):
-//   warp 12     TMA: the unit's K pages, a lane per page, to where the MMA
-//               reads them (the swizzle of a K-major operand), and the page
-//               scales by asynchronous copies of eight lanes
-//   warps 8-11  converters. Each thread fetches 16-byte chunks of V, kDepth
-//               units ahead, by asynchronous copies to a place of its own, and
-//               turns them into an fp16 tile (fp16 holds every E4M3 value;
-//               128-byte swizzle, entry-major, read as an MN-major operand),
-//               V of entries that no row sees zero. At the start of a segment
-//               the query rows: shifted by a power of two per row so that the
+// Roles (512 threads):
+//   warps 14,15 the unit's K pages to where the MMA reads them (the swizzle of
+//               a K-major operand), and the page scales. 128-wide heads: warp
+//               14 by TMA, a lane per page; 64-wide ones: both warps in turn by
+//               asynchronous copies. A box of 16 rows takes about 150 cycles
+//               whatever its rows hold, a copy instruction always 512 bytes
+//               (128 wide: 181 us by boxes, 192 by copies; 64 wide: 85 and 80)
+//   warps 8-11  converters, kTeam warps to a unit. Each thread fetches 16-byte chunks of V, kDepth units ahead, by
+//               asynchronous copies to a place of its own, and turns them into
+//               an fp16 tile (fp16 holds every E4M3 value; 128-byte swizzle,
+//               entry-major, read as an MN-major operand), V of entries that
+//               no row sees zero. A unit of 64-wide heads to a warp each, in
+//               turn (80 us, all four warps on every unit 85); four warps to
+//               each of 128-wide ones, whose V tiles have fewer places (178 us,
+//               a warp each 261). At the start of a segment the query rows:
+//               shifted by a power of two per row so that the
 //               largest value lies in [128, 256) and split into two E4M3
 //               terms, q = hi + lo, which hold the 8 bits of a bf16 value
 //               exactly down to 1/1024 of the row's largest and to 2^-18 of
 //               that below.
-//   warp 13     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
+//   warp 12     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
 //               N=64, E4M3 operands: the codes themselves)
-//   warp 14     one elected lane issues O += P_t V_t (fp16, A = P_t from
+//   warp 13     one elected lane issues O += P_t V_t (fp16, A = P_t from
 //               tensor memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
@@ -33,21 +39,20 @@
 // about 100, 40 and 100 cycles each; with both products and six commits in one
 // warp that, 1550 cycles a unit, was what bounded the kernel.
 //
-// A TMA box of one page (16 rows) takes about 150 cycles, whoever issues it:
-// K and V both by TMA took 1300 cycles a unit, both by the converters' copies
-// 1800; half of it each way, neither holds the kernel. K codes as MMA operands
-// leave only V to be widened: with K widened too the shared memory carried
-// 128 KB a unit, a quarter more than now, at 128 bytes a cycle.
+// K codes as MMA operands leave only V to be widened: with K widened too the
+// shared memory carried 128 KB a unit, a quarter more than now, at 128 bytes a
+// cycle.
 //
-// A unit takes some 1170 cycles (64-wide heads: 1100), where its bytes would
-// take 730 (370) and its products 640; no stage by itself is what holds it:
-// without any one of the copies, the exponentials or a product it is no more
-// than a tenth faster. K by a warp's own copies (220 us), units of 128 entries
-// (64-wide heads 93 us, 128-wide ones 250), a third softmax group for 64-wide
-// heads (100) and scores of two units in one product (242, then 235 without)
-// did not help. 128 requests of 512 to 8192 entries, 11 rows of
-// 8 heads to each of 4 of 128: 190 us, 3.1 TB/s, 47% of the measured copy; 64
-// of 1024 to 4096, up to 10 rows of 8 heads to each of 8 of 64: 87 us, 27%.
+// A unit takes some 1150 cycles (64-wide heads: 1000), where its bytes would
+// take 730 (370) and its products 640; no stage by itself holds it: without
+// the softmax it is 8% faster (64-wide heads 15%), without the copies 3% (7%),
+// without the widening 4% (2%), without the exponentials or either product no
+// more than 4%. Units of 128 entries (64-wide heads 93 us where 87 were taken
+// then, 128-wide ones 250 for 190), a third softmax group for 64-wide heads
+// (100 for 87) and scores of two units in one product (242 for 235) did not
+// help. 128 requests of 512 to 8192 entries, 11 rows of 8 heads to each of 4
+// of 128: 178 us, 3.3 TB/s, 50% of the measured copy; 64 of 1024 to 4096, up
+// to 10 rows of 8 heads to each of 8 of 64: 80 us, 30%.
 #include "attn_kv8.cuh"
 
 namespace pe {
@@ -55,12 +60,13 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 480;
+constexpr int kThreads = 512;
 constexpr int kTile = kUmmaPages * kPage;   // entries of a unit
 constexpr int kRows = kUmmaRows;
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpConv = 8, kWarpTma = 12, kWarpS = 13, kWarpPv = 14;
+constexpr int kWarpConv = 8, kWarpS = 12, kWarpPv = 13, kWarpK = 14;
 constexpr int kDepth = 4;                   // units whose V copies are in flight
+constexpr int kBehind = 1;                  // units whose K copies a warp has in flight while it waits for the one before
 constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
@@ -157,7 +163,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 template <int HD>
 struct Layout {
-    static constexpr int kTeam = HD == 64 ? 1 : 2;           // converter warps to a unit
+    static constexpr bool kTmaK = HD == 128;                 // K by TMA boxes, or by copies of two warps
+    static constexpr int kTeam = HD == 64 ? 1 : 4;           // converter warps to a unit
     static constexpr int kTurns = HD == 64 ? 6 : 4;          // places of K codes, fp16 V tiles and scores
     static constexpr int kCodes = kTile * HD;                // codes of K or V of a unit
     static constexpr int kCvTile = kTile * HD * 2;
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         s_abort = 0;
         for (int s = 0; s < kTurns; ++s) {
-            mbar_init(&k_full[s], 1 + 2 * kUmmaPages);
+            mbar_init(&k_full[s], L::kTmaK ? 1 + 2 * kUmmaPages : 1);
             mbar_init(&cv_full[s], L::kTeam);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
-    if (warp == kWarpTma) {
+    if (L::kTmaK && warp == kWarpK) {
         const uint64_t policy = l2_policy_evict_first();
         for (int i = 0; i < n; ++i) {
             const int x = i % kTurns;
@@ -263,7 +270,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         copies_commit();
         copies_wait<0>();
         __syncwarp();
-    } else if (warp >= kWarpS) {
+    } else if (!L::kTmaK && warp >= kWarpK) {
+        // two warps, a unit each in turn; chunk c of a row goes where the swizzle of a K-major operand has it
+        constexpr int kChunks = HD / 16, kPass = 32 / kChunks, kPasses = kPage / kPass;
+        const uint64_t policy = l2_policy_evict_first();
+        const int row = lane / kChunks, c = lane % kChunks;
+        const uint8_t* from = p.k_codes + lane * 16;
+        uint32_t to[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = row + x * kPass;
+            to[x] = smem_u32(sm + L::kKRing) + row * HD + ((HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+        }
+        const int first = warp - kWarpK;
+        for (int i = first; i < n + 2 * kBehind; i += 2) {
+            const int x = i % kTurns;
+            if (i < n) {
+                if (i >= kTurns) ok = wait(&s_full[x], turn(i) ^ 1u);   // S of the unit before it in this place
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < kUmmaPages; ++q) {
+                    const int tile = s_tile[i * kUmmaPages + q];
+                    if (tile < 0) continue;
+                    const uint8_t* src = from + static_cast<long long>(tile) * (kPage * HD);
+#pragma unroll
+                    for (int j = 0; j < kPasses; ++j)
+                        copy_async<16>(to[j & 1] + x * L::kCodes + q * kPage * HD + j * 512, src + j * 512, policy);
+                }
+                if (lane < 2 * kUmmaPages) {   // a page's K or V scale each
+                    float* dst = s_scale + (i % kScales) * 8 + lane;
+                    const int tile = s_tile[i * kUmmaPages + lane % kUmmaPages];
+                    if (tile >= 0) copy_async<4>(smem_u32(dst), (lane < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
+                    else *dst = 0.f;
+                }
+            }
+            copies_commit();
+            if (i >= 2 * kBehind) {
+                copies_wait<kBehind>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_full[(i - 2 * kBehind) % kTurns]);
+            }
+        }
+        copies_wait<0>();
+        __syncwarp();
+    } else if (warp == kWarpS || warp == kWarpPv) {
         // The whole warp walks the units and one elected lane issues: in
         // warp-uniform control flow the descriptors stay in uniform registers.
         const bool scores = warp != kWarpPv;
@@ -313,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         __syncwarp();
-    } else if (warp >= kWarpConv) {
+    } else if (warp >= kWarpConv && warp < kWarpS) {
         constexpr int kTeam = L::kTeam, kTeams = 4 / kTeam, kAhead = kDepth / kTeams;
         const int ct = tid & 127, team = (warp - kWarpConv) / kTeam, part = (warp - kWarpConv) % kTeam;
         // a pass of a warp covers kPass rows of its part of the unit; this lane's chunk of them
@@ -469,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         queries(n - 1);
         copies_wait<0>();
-    } else {
+    } else if (warp < kWarpConv) {
         // ------------------------------------------------ softmax: thread = query row
         const int grp = warp >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
