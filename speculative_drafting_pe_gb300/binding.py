@@ -555,6 +555,9 @@ def verify_rebuild_refeed(drafts, target_tokens, page_table, num_pages, n_real, 
 #
 # The calls below run where their tensors live, on that device's current
 # stream unless `stream` is given; all tensors of a call are on one device.
+# What a call allocates (outputs, scratch) belongs to the stream that it runs
+# on: the allocator gives no memory of another stream's pending work to it, and
+# scratch goes back to that stream alone.
 # They stand in the loop of a server, where a call of a few microseconds on the
 # GPU waits for the host, so their checks are plain comparisons.
 
@@ -566,6 +569,16 @@ def _need_is(name, t, dtype, dev, shape):
     if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _empty(shape, dtype, dev, stream):
+    """New memory of the stream that the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _run(fn, dev, stream, *args):
@@ -631,7 +644,7 @@ def linear_w4(w_codes, w_scale, x, group, zeros=None, y=None, stream=None):
     if zeros is not None:
         _need_is("zeros", zeros, _BYTE, dev, shape)
     if y is None:
-        y = torch.empty((N, M), dtype=_FLOAT, device=dev)
+        y = _empty((N, M), _FLOAT, dev, stream)
     elif y.dtype is not _FLOAT or y.device != dev or y.shape != (N, M):
         raise ValueError(f"y must be float32 {(N, M)} on {dev}")
     _run(lib.pe_linear_w4, dev, stream, M, N, Kd, group, w_codes.data_ptr(),
@@ -657,8 +670,7 @@ def assign_pages(seq_lens, new_lens, page_counts, page_table, free_pages, free_c
     cap = free_pages.shape[0]
     _need_is("free_pages", free_pages, _INT, dev, (cap,))
     _need_is("free_count", free_count, _INT, dev, (1,))
-    slots = torch.empty((B, n_max), dtype=_INT, device=dev)
-    counts, left, status = torch.empty_like(seq_lens), torch.empty_like(free_count), torch.empty_like(seq_lens)
+    slots, counts, left, status = (_empty(s, _INT, dev, stream) for s in ((B, n_max), shape, (1,), shape))
     _run(lib.pe_assign_pages, dev, stream, B, seq_lens.data_ptr(), new_lens.data_ptr(), page_counts.data_ptr(),
          counts.data_ptr(), page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap,
          free_count.data_ptr(), left.data_ptr(), n_max, slots.data_ptr(), status.data_ptr())
@@ -680,7 +692,7 @@ def release_pages(keep_lens, page_counts, page_table, free_pages, free_count, nu
     cap = free_pages.shape[0]
     _need_is("free_pages", free_pages, _INT, dev, (cap,))
     _need_is("free_count", free_count, _INT, dev, (1,))
-    status = torch.empty_like(keep_lens)
+    status = _empty(shape, _INT, dev, stream)
     _run(lib.pe_release_pages, dev, stream, B, keep_lens.data_ptr(), page_counts.data_ptr(), page_counts.data_ptr(),
          page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap, free_count.data_ptr(),
          free_count.data_ptr(), status.data_ptr())
@@ -715,7 +727,7 @@ def kv8_append(k, v, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, r
         raise ValueError(f"k and v must be bfloat16 [B, n, nkv, hd] on {dev}")
     pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
     if status is None:
-        status = torch.empty_like(seq_lens)
+        status = _empty((B,), _INT, dev, stream)
     else:
         _need_is("status", status, _INT, dev, (B,))
     _run(lib.pe_kv8_append, dev, stream, B, n, nkv, hd, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
@@ -749,18 +761,18 @@ def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, s
     nkv = k_codes.shape[1] if k_codes.dim() == 4 else 0
     pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
     if out is None:
-        out = torch.empty((B, K, nq, hd), dtype=_BF16, device=dev)
+        out = _empty((B, K, nq, hd), _BF16, dev, stream)
     elif out.dtype is not _BF16 or out.device != dev or out.shape != q.shape:
         raise ValueError(f"out must be bfloat16 {tuple(q.shape)} on {dev}")
     if status is None:
-        status = torch.empty_like(seq_lens)
+        status = _empty((B,), _INT, dev, stream)
     else:
         _need_is("status", status, _INT, dev, (B,))
     if dev.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {dev}")
     max_pages = page_table.shape[1]
     need = _kv8_scratch(dev.index, B, K, nq, nkv, hd, max_pages)
-    ws = torch.empty(need, dtype=_FLOAT, device=dev)
+    ws = _empty(need, _FLOAT, dev, stream)
     _run(lib.pe_attention_kv8, dev, stream, B, K, nq, nkv, hd, q.data_ptr(), _row_stride(q, "q"),
          seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(), max_pages, pages,
          k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),

@@ -238,3 +238,40 @@ def test_attention_into_rows_and_scratch_at_sixteen_bytes(hd):
     assert rc == 0 and (status == 0).all()
     assert torch.equal(wide[:, 8:8 + width].reshape(want.shape), want)
     assert (wide[:, :8] == 3).all() and (wide[:, 8 + width:] == 3).all()
+
+
+def test_calls_on_a_given_stream_allocate_for_it(monkeypatch):
+    rng = np.random.default_rng(4)
+    nkv, hd, B, K = 2, 64, 3, 6
+    kc, ks = _pool(rng, 30, nkv, hd)
+    vc, vs = _pool(rng, 30, nkv, hd)
+    q = torch.as_tensor(rng.standard_normal((B, K, 16, hd))).to(torch.bfloat16).cuda()
+    kv = torch.as_tensor(rng.standard_normal((B, K, nkv, hd))).to(torch.bfloat16).cuda()
+    w = torch.as_tensor(rng.integers(0, 256, (80, 128), dtype=np.uint8)).cuda()
+    s = torch.ones(80, 4, device="cuda")
+    x = torch.ones(2, 256, dtype=torch.bfloat16, device="cuda")
+
+    def run(stream):
+        cache = [torch.as_tensor(a).cuda() for a in (kc, vc, ks, vs)]
+        table, free, left = _i(np.full((B, 8), -1)), _i(np.arange(30)), _i([30])
+        lens, new, counts = _i([0, 0, 0]), _i([100, 3, 60]), _i([0, 0, 0])
+        S = _i([94, 0, 54])
+        torch.cuda.synchronize()
+        seen = []
+        with monkeypatch.context() as m:
+            real = torch.empty
+            m.setattr(torch, "empty", lambda *a, **k: seen.append(torch.cuda.current_stream()) or real(*a, **k))
+            o = binding.assign_pages(lens, new, counts, table, free, left, 30, 100, stream=stream)
+            written = binding.kv8_append(kv, kv, S, table, *cache, rows=_i([6, 3, 6]), stream=stream)
+            out, seen_ok = binding.attention_kv8(q, S, table, *cache, rows=_i([6, 3, 6]), stream=stream)
+            y = binding.linear_w4(w, s, x, 64, stream=stream)
+            back = binding.release_pages(lens, o["page_counts"], table, free, o["free_count"], 30, stream=stream)
+        torch.cuda.synchronize()
+        return [o["slot_mapping"], o["status"], written, out, seen_ok, y, back, free, table, *cache], seen
+
+    side = torch.cuda.Stream()
+    want, _ = run(None)
+    got, seen = run(side)
+    assert len(seen) >= 10 and all(t == side for t in seen)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
