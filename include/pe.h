@@ -50,7 +50,7 @@ extern "C" {
 #define PE_REQ_CAPACITY    1    /* entries needed exceed max_pages * page_size */
 #define PE_REQ_BAD_PAGE    2    /* a needed page-table entry is outside [0, num_pages) */
 #define PE_REQ_BAD_INPUT   3    /* token id outside [0, V), negative length */
-#define PE_REQ_TIMEOUT     4    /* pe_attention_kv8: a device-side wait gave up; the request's output is zero */
+#define PE_REQ_TIMEOUT     4    /* pe_attention_kv8: a device-side wait gave up; all outputs of the call are zero */
 
 /* bits of the device error word (pe_device_errors) */
 #define PE_DEVERR_GEMM_TIMEOUT  1u
@@ -346,7 +346,8 @@ int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const voi
  *          (0..255), or NULL: every zero point is 8
  *  x       [N, Kd] bf16, rows ld_x elements apart; y [N, M] fp32 OUT, rows ld_y apart
  * group is 32, 64 or 128 (the last group of a row may be short); Kd a
- * multiple of 32; w and x 16-byte aligned, ld_x a multiple of 8. Products and
+ * multiple of 32; w and x 16-byte aligned, w_scale and y to their elements,
+ * ld_x a multiple of 8. Products and
  * sums in fp32; the weights are not rounded. A row of x that holds an infinity
  * or NaN gives infinities or NaN in its row of y, and in no other. No scratch; the
  * device that holds the tensors must be current. Rows of x go 8 or 16 at a time,

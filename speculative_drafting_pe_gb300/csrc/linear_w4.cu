@@ -459,6 +459,11 @@ extern "C" int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, con
         set_error("w and x must be 16-byte aligned");
         return PE_ERR_ARG;
     }
+    const uintptr_t size = scale_dtype == PE_DTYPE_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(w_scale) % size != 0 || (reinterpret_cast<uintptr_t>(y) & 3u) != 0) {
+        set_error("w_scale and y must be aligned to their elements");
+        return PE_ERR_ARG;
+    }
     if (M > 0x7FFFFFFF - 256 || N > 8 * 65535) { set_error("M or N too large"); return PE_ERR_ARG; }
     int dev = 0, sms = 0;
     const int rc = current_device(&dev, &sms);

@@ -29,6 +29,12 @@ def test_linear_w4_refusals(lib):
     assert call(group=16) == -2 and call(group=0) == -2
 
 
+def test_linear_w4_refuses_scales_and_outputs_off_their_type(lib):
+    v = ctypes.c_void_p
+    for kind, s, y in ((0, 65, 64), (0, 66, 66), (1, 66, 64), (1, 68, 65)):
+        assert lib.pe_linear_w4(16, 1, 64, 32, P, kind, v(s), None, P, 64, v(y), 16, None) == -1, (kind, s, y)
+
+
 def test_assign_and_release_refusals(lib):
     def assign(B=1, s=P, n=P, c=P, co=ODD, t=P, mp=1, pages=1, f=P, cap=1, fc=P, fo=ODD, n_max=1, sl=P, st=P):
         return lib.pe_assign_pages(B, s, n, c, co, t, mp, pages, f, cap, fc, fo, n_max, sl, st, None)
