@@ -127,10 +127,9 @@ __global__ void __launch_bounds__(kAssignThreads)
 constexpr int kReleaseThreads = 1024;
 
 __global__ void __launch_bounds__(kReleaseThreads)
-    k_release_pages(int B, const int32_t* __restrict__ keep_lens, const int32_t* __restrict__ counts,
-                    int32_t* __restrict__ counts_out, int32_t* page_table, int max_pages, int32_t* free_pages,
-                    int free_cap, const int32_t* __restrict__ free_count, int32_t* __restrict__ free_count_out,
-                    int num_pages, int32_t* __restrict__ status) {
+    k_release_pages(int B, const int32_t* keep_lens, const int32_t* counts, int32_t* counts_out, int32_t* page_table,
+                    int max_pages, int32_t* free_pages, int free_cap, const int32_t* free_count,
+                    int32_t* free_count_out, int num_pages, int32_t* status) {   // counts and free_count in place as well
     __shared__ long long s_sum[kReleaseThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int F = min(max(free_count[0], 0), free_cap);
