@@ -275,3 +275,45 @@ def test_calls_on_a_given_stream_allocate_for_it(monkeypatch):
     assert len(seen) >= 10 and all(t == side for t in seen)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("K,nq", [(1, 4), (6, 4)])
+def test_cache_past_four_gigabytes(K, nq):
+    # the same rows written and read through pages at the end of a cache of 4.7 GB a half, and through low ones
+    nkv, hd, pages = 1, 128, 2_300_000
+    rng = np.random.default_rng(K)
+    S, n = np.array([37, 5]), 90
+    k, v = (torch.as_tensor(rng.standard_normal((2, n, nkv, hd))).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.as_tensor(rng.standard_normal((2, K, nq, hd))).to(torch.bfloat16).cuda()
+    low = rng.permutation(20)[:16].reshape(2, 8).astype(np.int32)
+    results = []
+    for count, table in ((20, low), (pages, pages - 1 - low)):
+        cache = [torch.empty((count, nkv, PAGE, hd), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        cache += [torch.empty((count, nkv), device="cuda") for _ in range(2)]
+        zero = _i([0, 0])
+        assert (binding.kv8_append(k, v, zero, _i(table), *cache) == 0).all()
+        out, status = binding.attention_kv8(q, _i(S), _i(table), *cache)
+        assert (status == 0).all()
+        at = torch.as_tensor(table.ravel().astype(np.int64)).cuda()
+        results.append([out] + [c[at].view(2, 8, -1)[:, :5].clone() for c in cache])
+        del cache
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_attention_of_thousands_of_requests():
+    rng = np.random.default_rng(6)
+    B, K, nq, nkv, hd = 2500, 2, 2, 1, 64
+    kc, ks = _pool(rng, 40, nkv, hd)
+    vc, vs = _pool(rng, 40, nkv, hd)
+    S, rows = rng.integers(0, 40, B).astype(np.int32), rng.integers(0, K + 1, B).astype(np.int32)
+    S[rng.random(B) < 0.05] = -1
+    table = rng.integers(0, 40, (B, 3)).astype(np.int32)
+    q = torch.as_tensor(rng.standard_normal((B, K, nq, hd))).to(torch.bfloat16)
+    dev = [torch.as_tensor(a).cuda() for a in (kc, vc, ks, vs)]
+    got, status = binding.attention_kv8(q.cuda(), _i(S), _i(table), *dev, rows=_i(rows))
+    torch.cuda.synchronize()
+    ref, want, size = lowbit.attention_kv8(q.double().numpy(), S, rows, table, kc, vc, ks, vs, hd ** -0.5)
+    np.testing.assert_array_equal(status.cpu().numpy(), want)
+    top = np.abs(lowbit.e4m3_decode(vc) * vs.astype(np.float64)[:, :, None, None]).max()
+    _check_attention(_cpu(got), ref, size, top, 42)
