@@ -86,7 +86,7 @@ struct Smem {
         return HD == 128 ? t : (t & 1) | ((t >> 1) << 2);
     }
 };
-static_assert(Smem<128, 2>::kBytes <= 232448 - 128, "shared memory of a block");
+static_assert(Smem<128, 2>::kBytes <= 232448 - 2048, "shared memory of a block");
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     pdl_launch_dependents();
     int idle;
-    const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, s_info, s_tile, reinterpret_cast<int2*>(sm), idle);   // the list in the ring's place
+    const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, s_info, s_tile, idle);
 
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kTile + lane * kCols;

@@ -143,111 +143,110 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 // MAX, which is what the tables hold (the planner's grid sees to that).
 // Behind each run of units lie PAD positions without work: what the end of a
 // segment costs, so that the shares' times are even, not their units alone.
-// `list` is scratch for two ints per position of the share. The requests of
-// the share are listed first and then all threads look their pages up, so the
-// dependent loads of all pages are in flight together.
+// The requests of the share are listed first, from one scan over the batch, and
+// then all threads look their pages up: two dependent loads (lengths, pages)
+// and three barriers (B=1 K=7 13.6 us; with a scan for the total, one for the
+// list and the lengths read again 14.5).
 template <int NT, int PPU, int PAD, int MAX>
-__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int2* list, int& idle) {
-    constexpr int kWarps = NT / 32;
-    __shared__ int s_scan[2][kWarps];
+__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int& idle) {
+    constexpr int kWarps = NT / 32, kList = 64;
+    static_assert(kWarps <= 32 && MAX / (1 + PAD) + 2 <= kList, "requests of a share");
+    __shared__ int s_span[kWarps], s_some[kWarps];
+    __shared__ int4 s_list[kList];   // request, its first position, units of a head, pages; at its rank among the requests with units
+    __shared__ int s_edge[2];        // ranks of the share's first and last request
+    constexpr unsigned kAll = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Req mine0 = tid < p.B ? request_of<PPU, PAD>(p, tid) : Req{};   // most batches fit the CTA's threads
-    int total = mine0.span;
-    for (int b = tid + NT; b < p.B; b += NT) total += request_of<PPU, PAD>(p, b).span;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_scan[0][warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += s_scan[0][i];
+    int total = 0;
+    if (p.B > NT) {
+        for (int b = tid + NT; b < p.B; b += NT) total += request_of<PPU, PAD>(p, b).span;
+        total = __reduce_add_sync(kAll, total);
+        if (lane == 0) s_span[warp] = total;
+        __syncthreads();
+        total = __reduce_add_sync(kAll, lane < kWarps ? s_span[lane] : 0);
+        __syncthreads();
+    }
     const int grid = static_cast<int>(gridDim.x);
-    // a share per SM, whatever the page table has room for; more only where
-    // the tables of a share would not hold it
-    const int rounds = max(1, (total + p.sms * MAX - 1) / (p.sms * MAX)), shares = min(grid, rounds * p.sms);
-    const int per = max(least, (total + shares - 1) / shares);
+    int shares = 0, per = 0, lo = 0, hi = 0, base = 0, ranks = 0, rest = 0;
     idle = 0;
-    if (static_cast<int>(blockIdx.x) >= shares) return 0;
-    const long long at = static_cast<long long>(blockIdx.x) * per;
-    const int lo = static_cast<int>(min(at, static_cast<long long>(total)));
-    const int hi = static_cast<int>(min(static_cast<long long>(total), at + per));
-    // the requests that the share touches, in order: {request, its first position}
-    int base = 0, listed = 0, rest = 0;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
         const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, PAD>(p, b) : Req{});
-        rest |= b < p.B && r.rows < p.K && b % shares == static_cast<int>(blockIdx.x);
         int incl = r.span;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            const int v = __shfl_up_sync(kAll, incl, o);
             if (lane >= o) incl += v;
         }
+        const unsigned some = __ballot_sync(kAll, r.span > 0);
         if (b0 > 0) __syncthreads();   // the last round's sums have been read
-        if (lane == 31) s_scan[1][warp] = incl;
-        __syncthreads();
-        int below = base;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) below += s_scan[1][i];
-            base += s_scan[1][i];
+        if (lane == 31) {
+            s_span[warp] = incl;
+            s_some[warp] = __popc(some);
         }
-        const int u0 = below + incl - r.span;
-        const bool mine = r.span > 0 && u0 < hi && u0 + r.span > lo;
-        const unsigned vote = __ballot_sync(0xffffffffu, mine);
         __syncthreads();
-        if (lane == 0) s_scan[1][warp] = __popc(vote);
-        __syncthreads();
-        int rank = listed + __popc(vote & ((1u << lane) - 1u));
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) rank += s_scan[1][i];
-            listed += s_scan[1][i];
+        const int span = lane < kWarps ? s_span[lane] : 0, count = lane < kWarps ? s_some[lane] : 0;
+        const int spans = __reduce_add_sync(kAll, span);
+        if (b0 == 0) {
+            total += spans;
+            // a share per SM, whatever the page table has room for; more only
+            // where the tables of a share would not hold it
+            const int rounds = max(1, (total + p.sms * MAX - 1) / (p.sms * MAX));
+            shares = min(grid, rounds * p.sms);
+            per = max(least, (total + shares - 1) / shares);
+            if (static_cast<int>(blockIdx.x) >= shares) return 0;
+            const long long at = static_cast<long long>(blockIdx.x) * per;
+            lo = static_cast<int>(min(at, static_cast<long long>(total)));
+            hi = static_cast<int>(min(static_cast<long long>(total), at + per));
         }
-        if (mine) list[rank] = make_int2(b, u0);
+        rest |= b < p.B && r.rows < p.K && b % shares == static_cast<int>(blockIdx.x);
+        const int u0 = base + __reduce_add_sync(kAll, lane < warp ? span : 0) + incl - r.span;
+        const int rank = ranks + __reduce_add_sync(kAll, lane < warp ? count : 0) + __popc(some & ((1u << lane) - 1u));
+        if (r.span > 0 && u0 < hi && u0 + r.span > lo) {
+            s_list[rank % kList] = make_int4(b, u0, r.run, r.pages);
+            if (u0 <= lo) s_edge[0] = rank;
+            if (u0 + r.span >= hi) s_edge[1] = rank;
+        }
+        base += spans;
+        ranks += __reduce_add_sync(kAll, count);
     }
     idle = __syncthreads_or(rest) != 0 ? shares : 0;
-    // Units of the listed requests ahead of position u (in listed request j,
-    // of units r.run a head): the positions less the padding of the runs ahead.
-    auto units_to = [&](int j, int run, int u) {
-        const int off = u - list[j].y, head = off / (run + PAD), in = off - head * (run + PAD);
-        return list[j].y - list[0].y - PAD * p.nkv * j + head * run + min(in, run);
+    if (tid == 0 && blockIdx.x == 0) p.cut[grid] = make_int4(per, shares, 0, 0);
+    if (lo >= hi) {
+        if (tid == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return 0;
+    }
+    const int rank0 = s_edge[0], listed = s_edge[1] - rank0 + 1;
+    const int4 front = s_list[rank0 % kList], back = s_list[(rank0 + listed - 1) % kList];
+    // Units of the listed requests ahead of position `in` of head `head` of
+    // listed request j: the positions less the padding of the runs ahead.
+    auto units_to = [&](int j, const int4& of, int head, int in) {
+        return of.y - front.y - PAD * p.nkv * j + head * of.z + min(in, of.z);
     };
-    int n = 0, skip = 0;
-    if (listed > 0) {
-        skip = units_to(0, request_of<PPU, PAD>(p, list[0].x).run, lo);
-        n = units_to(listed - 1, request_of<PPU, PAD>(p, list[listed - 1].x).run, hi) - skip;
-    }
-    if (tid == 0) {
-        int4 cut = make_int4(0, 0, 0, 0);
-        if (listed > 0) {
-            const int run = request_of<PPU, PAD>(p, list[0].x).run, off = lo - list[0].y;
-            const int head = off / (run + PAD), in = off - head * (run + PAD);
-            if (in < run) cut = make_int4(list[0].x, head, in, run);
-        }
-        p.cut[blockIdx.x] = cut;
-        if (blockIdx.x == 0) p.cut[grid] = make_int4(per, shares, 0, 0);
-    }
+    const int head0 = (lo - front.y) / (front.z + PAD), in0 = lo - front.y - head0 * (front.z + PAD);
+    const int head1 = (hi - back.y) / (back.z + PAD), in1 = hi - back.y - head1 * (back.z + PAD);
+    const int skip = units_to(0, front, head0, in0), n = units_to(listed - 1, back, head1, in1) - skip;
+    if (tid == NT - 1)
+        p.cut[blockIdx.x] = in0 < front.z ? make_int4(front.x, head0, in0, front.z) : make_int4(0, 0, 0, 0);
     for (int x = tid; x < (hi - lo) * PPU; x += NT) {
         const int u = lo + x / PPU;
         int j = 0;   // the last listed request that begins at or before u
         for (int step = listed; step > 1;) {
             step = (step + 1) / 2;
-            if (j + step < listed && list[j + step].y <= u) j += step;
+            if (j + step < listed && s_list[(rank0 + j + step) % kList].y <= u) j += step;
         }
-        while (j + 1 < listed && list[j + 1].y <= u) ++j;
-        const int b = list[j].x, off = u - list[j].y;
-        const Req r = request_of<PPU, PAD>(p, b);
-        const int head = off / (r.run + PAD), in = off - head * (r.run + PAD);
-        if (in >= r.run) continue;
-        const int i = units_to(j, r.run, u) - skip, q = x % PPU, page = in * PPU + q;
+        while (j + 1 < listed && s_list[(rank0 + j + 1) % kList].y <= u) ++j;
+        const int4 of = s_list[(rank0 + j) % kList];
+        const int head = (u - of.y) / (of.z + PAD), in = u - of.y - head * (of.z + PAD);
+        if (in >= of.z) continue;
+        const int i = units_to(j, of, head, in) - skip, q = x % PPU, page = in * PPU + q;
         int id = -2;
-        if (page < r.pages) {
-            id = p.page_table[static_cast<size_t>(b) * p.max_pages + page];
+        if (page < of.w) {
+            id = p.page_table[static_cast<size_t>(of.x) * p.max_pages + page];
             id = id >= 0 && id < p.num_pages ? id * p.nkv + head : -1;
         }
         tile[i * PPU + q] = id;
-        if (q == 0 && (i == 0 || in == 0)) info[i] = make_int4(b, head, in, r.run);
+        if (q == 0 && (i == 0 || in == 0)) info[i] = make_int4(of.x, head, in, of.z);
     }
     __syncthreads();
     return n;

@@ -185,7 +185,7 @@ struct Layout {
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
-static_assert(Layout<128>::kBytes <= 232448 - 128 && Layout<64>::kBytes <= 232448 - 128, "shared memory of a block");
+static_assert(Layout<128>::kBytes <= 232448 - 2048 && Layout<64>::kBytes <= 232448 - 2048, "shared memory of a block");
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const Kv8Params p) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     int idle;
     const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(
-        p, kUmmaLeast, s_info, s_tile, reinterpret_cast<int2*>(sm + L::kVRing), idle);
+        p, kUmmaLeast, s_info, s_tile, idle);
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + kTurns * kTile;   // S_t in columns 64 (t mod kTurns) ..; group x's output x * HD behind them
