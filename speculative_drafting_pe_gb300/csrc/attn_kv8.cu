@@ -8,7 +8,7 @@
 // one pass with a running maximum (base 2). The page scales never touch the
 // codes: ks multiplies the page's scores, vs its weights, both in fp32.
 //
-// This file: the kernel for up to 16 query rows of a head (single tokens),
+// This file: the kernel for few query rows of a head (single tokens),
 // whose unit is one page, the merge and the entry point; the line of units
 // that both kernels divide is described in attn_kv8.cuh.
 //
@@ -30,10 +30,10 @@
 //
 // Bound by the cache's bytes while it streams (a CTA's twelve warps take 1900
 // cycles for twelve pages of K and V, 48 KB, the rate of the measured copy);
-// around that stand the launch and the look-up of the share (about 5 us), a
-// join of the warps per segment (2 us) and the merge. 64 requests of 512 to
-// 8192 entries, one row of 8 heads to each of 4 of 128: 66 us, 4.3 TB/s, 65%
-// of the measured copy; one of 131072 entries 38 us, 53%.
+// around that stand the launch and the look-up of the share (about 4 us), a
+// join of the warps per segment (1.7 us) and the merge. 64 requests of 512 to
+// 8192 entries, one row of 8 heads to each of 4 of 128: 65 us, 4.4 TB/s, 66%
+// of the measured copy; one of 131072 entries 36.7 us, 55%.
 #include <algorithm>
 
 #include "attn_kv8.cuh"
@@ -86,7 +86,7 @@ struct Smem {
         return HD == 128 ? t : (t & 1) | ((t >> 1) << 2);
     }
 };
-static_assert(Smem<128, 2>::kBytes <= 232448 - 2048, "shared memory of a block");
+static_assert(Smem<128, 1>::kBytes <= 232448 - 2048 && Smem<64, 2>::kBytes <= 232448 - 2048, "shared memory of a block");
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each a run of its parts, and their sums meet in shared memory.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeBatch = 8;
-constexpr int kMergeBlocks = 16;   // blocks for an SM at most
+constexpr int kMergeBlocks = 16;   // blocks for an SM at most (6 to 40 measure alike)
 
 struct Joined {
     float M = -INFINITY, bad = 0.f, total = 0.f;
@@ -590,10 +590,11 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, 
     }
 }
 
-// Query rows of a head from which the tensor-memory kernel is taken: up to 16
-// rows one tile of the register kernel covers them; above, it would read the
-// cache once per 16 rows.
-constexpr int kUmmaFrom = 17;
+// Query rows of a head from which the tensor-memory kernel is taken; it reads
+// the cache once for up to 128 rows, but its unit takes as long for few. 64
+// requests: 16 rows of 128-wide heads 87 us, by the register kernel 90, 8 rows
+// 86 and 65; 16 rows of 64-wide heads 82 and 60.
+constexpr int umma_from(int hd) { return hd == 64 ? 17 : 9; }
 
 int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     int dev = 0, sms = 0;
@@ -602,7 +603,7 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     Plan a{};
     a.dev = dev;
     const int rows = K * (nq / nkv);
-    const bool umma = rows >= kUmmaFrom;
+    const bool umma = rows >= umma_from(hd);
     a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
     a.sms = sms;
     const int pages = umma ? kUmmaPages : 1, pad = umma ? kUmmaPad : kPad;
@@ -657,7 +658,9 @@ int check_shape(int B, int K, int nq, int nkv, int hd, int max_pages) {
 namespace kv8 {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
     const int rows = p.K * (p.nq / p.nkv);
-    const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;   // four warps to a row
+    // four warps to a row where rows are few (B=1 K=1, 131072 entries: 36.6 us,
+    // one warp 40.9; B=128 K=11: 195 us, one warp 177)
+    const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;
     const int block_rows = std::max(1, kMergeThreads / (hd / 4) / (share ? 4 : 1));
     const long long runs = std::min<long long>(a.grid - 1, static_cast<long long>(p.B) * p.nkv);   // cut ones at most
     const long long blocks = runs * ((rows + block_rows - 1) / block_rows);
@@ -739,8 +742,8 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.part = ws + a.cut_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.tr == kUmmaRows) rc = launch_umma(p, a, head_dim, s);
-    else if (a.tr == 8) rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
-    else rc = head_dim == 128 ? launch_rows<128, 2>(p, a, s) : launch_rows<64, 2>(p, a, s);
+    else if (a.tr == 16) rc = launch_rows<64, 2>(p, a, s);   // 128-wide heads: umma_from
+    else rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
     // a single share covers every head whole
     return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
 }

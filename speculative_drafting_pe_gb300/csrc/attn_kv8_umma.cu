@@ -10,17 +10,17 @@
 //               asynchronous copies. A box of 16 rows takes about 150 cycles
 //               whatever its rows hold, a copy instruction always 512 bytes
 //               (128 wide: 181 us by boxes, 192 by copies; 64 wide: 85 and 80)
-//   warps 8-11  converters, kTeam warps to a unit. Each thread fetches 16-byte chunks of V, kDepth units ahead, by
-//               asynchronous copies to a place of its own, and turns them into
-//               an fp16 tile (fp16 holds every E4M3 value; 128-byte swizzle,
-//               entry-major, read as an MN-major operand), V of entries that
-//               no row sees zero. A unit of 64-wide heads to a warp each, in
-//               turn (80 us, all four warps on every unit 85); four warps to
-//               each of 128-wide ones, whose V tiles have fewer places (178 us,
-//               a warp each 261). At the start of a segment the query rows:
-//               shifted by a power of two per row so that the
-//               largest value lies in [128, 256) and split into two E4M3
-//               terms, q = hi + lo, which hold the 8 bits of a bf16 value
+//   warps 8-11  converters, kTeam warps to a unit. Each thread fetches 16-byte
+//               chunks of V, kDepth units ahead, by asynchronous copies to a
+//               place of its own, and turns them into an fp16 tile (fp16 holds
+//               every E4M3 value; 128-byte swizzle, entry-major, read as an
+//               MN-major operand), V of entries that no row sees zero. A unit
+//               of 64-wide heads to a warp each, in turn (80 us, all four warps
+//               on every unit 85); four warps to each of 128-wide ones, whose V
+//               tiles have fewer places (178 us, a warp each 261). At the start
+//               of a segment the query rows: shifted by a power of two per row
+//               so that the largest value lies in [128, 256) and split into two
+//               E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16 value
 //               exactly down to 1/1024 of the row's largest and to 2^-18 of
 //               that below.
 //   warp 12     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
@@ -51,8 +51,8 @@
 // then, 128-wide ones 250 for 190), a third softmax group for 64-wide heads
 // (100 for 87) and scores of two units in one product (242 for 235) did not
 // help. 128 requests of 512 to 8192 entries, 11 rows of 8 heads to each of 4
-// of 128: 178 us, 3.3 TB/s, 50% of the measured copy; 64 of 1024 to 4096, up
-// to 10 rows of 8 heads to each of 8 of 64: 80 us, 30%.
+// of 128: 177 us, 3.4 TB/s, 50% of the measured copy; 64 of 1024 to 4096, up
+// to 10 rows of 8 heads to each of 8 of 64: 79 us, 30%.
 #include "attn_kv8.cuh"
 
 namespace pe {
