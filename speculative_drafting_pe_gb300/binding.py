@@ -581,6 +581,11 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _like(t, stream):
+    """The same for a contiguous tensor's type and shape (a little quicker)."""
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _run(fn, dev, stream, *args):
     """Call an entry point with `dev` current, on `stream` or the device's current stream."""
     index = dev.index
@@ -604,6 +609,8 @@ def _row_stride(t, name):
     if t.is_contiguous():
         return sizes[-1] * sizes[-2] if inner == 2 else sizes[-1]
     strides = t.stride()
+    if len(sizes) == 4 and strides[3] == 1 and strides[2] == sizes[3] and strides[0] == strides[1] * sizes[1]:
+        return strides[1]      # columns of wider rows
     lead, dense = len(sizes) - inner, 1
     for d in range(len(sizes) - 1, lead - 1, -1):
         if sizes[d] != 1 and strides[d] != dense:
@@ -670,7 +677,8 @@ def assign_pages(seq_lens, new_lens, page_counts, page_table, free_pages, free_c
     cap = free_pages.shape[0]
     _need_is("free_pages", free_pages, _INT, dev, (cap,))
     _need_is("free_count", free_count, _INT, dev, (1,))
-    slots, counts, left, status = (_empty(s, _INT, dev, stream) for s in ((B, n_max), shape, (1,), shape))
+    slots, left = _empty((B, n_max), _INT, dev, stream), _like(free_count, stream)
+    counts, status = _like(seq_lens, stream), _like(seq_lens, stream)
     _run(lib.pe_assign_pages, dev, stream, B, seq_lens.data_ptr(), new_lens.data_ptr(), page_counts.data_ptr(),
          counts.data_ptr(), page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap,
          free_count.data_ptr(), left.data_ptr(), n_max, slots.data_ptr(), status.data_ptr())
@@ -692,7 +700,7 @@ def release_pages(keep_lens, page_counts, page_table, free_pages, free_count, nu
     cap = free_pages.shape[0]
     _need_is("free_pages", free_pages, _INT, dev, (cap,))
     _need_is("free_count", free_count, _INT, dev, (1,))
-    status = _empty(shape, _INT, dev, stream)
+    status = _like(keep_lens, stream)
     _run(lib.pe_release_pages, dev, stream, B, keep_lens.data_ptr(), page_counts.data_ptr(), page_counts.data_ptr(),
          page_table.data_ptr(), max_pages, num_pages, free_pages.data_ptr(), cap, free_count.data_ptr(),
          free_count.data_ptr(), status.data_ptr())
@@ -727,7 +735,7 @@ def kv8_append(k, v, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, r
         raise ValueError(f"k and v must be bfloat16 [B, n, nkv, hd] on {dev}")
     pages = _check_kv8(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_scale, v_scale)
     if status is None:
-        status = _empty((B,), _INT, dev, stream)
+        status = _like(seq_lens, stream)
     else:
         _need_is("status", status, _INT, dev, (B,))
     _run(lib.pe_kv8_append, dev, stream, B, n, nkv, hd, k.data_ptr(), _row_stride(k, "k"), v.data_ptr(),
@@ -765,7 +773,7 @@ def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, s
     elif out.dtype is not _BF16 or out.device != dev or out.shape != q.shape:
         raise ValueError(f"out must be bfloat16 {tuple(q.shape)} on {dev}")
     if status is None:
-        status = _empty((B,), _INT, dev, stream)
+        status = _like(seq_lens, stream)
     else:
         _need_is("status", status, _INT, dev, (B,))
     if dev.type != "cuda":
