@@ -13,10 +13,11 @@
 // One warp owns one (request, page, head, K or V): it reads the page's new
 // rows once (8 bytes a lane), keeps them in registers, takes the maximum by
 // shuffles and stores the codes (4 bytes a lane), so no two warps write one
-// page and nothing is read twice. Bound by latency: a warp's loads (length,
-// page, rows, committed codes and scale) depend on one another. 8 rows of 32
-// requests, 4 heads of 128, take 5.0 us; 8 prompts of up to 2048 rows, 8 heads
-// of 64, 7.4 us, 0.94 TB/s.
+// page and nothing is read twice. Bound by latency: lengths, then page and
+// rows together, then committed codes and scale. 8 rows of 32 requests, 4 heads
+// of 128, take 3.4 us (with the rows behind the pages 5.0); 8 prompts of up to
+// 2048 rows, 8 heads of 64, 5.7 us, 1.2 TB/s (7.6 where warps without a page
+// look the request's others up as well).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -93,14 +94,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const AppendParams p
     else if (n > 0) {
         p0 = S / kPage;
         p1 = (S + n + kPage - 1) / kPage;
-        int bad = 0;
-        for (int i = p0 + lane; i < p1; i += 32) bad |= row[i] < 0 || row[i] >= p.num_pages;
-        if (__any_sync(0xffffffffu, bad)) st = PE_REQ_BAD_PAGE;
     }
-    if (pi == 0 && head == 0 && kv == 0 && lane == 0) p.status[b] = st;
-    if (st != PE_REQ_OK || p0 + pi >= p1) return;
-
-    const int page = row[p0 + pi];
+    const bool mine = p0 + pi < p1, tells = pi == 0 && head == 0 && kv == 0;
+    if (!mine && !tells) return;
+    // the new rows are on their way while the pages are looked up
     const int first = (p0 + pi) * kPage - S;      // the new row at the page's entry 0 (negative: committed)
     const int sub = lane / kLanes, d = (lane % kLanes) * 4;
     const long long ld = kv == 0 ? p.ld[0] : p.ld[1];
@@ -110,8 +107,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const AppendParams p
     for (int i = 0; i < kSteps; ++i) {
         const int r = first + i * kPer + sub;
         v[i] = make_uint2(0u, 0u);
-        if (r >= 0 && r < n) v[i] = *reinterpret_cast<const uint2*>(x + r * ld);
+        if (mine && r >= 0 && r < n) v[i] = *reinterpret_cast<const uint2*>(x + r * ld);
     }
+    const int page = mine ? row[p0 + pi] : -1;
+    int bad = 0;
+    for (int i = p0 + lane; i < p1; i += 32) bad |= row[i] < 0 || row[i] >= p.num_pages;
+    if (__any_sync(0xffffffffu, bad)) st = PE_REQ_BAD_PAGE;
+    if (tells && lane == 0) p.status[b] = st;
+    if (st != PE_REQ_OK || !mine) return;
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
