@@ -25,8 +25,8 @@
 // whole 16-byte chunks; pairs of V rows are interleaved by byte permutes; P^T
 // comes out of S^T's layout by two 8x8 transposes. Queries enter as fp16 after
 // an exact shift by a power of two per row, scores and sums are fp32, weights
-// go to fp16 (2^-11) relative to the row's running maximum and the largest V
-// scale seen.
+// times V's scale go to fp16 (2^-11) relative to the row's largest such product
+// so far (kLift).
 //
 // Bound by the cache's bytes while it streams (a CTA's twelve warps take 1900
 // cycles for twelve pages of K and V, 48 KB, the rate of the measured copy);
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kMt; ++j)
 #pragma unroll
             for (int a = 0; a < NT; ++a) o[j][a][0] = o[j][a][1] = o[j][a][2] = o[j][a][3] = 0.f;
-        float m[NT][2], l[NT][2], vref = 0.f, vinv = 0.f;
+        float m[NT][2], l[NT][2], mo[NT][2];
 #pragma unroll
-        for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
+        for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = mo[a][0] = mo[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
 
         if (i < seg + len) {
             // queries: row a * 8 + g, this lane's quarter of the dimensions
@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (e0 + g + 4 * (x & 2) > lim[a][x & 1]) s[a][x] = -INFINITY;
                         }
                 }
-                float top[NT][2];
+                float top[NT][2], vpart, vlg;
+                split_scale(vs, vpart, vlg);
                 bool up = false;
 #pragma unroll
                 for (int a = 0; a < NT; ++a)
@@ -285,28 +286,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 4));
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 8));
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 16));
-                        up |= top[a][x] > m[a][x] + kRescale;
+                        up |= top[a][x] > m[a][x] + kRescale || top[a][x] + vlg > mo[a][x] + kRescale;
                     }
-                const float av = fabsf(vs);
-                const bool grow = av > 16.f * vref;
-                if (__any_sync(0xffffffffu, up) || grow) {
-                    float fv = 1.f;
-                    if (grow) {
-                        fv = vref / av;
-                        vref = av;
-                        vinv = 1.f / av;
-                    }
+                if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            float f = 1.f;
                             if (top[a][x] > m[a][x] + kRescale) {
-                                f = m[a][x] == -INFINITY ? 0.f : ex2(m[a][x] - top[a][x]);
+                                l[a][x] *= m[a][x] == -INFINITY ? 0.f : ex2(m[a][x] - top[a][x]);
                                 m[a][x] = top[a][x];
                             }
-                            l[a][x] *= f;
-                            f *= fv;
+                            float f = 1.f;
+                            if (top[a][x] + vlg > mo[a][x] + kRescale) {
+                                f = mo[a][x] == -INFINITY ? 0.f : ex2(mo[a][x] - (top[a][x] + vlg));
+                                mo[a][x] = top[a][x] + vlg;
+                            }
 #pragma unroll
                             for (int j = 0; j < kMt; ++j) {
                                 o[j][a][x] *= f;
@@ -314,17 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                 }
-                const float vr = vs * vinv;
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
+                    // 0 in the place of both maxima where a row has seen no entry
                     const float m0 = m[a][0] == -INFINITY ? 0.f : m[a][0], m1 = m[a][1] == -INFINITY ? 0.f : m[a][1];
+                    const float o0 = mo[a][0] == -INFINITY ? 0.f : mo[a][0], o1 = mo[a][1] == -INFINITY ? 0.f : mo[a][1];
+                    const float r0 = vpart * lift(m0 - o0 + kLift, vlg), r1 = vpart * lift(m1 - o1 + kLift, vlg);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float w0 = ex2(s[a][2 * h] - m0), w1 = ex2(s[a][2 * h + 1] - m1);
                         l[a][0] += w0;
                         l[a][1] += w1;
-                        pb[a][h] = transpose8x8(pack_f16(w0 * vr, w1 * vr));
+                        pb[a][h] = transpose8x8(pack_f16(w0 * r0, w1 * r1));
                     }
                 }
 #pragma unroll
@@ -363,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
-                const float f = m[a][x] == -INFINITY ? vref : vref * ex2(m[a][x] - M);
+                const float f = unlift(mo[a][x], M);
 #pragma unroll
                 for (int j = 0; j < kMt; ++j) {
                     o[j][a][x] *= f;

@@ -21,6 +21,15 @@ namespace kv8 {
 
 constexpr int kPage = 16;
 constexpr float kRescale = 8.f;    // running maximum (log2) moves only by more than this
+// Weights meet V as fp16. What a row sums up is w * scale of v, and the scales
+// of V's pages may lie far apart, so next to the scores' running maximum m a
+// row has one of its contributions, mo, the maximum of score + log2(scale) over
+// the pages, and the fp16 weights are w * scale * 2^(m - mo + kLift): the
+// largest one stands between 2^kLift and 2^(kLift + kRescale + 2), and what
+// falls below fp16's normal range, 2^-14, is 2^-19 of it at most. (Taken
+// relative to the largest scale alone, a page of values below 2^-14 of the
+// largest lost its bits even where it had all the weight.)
+constexpr float kLift = 5.f;
 // mark in the place of a row's sum: the request's outputs are zero
 constexpr float kMarkBadPage = -1.f;
 
@@ -72,6 +81,18 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// v = part * 2^lg exactly, |part| in [1, 2) for scales of 2^-104 to 2^127 (a
+// smaller one is a smaller part, so that 2^-lg and what is summed stay normal)
+__device__ __forceinline__ void split_scale(float v, float& part, float& lg) {
+    const uint32_t e = min(max((__float_as_uint(v) >> 23) & 0xFFu, 23u), 253u);
+    part = v * __uint_as_float((254u - e) << 23);
+    lg = static_cast<float>(static_cast<int>(e) - 127);
+}
+// what scales a weight 2^(score - m) by, next to `part`; from: m - mo + kLift.
+// Never an infinity, which would meet weights of 0
+__device__ __forceinline__ float lift(float from, float lg) { return ex2(fminf(from + lg, 127.f)); }
+// a sum of such products back to the values that belong to M
+__device__ __forceinline__ float unlift(float mo, float M) { return mo == -INFINITY ? 0.f : ex2(mo - kLift - M); }
 __device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
     uint32_t r;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
@@ -101,10 +122,6 @@ __device__ __forceinline__ void copy_async(uint32_t smem, const void* src, uint6
         asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], %3, %2;" ::"r"(smem), "l"(src), "l"(policy), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// an arrival on `bar` once this thread's copies so far are there
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 

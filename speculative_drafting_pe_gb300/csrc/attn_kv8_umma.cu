@@ -68,6 +68,7 @@ constexpr int kWarpConv = 8, kWarpS = 12, kWarpPv = 13, kWarpK = 14;
 constexpr int kDepth = 4;                   // units whose V copies are in flight
 constexpr int kBehind = 1;                  // units whose K copies a warp has in flight while it waits for the one before
 constexpr int kScales = 16;                 // units whose page scales are kept: fetched kDepth ahead, read a few behind
+constexpr int kScaleRec = 3 * kUmmaPages;   // floats of a unit's scales
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 // true in one lane of a converged warp
@@ -177,8 +178,8 @@ struct Layout {
     static constexpr int kUnit = kInfo + kUmmaUnits * 16;
     static constexpr int kCs = kUnit + kUmmaUnits * kUmmaPages * 4;   // [kCsTurns][kRows]
     static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
-    static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages]
-    static constexpr int kNan = kScale + kScales * 32;        // [kTurns][kTile] bytes
+    static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages as its part and its lg]
+    static constexpr int kNan = kScale + kScales * kScaleRec * 4;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
     // k_full, cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
     static constexpr int kBars = 5 * kTurns + 4;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         s_abort = 0;
         for (int s = 0; s < kTurns; ++s) {
-            mbar_init(&k_full[s], L::kTmaK ? 1 + 2 * kUmmaPages : 1);
+            mbar_init(&k_full[s], L::kTmaK ? 2 : 1);
             mbar_init(&cv_full[s], L::kTeam);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
@@ -242,13 +243,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
+    // the K and V scales of unit i's pages, a lane each: fetched, and once they are there V's taken apart
+    const uint64_t policy_s = l2_policy_evict_first();
+    auto fetch_scales = [&](int i) {
+        if (lane < 2 * kUmmaPages) {
+            float* to = s_scale + (i % kScales) * kScaleRec + lane;
+            const int tile = s_tile[i * kUmmaPages + lane % kUmmaPages];
+            if (tile >= 0) copy_async<4>(smem_u32(to), (lane < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy_s);
+            else *to = 0.f;
+        }
+    };
+    auto split_scales = [&](int i) {
+        if (lane >= kUmmaPages && lane < 2 * kUmmaPages) {
+            float* at = s_scale + (i % kScales) * kScaleRec + lane;
+            split_scale(*at, at[0], at[kUmmaPages]);
+        }
+    };
 
     if (L::kTmaK && warp == kWarpK) {
         const uint64_t policy = l2_policy_evict_first();
         for (int i = 0; i < n; ++i) {
             const int x = i % kTurns;
-            const int tile = lane < 2 * kUmmaPages ? s_tile[i * kUmmaPages + lane % kUmmaPages] : -1;
-            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) / 2 * kPage * HD);
+            const int tile = lane < kUmmaPages ? s_tile[i * kUmmaPages + lane] : -1;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) * kPage * HD);
             if (i >= kTurns) ok = wait(&s_full[x], turn(i) ^ 1u);   // S of the unit before it in this place
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -256,18 +273,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane < kUmmaPages && tile >= 0)
                 tma_load_2d(sm + L::kKRing + x * L::kCodes + lane * kPage * HD, &tmK, &k_full[x], 0, tile * kPage, policy);
-            if (lane < 2 * kUmmaPages) {   // a page's K or V scale each
-                float* to = s_scale + (i % kScales) * 8 + lane;
-                if (tile >= 0) {
-                    copy_async<4>(smem_u32(to), (lane < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
-                    copies_arrive(&k_full[x]);
-                } else {
-                    *to = 0.f;
-                    mbar_arrive(&k_full[x]);
-                }
-            }
         }
-        copies_commit();
+        __syncwarp();
+    } else if (L::kTmaK && warp == kWarpK + 1) {
+        for (int i = 0; i < n + kDepth; ++i) {
+            if (i < n) fetch_scales(i);
+            copies_commit();
+            const int u = i - kDepth, x = u % kTurns;
+            if (u < 0) continue;
+            if (u >= kTurns) ok = wait(&s_full[x], turn(u) ^ 1u);   // an arrival counts for this unit, not the one before it
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            copies_wait<kDepth>();
+            split_scales(u);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_full[x]);
+        }
         copies_wait<0>();
         __syncwarp();
     } else if (!L::kTmaK && warp >= kWarpK) {
@@ -298,16 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < kPasses; ++j)
                         copy_async<16>(to[j & 1] + x * L::kCodes + q * kPage * HD + j * 512, src + j * 512, policy);
                 }
-                if (lane < 2 * kUmmaPages) {   // a page's K or V scale each
-                    float* dst = s_scale + (i % kScales) * 8 + lane;
-                    const int tile = s_tile[i * kUmmaPages + lane % kUmmaPages];
-                    if (tile >= 0) copy_async<4>(smem_u32(dst), (lane < kUmmaPages ? p.k_scale : p.v_scale) + tile, policy);
-                    else *dst = 0.f;
-                }
+                fetch_scales(i);
             }
             copies_commit();
             if (i >= 2 * kBehind) {
                 copies_wait<kBehind>();
+                split_scales(i - 2 * kBehind);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&k_full[(i - 2 * kBehind) % kTurns]);
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j = row / G, lim = S + j;
             const int first = seg + ((seg ^ grp) & 1);  // this group's first unit of the segment
             const int count = first < seg + len ? (seg + len - first + 1) / 2 : 0;
-            float m = -INFINITY, l = 0.f, vref = 0.f, vinv = 0.f, mark = 0.f, cs = 0.f;
+            float m = -INFINITY, mo = -INFINITY, l = 0.f, mark = 0.f, cs = 0.f;
             for (int i = first; i < seg + len; i += 2) {
                 const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i % kTurns) * kTile);
                 if (ok) ok = wait(&s_full[i % kTurns], turn(i));
@@ -548,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 if (busy) {
                     if (i == first) cs = s_cs[(no & (kCsTurns - 1)) * kRows + row];
-                    const float4 ks = *reinterpret_cast<const float4*>(s_scale + (i % kScales) * 8);
-                    const float4 vs = *reinterpret_cast<const float4*>(s_scale + (i % kScales) * 8 + 4);
+                    const float4* sc = reinterpret_cast<const float4*>(s_scale + (i % kScales) * kScaleRec);
+                    const float4 ks = sc[0], vpart = sc[1], vlg = sc[2];
                     const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUmmaPages);
                     float s[kTile];
                     tmem_ld64(t_s, s);
@@ -586,26 +603,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (e0 + x > lim) s[x] = -INFINITY;
                         }
                     }
-                    float top = -INFINITY;
+                    const float vl[4] = {vlg.x, vlg.y, vlg.z, vlg.w};
+                    float top = -INFINITY, most = -INFINITY;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float* sq = s + q * 16;
                         float t4[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) t4[x] = fmaxf(fmaxf(sq[x], sq[x + 4]), fmaxf(sq[x + 8], sq[x + 12]));
-                        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q]);
+                        const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q];
+                        top = fmaxf(top, t);
+                        most = fmaxf(most, t + vl[q]);
                     }
-                    float f = 1.f;
                     if (top > m + kRescale) {
-                        f = m == -INFINITY ? 0.f : ex2(m - top);
-                        l *= f;
+                        l *= m == -INFINITY ? 0.f : ex2(m - top);
                         m = top;
                     }
-                    const float av = fmaxf(fmaxf(fabsf(vs.x), fabsf(vs.y)), fmaxf(fabsf(vs.z), fabsf(vs.w)));
-                    if (av > 16.f * vref) {
-                        f *= vref / av;
-                        vref = av;
-                        vinv = 1.f / av;
+                    float f = 1.f;
+                    if (most > mo + kRescale) {
+                        f = mo == -INFINITY ? 0.f : ex2(mo - most);
+                        mo = most;
                     }
                     if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
                         // this group's last P.V has to be done
@@ -624,7 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float mm = m == -INFINITY ? 0.f : -m;
                     const uint64_t m2 = f2(mm, mm);
-                    const float vr[4] = {vs.x * vinv, vs.y * vinv, vs.z * vinv, vs.w * vinv};
+                    // 0 in the place of both maxima where a row has seen no entry
+                    const float from = (mo == -INFINITY ? 0.f : -mo) - mm + kLift;
+                    const float vr[4] = {vpart.x * lift(from, vl[0]), vpart.y * lift(from, vl[1]),
+                                         vpart.z * lift(from, vl[2]), vpart.w * lift(from, vl[3])};
                     uint64_t sum[2] = {0ull, 0ull};
                     uint32_t pk[32];
 #pragma unroll
@@ -652,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after_sync();
             // the two groups' sums of each row; each group writes half of the dimensions
-            s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, vref, 0.f);
+            s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, mo, 0.f);
             named_bar_sync(1, kSoft);
             const float4 xa = s_ex[row], xb = s_ex[kRows + row];
             const float bad = fminf(fminf(xa.y, xb.y), 0.f);   // a NaN sum is not less than 0
@@ -661,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float sum = (xa.y <= 0.f ? 0.f : xa.y * fa) + (xb.y <= 0.f ? 0.f : xb.y * fb);
             const bool whole = len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            const float ga = fa * xa.z * inv, gb = fb * xb.z * inv;
+            const float ga = unlift(xa.z, M) * inv, gb = unlift(xb.z, M) * inv;
             __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
                                  static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
             const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;

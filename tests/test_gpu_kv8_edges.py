@@ -1,0 +1,150 @@
+"""The attention over the 8-bit cache where its roundings, its shares of the work and its rules for what is not finite
+show: every kernel behind the entry point (few and many query rows, 64- and 128-wide heads) against float64."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import lowbit
+from speculative_drafting_pe_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+PAGE = 16
+# K, query heads, kv heads, width: the kernel of few rows and the tensor-memory one, of either width
+KERNELS = [(4, 4, 2, 128), (4, 8, 2, 64), (4, 16, 2, 128), (4, 16, 2, 64)]
+NAMES = ["few rows, 128 wide", "few rows, 64 wide", "many rows, 128 wide", "many rows, 64 wide"]
+
+
+def _dev(a):
+    return torch.as_tensor(np.ascontiguousarray(a), device="cuda")
+
+
+def _bf16(a):
+    t = torch.as_tensor(np.asarray(a, dtype=np.float32)).to(torch.bfloat16)
+    return t.double().numpy(), t.cuda()
+
+
+def _cache(rng, pages, nkv, hd, top=4):
+    """Random codes of full range and power-of-two scales."""
+    x = rng.standard_normal((pages, nkv, PAGE, hd))
+    s = np.exp2(rng.integers(-2, top, (pages, nkv))).astype(np.float32) * np.float32(2.0 ** -7)
+    return lowbit.e4m3_encode(x * 2.0 ** 7), s
+
+
+def _exact(q, S, table, kc, vc, ks, vs, scale):
+    """Outputs, how far they may be off, and sum_e w_e |v_e|.
+
+    Half a step of the bf16 output, 2^-8 |o|. Every weight rounded to fp16 (2^-11) after fp32 steps and an exponential
+    (2^-13). A weight below fp16's normal range is off by 2^-25 at most where the row's largest w |scale of v| stands
+    at 2^5 or above, so by 2^-30 of that, times a code of 448, for each of L entries. Scores: sums in fp32 of eight
+    products of 32 dimensions (few rows: 16), each off by 2^-22 of what is summed in size; and the queries as they
+    enter. Few rows: an fp16 copy whose largest value lies in [1, 2), off by 2^-25 at most. Many rows: two E4M3 terms,
+    the largest value in [128, 256), together off by 2^-10 at most, where a value is below 1/4. A score off by d
+    changes a weight by a factor of exp(+-2 d) at most."""
+    B, K, nq, hd = q.shape
+    nkv = kc.shape[1]
+    many = K * nq // nkv > (8 if hd == 128 else 16)
+    out, lim, size = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    top = np.exp2(np.floor(np.log2(np.maximum(np.abs(q).max(-1, keepdims=True), 1e-300))))
+    dq = np.where(np.abs(q) < top * 2.0 ** -9, top * 2.0 ** -17, 0) if many else top * 2.0 ** -25
+    dq = dq + 2.0 ** -19 * np.abs(q)
+    for b in range(B):
+        ids = table[b, :-(-(S[b] + K) // PAGE)]
+        kk = lowbit.e4m3_decode(kc[ids]) * ks[ids].astype(np.float64)[:, :, None, None]
+        sv = vs[ids].astype(np.float64)
+        vv = lowbit.e4m3_decode(vc[ids]) * sv[:, :, None, None]
+        for g in range(nkv):
+            ke, ve, se = kk[:, g].reshape(-1, hd), vv[:, g].reshape(-1, hd), np.repeat(np.abs(sv[:, g]), PAGE)
+            ka = np.abs(ke)
+            for h in range(g * nq // nkv, (g + 1) * nq // nkv):
+                for j in range(K):
+                    n = S[b] + j + 1
+                    x = scale * (ke[:n] @ q[b, j, h])
+                    w = np.exp(x - x.max())
+                    w /= w.sum()
+                    o = w @ ve[:n]
+                    d = w * np.expm1(2 * scale * (ka[:n] @ dq[b, j, h]))
+                    out[b, j, h], size[b, j, h] = o, w @ np.abs(ve[:n])
+                    lim[b, j, h] = (2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13) * size[b, j, h] +
+                                    n * 2.0 ** -30 * 448 * (w * se[:n]).max() + d @ np.abs(ve[:n] - o))
+    return out, lim, size
+
+
+def _call(q, S, table, kc, vc, ks, vs):
+    lens, cache = _dev(np.asarray(S, np.int32)), map(_dev, (kc, vc, ks, vs))
+    got, status = binding.attention_kv8(q, lens, _dev(table), *cache)
+    torch.cuda.synchronize()
+    assert (status == 0).all()
+    return got.double().cpu().numpy()
+
+
+def _check(got, ref, lim):
+    err = np.abs(got - ref)
+    assert np.isfinite(got).all() and (err <= lim).all(), (err / np.maximum(lim, 1e-300)).max()
+
+
+def _check_copies(q, S, table, kc, vc, ks, vs, copies, ref, lim):
+    """The batch `copies` times over: a warp has several pages of a request, or one."""
+    got = _call(q.repeat(copies, 1, 1, 1), np.tile(S, copies), np.tile(table, (copies, 1)), kc, vc, ks, vs)
+    for c in range(copies):
+        _check(got[c * len(S):(c + 1) * len(S)], ref, lim)
+
+
+# ---------------------------------------------------------------- scales of V far apart
+
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+@pytest.mark.parametrize("low", [-12, -24, -60])
+def test_small_values_that_have_the_weight(K, nq, nkv, hd, low):
+    # pages of large values that hardly any weight falls on, among pages of values 2^low as large that have it: the
+    # output is theirs, to the precision of any other
+    rng = np.random.default_rng(K + hd)
+    S = [300, 75]
+    table = rng.permutation(60)[:40].reshape(2, 20).astype(np.int32)
+    kc, ks = _cache(rng, 60, nkv, hd)
+    vc, vs = _cache(rng, 60, nkv, hd)
+    loud = np.zeros(60, dtype=bool)
+    loud[table[0, [0, 3, 4, 9, 18]]] = loud[table[1, [1, 4]]] = True
+    kc = np.where(loud[:, None, None, None], kc | 0x80, kc & 0x7F)   # queries are positive
+    ks[:] = 2.0 ** -7
+    vs[~loud] *= np.float32(2.0 ** low)
+    qx, qt = _bf16(5 * (np.abs(rng.standard_normal((2, K, nq, hd))) + 0.5))
+    ref, lim, size = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
+    assert size.max() < 2.0 ** (low + 5)      # the large values have no say
+    for copies in (1, 60):
+        _check_copies(qt, S, table, kc, vc, ks, vs, copies, ref, lim)
+
+
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+def test_scales_of_every_kind(K, nq, nkv, hd):
+    # scales that are no powers of two, negative, zero, subnormal and near the ends of their range, from page to page
+    rng = np.random.default_rng(nq + hd)
+    S = [333, 100, 4]
+    table = rng.permutation(66).reshape(3, 22).astype(np.int32)
+    kc, ks = _cache(rng, 66, nkv, hd)
+    vc, vs = _cache(rng, 66, nkv, hd)
+    ks *= rng.uniform(0.2, 1.0, ks.shape).astype(np.float32) * rng.choice([-1, 1], ks.shape).astype(np.float32)
+    vs *= rng.uniform(0.2, 1.0, vs.shape).astype(np.float32) * rng.choice([-1, 1], vs.shape).astype(np.float32)
+    ks[table[0, [2, 11]]], vs[table[0, [5, 13]]], vs[table[0, 7]] = 0.0, 0.0, 2.0 ** -126
+    vs[table[1, [0, 3]]], ks[table[1, 2]] = 2.0 ** -140, 2.0 ** -130
+    vs[table[1, 5]] = 2.0 ** 100
+    vs[table[2]] = 2.0 ** -90
+    qx, qt = _bf16(2.0 * rng.standard_normal((3, K, nq, hd)))
+    ref, lim, size = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
+    for copies in (1, 60):
+        _check_copies(qt, S, table, kc, vc, ks, vs, copies, ref, lim)
+
+
+def test_pages_of_zeros_beside_others():
+    # rows of zeros are stored with the smallest scale there is; whichever has the weight, the sum is right
+    hd, nkv = 64, 1
+    rng = np.random.default_rng(3)
+    kc, ks = _cache(rng, 8, nkv, hd)
+    vc, vs = _cache(rng, 8, nkv, hd)
+    vc[[1, 4]], vs[[1, 4]] = 0, 2.0 ** -126
+    ks[[1, 4]] *= 16
+    table = np.array([[1, 0, 4, 5, 2, 3, 7, 6]], dtype=np.int32)
+    for K, nq in ((1, 4), (4, 8)):
+        qx, qt = _bf16(4.0 * rng.standard_normal((1, K, nq, hd)))
+        ref, lim, size = _exact(qx, [120], table, kc, vc, ks, vs, hd ** -0.5)
+        _check(_call(qt, [120], table, kc, vc, ks, vs), ref, lim)
