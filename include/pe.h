@@ -425,8 +425,17 @@ int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void*
  *         [0, num_pages) is PE_REQ_BAD_PAGE
  * K * (nq/nkv) <= 128, hd 64 or 128; q, out and codes 16-byte aligned, ld_q and
  * ld_out multiples of 8; B * nkv * (max_pages + 32) < 2^30.
- * Entries that no row sees may hold anything. A NaN among the entries that
- * only some rows of the pass see makes those rows NaN and no others. */
+ * Entries that no row sees may hold anything. A NaN code of K makes the rows
+ * that see its entry NaN, one of V that dimension of them (all of them where
+ * the entry stands in a page that some row does not see whole, or within three
+ * pages of one), and neither any other row. A row of q that holds an infinity
+ * or a NaN is NaN.
+ * Rounded to fewer than 32 bits, besides the output: the weights times their
+ * page's V scale, to fp16 relative to the row's largest such product (2^-11 of
+ * each; products below 2^-19 of the largest: 2^-30 of it), and the queries.
+ * Up to 8 rows for a kv head, K * (nq/nkv) (64-wide heads: 16), a value of q is
+ * off by 2^-25 of its row's largest at most and exact from 2^-17 of that on;
+ * with more rows by 2^-17 of the largest, and exact from 2^-9 of it on. */
 int pe_attention_kv8_scratch(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                              int32_t max_pages, int64_t* ws_floats);
 int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,

@@ -21,8 +21,8 @@
 //               of a segment the query rows: shifted by a power of two per row
 //               so that the largest value lies in [128, 256) and split into two
 //               E4M3 terms, q = hi + lo, which hold the 8 bits of a bf16 value
-//               exactly down to 1/1024 of the row's largest and to 2^-18 of
-//               that below.
+//               exactly from 1/4 on, 2^-9 of the row's largest, and to half of
+//               E4M3's smallest step, 2^-17 of the largest, below.
 //   warp 12     one elected lane issues S_t = Q_hi K_t^T + Q_lo K_t^T (M=128,
 //               N=64, E4M3 operands: the codes themselves)
 //   warp 13     one elected lane issues O += P_t V_t (fp16, A = P_t from

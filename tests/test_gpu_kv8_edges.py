@@ -148,3 +148,67 @@ def test_pages_of_zeros_beside_others():
         qx, qt = _bf16(4.0 * rng.standard_normal((1, K, nq, hd)))
         ref, lim, size = _exact(qx, [120], table, kc, vc, ks, vs, hd ** -0.5)
         _check(_call(qt, [120], table, kc, vc, ks, vs), ref, lim)
+
+
+# ---------------------------------------------------------------- what is not finite
+
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+@pytest.mark.parametrize("S", [45, 700])
+def test_nan_in_the_cache_stays_with_the_rows_that_see_it(K, nq, nkv, hd, S):
+    # entry S + 2 belongs to row 2; rows 0 and 1 do not see it
+    rng = np.random.default_rng(S + hd)
+    kc, ks = _cache(rng, 50, nkv, hd)
+    vc, vs = _cache(rng, 50, nkv, hd)
+    table = rng.permutation(50)[:48].reshape(1, 48).astype(np.int32)
+    G, at = nq // nkv, (table[0, (S + 2) // PAGE], nkv - 1, (S + 2) % PAGE)
+    _, qt = _bf16(rng.standard_normal((1, K, nq, hd)))
+    clean = _call(qt, [S], table, kc, vc, ks, vs)
+    assert np.isfinite(clean).all()
+    for codes in (kc, vc):
+        for nan in (0x7F, 0xFF):
+            for d in (0, 5, hd // 2 + 3, hd - 1):
+                had = codes[at + (d,)]
+                codes[at + (d,)] = nan
+                got = _call(qt, [S], table, kc, vc, ks, vs)
+                codes[at + (d,)] = had
+                np.testing.assert_array_equal(got[0, :2], clean[0, :2])
+                np.testing.assert_array_equal(got[0, :, :-G], clean[0, :, :-G])   # the other kv head
+                assert np.isnan(got[0, 2:, -G:, d]).all()
+
+
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+def test_queries_that_are_not_finite_spoil_their_row_alone(K, nq, nkv, hd):
+    rng = np.random.default_rng(hd + nq)
+    S = [200, 31]
+    kc, ks = _cache(rng, 40, nkv, hd)
+    vc, vs = _cache(rng, 40, nkv, hd)
+    table = rng.permutation(40)[:32].reshape(2, 16).astype(np.int32)
+    q = rng.standard_normal((2, K, nq, hd))
+    clean = _call(_bf16(q)[1], S, table, kc, vc, ks, vs)
+    spoilt = np.zeros((2, K, nq), dtype=bool)
+    for i, x in enumerate((np.inf, -np.inf, np.nan)):
+        b, j, h = i % 2, (2 * i + 1) % K, (3 * i + 1) % nq
+        q[b, j, h, (7 * i + hd - 3) % hd] = x
+        spoilt[b, j, h] = True
+    got = _call(_bf16(q)[1], S, table, kc, vc, ks, vs)
+    assert np.isnan(got[spoilt]).all()
+    np.testing.assert_array_equal(got[~spoilt], clean[~spoilt])
+
+
+# ---------------------------------------------------------------- queries of uneven size
+
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+def test_queries_with_one_dimension_far_above_the_others(K, nq, nkv, hd):
+    # the first dimension of a query is 2^12 times the others, and nearly nothing in the keys
+    rng = np.random.default_rng(hd + nq)
+    S = [150, 40]
+    kc, ks = _cache(rng, 40, nkv, hd)
+    vc, vs = _cache(rng, 40, nkv, hd)
+    ks[:] = 2.0 ** -7
+    kc[..., 0] &= 0x87        # no larger than 7/8 of E4M3's smallest normal value
+    table = rng.permutation(40)[:30].reshape(2, 15).astype(np.int32)
+    q = rng.standard_normal((2, K, nq, hd)) * 2.0 ** -2
+    q[..., 0] = rng.choice([-1, 1], q.shape[:3]) * rng.uniform(0.6, 1.9, q.shape[:3]) * 2.0 ** 10
+    qx, qt = _bf16(q)
+    ref, lim, size = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
+    _check(_call(qt, S, table, kc, vc, ks, vs), ref, lim)
