@@ -347,11 +347,14 @@ int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const voi
  *  x       [N, Kd] bf16, rows ld_x elements apart; y [N, M] fp32 OUT, rows ld_y apart
  * group is 32, 64 or 128 (the last group of a row may be short); Kd a
  * multiple of 32; w and x 16-byte aligned, w_scale and y to their elements,
- * ld_x a multiple of 8. Products and
- * sums in fp32; the weights are not rounded. A row of x that holds an infinity
- * or NaN gives infinities or NaN in its row of y, and in no other. No scratch; the
- * device that holds the tensors must be current. Rows of x go 8 or 16 at a time,
- * and each of these reads the weights again; N <= 524280. */
+ * ld_x a multiple of 8. Products and sums in fp32; the weights are not rounded,
+ * x only where it is below 2^-28 of the largest value of its 256 columns. Scales
+ * of magnitudes up to 2^96: x is shifted by powers of two so that a group's sum
+ * can stand at 2^31, and its product with the scale has to be finite. A row of
+ * x that holds an infinity or NaN gives infinities or NaN in its row of y, and
+ * in no other. No scratch; the device that holds the tensors must be current.
+ * Rows of x go 8 or 16 at a time, and each of these reads and decodes the
+ * weights again; N <= 524280. */
 int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,
                  const void* w_scale, const uint8_t* w_zero, const void* x, int64_t ld_x, float* y, int64_t ld_y,
                  void* stream);
