@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 o[j][a][2 + x] *= f;
                             }
                         }
+                    __syncwarp();
                 }
                 uint32_t pb[NT][2];
 #pragma unroll

@@ -98,7 +98,9 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t smem_addr) {
     return d;
 }
 
-// 32 consecutive columns of the lane's TMEM row
+// 32 consecutive columns of the lane's TMEM row. These are instructions of a
+// whole warp: where its lanes can have taken different ways before, a
+// __syncwarp stands in front.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
     asm volatile(
@@ -661,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float2 sa = unf2(add2(sum[0], sum[1]));
                     l += sa.x + sa.y;
+                    __syncwarp();
                     tmem_st32(t_s, pk);
                 }
                 tc_fence_before_sync();
@@ -695,7 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v[32];
 #pragma unroll
                     for (int x = 0; x < 32; ++x) v[x] = 0.f;
+                    // (a warp's rows part ways below: whole again before it loads)
                     const uint32_t col = t_o + lane_off + static_cast<uint32_t>(grp * (HD / 2) + c);
+                    __syncwarp();
                     if (has_a && all_ok) {
                         float o[32];
                         tmem_ld32(col, o);
@@ -703,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 32; ++x) v[x] = o[x] * ga;
                     }
+                    __syncwarp();
                     if (has_b && all_ok) {
                         float o[32];
                         tmem_ld32(col + HD, o);
@@ -743,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (whole && head == 0 && tid == 0) p.status[b] = status_of(bad);
+            __syncwarp();
             tc_fence_before_sync();
             named_bar_sync(1, kSoft);     // both have read both accumulators and the sums
             tc_fence_after_sync();

@@ -212,3 +212,21 @@ def test_queries_with_one_dimension_far_above_the_others(K, nq, nkv, hd):
     qx, qt = _bf16(q)
     ref, lim, size = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
     _check(_call(qt, S, table, kc, vc, ks, vs), ref, lim)
+
+
+# ---------------------------------------------------------------- rows that end anywhere in a warp
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("rows", [1, 7, 9, 15, 17, 31, 33, 40, 63, 65, 88, 97, 127, 128])
+def test_any_number_of_rows(rows, hd):
+    # heads that one CTA has whole, and heads that several share
+    rng = np.random.default_rng(rows)
+    S = [130, 3]
+    kc, ks = _cache(rng, 40, 1, hd)
+    vc, vs = _cache(rng, 40, 1, hd)
+    table = rng.permutation(40)[:34].reshape(2, 17).astype(np.int32)
+    for K, nq in {(rows, 1), (1, rows)}:
+        qx, qt = _bf16(rng.standard_normal((2, K, nq, hd)))
+        ref, lim, _ = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
+        for copies in (1, 40):
+            _check_copies(qt, S, table, kc, vc, ks, vs, copies, ref, lim)
