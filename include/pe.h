@@ -422,8 +422,10 @@ int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void*
  *  q      [B, K, nq, hd] bf16, rows ld_q elements apart
  *  out    [B, K, nq, hd] bf16 OUT, rows ld_out apart; rows past rows[b], and
  *         all rows of a request that is not OK, are zero
- *  ws     scratch of pe_attention_kv8_scratch floats, 16-byte aligned; needs no
- *         initial value, and calls that can overlap need one each
+ *  ws     scratch of pe_attention_kv8_scratch floats (two partial results of
+ *         up to 128 rows for each multiprocessor, 20 MB at most, whatever
+ *         max_pages is), 16-byte aligned; needs no initial value, and calls
+ *         that can overlap need one each
  *  status [B] OUT; a page-table entry of a needed page that is outside
  *         [0, num_pages) is PE_REQ_BAD_PAGE
  * K * (nq/nkv) <= 128, hd 64 or 128; q, out and codes 16-byte aligned, ld_q and

@@ -47,7 +47,7 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 2;         // units in flight per warp: 96 KB per SM. More only lengthens the queue
                                    // in front of every other load
-constexpr int kMaxUnits = 1024;    // units of one CTA
+constexpr int kMaxUnits = 1024;    // units of a window
 constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per warp
 constexpr int kPad = 32;           // a segment's end in units (B=64, 512..8192 entries: 66 us, with 0 73)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -88,26 +88,20 @@ struct Smem {
 };
 static_assert(Smem<128, 1>::kBytes <= 232448 - 2048 && Smem<64, 2>::kBytes <= 232448 - 2048, "shared memory of a block");
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_attn_kv8(const Kv8Params p) {
+// The n units of a window; FIRST: of the share's first one.
+template <int HD, int NT, bool FIRST>
+__device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, int n, const Window* win) {
     using L = Smem<HD, NT>;
     constexpr int kRows = L::kRows;
     constexpr int kSteps = HD / 16;       // MMA steps over the head dimension = words of a lane's quarter of a K row
     constexpr int kCols = HD / 8;         // dimensions of a lane's part of a V row
     constexpr int kMt = kCols / 2;        // 16-dimension tiles of the output
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * kStages * 2 * L::kTile;
     float* s_o = reinterpret_cast<float*>(sm + L::kO);
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
-
-    pdl_launch_dependents();
-    int idle;
-    const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, s_info, s_tile, idle);
 
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t ring_at = smem_u32(ring) + lane * 16, ring_v = smem_u32(ring) + L::kTile + lane * kCols;
@@ -338,6 +332,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
 
+        // what this head's earlier windows left: a thread per row and four dimensions
+        const bool early = FIRST ? page0 > 0 : seg == 0 && win->early, carry = !FIRST && seg == 0 && win->carry;
+        float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (early ? 0 : 1)) * part_floats(kRows, HD);
+        static_assert(kRows * (HD / 4) <= kThreads, "the end of a segment");
+        const int r = tid / (HD / 4), q = tid - r * (HD / 4);
+        float M0 = -INFINITY, sum0 = 0.f;
+        float4 acc0 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (carry && r < kRows) {
+            acc0 = *reinterpret_cast<const float4*>(part + r * HD + q * 4);
+            M0 = part[kRows * HD + r];
+            sum0 = part[kRows * HD + kRows + r];
+        }
         // Join the warps: maxima and sums through a table that two segments
         // take in turn, then every warp's output relative to the common
         // maximum, two warps to a slot.
@@ -391,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncthreads();
         }
-        for (int item = tid; item < kRows * (HD / 4); item += kThreads) {
-            const int r = item / (HD / 4), q = item - r * (HD / 4);
+        if (r < kRows) {
             float M = -INFINITY, bad = 0.f, sum = 0.f;
             float2 ml[kWarps];
 #pragma unroll
@@ -411,7 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4 v = *(reinterpret_cast<const float4*>(s_o + (w * kRows + r) * HD) + (q ^ L::swizzle(r)));
                 acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
             }
-            if (len == info.w) {   // the whole head: write the output
+            if (carry) {
+                const float top = fmaxf(M, M0), f = M == top ? 1.f : ex2(M - top), f0 = M0 == top ? 1.f : ex2(M0 - top);
+                bad = fminf(bad, sum0 < 0.f ? sum0 : 0.f);
+                sum = sum * f + (sum0 < 0.f ? 0.f : sum0 * f0);
+                acc = make_float4(acc.x * f + acc0.x * f0, acc.y * f + acc0.y * f0, acc.z * f + acc0.z * f0, acc.w * f + acc0.w * f0);
+                M = top;
+            }
+            if (!early && page0 + len == info.w) {   // the whole head: write the output
                 if (r < live) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     if (bad < 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -423,20 +435,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[0] = __floats2bfloat162_rn(acc.x, acc.y);
                     dst[1] = __floats2bfloat162_rn(acc.z, acc.w);
                 }
-                if (info.y == 0 && item == 0) p.status[b] = status_of(bad);
+                if (info.y == 0 && tid == 0) p.status[b] = status_of(bad);
             } else {
-                float* dst = p.part + static_cast<size_t>(2 * blockIdx.x + (page0 > 0 ? 0 : 1)) * part_floats(kRows, HD);
-                *reinterpret_cast<float4*>(dst + r * HD + q * 4) = acc;
+                *reinterpret_cast<float4*>(part + r * HD + q * 4) = acc;
                 if (q == 0) {
-                    dst[kRows * HD + r] = M;
-                    dst[kRows * HD + kRows + r] = bad < 0.f ? bad : sum;
+                    part[kRows * HD + r] = M;
+                    part[kRows * HD + kRows + r] = bad < 0.f ? bad : sum;
                 }
             }
         }
         seg += len;
     }
     copies_wait<0>();
-    if (idle) zero_idle_rows_by<1, kPad>(p, HD, idle, warp, kWarps);
+}
+
+// FIRST: every share's first window. Otherwise the others.
+template <int HD, int NT, bool FIRST>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_kv8(const Kv8Params p) {
+    using L = Smem<HD, NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
+    int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
+    __shared__ Window s_win;
+    bool idle;
+
+    pdl_launch_dependents();
+    if constexpr (FIRST) {
+        const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, 0, s_info, s_tile, &s_win, idle);
+        attend_window<HD, NT, true>(p, sm, n, &s_win);
+        if (idle) zero_idle_rows_by<1, kPad>(p, HD, threadIdx.x >> 5, kWarps);
+    } else {
+        pdl_wait();
+        if (p.cut[gridDim.x].x <= kMaxUnits) return;
+        for (int w = 1;; ++w) {
+            const int n = gather_units<kThreads, 1, kPad, kMaxUnits>(p, kMinUnits, w, s_info, s_tile, &s_win, idle);
+            attend_window<HD, NT, false>(p, sm, n, &s_win);
+            if (!s_win.more) break;
+            __syncthreads();   // all warps are done with the tables
+        }
+    }
 }
 
 // Joins the parts of every head that several CTAs share, in unit order. The
@@ -605,17 +644,14 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     a.tr = umma ? kUmmaRows : (rows <= 8 ? 8 : 16);
     a.sms = sms;
     const int pages = umma ? kUmmaPages : 1, pad = umma ? kUmmaPad : kPad;
-    const int max_units = umma ? kUmmaUnits : kMaxUnits, least = umma ? kUmmaLeast : kMinUnits;
-    const long long most = static_cast<long long>(B) * nkv * ((max_pages + pages - 1) / pages + pad);
+    const int least = umma ? kUmmaLeast : kMinUnits;
+    const long long most = a.most = static_cast<long long>(B) * nkv * ((max_pages + pages - 1) / pages + pad);
     if (most > 0x3FFFFFFFll) {
         set_error("attention: batch * heads * pages is too large for one call");
         return PE_ERR_UNSUPPORTED;
     }
-    // one CTA per SM, and as many rounds as keep a CTA's share in its tables
-    const long long round = static_cast<long long>(sms) * max_units;
-    const long long slots = static_cast<long long>(sms) * ((most + round - 1) / round);
     const long long want = (most + least - 1) / least;
-    a.grid = static_cast<int>(want < slots ? want : slots);
+    a.grid = static_cast<int>(want < sms ? want : sms);
     a.cut_floats = (static_cast<size_t>(a.grid) + 2) / 2 * 8;
     a.ws_floats = a.cut_floats + 4 + 2 * static_cast<size_t>(a.grid) * part_floats(a.tr, hd);
     *out = a;
@@ -624,11 +660,14 @@ int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
 
 template <int HD, int NT>
 int launch_rows(const Kv8Params& p, const Plan& a, cudaStream_t s) {
-    constexpr auto kern = k_attn_kv8<HD, NT>;
+    constexpr auto first = k_attn_kv8<HD, NT, true>, rest = k_attn_kv8<HD, NT, false>;
     constexpr int smem = Smem<HD, NT>::kBytes;
-    const int rc = allow_smem<kern>(a.dev, smem);
+    int rc = allow_smem<first>(a.dev, smem);
     if (rc != PE_OK) return rc;
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), smem, s, false, p));
+    PE_CUDA_TRY(launch_ex(first, dim3(a.grid), dim3(kThreads), smem, s, false, p));
+    if (a.most <= static_cast<long long>(a.grid) * kMaxUnits) return PE_OK;
+    if ((rc = allow_smem<rest>(a.dev, smem)) != PE_OK) return rc;
+    PE_CUDA_TRY(launch_ex(rest, dim3(a.grid), dim3(kThreads), smem, s, true, p));
     return PE_OK;
 }
 
@@ -734,7 +773,6 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     p.out = static_cast<__nv_bfloat16*>(out);
     p.ld_out = ld_out;
     p.status = status;
-    p.sms = a.sms;
     p.cut = reinterpret_cast<int4*>(ws);
     // whole sectors: a 16-byte aligned `ws` may be half of one off
     p.part = ws + a.cut_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);

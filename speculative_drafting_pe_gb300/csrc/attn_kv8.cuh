@@ -5,10 +5,17 @@
 // A unit is PPU pages of one kv head, with all the query rows over it. All
 // units of the batch stand in one line (request, kv head, page) and every CTA
 // takes an equal share of it, so ragged lengths, many requests and a single
-// long one are split alike; the lengths stay on the device. A run of units of
-// one head within a CTA is a segment. A CTA writes the heads that it covers
-// whole; a head that several CTAs share leaves one partial tile per CTA in
-// scratch, and k_kv8_merge joins them in order.
+// long one are split alike; the lengths stay on the device. A CTA has tables of
+// so many units in shared memory and takes a longer share in windows of that
+// length: the launch and its scratch follow the device, not the width of the
+// page table. The first window is one kernel, without a loop around it; where
+// the page table has room for more, a second one follows and takes the others,
+// or returns at once (0.7 to 1.5 us; in one kernel a loop over the windows, in
+// line or out of line, cost the many-rows kernel 2 to 8% in registers).
+// A run of units of one head within a window is a segment. A CTA writes the heads that it covers whole; a head that several
+// CTAs share leaves one partial tile per CTA in scratch, and k_kv8_merge joins
+// them in order. A head that goes on in the CTA's next window leaves its sums
+// at the same place, and the next segment's end adds them to its own.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -48,7 +55,6 @@ struct Kv8Params {
     __nv_bfloat16* out;
     long long ld_out;
     int32_t* status;
-    int sms;           // shares of the line, unless a share's tables were too small
     int4* cut;         // [grid] OUT: the run that CTA c's share begins inside of: {request, head, unit of the
                        // run (0: none, -1: this CTA gave up), units of the run}; [grid]: {positions of a share, shares}
     float* part;       // [2 * grid] partial tiles (part_floats each): of a CTA's run that began in an earlier share, and of the other one
@@ -138,9 +144,9 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t w, int& any) {
 // this CTA's to look after. gather_units says whether there are any, so that a
 // batch without them pays nothing. By warp my_warp of the CTA's `warps` first.
 template <int PPU, int PAD>
-__device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int shares, int my_warp, int warps) {
+__device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, int my_warp, int warps) {
     const int lane = threadIdx.x & 31;
-    for (int b = blockIdx.x; b < p.B; b += shares) {
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const Req r = request_of<PPU, PAD>(p, b);
         if (my_warp == 0 && lane == 0 && r.span == 0) p.status[b] = r.st;
         for (int j = r.rows + my_warp; j < p.K; j += warps) {
@@ -150,14 +156,21 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
     }
 }
 
-// This CTA's share of the line, and its units' pages in shared memory:
+// What a CTA has in its tables, besides the units.
+struct Window {
+    int w;              // its number
+    bool carry, early;  // of the first segment: its head's sums so far stand in scratch; its run began in an earlier share
+    bool more;          // the share goes on
+};
+
+// Window w of this CTA's share of the line, and its units' pages in shared memory:
 // info[i] of a unit that begins a segment = {request, head, unit within its
 // run, units of the run}; of page q of unit i, entry i * PPU + q of tile
 // (page * nkv + head, -1: outside the pool, -2: behind the request's last
-// page). Returns the number of units; idle: 0, or where zero_idle_rows_by has
-// work the number of CTAs with a share.
-// All NT threads of the CTA. A share is at least `least` positions, and at most
-// MAX, which is what the tables hold (the planner's grid sees to that).
+// page). Returns the number of units. idle: whether zero_idle_rows_by has work.
+// All NT threads of the CTA, after a barrier behind the last use of the tables.
+// A share is at least `least` positions, a window at most MAX, which is what
+// the tables hold.
 // Behind each run of units lie PAD positions without work: what the end of a
 // segment costs, so that the shares' times are even, not their units alone.
 // The requests of the share are listed first, from one scan over the batch, and
@@ -165,12 +178,12 @@ __device__ __forceinline__ void zero_idle_rows_by(const Kv8Params& p, int hd, in
 // and three barriers (B=1 K=7 13.6 us; with a scan for the total, one for the
 // list and the lengths read again 14.5).
 template <int NT, int PPU, int PAD, int MAX>
-__device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile, int& idle) {
-    constexpr int kWarps = NT / 32, kList = 64;
+__device__ int gather_units(const Kv8Params& p, int least, int w, int4* info, int* tile, Window* win, bool& idle) {
+    constexpr int kWarps = NT / 32, kList = 128;
     static_assert(kWarps <= 32 && MAX / (1 + PAD) + 2 <= kList, "requests of a share");
     __shared__ int s_span[kWarps], s_some[kWarps];
-    __shared__ int4 s_list[kList];   // request, its first position, units of a head, pages; at its rank among the requests with units
-    __shared__ int s_edge[2];        // ranks of the share's first and last request
+    __shared__ int4 s_list[kList];   // of the window: request, its first position, units of a head, pages; at its rank among the requests with units
+    __shared__ int s_edge[2];        // ranks of the window's first and last request
     constexpr unsigned kAll = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Req mine0 = tid < p.B ? request_of<PPU, PAD>(p, tid) : Req{};   // most batches fit the CTA's threads
@@ -184,8 +197,8 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         __syncthreads();
     }
     const int grid = static_cast<int>(gridDim.x);
-    int shares = 0, per = 0, lo = 0, hi = 0, base = 0, ranks = 0, rest = 0;
-    idle = 0;
+    int per = 0, share = 0, lo = 0, hi = 0, base = 0, ranks = 0, rest = 0;
+    bool more = false;
     for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + tid;
         const Req r = b0 == 0 ? mine0 : (b < p.B ? request_of<PPU, PAD>(p, b) : Req{});
@@ -206,17 +219,15 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         const int spans = __reduce_add_sync(kAll, span);
         if (b0 == 0) {
             total += spans;
-            // a share per SM, whatever the page table has room for; more only
-            // where the tables of a share would not hold it
-            const int rounds = max(1, (total + p.sms * MAX - 1) / (p.sms * MAX));
-            shares = min(grid, rounds * p.sms);
-            per = max(least, (total + shares - 1) / shares);
-            if (static_cast<int>(blockIdx.x) >= shares) return 0;
+            per = max(least, (total + grid - 1) / grid);
             const long long at = static_cast<long long>(blockIdx.x) * per;
-            lo = static_cast<int>(min(at, static_cast<long long>(total)));
+            share = static_cast<int>(min(at, static_cast<long long>(total)));
+            lo = share + w * MAX;
             hi = static_cast<int>(min(static_cast<long long>(total), at + per));
+            more = hi - lo > MAX;
+            hi = more ? lo + MAX : hi;
         }
-        rest |= b < p.B && r.rows < p.K && b % shares == static_cast<int>(blockIdx.x);
+        rest |= b < p.B && r.rows < p.K && b % grid == static_cast<int>(blockIdx.x);
         const int u0 = base + __reduce_add_sync(kAll, lane < warp ? span : 0) + incl - r.span;
         const int rank = ranks + __reduce_add_sync(kAll, lane < warp ? count : 0) + __popc(some & ((1u << lane) - 1u));
         if (r.span > 0 && u0 < hi && u0 + r.span > lo) {
@@ -227,10 +238,14 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         base += spans;
         ranks += __reduce_add_sync(kAll, count);
     }
-    idle = __syncthreads_or(rest) != 0 ? shares : 0;
-    if (tid == 0 && blockIdx.x == 0) p.cut[grid] = make_int4(per, shares, 0, 0);
+    idle = __syncthreads_or(rest) != 0;
+    if (tid == 0 && blockIdx.x == 0 && w == 0) p.cut[grid] = make_int4(per, grid, 0, 0);
     if (lo >= hi) {
-        if (tid == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (tid == 0) {
+            if (w == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+            *win = Window{w, false, false, false};
+        }
+        __syncthreads();
         return 0;
     }
     const int rank0 = s_edge[0], listed = s_edge[1] - rank0 + 1;
@@ -243,8 +258,9 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
     const int head0 = (lo - front.y) / (front.z + PAD), in0 = lo - front.y - head0 * (front.z + PAD);
     const int head1 = (hi - back.y) / (back.z + PAD), in1 = hi - back.y - head1 * (back.z + PAD);
     const int skip = units_to(0, front, head0, in0), n = units_to(listed - 1, back, head1, in1) - skip;
-    if (tid == NT - 1)
-        p.cut[blockIdx.x] = in0 < front.z ? make_int4(front.x, head0, in0, front.z) : make_int4(0, 0, 0, 0);
+    const bool inside = in0 > 0 && in0 < front.z;   // the window begins inside of a run
+    if (tid == NT - 1 && w == 0)
+        p.cut[blockIdx.x] = inside ? make_int4(front.x, head0, in0, front.z) : make_int4(0, 0, 0, 0);
     for (int x = tid; x < (hi - lo) * PPU; x += NT) {
         const int u = lo + x / PPU;
         int j = 0;   // the last listed request that begins at or before u
@@ -265,6 +281,7 @@ __device__ int gather_units(const Kv8Params& p, int least, int4* info, int* tile
         tile[i * PPU + q] = id;
         if (q == 0 && (i == 0 || in == 0)) info[i] = make_int4(of.x, head, in, of.z);
     }
+    if (tid == 0) *win = Window{w, inside && w > 0, inside && lo - in0 < share, more};
     __syncthreads();
     return n;
 }
@@ -275,14 +292,15 @@ __device__ __forceinline__ int status_of(float mark) {
 
 struct Plan {
     int tr;                  // rows of a tile
-    int grid, sms, dev;
+    int grid, sms, dev;      // a CTA per multiprocessor at most
+    long long most;          // positions of the line at most
     size_t cut_floats, ws_floats;
 };
 
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
 // rows past which the tensor-memory kernel takes over, and its launch
 int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s);
-constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 448;
+constexpr int kUmmaPages = 4, kUmmaRows = 128, kUmmaUnits = 640;
 // A share's positions at least (B=1 K=7, 2048 entries: 14.9 us, with 1 15.5, with 6 16.6), and the units' worth of a
 // segment's end (B=128 K=11: 190 us, with 0 208; 64-wide heads 87 and 91; as all of these were then)
 constexpr int kUmmaLeast = 3, kUmmaPad = 7;

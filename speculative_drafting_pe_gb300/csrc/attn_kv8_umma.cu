@@ -71,6 +71,9 @@ constexpr int kScales = 16;                 // units whose page scales are kept:
 constexpr int kScaleRec = 3 * kUmmaPages;   // floats of a unit's scales
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -183,21 +186,37 @@ struct Layout {
     static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][ks of 4 pages, vs of 4 pages as its part and its lg]
     static constexpr int kNan = kScale + kScales * kScaleRec * 4;        // [kTurns][kTile] bytes
     static constexpr int kBar = kNan + kTurns * kTile;
-    // k_full, cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
     static constexpr int kBars = 5 * kTurns + 4;
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448 - 2048 && Layout<64>::kBytes <= 232448 - 2048, "shared memory of a block");
+// the barriers of a window: k_full, cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
 template <int HD>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const Kv8Params p) {
+__device__ __forceinline__ void init_bars(uint64_t* bars) {
     using L = Layout<HD>;
     constexpr int kTurns = L::kTurns;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ int s_abort;
-    const volatile int* abort = &s_abort;
+    for (int s = 0; s < kTurns; ++s) {
+        mbar_init(&bars[s], L::kTmaK ? 2 : 1);
+        mbar_init(&bars[kTurns + s], L::kTeam);
+        mbar_init(&bars[2 * kTurns + s], 1);
+        mbar_init(&bars[3 * kTurns + s], 4);
+        mbar_init(&bars[4 * kTurns + s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+        mbar_init(&bars[5 * kTurns + s], 4);
+        mbar_init(&bars[5 * kTurns + 2 + s], 1);
+    }
+    fence_mbar_init();
+}
+
+// The n units of a window by every role; FIRST: of the share's first one. false
+// in the threads of a role that gave up waiting.
+template <int HD, bool FIRST>
+__device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8Params& p, uint8_t* sm, int n, const Window* win,
+                                              bool idle, const volatile int* abort) {
+    using L = Layout<HD>;
+    constexpr int kTurns = L::kTurns;
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
     float* s_cs = reinterpret_cast<float*>(sm + L::kCs);
@@ -211,36 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* pv_done = p_full + kTurns;
     uint64_t* q_full = pv_done + kTurns;
     uint64_t* q_empty = q_full + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.nq / p.nkv;
 
-    pdl_launch_dependents();
-    if (tid == 0) {
-        s_abort = 0;
-        for (int s = 0; s < kTurns; ++s) {
-            mbar_init(&k_full[s], L::kTmaK ? 2 : 1);
-            mbar_init(&cv_full[s], L::kTeam);
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
-            mbar_init(&pv_done[s], 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&q_full[s], 4);
-            mbar_init(&q_empty[s], 1);
-        }
-        fence_mbar_init();
-    }
-    if (warp == kWarpS) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before_sync();
-    int idle;
-    const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(
-        p, kUmmaLeast, s_info, s_tile, idle);
-    tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L::kTmem);
     const uint32_t t_o = tmem + kTurns * kTile;   // S_t in columns 64 (t mod kTurns) ..; group x's output x * HD behind them
     bool ok = true;
     auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
@@ -382,6 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
+        }
+        if (!FIRST && ok && win->more) {   // what this warp committed has arrived: the next window takes the barriers anew
+            for (int i = max(0, n - kTurns); i < n; ++i) ok = ok && wait(scores ? &s_full[i % kTurns] : &pv_done[i % kTurns], turn(i));
+            for (int x = max(0, no - 1); scores && x <= no; ++x) ok = ok && wait(&q_empty[x & 1], static_cast<uint32_t>((x >> 1) & 1));
+            ok = __all_sync(0xffffffffu, ok);
         }
         __syncwarp();
     } else if (warp >= kWarpConv && warp < kWarpS) {
@@ -675,20 +673,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after_sync();
             // the two groups' sums of each row; each group writes half of the dimensions
+            // and what the head's earlier windows left
+            const bool early = FIRST ? info.z > 0 : seg == 0 && win->early, carry = !FIRST && seg == 0 && win->carry && row < R;
+            float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (early ? 0 : 1)) * part_floats(kRows, HD);
+            const float M0 = carry ? part[kRows * HD + row] : -INFINITY, sum0 = carry ? part[kRows * HD + kRows + row] : 0.f;
             s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, mo, 0.f);
             named_bar_sync(1, kSoft);
             const float4 xa = s_ex[row], xb = s_ex[kRows + row];
-            const float bad = fminf(fminf(xa.y, xb.y), 0.f);   // a NaN sum is not less than 0
-            const float M = fmaxf(xa.x, xb.x);
+            const float bad = fminf(fminf(fminf(xa.y, xb.y), sum0), 0.f);   // a NaN sum is not less than 0
+            const float M = fmaxf(fmaxf(xa.x, xb.x), M0), f0 = M0 == M ? 1.f : ex2(M0 - M);
             const float fa = xa.y <= 0.f ? 0.f : ex2(xa.x - M), fb = xb.y <= 0.f ? 0.f : ex2(xb.x - M);
-            const float sum = (xa.y <= 0.f ? 0.f : xa.y * fa) + (xb.y <= 0.f ? 0.f : xb.y * fb);
-            const bool whole = len == info.w;
+            const float sum = (xa.y <= 0.f ? 0.f : xa.y * fa) + (xb.y <= 0.f ? 0.f : xb.y * fb) + (sum0 <= 0.f ? 0.f : sum0 * f0);
+            const bool whole = !early && info.z + len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const float ga = unlift(xa.z, M) * inv, gb = unlift(xb.z, M) * inv;
             __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
                                  static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
             const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;
-            float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (info.z > 0 ? 0 : 1)) * part_floats(kRows, HD);
             const bool all_ok = __all_sync(0xffffffffu, !(bad < 0.f));
             // which groups had a tile: the same for the whole segment
             const bool has_a = (seg & 1) == 0 || len > 1, has_b = (seg & 1) == 1 || len > 1;
@@ -717,6 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int x = 0; x < 32; ++x) v[x] = fmaf(o[x], gb, v[x]);
                     }
                     if (row >= R) continue;
+                    if (carry && all_ok) {
+                        const float4* had = reinterpret_cast<const float4*>(part + row * HD + grp * (HD / 2) + c);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float4 o = had[x];
+                            v[4 * x] = fmaf(o.x, f0 * inv, v[4 * x]);
+                            v[4 * x + 1] = fmaf(o.y, f0 * inv, v[4 * x + 1]);
+                            v[4 * x + 2] = fmaf(o.z, f0 * inv, v[4 * x + 2]);
+                            v[4 * x + 3] = fmaf(o.w, f0 * inv, v[4 * x + 3]);
+                        }
+                    }
                     if (whole) {
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -755,7 +767,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             seg += len;
         }
-        if (idle) zero_idle_rows_by<kUmmaPages, kUmmaPad>(p, HD, idle, warp, kSoft / 32);
+        if (FIRST && idle) zero_idle_rows_by<kUmmaPages, kUmmaPad>(p, HD, warp, kSoft / 32);
+    }
+    return ok;
+}
+
+// FIRST: every share's first window. Otherwise the others.
+template <int HD, bool FIRST>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_kv8_umma(const __grid_constant__ CUtensorMap tmK, const Kv8Params p) {
+    using L = Layout<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int s_abort;
+    __shared__ Window s_win;
+    int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
+    int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmem);
+    const int tid = threadIdx.x, warp = tid >> 5;
+
+    pdl_launch_dependents();
+    if constexpr (!FIRST) {
+        pdl_wait();
+        // no share has another window, or this CTA gave up in the first
+        if (p.cut[gridDim.x].x <= kUmmaUnits || p.cut[blockIdx.x].z < 0) return;
+    }
+    if (tid == 0) {
+        s_abort = 0;
+        init_bars<HD>(bars);
+    }
+    if (warp == kWarpS) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    bool idle, ok = true;
+    if constexpr (FIRST) {
+        const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(p, kUmmaLeast, 0, s_info, s_tile, &s_win, idle);
+        tc_fence_after_sync();
+        ok = attend_window<HD, true>(tmK, p, sm, n, &s_win, idle, &s_abort);
+    } else {
+        for (int w = 1;; ++w) {
+            const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(p, kUmmaLeast, w, s_info, s_tile, &s_win, idle);
+            if (w == 1) tc_fence_after_sync();
+            ok = attend_window<HD, false>(tmK, p, sm, n, &s_win, false, &s_abort);
+            if (!s_win.more) break;
+            if (!ok) s_abort = 1;
+            __syncthreads();       // the tables and the barriers are not in use
+            if (*static_cast<volatile int*>(&s_abort)) break;
+            // units, segments and phases count from 0 again
+            if (tid == 0) {
+                for (int x = 0; x < L::kBars; ++x) mbar_inval(&bars[x]);
+                init_bars<HD>(bars);
+            }
+        }
     }
     if (!ok) {
         s_abort = 1;              // the other roles' waits end too
@@ -766,16 +832,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && s_abort) p.cut[blockIdx.x].z = -1;   // the merge refuses the call's results
     if (warp == kWarpS) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(*tmem_slot, 512);
     }
 }
 
 template <int HD>
 int launch_hd(const CUtensorMap& tk, const Kv8Params& p, const Plan& a, cudaStream_t s) {
-    constexpr auto kern = k_attn_kv8_umma<HD>;
-    const int rc = allow_smem<kern>(a.dev, Layout<HD>::kBytes);
+    constexpr auto first = k_attn_kv8_umma<HD, true>, rest = k_attn_kv8_umma<HD, false>;
+    constexpr int smem = Layout<HD>::kBytes;
+    int rc = allow_smem<first>(a.dev, smem);
     if (rc != PE_OK) return rc;
-    PE_CUDA_TRY(launch_ex(kern, dim3(a.grid), dim3(kThreads), Layout<HD>::kBytes, s, false, tk, p));
+    PE_CUDA_TRY(launch_ex(first, dim3(a.grid), dim3(kThreads), smem, s, false, tk, p));
+    if (a.most <= static_cast<long long>(a.grid) * kUmmaUnits) return PE_OK;
+    if ((rc = allow_smem<rest>(a.dev, smem)) != PE_OK) return rc;
+    PE_CUDA_TRY(launch_ex(rest, dim3(a.grid), dim3(kThreads), smem, s, true, tk, p));
     return PE_OK;
 }
 

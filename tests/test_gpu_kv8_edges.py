@@ -230,3 +230,73 @@ def test_any_number_of_rows(rows, hd):
         ref, lim, _ = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
         for copies in (1, 40):
             _check_copies(qt, S, table, kc, vc, ks, vs, copies, ref, lim)
+
+
+# ---------------------------------------------------------------- no page is lost, none counts twice
+
+def _marked(rng, pages, nkv, hd, share):
+    """Values 1 in one dimension of each page (by its place in the table, `share` pages to a dimension in turn), and
+    keys of any kind."""
+    kc, ks = _cache(rng, 64, nkv, hd)
+    at = torch.as_tensor(rng.integers(0, 64, pages)).cuda()
+    kc, ks = _dev(kc)[at].contiguous(), _dev(ks)[at].contiguous()
+    vc = torch.zeros(pages, nkv, PAGE, hd, dtype=torch.uint8, device="cuda")
+    place = torch.arange(pages, device="cuda")
+    vc[place, :, :, place // share % hd] = 0x38
+    return kc, ks, vc, torch.ones(pages, nkv, device="cuda")
+
+
+MANY = [
+    # B, K, query heads, kv heads, width, entries
+    (1, 1, 8, 1, 128, [70000]), (2, 2, 8, 1, 64, [30000, 12345]), (1, 7, 8, 1, 128, [65000]),
+    (3, 5, 16, 2, 64, [9000, 40000, 77]), (300, 1, 1, 1, 64, [5000, 3, 12000, 640]),
+    # shares longer than a CTA's tables, heads cut by them once and several times
+    (8, 1, 8, 8, 128, [40000]), (8, 2, 8, 8, 64, [40000]), (16, 3, 64, 8, 64, [36000]), (16, 5, 16, 8, 128, [36000]),
+    (50, 1, 8, 8, 64, [9600]), (64, 5, 16, 8, 64, [9600]), (64, 9, 8, 8, 128, [9600]),
+    (120, 1, 8, 8, 128, [50000, 100]), (60, 2, 64, 8, 64, [60000, 31000, 9]), (40, 9, 8, 8, 128, [100000, 5]),
+    (40, 5, 32, 8, 64, [90000, 120000])]
+
+
+@pytest.mark.parametrize("B,K,nq,nkv,hd,lens", MANY)
+def test_every_page_counts_once(B, K, nq, nkv, hd, lens):
+    # queries of zero see every entry alike: dimension d of the output is the share of the entries whose page marks it
+    S = np.resize(lens, B).astype(np.int64)
+    pages = -(-(int(S.max()) + K) // PAGE)
+    rng = np.random.default_rng(B + K)
+    for share in (1, -(-pages // hd)):       # neighbours in dimensions of their own, or in runs
+        kc, ks, vc, vs = _marked(rng, pages, nkv, hd, share)
+        table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+        q = torch.zeros(B, K, nq, hd, dtype=torch.bfloat16, device="cuda")
+        got, status = binding.attention_kv8(q, _dev(S.astype(np.int32)), table, kc, vc, ks, vs)
+        assert (status == 0).all()
+        got = got.double().cpu().numpy()
+        dim = np.arange(pages * PAGE) // PAGE // share % hd
+        for s in set(lens):
+            want = np.stack([np.bincount(dim[:s + j + 1], minlength=hd) / (s + j + 1) for j in range(K)])
+            # the bf16 output, the sums' fp32 steps; every weight is a power of two
+            err = np.abs(got[S == s] - want[None, :, None, :])
+            assert (err <= (2.0 ** -8 + 2.0 ** -14) * want[None, :, None, :]).all(), (s, err.max())
+
+
+@pytest.mark.parametrize("B,K,nq,nkv,hd,S", [(8, 1, 8, 8, 128, 40000), (16, 3, 64, 8, 64, 36000),
+                                             (64, 9, 8, 8, 128, 9600), (1, 2, 8, 1, 64, 50000)])
+def test_long_requests_with_scores_of_every_size(B, K, nq, nkv, hd, S):
+    # the same request B times over: shares and their joins lie elsewhere in each
+    rng = np.random.default_rng(B)
+    kc, ks = _cache(rng, 200, nkv, hd)
+    vc, vs = _cache(rng, 200, nkv, hd)
+    ks *= 4
+    table = rng.integers(0, 200, (1, -(-(S + K) // PAGE))).astype(np.int32)
+    qx, qt = _bf16(rng.standard_normal((1, K, nq, hd)))
+    ref, lim, size = _exact(qx, [S], table, kc, vc, ks, vs, hd ** -0.5)
+    got = _call(qt.expand(B, K, nq, hd).contiguous(), [S] * B, np.repeat(table, B, 0), kc, vc, ks, vs)
+    _check(got, ref, lim)
+
+
+@pytest.mark.parametrize("K", [1, 9])
+def test_scratch_does_not_follow_the_page_table(K):
+    # two partial tiles for each multiprocessor and a table of cuts, however many pages a request could have
+    need = [binding._kv8_scratch(0, 256, K, 64, 8, 128, pages) for pages in (64, 512, 8192, 100000)]
+    tile = (128 if K > 1 else 8) * (128 + 2)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert len(set(need)) == 1 and need[0] <= sms * (2 * tile + 4) + 16
