@@ -500,6 +500,13 @@ int pe_device_errors(pe_handle* h, void* stream, uint32_t* out_bits);
  * for draft passes of at most 64 rows). */
 int pe_test_stall_chain(pe_handle* h, void* stream);
 
+/* The same for pe_attention_kv8: the next call in this process that goes by its
+ * tensor-memory kernel (more than 8 query rows of a kv head, 64-wide heads more
+ * than 16) has every barrier of one kind (1: K codes, 2: V tiles, 3: weights)
+ * wait for one arrival more than there are, so its waits give up after their
+ * limit (1 s) and the call reports PE_REQ_TIMEOUT. Later calls are not touched. */
+int pe_test_stall_attention_kv8(int32_t barrier);
+
 /* Kernel kinds of the draft pass, for launch accounting and profiling. */
 #define PE_KERNEL_FC         0
 #define PE_KERNEL_ROW_BUILD  1

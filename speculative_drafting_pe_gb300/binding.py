@@ -29,7 +29,7 @@ EXPORTS = (
     "pe_init_drafter_fp8", "pe_linear_fp8", "pe_draft_refeed", "pe_verify_rebuild_refeed",
     "pe_sample_drafts", "pe_verify_stochastic",
     "pe_linear_w4", "pe_assign_pages", "pe_release_pages", "pe_kv8_append", "pe_attention_kv8_scratch",
-    "pe_attention_kv8",
+    "pe_attention_kv8", "pe_test_stall_attention_kv8",
 )
 KERNEL_KINDS = ("fc", "row_build", "rmsnorm", "qkv", "attention", "o_proj", "gate_up", "down", "lm_head", "argmax",
                 "layer_chain")
@@ -157,6 +157,7 @@ def load():
             ("pe_release_pages", [_i32] + [_vp] * 4 + [_i32] * 2 + [_vp, _i32] + [_vp] * 4),
             ("pe_kv8_append", [_i32] * 4 + [_vp, _i64, _vp, _i64] + [_vp] * 3 + [_i32] * 2 + [_vp] * 6),
             ("pe_attention_kv8_scratch", [_i32] * 6 + [ctypes.POINTER(_i64)]),
+            ("pe_test_stall_attention_kv8", [_i32]),
             ("pe_attention_kv8", [_i32] * 5 + [_vp, _i64, _vp, _vp, _vp, _i32, _i32] + [_vp] * 4 +
              [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp])):
         fn = getattr(lib, name)
@@ -787,3 +788,9 @@ def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, s
          hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out, "out"), ws.data_ptr(), need,
          status.data_ptr())
     return out, status
+
+
+def test_stall_attention_kv8(barrier):
+    """Host-side fault injection (tests only): in the next attention_kv8 call by the tensor-memory kernel no wait for
+    K codes (1), V tiles (2) or weights (3) can complete; they must give up."""
+    _check(load().pe_test_stall_attention_kv8(barrier))

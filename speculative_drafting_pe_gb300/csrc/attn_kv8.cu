@@ -780,6 +780,5 @@ extern "C" int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     if (a.tr == kUmmaRows) rc = launch_umma(p, a, head_dim, s);
     else if (a.tr == 16) rc = launch_rows<64, 2>(p, a, s);   // 128-wide heads: umma_from
     else rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
-    // a single share covers every head whole
-    return rc != PE_OK || a.grid == 1 ? rc : launch_merge(p, a, head_dim, s);
+    return rc != PE_OK ? rc : launch_merge(p, a, head_dim, s);   // also where no head is shared: it reports a wait that gave up
 }

@@ -57,6 +57,7 @@ struct Kv8Params {
     int32_t* status;
     int4* cut;         // [grid] OUT: the run that CTA c's share begins inside of: {request, head, unit of the
                        // run (0: none, -1: this CTA gave up), units of the run}; [grid]: {positions of a share, shares}
+    int stall;         // tests: the barrier (a kStall*) that waits for an arrival too many
     float* part;       // [2 * grid] partial tiles (part_floats each): of a CTA's run that began in an earlier share, and of the other one
 };
 
@@ -289,6 +290,8 @@ __device__ int gather_units(const Kv8Params& p, int least, int w, int4* info, in
 __device__ __forceinline__ int status_of(float mark) {
     return mark == 0.f ? PE_REQ_OK : PE_REQ_BAD_PAGE;
 }
+
+constexpr int kStallK = 1, kStallV = 2, kStallP = 3;   // K codes, V tiles, weights
 
 struct Plan {
     int tr;                  // rows of a tile

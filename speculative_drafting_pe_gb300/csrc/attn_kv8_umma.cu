@@ -193,14 +193,14 @@ struct Layout {
 static_assert(Layout<128>::kBytes <= 232448 - 2048 && Layout<64>::kBytes <= 232448 - 2048, "shared memory of a block");
 // the barriers of a window: k_full, cv_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [2]
 template <int HD>
-__device__ __forceinline__ void init_bars(uint64_t* bars) {
+__device__ __forceinline__ void init_bars(uint64_t* bars, int stall) {
     using L = Layout<HD>;
     constexpr int kTurns = L::kTurns;
     for (int s = 0; s < kTurns; ++s) {
-        mbar_init(&bars[s], L::kTmaK ? 2 : 1);
-        mbar_init(&bars[kTurns + s], L::kTeam);
+        mbar_init(&bars[s], (L::kTmaK ? 2 : 1) + (stall == kStallK));
+        mbar_init(&bars[kTurns + s], L::kTeam + (stall == kStallV));
         mbar_init(&bars[2 * kTurns + s], 1);
-        mbar_init(&bars[3 * kTurns + s], 4);
+        mbar_init(&bars[3 * kTurns + s], 4 + (stall == kStallP));
         mbar_init(&bars[4 * kTurns + s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -210,11 +210,21 @@ __device__ __forceinline__ void init_bars(uint64_t* bars) {
     fence_mbar_init();
 }
 
+// What the CTA has set going in this window, units of each kind.
+struct Issued {
+    int k, s, pv;   // TMA copies of K, score products, P.V products
+};
+// Waits for the phase a millisecond at most.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000ull) {}
+}
+
 // The n units of a window by every role; FIRST: of the share's first one. false
 // in the threads of a role that gave up waiting.
 template <int HD, bool FIRST>
 __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8Params& p, uint8_t* sm, int n, const Window* win,
-                                              bool idle, const volatile int* abort) {
+                                              bool idle, const volatile int* abort, Issued* issued) {
     using L = Layout<HD>;
     constexpr int kTurns = L::kTurns;
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
@@ -257,7 +267,8 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
 
     if (L::kTmaK && warp == kWarpK) {
         const uint64_t policy = l2_policy_evict_first();
-        for (int i = 0; i < n; ++i) {
+        int i = 0;
+        for (; i < n; ++i) {
             const int x = i % kTurns;
             const int tile = lane < kUmmaPages ? s_tile[i * kUmmaPages + lane] : -1;
             const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)) * kPage * HD);
@@ -269,6 +280,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
             if (lane < kUmmaPages && tile >= 0)
                 tma_load_2d(sm + L::kKRing + x * L::kCodes + lane * kPage * HD, &tmK, &k_full[x], 0, tile * kPage, policy);
         }
+        if (lane == 0) issued->k = i;
         __syncwarp();
     } else if (L::kTmaK && warp == kWarpK + 1) {
         for (int i = 0; i < n + kDepth; ++i) {
@@ -335,8 +347,8 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
         const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
         const uint32_t q_base = smem_u32(sm + L::kQ), k_base = smem_u32(sm + L::kKRing);
         const uint32_t cv_base = smem_u32(sm + L::kConv);
-        int seg = 0, end = 0, no = -1;
-        for (int i = 0; i < n; ++i) {
+        int seg = 0, end = 0, no = -1, i = 0;
+        for (; i < n; ++i) {
             const int x = i % kTurns;
             if (i == end) {
                 seg = i;
@@ -376,6 +388,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
             }
             __syncwarp();
         }
+        if (lane == 0) (scores ? issued->s : issued->pv) = i;
         if (!FIRST && ok && win->more) {   // what this warp committed has arrived: the next window takes the barriers anew
             for (int i = max(0, n - kTurns); i < n; ++i) ok = ok && wait(scores ? &s_full[i % kTurns] : &pv_done[i % kTurns], turn(i));
             for (int x = max(0, no - 1); scores && x <= no; ++x) ok = ok && wait(&q_empty[x & 1], static_cast<uint32_t>((x >> 1) & 1));
@@ -781,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int s_abort;
     __shared__ Window s_win;
+    __shared__ Issued s_issued;
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kUnit);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
@@ -795,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) {
         s_abort = 0;
-        init_bars<HD>(bars);
+        s_issued = Issued{0, 0, 0};
+        init_bars<HD>(bars, p.stall);
     }
     if (warp == kWarpS) {
         tmem_alloc(tmem_slot, 512);
@@ -806,12 +821,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FIRST) {
         const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(p, kUmmaLeast, 0, s_info, s_tile, &s_win, idle);
         tc_fence_after_sync();
-        ok = attend_window<HD, true>(tmK, p, sm, n, &s_win, idle, &s_abort);
+        ok = attend_window<HD, true>(tmK, p, sm, n, &s_win, idle, &s_abort, &s_issued);
     } else {
         for (int w = 1;; ++w) {
             const int n = gather_units<kThreads, kUmmaPages, kUmmaPad, kUmmaUnits>(p, kUmmaLeast, w, s_info, s_tile, &s_win, idle);
             if (w == 1) tc_fence_after_sync();
-            ok = attend_window<HD, false>(tmK, p, sm, n, &s_win, false, &s_abort);
+            ok = attend_window<HD, false>(tmK, p, sm, n, &s_win, false, &s_abort, &s_issued);
             if (!s_win.more) break;
             if (!ok) s_abort = 1;
             __syncthreads();       // the tables and the barriers are not in use
@@ -819,17 +834,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             // units, segments and phases count from 0 again
             if (tid == 0) {
                 for (int x = 0; x < L::kBars; ++x) mbar_inval(&bars[x]);
-                init_bars<HD>(bars);
+                init_bars<HD>(bars, p.stall);
             }
         }
     }
-    if (!ok) {
-        s_abort = 1;              // the other roles' waits end too
-        __nanosleep(100000);      // copies still in flight land
-    }
+    if (!ok) s_abort = 1;         // the other roles' waits end too
     tc_fence_before_sync();
     __syncthreads();
-    if (tid == 0 && s_abort) p.cut[blockIdx.x].z = -1;   // the merge refuses the call's results
+    if (s_abort) {
+        if (tid == 0) p.cut[blockIdx.x].z = -1;   // the merge refuses the call's results
+        if (warp == kWarpS) {
+            // what is in flight lands before the shared and tensor memory go
+            // (the lanes' own copies have been waited for)
+            constexpr int kTurns = L::kTurns;
+            auto last = [&](uint64_t* of, int i) { settle(&of[i % kTurns], static_cast<uint32_t>((i / kTurns) & 1)); };
+            for (int i = max(0, s_issued.k - kTurns); i < s_issued.k; ++i) last(bars, i);
+            if (s_issued.s > 0) last(bars + 2 * kTurns, s_issued.s - 1);
+            if (s_issued.pv > 0) last(bars + 4 * kTurns, s_issued.pv - 1);
+            __syncwarp();
+        }
+    }
     if (warp == kWarpS) {
         tc_fence_after_sync();
         tmem_dealloc(*tmem_slot, 512);
@@ -852,11 +876,24 @@ int launch_hd(const CUtensorMap& tk, const Kv8Params& p, const Plan& a, cudaStre
 }  // namespace
 
 namespace kv8 {
-int launch_umma(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
+static std::atomic<int> next_stall;   // of pe_test_stall_attention_kv8
+
+int launch_umma(const Kv8Params& params, const Plan& a, int hd, cudaStream_t s) {
     CUtensorMap tk;
+    Kv8Params p = params;
     const int rc = encode_tmap_codes(&tk, p.k_codes, hd, static_cast<uint64_t>(p.num_pages) * p.nkv * kPage);
     if (rc != PE_OK) return rc;
+    if (next_stall.load(std::memory_order_relaxed) != 0) p.stall = next_stall.exchange(0);
     return hd == 128 ? launch_hd<128>(tk, p, a, s) : launch_hd<64>(tk, p, a, s);
 }
 }  // namespace kv8
 }  // namespace pe
+
+extern "C" int pe_test_stall_attention_kv8(int32_t barrier) {
+    if (barrier < pe::kv8::kStallK || barrier > pe::kv8::kStallP) {
+        pe::set_error("barrier must be 1, 2 or 3");
+        return PE_ERR_ARG;
+    }
+    pe::kv8::next_stall.store(barrier);
+    return PE_OK;
+}

@@ -300,3 +300,39 @@ def test_scratch_does_not_follow_the_page_table(K):
     tile = (128 if K > 1 else 8) * (128 + 2)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     assert len(set(need)) == 1 and need[0] <= sms * (2 * tile + 4) + 16
+
+
+# ---------------------------------------------------------------- a wait that gives up
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("barrier,width", [(1, 60), (2, 60), (3, 60), (2, 60000)])
+def test_waits_that_give_up_refuse_the_call_and_leave_the_next_alone(barrier, width, hd):
+    # Host-side injection: a barrier of the tensor-memory kernel waits for one arrival more than there are. Its waits
+    # end after their limit; every request with rows reports it, and all outputs are zero.
+    import time
+
+    rng = np.random.default_rng(barrier + hd)
+    B, K, nq, nkv = 5, 6, 16, 2
+    S, rows = [900, 30, 7, -1, 300], [6, 3, 0, 6, 6]
+    kc, ks = _cache(rng, 80, nkv, hd)
+    vc, vs = _cache(rng, 80, nkv, hd)
+    table = rng.integers(0, 80, (B, width)).astype(np.int32)
+    _, qt = _bf16(rng.standard_normal((B, K, nq, hd)))
+    args = [qt] + [_dev(a) for a in (np.asarray(S, np.int32), table, kc, vc, ks, vs)]
+    rows = _dev(np.asarray(rows, np.int32))
+    clean, status = binding.attention_kv8(*args, rows=rows)
+    assert status.tolist() == [0, 0, 0, binding.PE_REQ_BAD_INPUT, 0] and (clean[0] != 0).any()
+    torch.cuda.synchronize()
+    binding.test_stall_attention_kv8(barrier)
+    few, status = binding.attention_kv8(qt[:, :1, :nkv].contiguous(), *args[1:])   # few rows: another kernel
+    assert (status[[0, 1, 2, 4]] == 0).all()
+    t0 = time.time()
+    out = torch.full_like(qt, 3.0)
+    out, status = binding.attention_kv8(*args, rows=rows, out=out)
+    torch.cuda.synchronize()
+    assert 0.5 < time.time() - t0 < 20.0
+    late = binding.PE_REQ_TIMEOUT
+    assert status.tolist() == [late, late, 0, binding.PE_REQ_BAD_INPUT, late] and (out == 0).all()
+    out, status = binding.attention_kv8(*args, rows=rows)
+    torch.cuda.synchronize()
+    assert status.tolist() == [0, 0, 0, binding.PE_REQ_BAD_INPUT, 0] and torch.equal(out, clean)

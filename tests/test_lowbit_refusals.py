@@ -119,3 +119,8 @@ def test_restatement_of_pages_keeps_every_page_once():
         counts, table, free, F, st = lowbit.release_pages(S, counts, table, free, F, 64)
         held = [p for b in range(6) for p in table[b, :counts[b]]]
         assert sorted(held + free[:F].tolist()) == list(range(64)) and (counts == -(-S // 16)).all()
+
+
+def test_stalls_of_no_barrier(lib):
+    for barrier in (0, 4, -1):
+        assert lib.pe_test_stall_attention_kv8(barrier) == -1
