@@ -52,12 +52,6 @@ constexpr int kMinUnits = kWarps;  // a CTA's share is at least one unit per war
 constexpr int kPad = 32;           // a segment's end in units (B=64, 512..8192 entries: 66 us, with 0 73)
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -485,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of them with nothing to do, took 18.6 us at B=128 K=11). A
 // thread per row and four dimensions; the parts are read eight at a time, all
 // loads of a batch in flight, and folded with a running maximum. Where rows
-// are few and parts many (one long request), SHARE warps take a row together,
-// each a run of its parts, and their sums meet in shared memory.
+// are few and parts many (one long request), SHARE teams of threads take a row
+// together, each a run of its parts, and their sums meet in shared memory.
 constexpr int kMergeThreads = 128;
 constexpr int kMergeBatch = 8;
 constexpr int kMergeBlocks = 16;   // blocks for an SM at most (6 to 40 measure alike)
@@ -695,8 +689,9 @@ int check_shape(int B, int K, int nq, int nkv, int hd, int max_pages) {
 namespace kv8 {
 int launch_merge(const Kv8Params& p, const Plan& a, int hd, cudaStream_t s) {
     const int rows = p.K * (p.nq / p.nkv);
-    // four warps to a row where rows are few (B=1 K=1, 131072 entries: 36.6 us,
-    // one warp 40.9; B=128 K=11: 195 us, one warp 177)
+    // four teams (a warp, of 64-wide heads half of one) to a row where rows are
+    // few (B=1 K=1, 131072 entries: 36.6 us, one team 40.9; B=128 K=11: 195 us,
+    // one team 177)
     const bool share = static_cast<long long>(p.B) * p.nkv * rows <= 1024;
     const int block_rows = std::max(1, kMergeThreads / (hd / 4) / (share ? 4 : 1));
     const long long runs = std::min<long long>(a.grid - 1, static_cast<long long>(p.B) * p.nkv);   // cut ones at most

@@ -308,7 +308,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int r = row + x * kPass;
-            to[x] = smem_u32(sm + L::kKRing) + row * HD + ((HD == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+            to[x] = smem_u32(sm + L::kKRing) + row * HD + ((c ^ ((r >> 1) & 3)) << 4);   // (64 wide)
         }
         const int first = warp - kWarpK;
         for (int i = first; i < n + 2 * kBehind; i += 2) {
@@ -879,10 +879,12 @@ namespace kv8 {
 static std::atomic<int> next_stall;   // of pe_test_stall_attention_kv8
 
 int launch_umma(const Kv8Params& params, const Plan& a, int hd, cudaStream_t s) {
-    CUtensorMap tk;
+    CUtensorMap tk{};   // 64-wide heads: not read
     Kv8Params p = params;
-    const int rc = encode_tmap_codes(&tk, p.k_codes, hd, static_cast<uint64_t>(p.num_pages) * p.nkv * kPage);
-    if (rc != PE_OK) return rc;
+    if (hd == 128) {
+        const int rc = encode_tmap_codes(&tk, p.k_codes, static_cast<uint64_t>(p.num_pages) * p.nkv * kPage);
+        if (rc != PE_OK) return rc;
+    }
     if (next_stall.load(std::memory_order_relaxed) != 0) p.stall = next_stall.exchange(0);
     return hd == 128 ? launch_hd<128>(tk, p, a, s) : launch_hd<64>(tk, p, a, s);
 }

@@ -31,9 +31,9 @@ int encode_tmap_2d(CUtensorMap* map, const void* base, int dtype, uint64_t inner
 // the same over one-byte elements (FP8 weight codes)
 int encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
 
-// 8-bit KV cache codes as [lines][hd] bytes (16 lines per page and head); box =
-// one page of one head, swizzled over the row's hd bytes
-int encode_tmap_codes(CUtensorMap* map, const void* codes, int hd, uint64_t lines);
+// 8-bit KV cache codes of 128-wide heads as [lines][128] bytes (16 lines per
+// page and head); box = one page of one head, swizzled over the row's 128 bytes
+int encode_tmap_codes(CUtensorMap* map, const void* codes, uint64_t lines);
 
 // ---------------------------------------------------------------- GEMM
 
@@ -292,14 +292,6 @@ __host__ __device__ inline size_t attn_piece_floats(int Rq, int hd) {
     return static_cast<size_t>(Rq) * hd + 2 * static_cast<size_t>((Rq + 3) & ~3);
 }
 int encode_tmap_q(CUtensorMap* map, const void* q, int hd, int nq, int rows, int G, int K);
-
-// ---------------------------------------------------------------- 8-bit KV cache
-
-// new rows k, v [B, n_max, nkv, hd] bf16 (row strides ld_k, ld_v) into the cache
-int launch_kv8_append(int B, int n_max, int nkv, int hd, const void* k, const void* v, int64_t ld_k, int64_t ld_v,
-                      const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table, int max_pages,
-                      int num_pages, uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale,
-                      int32_t* status, cudaStream_t s, bool pdl);
 
 // ---------------------------------------------------------------- verify
 

@@ -41,20 +41,13 @@ struct AppendParams {
     int32_t* status;
 };
 
-// the exponent of the smallest power of two s >= 2^-126 with amax <= 448 s
+// the smallest power of two s >= 2^-126 with amax <= 448 s
 __device__ __forceinline__ float scale_for(float amax) {
     const uint32_t u = __float_as_uint(amax);
     // amax = 2^(E-127) * 1.m; 448 = 1.75 * 2^8
     int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     e = max(e, 1);
     return __uint_as_float(static_cast<uint32_t>(e) << 23);
-}
-
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
 __device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
@@ -166,38 +159,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const AppendParams p
 }
 
 }  // namespace
-
-int launch_kv8_append(int B, int n_max, int nkv, int hd, const void* k, const void* v, int64_t ld_k, int64_t ld_v,
-                      const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table, int max_pages,
-                      int num_pages, uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale,
-                      int32_t* status, cudaStream_t s, bool pdl) {
-    AppendParams p{};
-    p.B = B;
-    p.n_max = n_max;
-    p.nkv = nkv;
-    p.P = (n_max + kPage - 2) / kPage + 1;
-    p.max_pages = max_pages;
-    p.num_pages = num_pages;
-    p.x[0] = static_cast<const __nv_bfloat16*>(k);
-    p.x[1] = static_cast<const __nv_bfloat16*>(v);
-    p.ld[0] = ld_k;
-    p.ld[1] = ld_v;
-    p.seq_lens = seq_lens;
-    p.rows = rows;
-    p.page_table = page_table;
-    p.codes[0] = k_codes;
-    p.codes[1] = v_codes;
-    p.scale[0] = k_scale;
-    p.scale[1] = v_scale;
-    p.status = status;
-    const long long units = 2ll * B * p.P * nkv;
-    const long long blocks = (units + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFFll) { set_error("pe_kv8_append: too many rows for one call"); return PE_ERR_ARG; }
-    auto kern = hd == 128 ? k_kv8_append<128> : k_kv8_append<64>;
-    PE_CUDA_TRY(launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, s, pdl, p));
-    return PE_OK;
-}
-
 }  // namespace pe
 
 using namespace pe;
@@ -227,6 +188,30 @@ extern "C" int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, 
         set_error("k and v must be 8-byte aligned, the code arrays 16-byte aligned");
         return PE_ERR_ARG;
     }
-    return launch_kv8_append(B, n_max, nkv, hd, k, v, ld_k, ld_v, seq_lens, rows, page_table, max_pages, num_pages,
-                             k_codes, v_codes, k_scale, v_scale, status, static_cast<cudaStream_t>(stream), false);
+    AppendParams p{};
+    p.B = B;
+    p.n_max = n_max;
+    p.nkv = nkv;
+    p.P = (n_max + kPage - 2) / kPage + 1;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.x[0] = static_cast<const __nv_bfloat16*>(k);
+    p.x[1] = static_cast<const __nv_bfloat16*>(v);
+    p.ld[0] = ld_k;
+    p.ld[1] = ld_v;
+    p.seq_lens = seq_lens;
+    p.rows = rows;
+    p.page_table = page_table;
+    p.codes[0] = k_codes;
+    p.codes[1] = v_codes;
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.status = status;
+    const long long units = 2ll * B * p.P * nkv;
+    const long long blocks = (units + kWarps - 1) / kWarps;
+    if (blocks > 0x7FFFFFFFll) { set_error("pe_kv8_append: too many rows for one call"); return PE_ERR_ARG; }
+    auto kern = hd == 128 ? k_kv8_append<128> : k_kv8_append<64>;
+    PE_CUDA_TRY(launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), false,
+                          p));
+    return PE_OK;
 }

@@ -150,18 +150,18 @@ int encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64
     return PE_OK;
 }
 
-int encode_tmap_codes(CUtensorMap* map, const void* codes, int hd, uint64_t lines) {
+int encode_tmap_codes(CUtensorMap* map, const void* codes, uint64_t lines) {
     EncodeTiledFn fn = get_encode_fn();
     if (fn == nullptr) {
         set_error("cuTensorMapEncodeTiled entry point not available");
         return PE_ERR_CUDA;
     }
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(hd), lines};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(hd)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(hd), 16};
+    cuuint64_t dims[2] = {128, lines};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, 16};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled (KV codes) failed with code " + std::to_string(static_cast<int>(r)));
