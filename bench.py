@@ -727,7 +727,7 @@ def bench_ours(args):
 def read_profile_traffic(kernel, workload):
     """DRAM bytes per launch of `kernel` from the committed ncu summary
     profiles/traffic_<kernel>_<workload>.md, if that summary was taken on the
-    current kernel sources (its source_hash line); else None."""
+    current sources of that kernel (its source_hash line); else None."""
     path = os.path.join(ROOT, "profiles", f"traffic_{kernel}_{workload}.md")
     if not os.path.exists(path):
         return None
@@ -737,7 +737,7 @@ def read_profile_traffic(kernel, workload):
             if ":" in line and line.strip().startswith(("source_hash", "dram_bytes_per_launch")):
                 k, v = line.split(":", 1)
                 fields[k.strip()] = v.strip().strip("`")
-    if fields.get("source_hash") != kernel_source_hash():
+    if fields.get("source_hash") != kernel_source_hash(unit=PROFILED_UNITS.get(kernel)):
         return None
     try:
         return float(fields["dram_bytes_per_launch"])
@@ -745,22 +745,36 @@ def read_profile_traffic(kernel, workload):
         return None
 
 
-def kernel_source_hash(csrc=None):
-    """Hash of the kernel sources (all of csrc) with comments and whitespace
-    removed: a comment edit does not change the kernels the profile counters
-    were taken on, any code edit does."""
+# the translation unit of a profiled kernel
+PROFILED_UNITS = {"lm_head": "gemm.cu"}
+
+
+def kernel_source_hash(csrc=None, unit=None):
+    """Hash of the kernel sources with comments and whitespace removed: a
+    comment edit does not change the kernels the profile counters were taken
+    on, any code edit does. unit: that source and what it includes (csrc's own
+    files); None: all of csrc."""
     import hashlib
     import re
     h = hashlib.sha256()
     csrc = csrc or os.path.join(ROOT, "speculative_drafting_pe_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(csrc, name), encoding="utf-8") as f:
-                text = f.read()
-            text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
-            text = re.sub(r"//[^\n]*", " ", text)
-            text = re.sub(r"\s+", " ", text).strip()
-            h.update(name.encode() + b"\0" + text.encode())
+    names = {n for n in os.listdir(csrc) if n.endswith((".cu", ".cuh", ".h"))}
+    if unit is not None:
+        found, todo = set(), [unit]
+        while todo:
+            name = todo.pop()
+            if name in names and name not in found:
+                found.add(name)
+                with open(os.path.join(csrc, name), encoding="utf-8") as f:
+                    todo += re.findall(r'^\s*#\s*include\s+"([^"]+)"', f.read(), flags=re.M)
+        names = found
+    for name in sorted(names):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            text = f.read()
+        text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)
+        text = re.sub(r"//[^\n]*", " ", text)
+        text = re.sub(r"\s+", " ", text).strip()
+        h.update(name.encode() + b"\0" + text.encode())
     return h.hexdigest()[:16]
 
 

@@ -20,8 +20,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
-#include "internal.h"
+#include "lowbit.cuh"
 
 namespace pe {
 namespace kv8 {

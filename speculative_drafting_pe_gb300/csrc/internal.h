@@ -1,7 +1,6 @@
 // Internal declarations shared by the libpe.so translation units.
 #pragma once
 
-#include <atomic>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -30,10 +29,6 @@ int encode_tmap_2d(CUtensorMap* map, const void* base, int dtype, uint64_t inner
                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
 // the same over one-byte elements (FP8 weight codes)
 int encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
-
-// 8-bit KV cache codes of 128-wide heads as [lines][128] bytes (16 lines per
-// page and head); box = one page of one head, swizzled over the row's 128 bytes
-int encode_tmap_codes(CUtensorMap* map, const void* codes, uint64_t lines);
 
 // ---------------------------------------------------------------- GEMM
 
@@ -346,31 +341,6 @@ cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-// Multiprocessors of the current device. The driver is asked once per device:
-// a call that is a launch of a few microseconds waits for such questions.
-inline int current_device(int* dev, int* sms) {
-    static std::atomic<int> known[64];
-    PE_CUDA_TRY(cudaGetDevice(dev));
-    const bool kept = *dev >= 0 && *dev < 64;
-    *sms = kept ? known[*dev].load(std::memory_order_relaxed) : 0;
-    if (*sms == 0) {
-        PE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev));
-        if (kept) known[*dev].store(*sms, std::memory_order_relaxed);
-    }
-    return PE_OK;
-}
-// Lets a kernel have `bytes` of dynamic shared memory (the same in every call)
-// on device dev; likewise.
-template <auto kern>
-int allow_smem(int dev, int bytes) {
-    static std::atomic<bool> done[64];
-    const bool kept = dev >= 0 && dev < 64;
-    if (kept && done[dev].load(std::memory_order_relaxed)) return PE_OK;
-    PE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    if (kept) done[dev].store(true, std::memory_order_relaxed);
-    return PE_OK;
 }
 
 }  // namespace pe

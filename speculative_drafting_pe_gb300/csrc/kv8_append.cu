@@ -20,8 +20,7 @@
 // look the request's others up as well).
 #include <cuda_fp16.h>
 
-#include "common.cuh"
-#include "internal.h"
+#include "lowbit.cuh"
 
 namespace pe {
 namespace {

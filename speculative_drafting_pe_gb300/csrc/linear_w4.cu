@@ -35,8 +35,7 @@
 // rows 7.8 us.
 #include <cuda_fp16.h>
 
-#include "common.cuh"
-#include "internal.h"
+#include "lowbit.cuh"
 
 namespace pe {
 namespace {

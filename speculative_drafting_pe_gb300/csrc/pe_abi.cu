@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "lowbit.cuh"
 
 struct pe_handle {
     pe_config cfg;                // dtype is the activation dtype (bf16 for an FP8-weight drafter)

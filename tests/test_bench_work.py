@@ -3,6 +3,7 @@ roofline divides by, the kernel-source hash that decides whether a profile's
 DRAM counters still apply, and the benchmark's options."""
 
 import dataclasses
+import os
 
 import pytest
 
@@ -70,6 +71,22 @@ def test_source_hash_ignores_comments_and_whitespace(tmp_path):
     assert bench.kernel_source_hash(str(tmp_path)) == h0
     src.write_text("__global__ void k(int* x) { x[0] = 2; }\n")
     assert bench.kernel_source_hash(str(tmp_path)) != h0
+
+
+def test_source_hash_of_a_unit_follows_what_it_includes(tmp_path):
+    (tmp_path / "a.cu").write_text('#include <cstdint>\n#include "x.cuh"\nint a;\n')
+    (tmp_path / "x.cuh").write_text('#include "y.h"\nint x;\n')
+    (tmp_path / "y.h").write_text("int y;\n")
+    h0 = bench.kernel_source_hash(str(tmp_path), unit="a.cu")
+    (tmp_path / "b.cu").write_text("int b;\n")          # another kernel
+    assert bench.kernel_source_hash(str(tmp_path), unit="a.cu") == h0
+    (tmp_path / "y.h").write_text("int y = 1;\n")
+    assert bench.kernel_source_hash(str(tmp_path), unit="a.cu") != h0
+
+
+def test_profiled_units_are_sources():
+    for unit in bench.PROFILED_UNITS.values():
+        assert os.path.exists(os.path.join(bench.ROOT, "speculative_drafting_pe_gb300", "csrc", unit))
 
 
 def test_max_prefix_option_caps_both_ends():
