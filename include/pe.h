@@ -354,7 +354,7 @@ int pe_linear_noalloc(int32_t dtype, int32_t M, int32_t N, int32_t Kd, const voi
  * x that holds an infinity or NaN gives infinities or NaN in its row of y, and
  * in no other. No scratch; the device that holds the tensors must be current.
  * Rows of x go 8 or 16 at a time, and each of these reads and decodes the
- * weights again; N <= 524280. */
+ * weights again: from some 32 rows on pe_linear_fp8 is quicker. N <= 524280. */
 int pe_linear_w4(int32_t M, int32_t N, int32_t Kd, int32_t group, const uint8_t* w, int32_t scale_dtype,
                  const void* w_scale, const uint8_t* w_zero, const void* x, int64_t ld_x, float* y, int64_t ld_y,
                  void* stream);
@@ -407,8 +407,10 @@ int pe_release_pages(int32_t B, const int32_t* keep_lens, const int32_t* page_co
  * the nearest (ties to even). A page with committed entries keeps its scale if
  * that is larger; if not, their codes are moved to the new one. Infinities
  * become +-448, a NaN the NaN code. Nothing else of the cache is touched;
- * codes behind the last new row keep their bytes. Pages that two requests
- * share must be full: two that append to one page race.
+ * codes behind the last new row keep their bytes. A page never returns to a
+ * smaller scale while it has committed entries, also where the larger one came
+ * from rows that were rejected since. Pages that two requests share, or that
+ * stand in a row of the table twice, must be full: two appends to one page race.
  * k, v 8-byte aligned, ld_k and ld_v multiples of 4, codes 16-byte aligned. */
 int pe_kv8_append(int32_t B, int32_t n_max, int32_t nkv, int32_t hd, const void* k, int64_t ld_k, const void* v,
                   int64_t ld_v, const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table,

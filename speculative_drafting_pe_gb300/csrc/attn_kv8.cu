@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_kv8_merge(const Kv8Params p, 
 // Query rows of a head from which the tensor-memory kernel is taken; it reads
 // the cache once for up to 128 rows, but its unit takes as long for few. 64
 // requests: 16 rows of 128-wide heads 87 us, by the register kernel 90, 8 rows
-// 86 and 65; 16 rows of 64-wide heads 82 and 60.
+// 86 and 65; 16 rows of 64-wide heads 82 and 60 (as both were then; 89, 65, 62 now).
 constexpr int umma_from(int hd) { return hd == 64 ? 17 : 9; }
 
 int plan_kv8(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {

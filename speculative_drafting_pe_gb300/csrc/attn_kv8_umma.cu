@@ -6,8 +6,8 @@
 // Roles (512 threads):
 //   warps 14,15 the unit's K pages to where the MMA reads them (the swizzle of
 //               a K-major operand), and the page scales. 128-wide heads: warp
-//               14 by TMA, a lane per page; 64-wide ones: both warps in turn by
-//               asynchronous copies. A box of 16 rows takes about 150 cycles
+//               14 the codes by TMA, a lane per page, warp 15 the scales;
+//               64-wide ones: both warps in turn by asynchronous copies. A box of 16 rows takes about 150 cycles
 //               whatever its rows hold, a copy instruction always 512 bytes
 //               (128 wide: 181 us by boxes, 192 by copies; 64 wide: 85 and 80)
 //   warps 8-11  converters, kTeam warps to a unit. Each thread fetches 16-byte
@@ -51,8 +51,8 @@
 // then, 128-wide ones 250 for 190), a third softmax group for 64-wide heads
 // (100 for 87) and scores of two units in one product (242 for 235) did not
 // help. 128 requests of 512 to 8192 entries, 11 rows of 8 heads to each of 4
-// of 128: 177 us, 3.4 TB/s, 50% of the measured copy; 64 of 1024 to 4096, up
-// to 10 rows of 8 heads to each of 8 of 64: 79 us, 30%.
+// of 128: 181 us, 3.3 TB/s, 49% of the measured copy; 64 of 1024 to 4096, up
+// to 10 rows of 8 heads to each of 8 of 64: 81 us, 29%.
 #include "attn_kv8.cuh"
 
 namespace pe {

@@ -16,7 +16,7 @@
 // page and nothing is read twice. Bound by latency: lengths, then page and
 // rows together, then committed codes and scale. 8 rows of 32 requests, 4 heads
 // of 128, take 3.4 us (with the rows behind the pages 5.0); 8 prompts of up to
-// 2048 rows, 8 heads of 64, 5.7 us, 1.2 TB/s (7.6 where warps without a page
+// 2048 rows, 8 heads of 64, 6.0 us, 1.2 TB/s (7.6 where warps without a page
 // look the request's others up as well).
 #include <cuda_fp16.h>
 
