@@ -302,6 +302,43 @@ def test_scratch_does_not_follow_the_page_table(K):
     assert len(set(need)) == 1 and need[0] <= sms * (2 * tile + 4) + 16
 
 
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+def test_thousands_of_short_requests(K, nq, nkv, hd):
+    # segments of one unit, dozens of them to a CTA
+    rng = np.random.default_rng(nq)
+    S = rng.integers(0, 70, 40)
+    kc, ks = _cache(rng, 60, nkv, hd)
+    vc, vs = _cache(rng, 60, nkv, hd)
+    table = rng.integers(0, 60, (40, 5)).astype(np.int32)
+    qx, qt = _bf16(rng.standard_normal((40, K, nq, hd)))
+    ref, lim, _ = _exact(qx, S, table, kc, vc, ks, vs, hd ** -0.5)
+    _check_copies(qt, S, table, kc, vc, ks, vs, 100, ref, lim)
+
+
+@pytest.mark.parametrize("B,K,nq,nkv,hd,S,width", [(3, 1, 8, 8, 128, 900, 30000), (8, 1, 8, 8, 128, 40000, 2600),
+                                                   (8, 5, 16, 8, 64, 300, 30000), (16, 5, 16, 8, 128, 36000, 2300)])
+def test_windows_replayed_from_a_graph(B, K, nq, nkv, hd, S, width):
+    # tables with room for more than a CTA's, with and without that many entries
+    rng = np.random.default_rng(B)
+    kc, ks = _cache(rng, 100, nkv, hd)
+    vc, vs = _cache(rng, 100, nkv, hd)
+    table = _dev(rng.integers(0, 100, (B, width)).astype(np.int32))
+    lens = _dev(np.full(B, S, np.int32))
+    q = _bf16(rng.standard_normal((B, K, nq, hd)))[1]
+    cache = [_dev(a) for a in (kc, vc, ks, vs)]
+    want, status = binding.attention_kv8(q, lens, table, *cache)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, _ = binding.attention_kv8(q, lens, table, *cache)
+    for _ in range(5):
+        got.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and (status == 0).all()
+    narrow, _ = binding.attention_kv8(q, lens, table[:, :-(-(S + K) // PAGE)].contiguous(), *cache)
+    assert torch.equal(narrow, want)
+
+
 # ---------------------------------------------------------------- a wait that gives up
 
 @pytest.mark.parametrize("hd", [64, 128])
