@@ -451,6 +451,74 @@ int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
                      const float* k_scale, const float* v_scale, float scale, void* out, int64_t ld_out, float* ws,
                      int64_t ws_floats, int32_t* status, void* stream);
 
+/* A paged KV cache in 4 bits, about half the bytes of the 8-bit one:
+ *  k_codes, v_codes   [num_pages][nkv][16][hd/2] uint8: code n (0..15) of dimension 2i in the low half of byte i, of
+ *                     2i+1 in the high half
+ *  k_params, v_params [num_pages][nkv][16][2] bf16: scale and base of an entry; value = base + scale * n
+ * One layer's cache; the layers of a model are as many of them.
+ *
+ * pe_kv4_append turns new query and key rows to their positions and stores
+ * keys and values: rows[b] (NULL: n_max) new rows of request b at its entries
+ * S_b, S_b+1, ...
+ *  q, k, v [B, n_max, heads, hd] bf16, rows ld_* elements apart (columns of a
+ *          fused projection's output will do); rows past rows[b] are not read.
+ *          n_q_heads may be 0 (q and q_out are then not read)
+ *  rope_theta: row j of request b has position p = positions[b] + j (positions
+ *          NULL: S_b + j), and dimensions i and i + hd/2 of a head of q or k turn
+ *          by p * rope_theta^(-2i/hd); 0: nothing is turned. Otherwise at least 1
+ *  q_out   [B, n_max, nq, hd] bf16 OUT, rows ld_q_out apart (may be q itself):
+ *          the turned queries; zero past rows[b] and in requests that are not OK
+ *  status  [B] OUT; a request that is not OK writes nothing else.
+ *          PE_REQ_BAD_INPUT: a length or position below 0 or rows[b] above n_max
+ * Of the values x of a head of a row: base = bf16(min x), scale = bf16((max x -
+ * base) / 15), n the nearest (ties to even) to (x - base) / scale in 0..15, 0
+ * where scale is 0. A turned key is not rounded before. Angles are exact to
+ * 2^-31 of a turn at every position. A head of a row that holds an infinity or
+ * NaN, or magnitudes beyond 2^126, stands as NaN (scale and base). An entry
+ * depends on its row alone; nothing else of the cache is touched.
+ * q, k, v and q_out 8-byte aligned, their strides multiples of 4, the cache's
+ * arrays 16-byte aligned. */
+int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,
+                  int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v, float rope_theta,
+                  const int32_t* positions, const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table,
+                  int32_t max_pages, int32_t num_pages, uint8_t* k_codes, uint8_t* v_codes, void* k_params,
+                  void* v_params, void* q_out, int64_t ld_q_out, int32_t* status, void* stream);
+
+/* Attention of the K rows of each request over that cache, with the arguments
+ * of pe_attention_kv8 (k_params and v_params in the place of the scales, the
+ * cache's arrays 16-byte aligned) and its rules for rows, masks, scratch (of
+ * pe_attention_kv4_scratch floats), pages and status.
+ * Entries that no row sees may hold anything. An entry whose parameters are not
+ * finite makes the rows that see it NaN, and no other row. A row of q that
+ * holds an infinity or a NaN is NaN. */
+int pe_attention_kv4_scratch(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             int32_t max_pages, int64_t* ws_floats);
+int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,
+                     int64_t ld_q, const int32_t* seq_lens, const int32_t* rows, const int32_t* page_table,
+                     int32_t max_pages, int32_t num_pages, const uint8_t* k_codes, const uint8_t* v_codes,
+                     const void* k_params, const void* v_params, float scale, void* out, int64_t ld_out, float* ws,
+                     int64_t ws_floats, int32_t* status, void* stream);
+
+/* What rows of logits say of given tokens (beside pe_sample_drafts and
+ * pe_verify_stochastic): with p = softmax(logits / temperature) of a row,
+ *  logits       [R, V] bf16 or fp32 (dtype: PE_DTYPE_BF16 or PE_DTYPE_FP32), rows ld elements apart
+ *               (0: one row, of which several tokens are asked)
+ *  tokens       [R] int32
+ *  logprobs     [R] fp32 OUT: ln p[tokens[r]] (NaN for a token outside [0, V))
+ *  entropy      [R] fp32 OUT or NULL: -sum p ln p
+ *  top_tokens   [R, top] int32 OUT, top_logprobs [R, top] fp32 OUT: the top
+ *               likeliest tokens in order, of equal ones the lower index first
+ *               (top 0..32, at most V; NULL where it is 0), and ln p of each
+ * A logit of -inf is a token that cannot be (ln p = -inf, and it adds nothing to
+ * the entropy); -FLT_MAX is one like any other (ln p below fp32's range is -inf). A row that holds a NaN or +inf,
+ * or only -inf, has no probabilities: NaN in the place of each, NaN logits
+ * ordered behind all others. Finite logits have magnitudes up to 2^126 or are
+ * -FLT_MAX; the temperature is positive, 2^64 at most. Sums in fp32, each weight
+ * off by about 2^-22 of itself. */
+int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void* logits, int64_t ld, const int32_t* tokens,
+                      float temperature, float* logprobs, float* entropy, int32_t top, int32_t* top_tokens,
+                      float* top_logprobs, void* stream);
+
 /* One whole step (pe_draft, then pe_verify_rebuild on its drafts) captured
  * once into a CUDA graph and replayed with a single launch. The arguments are
  * those of pe_draft and pe_verify_rebuild (drafts are shared; draft_status and

@@ -30,6 +30,7 @@ EXPORTS = (
     "pe_sample_drafts", "pe_verify_stochastic",
     "pe_linear_w4", "pe_assign_pages", "pe_release_pages", "pe_kv8_append", "pe_attention_kv8_scratch",
     "pe_attention_kv8", "pe_test_stall_attention_kv8",
+    "pe_kv4_append", "pe_attention_kv4_scratch", "pe_attention_kv4", "pe_token_logprobs",
 )
 KERNEL_KINDS = ("fc", "row_build", "rmsnorm", "qkv", "attention", "o_proj", "gate_up", "down", "lm_head", "argmax",
                 "layer_chain")
@@ -157,6 +158,12 @@ def load():
             ("pe_release_pages", [_i32] + [_vp] * 4 + [_i32] * 2 + [_vp, _i32] + [_vp] * 4),
             ("pe_kv8_append", [_i32] * 4 + [_vp, _i64, _vp, _i64] + [_vp] * 3 + [_i32] * 2 + [_vp] * 6),
             ("pe_attention_kv8_scratch", [_i32] * 6 + [ctypes.POINTER(_i64)]),
+            ("pe_kv4_append", [_i32] * 5 + [_vp, _i64] * 3 + [ctypes.c_float] + [_vp] * 4 + [_i32] * 2 + [_vp] * 5 +
+             [_i64, _vp, _vp]),
+            ("pe_attention_kv4_scratch", [_i32] * 6 + [ctypes.POINTER(_i64)]),
+            ("pe_attention_kv4", [_i32] * 5 + [_vp, _i64] + [_vp] * 3 + [_i32] * 2 + [_vp] * 4 +
+             [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp]),
+            ("pe_token_logprobs", [_i32] * 3 + [_vp, _i64, _vp, ctypes.c_float, _vp, _vp, _i32, _vp, _vp, _vp]),
             ("pe_test_stall_attention_kv8", [_i32]),
             ("pe_attention_kv8", [_i32] * 5 + [_vp, _i64, _vp, _vp, _vp, _i32, _i32] + [_vp] * 4 +
              [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp])):
@@ -788,6 +795,135 @@ def attention_kv8(q, seq_lens, page_table, k_codes, v_codes, k_scale, v_scale, s
          hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out, "out"), ws.data_ptr(), need,
          status.data_ptr())
     return out, status
+
+
+def _check_kv4(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_params, v_params):
+    """The paged 4-bit cache of a call; returns its number of pages."""
+    _need_is("seq_lens", seq_lens, _INT, dev, (B,))
+    if rows is not None:
+        _need_is("rows", rows, _INT, dev, (B,))
+    _need_is("page_table", page_table, _INT, dev, (B, page_table.shape[-1]))
+    pages = k_codes.shape[0]
+    codes, params = (pages, nkv, 16, hd // 2), (pages, nkv, 16, 2)
+    _need_is("k_codes", k_codes, _BYTE, dev, codes)
+    _need_is("v_codes", v_codes, _BYTE, dev, codes)
+    _need_is("k_params", k_params, _BF16, dev, params)
+    _need_is("v_params", v_params, _BF16, dev, params)
+    return pages
+
+
+def kv4_append(k, v, seq_lens, page_table, k_codes, v_codes, k_params, v_params, rows=None, theta=0.0, positions=None,
+               q=None, q_out=None, status=None, stream=None):
+    """Turn new rows q [B, n, nq, hd] and k [B, n, nkv, hd] (bf16) to their positions and store k and v in the 4-bit
+    paged cache at entries seq_lens[b] ... Returns (q_out like q, or None without q; status [B]).
+
+    Rows may be strided (columns of a fused projection). rows [B] int32: new
+    rows of each request (None: n); q_out is zero behind them. theta: base of
+    the rotation (0: none). positions [B] int32: position of each request's
+    first row (None: seq_lens). Codes uint8 [pages, nkv, 16, hd / 2], their
+    scale and base bf16 [pages, nkv, 16, 2], updated in place. q_out may be q."""
+    lib = load()
+    dev = k.device
+    B, n, nkv, hd = k.shape
+    if k.dtype is not _BF16 or v.dtype is not _BF16 or v.device != dev or v.shape != k.shape:
+        raise ValueError(f"k and v must be bfloat16 [B, n, nkv, hd] on {dev}")
+    pages = _check_kv4(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_params, v_params)
+    if positions is not None:
+        _need_is("positions", positions, _INT, dev, (B,))
+    nq, ld_q, ld_out = 0, 0, 0
+    if q is not None:
+        nq = q.shape[2] if q.dim() == 4 else 0
+        if q.dtype is not _BF16 or q.device != dev or q.shape != (B, n, nq, hd) or nq < 1:
+            raise ValueError(f"q must be bfloat16 [B, n, nq, hd] on {dev}")
+        if q_out is None:
+            q_out = _empty((B, n, nq, hd), _BF16, dev, stream)
+        elif q_out.dtype is not _BF16 or q_out.device != dev or q_out.shape != q.shape:
+            raise ValueError(f"q_out must be bfloat16 {tuple(q.shape)} on {dev}")
+        ld_q, ld_out = _row_stride(q, "q"), _row_stride(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if status is None:
+        status = _like(seq_lens, stream)
+    else:
+        _need_is("status", status, _INT, dev, (B,))
+    _run(lib.pe_kv4_append, dev, stream, B, n, nq, nkv, hd, None if q is None else q.data_ptr(), ld_q, k.data_ptr(),
+         _row_stride(k, "k"), v.data_ptr(), _row_stride(v, "v"), theta,
+         None if positions is None else positions.data_ptr(), seq_lens.data_ptr(),
+         None if rows is None else rows.data_ptr(), page_table.data_ptr(), page_table.shape[1], pages,
+         k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr(),
+         None if q is None else q_out.data_ptr(), ld_out, status.data_ptr())
+    return q_out, status
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_scratch(index, B, K, nq, nkv, hd, max_pages):
+    """Floats of scratch of an attention call over the 4-bit cache on device `index`."""
+    n = ctypes.c_int64(0)
+    with torch.cuda.device(index):
+        _check(load().pe_attention_kv4_scratch(B, K, nq, nkv, hd, max_pages, ctypes.byref(n)))
+    return n.value
+
+
+def attention_kv4(q, seq_lens, page_table, k_codes, v_codes, k_params, v_params, scale=None, rows=None, out=None,
+                  status=None, stream=None):
+    """Attention of q [B, K, nq, hd] bf16 over the 4-bit paged cache: row j of request b sees entries
+    0 .. seq_lens[b] + j (append its own row first). Returns (out like q, status [B]).
+
+    scale: softmax scale (None: hd ** -0.5). rows [B] int32: live rows of each
+    request (None: K); the others are zero."""
+    lib = load()
+    dev = q.device
+    B, K, nq, hd = q.shape
+    if q.dtype is not _BF16:
+        raise ValueError("q must be bfloat16 [B, K, nq, hd]")
+    nkv = k_codes.shape[1] if k_codes.dim() == 4 else 0
+    pages = _check_kv4(dev, B, nkv, hd, seq_lens, rows, page_table, k_codes, v_codes, k_params, v_params)
+    if out is None:
+        out = _empty((B, K, nq, hd), _BF16, dev, stream)
+    elif out.dtype is not _BF16 or out.device != dev or out.shape != q.shape:
+        raise ValueError(f"out must be bfloat16 {tuple(q.shape)} on {dev}")
+    if status is None:
+        status = _like(seq_lens, stream)
+    else:
+        _need_is("status", status, _INT, dev, (B,))
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {dev}")
+    max_pages = page_table.shape[1]
+    need = _kv4_scratch(dev.index, B, K, nq, nkv, hd, max_pages)
+    ws = _empty(need, _FLOAT, dev, stream)
+    _run(lib.pe_attention_kv4, dev, stream, B, K, nq, nkv, hd, q.data_ptr(), _row_stride(q, "q"),
+         seq_lens.data_ptr(), None if rows is None else rows.data_ptr(), page_table.data_ptr(), max_pages, pages,
+         k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(), v_params.data_ptr(),
+         hd ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out, "out"), ws.data_ptr(), need,
+         status.data_ptr())
+    return out, status
+
+
+def token_logprobs(logits, tokens, top=0, temperature=1.0, stream=None):
+    """What logits [..., V] (bf16 or fp32; rows may be strided) say of tokens [...] int32, at a temperature.
+
+    Returns a dict of tensors: logprobs [...] and entropy [...] fp32,
+    top_tokens [..., top] int32 and top_logprobs [..., top] fp32, the top
+    likeliest tokens in order (equal ones by index) and theirs."""
+    lib = load()
+    dev = logits.device
+    kind = logits.dtype
+    if kind is not _BF16 and kind is not _FLOAT:
+        raise ValueError("logits must be bfloat16 or float32")
+    if logits.dim() < 2:
+        raise ValueError("logits must be [..., V]")
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    _need_is("tokens", tokens, _INT, dev, lead)
+    if not 0 <= top <= 32:
+        raise ValueError("top must lie in 0..32")
+    R = tokens.numel()
+    ld = V if logits.is_contiguous() else _row_stride(logits if logits.dim() == 2 else logits.unsqueeze(-2), "logits")
+    logprobs, entropy = _empty(lead, _FLOAT, dev, stream), _empty(lead, _FLOAT, dev, stream)
+    ids, best = _empty((*lead, top), _INT, dev, stream), _empty((*lead, top), _FLOAT, dev, stream)
+    _run(lib.pe_token_logprobs, dev, stream, R, V, PE_DTYPE_BF16 if kind is _BF16 else PE_DTYPE_FP32,
+         logits.data_ptr(), ld, tokens.data_ptr(), temperature, logprobs.data_ptr(), entropy.data_ptr(), top,
+         ids.data_ptr() if top else None, best.data_ptr() if top else None)
+    return dict(logprobs=logprobs, entropy=entropy, top_tokens=ids, top_logprobs=best)
 
 
 def test_stall_attention_kv8(barrier):

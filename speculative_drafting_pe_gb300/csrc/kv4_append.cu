@@ -1,0 +1,284 @@
+// The write side of the 4-bit paged KV cache (pe_kv4_append): new query and key
+// rows are turned to their positions, keys and values become 4-bit codes with
+// a scale and a base for each (entry, kv head), queries go back in bf16.
+//
+//   (a_i, b_i) = (x_i, x_{i+hd/2}) -> (a cos - b sin, b cos + a sin), angle p * theta^(-2i/hd)
+//   base = bf16(min x), scale = bf16((max x - base) / 15), code = rn((x - base) / scale) in 0..15
+//
+// over the values x of one head of one row. An entry's codes depend on its row
+// alone, so an append never touches an entry that is there, and what is
+// written does not depend on how the rows came in calls.
+//
+// The angle is p times a frequency that is held as a fraction of a turn in 64
+// bits: the product's lower half is the turn's remainder for every position,
+// without a double on the device (FP64 runs at a few operations a cycle and
+// SM). Its first 24 bits go through sincospif, the rest is a first-order term.
+//
+// A CTA takes `block` rows of one request, a warp a head of a row at a time (two
+// 64-wide ones): four values a lane, 8-byte loads, kBatch heads in flight. The
+// rows' sines and cosines are computed once, for all heads.
+#include <cmath>
+#include <cuda_fp16.h>
+
+#include "lowbit.cuh"
+
+namespace pe {
+namespace {
+
+constexpr int kPage = 16;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBatch = 4;        // heads of a warp whose loads are in flight together
+constexpr int kMaxBlock = 4;     // rows of a CTA
+
+struct AppendParams {
+    int n_max, nq, nkv, block, max_pages, num_pages;
+    const __nv_bfloat16* x[3];   // q, k, v
+    long long ld[3];
+    const int32_t* seq_lens;
+    const int32_t* rows;
+    const int32_t* positions;
+    const int32_t* page_table;
+    uint8_t* codes[2];
+    uint32_t* params[2];         // scale in the low half, base in the high one
+    __nv_bfloat16* q_out;
+    long long ld_q_out;
+    int32_t* status;
+    int turn;                    // whether there is a rotation
+    unsigned long long freq[64]; // turns per position, in 2^-64
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__ AppendParams p) {
+    constexpr int kLanes = HD / 4;          // lanes of a head, four values each
+    constexpr int kPer = 32 / kLanes;       // heads that a warp takes at a time
+    constexpr int kHalf = HD / 2;
+    __shared__ float2 s_cs[kMaxBlock * kHalf];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blocks = (p.n_max + p.block - 1) / p.block;
+    const int b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * p.block;
+    const int S = p.seq_lens[b];
+    const int n = p.rows != nullptr ? p.rows[b] : p.n_max;
+    const int first = p.positions != nullptr ? p.positions[b] : S;
+    int st = PE_REQ_OK;
+    if (S < 0 || n < 0 || n > p.n_max || (p.turn && (first < 0 || first > 0x7FFFFFFF - n))) st = PE_REQ_BAD_INPUT;
+    else if (static_cast<long long>(S) + n > static_cast<long long>(p.max_pages) * kPage) st = PE_REQ_CAPACITY;
+    const int live = st == PE_REQ_OK ? n : 0;
+    if (j0 > 0 && j0 >= live && p.q_out == nullptr) return;
+
+    const int sub = lane / kLanes, l = lane % kLanes;
+    const int heads = p.nq + 2 * p.nkv, groups = (heads + kPer - 1) / kPer;
+    const int rows = min(p.block, p.n_max - j0), tasks = rows * groups;
+    // this warp's tasks warp, warp + kWarps, ...: row and head of this lane's part
+    auto place = [&](int t, int& j, int& head) {
+        j = t / groups;
+        head = (t - j * groups) * kPer + sub;
+        j += j0;
+    };
+    auto load = [&](int t) {
+        int j, head;
+        place(t, j, head);
+        uint2 v = make_uint2(0u, 0u);
+        if (t < tasks && head < heads && j < live) {
+            const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
+            const int h = kind == 0 ? head : kind == 1 ? head - p.nq : head - p.nq - p.nkv;
+            const long long at = (static_cast<long long>(b) * p.n_max + j) * p.ld[kind] + h * HD + l * 4;
+            v = *reinterpret_cast<const uint2*>(p.x[kind] + at);
+        }
+        return v;
+    };
+    uint2 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) v[i] = load(warp + i * kWarps);
+
+    if (p.turn)
+        for (int x = tid; x < rows * kHalf; x += kThreads) {
+            const int j = x / kHalf, i = x - j * kHalf;
+            const unsigned long long turns = static_cast<unsigned long long>(static_cast<uint32_t>(first + j0 + j)) * p.freq[i];
+            // the remainder in half turns, -1 .. 1: 24 bits, which are a float, and the rest
+            const int32_t top = static_cast<int32_t>(turns >> 32) & ~0xFF;
+            const float rest = static_cast<float>(static_cast<uint32_t>(turns >> 8)) * 0x1p-55f * 3.14159265358979f;
+            float sn, cs;
+            sincospif(static_cast<float>(top) * 0x1p-31f, &sn, &cs);
+            s_cs[x] = make_float2(fmaf(-rest, sn, cs), fmaf(rest, cs, sn));
+        }
+    // every page that the request's new rows need, before any of them is written
+    const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
+    int bad = 0;
+    if (live > 0)
+        for (int i = S / kPage + tid; i < (S + live + kPage - 1) / kPage; i += kThreads)
+            bad |= table[i] < 0 || table[i] >= p.num_pages;
+    if (__syncthreads_or(bad)) st = PE_REQ_BAD_PAGE;
+    if (j0 == 0 && tid == 0) p.status[b] = st;
+
+    for (int t0 = warp; t0 < tasks; t0 += kBatch * kWarps) {
+        if (t0 != warp) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v[i] = load(t0 + i * kWarps);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int t = t0 + i * kWarps;
+            if (t >= tasks) break;
+            int j, head;
+            place(t, j, head);
+            const bool there = head < heads;
+            const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
+            if (st != PE_REQ_OK || j >= live) {   // no row here
+                if (there && kind == 0)
+                    *reinterpret_cast<uint2*>(p.q_out + (static_cast<long long>(b) * p.n_max + j) * p.ld_q_out +
+                                              head * HD + l * 4) = make_uint2(0u, 0u);
+                continue;
+            }
+            float x[4] = {__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xFFFF0000u),
+                          __uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xFFFF0000u)};
+            if (p.turn) {
+                float other[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(0xffffffffu, x[c], kLanes / 2);
+                if (kind != 2) {
+                    const bool upper = l >= kLanes / 2;
+                    const float4* cs = reinterpret_cast<const float4*>(s_cs + (j - j0) * kHalf + (l % (kLanes / 2)) * 4);
+                    const float4 c0 = cs[0], c1 = cs[1];
+                    const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[c] = fmaf(x[c], co[c], (upper ? other[c] : -other[c]) * si[c]);
+                }
+            }
+            if (kind == 0 && there)
+                *reinterpret_cast<uint2*>(p.q_out + (static_cast<long long>(b) * p.n_max + j) * p.ld_q_out + head * HD +
+                                          l * 4) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+            if (!__any_sync(0xffffffffu, kind != 0 && there)) continue;
+            float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            // NaN where a value is not finite: their difference is, and stays
+            // so (a plain minimum would lose it)
+            float odd = (x[0] - x[0]) + (x[1] - x[1]) + (x[2] - x[2]) + (x[3] - x[3]);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) {
+                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                odd += __shfl_xor_sync(0xffffffffu, odd, o);
+            }
+            if (kind == 0 || !there) continue;
+            uint32_t par = pack_bf16(0.f, lo);
+            const float base = __uint_as_float(par & 0xFFFF0000u);
+            par |= pack_bf16((hi - base) / 15.f, 0.f);
+            const float scale = __uint_as_float(par << 16);
+            uint32_t code = 0;
+            if (odd != 0.f || !(scale < INFINITY)) {
+                par = 0x7FC07FC0u;   // the entry is NaN
+            } else if (scale > 0.f) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) code |= min(__float2uint_rn((x[c] - base) / scale), 15u) << (4 * c);
+            }
+            const int side = kind - 1, e = S + j;
+            const int h = kind == 1 ? head - p.nq : head - p.nq - p.nkv;
+            const size_t at = (static_cast<size_t>(table[e / kPage]) * p.nkv + h) * kPage + e % kPage;
+            *reinterpret_cast<uint16_t*>((side == 0 ? p.codes[0] : p.codes[1]) + at * kHalf + l * 2) = static_cast<uint16_t>(code);
+            if (l == 0) (side == 0 ? p.params[0] : p.params[1])[at] = par;
+        }
+    }
+}
+
+// Turns per position of pair i, theta^(-2i/hd) / 2 pi, in 2^-64. The powers are
+// kept for the calls that follow with the same base and width.
+const unsigned long long* frequencies(float theta, int hd) {
+    static thread_local float had_theta = 0.f;
+    static thread_local int had_hd = 0;
+    static thread_local unsigned long long freq[64];
+    if (had_theta != theta || had_hd != hd) {
+        for (int i = 0; i < hd / 2; ++i) {
+            const double turns = std::pow(static_cast<double>(theta), -2.0 * i / hd) * 0.15915494309189533577;
+            freq[i] = static_cast<unsigned long long>(std::ldexp(turns, 64));
+        }
+        had_theta = theta;
+        had_hd = hd;
+    }
+    return freq;
+}
+
+}  // namespace
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                             float rope_theta, const int32_t* positions, const int32_t* seq_lens, const int32_t* rows,
+                             const int32_t* page_table, int32_t max_pages, int32_t num_pages, uint8_t* k_codes,
+                             uint8_t* v_codes, void* k_params, void* v_params, void* q_out, int64_t ld_q_out,
+                             int32_t* status, void* stream) {
+    const int nq = n_q_heads, nkv = n_kv_heads, hd = head_dim;
+    if (B < 1 || n_max < 1 || nkv < 1 || nq < 0) { set_error("B, n_max and nkv must be >= 1, nq >= 0"); return PE_ERR_ARG; }
+    if (hd != 64 && hd != 128) { set_error("head_dim must be 64 or 128"); return PE_ERR_UNSUPPORTED; }
+    if (max_pages < 1 || num_pages < 1) { set_error("max_pages and num_pages must be >= 1"); return PE_ERR_ARG; }
+    if (max_pages > 0x7FFFFFFF / kPage - 2 || n_max > 0x7FFFFFFF / kPage || nq > (1 << 20) || nkv > (1 << 20)) {
+        set_error("max_pages * 16 and n_max must fit a signed 32-bit entry index, head counts 2^20");
+        return PE_ERR_ARG;
+    }
+    if (!(rope_theta == 0.f || (rope_theta >= 1.f && rope_theta < INFINITY))) {
+        set_error("rope_theta must be 0 (no rotation) or at least 1");
+        return PE_ERR_ARG;
+    }
+    if (!k || !v || !seq_lens || !page_table || !k_codes || !v_codes || !k_params || !v_params || !status ||
+        (nq > 0 && (!q || !q_out))) {
+        set_error("null tensor argument");
+        return PE_ERR_ARG;
+    }
+    const int64_t wq = static_cast<int64_t>(nq) * hd, wkv = static_cast<int64_t>(nkv) * hd;
+    if (ld_k < wkv || ld_v < wkv || ld_k % 4 != 0 || ld_v % 4 != 0 ||
+        (nq > 0 && (ld_q < wq || ld_q_out < wq || ld_q % 4 != 0 || ld_q_out % 4 != 0))) {
+        set_error("row strides must be multiples of 4 and at least heads * head_dim");
+        return PE_ERR_ARG;
+    }
+    const uintptr_t in = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                         (nq > 0 ? reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) : 0);
+    if ((in & 7u) != 0 || ((reinterpret_cast<uintptr_t>(k_codes) | reinterpret_cast<uintptr_t>(v_codes)) & 15u) != 0 ||
+        ((reinterpret_cast<uintptr_t>(k_params) | reinterpret_cast<uintptr_t>(v_params)) & 15u) != 0) {
+        set_error("q, k, v and q_out must be 8-byte aligned, the code and parameter arrays 16-byte aligned");
+        return PE_ERR_ARG;
+    }
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != PE_OK) return rc;
+    AppendParams p{};
+    p.n_max = n_max;
+    p.nq = nq;
+    p.nkv = nkv;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.x[0] = static_cast<const __nv_bfloat16*>(q);
+    p.x[1] = static_cast<const __nv_bfloat16*>(k);
+    p.x[2] = static_cast<const __nv_bfloat16*>(v);
+    p.ld[0] = ld_q;
+    p.ld[1] = ld_k;
+    p.ld[2] = ld_v;
+    p.seq_lens = seq_lens;
+    p.rows = rows;
+    p.positions = positions;
+    p.page_table = page_table;
+    p.codes[0] = k_codes;
+    p.codes[1] = v_codes;
+    p.params[0] = static_cast<uint32_t*>(k_params);
+    p.params[1] = static_cast<uint32_t*>(v_params);
+    p.q_out = nq > 0 ? static_cast<__nv_bfloat16*>(q_out) : nullptr;
+    p.ld_q_out = ld_q_out;
+    p.status = status;
+    p.turn = rope_theta != 0.f;
+    if (p.turn) {
+        const unsigned long long* f = frequencies(rope_theta, hd);
+        for (int i = 0; i < hd / 2; ++i) p.freq[i] = f[i];
+    }
+    // a row to a CTA while that fills the device but once
+    p.block = static_cast<long long>(B) * n_max <= 8ll * sms ? 1 : kMaxBlock;
+    const long long blocks = static_cast<long long>(B) * ((n_max + p.block - 1) / p.block);
+    if (blocks > 0x7FFFFFFFll) { set_error("pe_kv4_append: too many rows for one call"); return PE_ERR_ARG; }
+    auto kern = hd == 128 ? k_kv4_append<128> : k_kv4_append<64>;
+    PE_CUDA_TRY(launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), false, p));
+    return PE_OK;
+}

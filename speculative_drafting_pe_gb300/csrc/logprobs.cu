@@ -1,0 +1,426 @@
+// Log probabilities of given tokens, the entropy and the likeliest tokens of
+// rows of logits (pe_token_logprobs). With y_i = (x_i - max x) / T and
+// Z = sum_i e^{y_i}:
+//
+//   logprob(t) = y_t - ln Z,   H = ln Z - (1/Z) sum_i e^{y_i} y_i   (y_i <= 0: no cancellation)
+//
+// and the k largest x by (value, lower index first), their log probabilities
+// from the same Z.
+//
+// One pass over a row: every thread keeps a running maximum of its own and its
+// sums relative to it, rescaled once for kVec values. A cluster of CTAs takes a
+// row where rows are few; the first CTA joins their sums through distributed
+// shared memory.
+//
+// The likeliest tokens cost the pass nothing. Each thread's maximum is known
+// behind it; of the warps' largest (for more than 16 alternatives: second
+// largest) ones the k-th (k/2-th) gives a bound that at least k values reach.
+// Only threads whose maximum reaches that bound can hold such values, a few of
+// 512, and only theirs are read again (from L2). Many values that equal the
+// bound are looked for in index order until there are k.
+#include <cfloat>
+
+#include "lowbit.cuh"
+
+namespace pe {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTop = 32;
+constexpr float kMaxTemperature = 0x1p64f;
+constexpr int kMaxCluster = 8;
+constexpr int kMinSegment = 8 * kThreads;   // values of a CTA at least, where a cluster shares a row
+constexpr int kCand = 2048 + 64;            // values above the bound that are kept; see `collect`
+constexpr int kTies = 512;                  // values equal to it that are
+constexpr unsigned kAll = 0xffffffffu;
+
+struct LogprobParams {
+    int R, V, k;
+    const void* logits;
+    long long ld;
+    const int32_t* tokens;
+    float inv_t;
+    float* logprobs;
+    float* entropy;
+    int32_t* top_tokens;
+    float* top_logprobs;
+};
+
+// orders like the values (-0 = 0), NaN below everything
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (x != x) return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t u) {
+    return u == 0u ? NAN : __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Sums relative to a maximum: z = sum e^{(x-m)/T}, s = sum e^{(x-m)/T} (x - m).
+struct Sums {
+    float m, z, s;
+};
+constexpr float kFloor = -FLT_MAX;   // the maximum of no value, and of values that are all a mask's lowest one
+constexpr float kFar = -1e30f;     // a difference below it is this one: its weight is 0 at every temperature (kMaxTemperature),
+                                   // and 0 times it is not NaN
+__device__ __forceinline__ void rescale(Sums& a, float m, float c) {   // to a maximum m >= a.m
+    const float d = fmaxf(a.m - m, kFar), f = exp2_fast(d * c);
+    a.s = f * fmaf(d, a.z, a.s);
+    a.z *= f;
+    a.m = m;
+}
+__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    if (a.z != 0.f) rescale(a, m, c);
+    if (b.z != 0.f) rescale(b, m, c);
+    return Sums{m, a.z + b.z, a.s + b.s};
+}
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int kN = 4;
+    __device__ static __forceinline__ void load(const float* p, float (&v)[4]) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    __device__ static __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void add(Sums& a, float& best, const float (&v)[N], float c) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+    best = fmaxf(best, top);
+    rescale(a, fmaxf(a.m, top), c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // a NaN goes on into both sums
+        const float y = max_nan(v[i] - a.m, kFar), e = exp2_fast(y * c);
+        a.z += e;
+        a.s = fmaf(e, y, a.s);
+    }
+}
+
+// The segment [lo, hi) of a row as its threads share it: values up to the first
+// 16-byte boundary and behind the last one singly, by threads 0 .. , and
+// vectors in between, vector x by thread x mod kThreads.
+template <typename T>
+struct Segment {
+    static constexpr int kN = Vec<T>::kN;
+    const T* row;
+    int lo, hi, body, vecs;   // body: first value of the vectors
+    __device__ Segment(const T* r, int l, int h) : row(r), lo(l), hi(h) {
+        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(r + l) / sizeof(T)) % kN);
+        body = min(h, l + (off == 0 ? 0 : kN - off));
+        vecs = (h - body) / kN;
+    }
+    __device__ int tail() const { return body + vecs * kN; }
+    // what of the values outside the vectors is thread t's (at most one at either end)
+    __device__ int front(int t) const { return lo + t < body ? lo + t : -1; }
+    __device__ int back(int t) const { return tail() + t < hi ? tail() + t : -1; }
+};
+
+// The cluster's barrier in two halves, for threads of a warp that may have parted.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams p) {
+    constexpr int kN = Vec<T>::kN, kBatch = kN == 4 ? 4 : 2;   // vectors whose loads are in flight together
+    __shared__ Sums s_sums[kWarps];
+    __shared__ uint32_t s_best[kWarps];
+    __shared__ int s_count, s_equal, s_ties[kTies], s_scan[kWarps];
+    __shared__ unsigned long long s_cand[kCand];
+    __shared__ unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
+    __shared__ float4 s_all[kMaxCluster];                         // the parts' sums (m, z, s), in the first CTA
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int parts = static_cast<int>(gridDim.x), part = blockIdx.x, r = blockIdx.y + blockIdx.z * gridDim.y;
+    if (r >= p.R) return;   // the whole cluster
+    if (parts > 1) cluster_arrive();   // this CTA runs
+    const float c = p.inv_t * 1.4426950408889634f;
+    const T* row = static_cast<const T*>(p.logits) + static_cast<long long>(r) * p.ld;
+    const int each = (p.V + parts - 1) / parts;
+    const Segment<T> seg(row, min(p.V, part * each), min(p.V, part * each + each));
+
+    Sums a{kFloor, 0.f, 0.f};
+    float mine = -INFINITY;   // this thread's largest value
+    const T* body = row + seg.body;
+    int x = tid;
+    for (; x + (kBatch - 1) * kThreads < seg.vecs; x += kBatch * kThreads) {
+        float v[kBatch][kN];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) Vec<T>::load(body + static_cast<size_t>(x + i * kThreads) * kN, v[i]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) add(a, mine, v[i], c);
+    }
+    for (; x < seg.vecs; x += kThreads) {
+        float v[kN];
+        Vec<T>::load(body + static_cast<size_t>(x) * kN, v);
+        add(a, mine, v, c);
+    }
+    {
+        const int f = seg.front(tid), t = seg.back(tid);
+        float v[1];
+        if (f >= 0) { v[0] = static_cast<float>(row[f]); add(a, mine, v, c); }
+        if (t >= 0) { v[0] = static_cast<float>(row[t]); add(a, mine, v, c); }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
+        a = join(a, b, c);
+    }
+    if (lane == 0) s_sums[warp] = a;
+    if (p.k > 0) {
+        // the warp's largest, or second largest, maximum
+        const uint32_t key = order_key(mine);
+        uint32_t best = __reduce_max_sync(kAll, key);
+        if (p.k > kWarps) {
+            const unsigned who = __ballot_sync(kAll, key == best);
+            best = __reduce_max_sync(kAll, lane == __ffs(who) - 1 ? 0u : key);
+        }
+        if (lane == 0) s_best[warp] = best;
+    }
+    if (tid == 0) s_count = s_equal = 0;
+    __syncthreads();
+    if (warp == 0) {
+        a = lane < kWarps ? s_sums[lane] : Sums{kFloor, 0.f, 0.f};
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
+            a = join(a, b, c);
+        }
+        if (lane == 0) s_sums[0] = a;
+    }
+
+    const int want = min(p.k, seg.hi - seg.lo);
+    if (want > 0) {
+        // the bound: so many warps have one (or two) maxima that are as large
+        const int rank = p.k > kWarps ? (p.k + 1) / 2 : p.k;
+        const uint32_t b = s_best[lane % kWarps];
+        int ahead = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint32_t o = s_best[w];
+            ahead += o > b || (o == b && w < lane % kWarps);
+        }
+        const uint32_t bound = __shfl_sync(kAll, b, __ffs(__ballot_sync(kAll, ahead == rank - 1)) - 1);
+        // values above the bound, and some that equal it, of the threads that have such
+        const float level = key_value(bound);
+        auto put = [&](float v, int i) {
+            if (v > level) {
+                const int n = atomicAdd(&s_count, 1);
+                if (n < kCand) s_cand[n] = (static_cast<unsigned long long>(order_key(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
+            } else if (v == level && *static_cast<volatile int*>(&s_equal) <= kTies) {
+                const int n = atomicAdd(&s_equal, 1);
+                if (n < kTies) s_ties[n] = i;
+            }
+        };
+        const bool has = mine >= level;
+        unsigned who = __ballot_sync(kAll, has);
+        while (who != 0) {
+            const int of = __ffs(who) - 1;
+            who &= who - 1;
+            for (int y = warp * 32 + of + lane * kThreads; y < seg.vecs; y += 32 * kThreads) {
+                float v[kN];
+                Vec<T>::load(body + static_cast<size_t>(y) * kN, v);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) put(v[i], seg.body + y * kN + i);
+            }
+        }
+        if (has) {
+            const int f = seg.front(tid), t = seg.back(tid);
+            if (f >= 0) put(static_cast<float>(row[f]), f);
+            if (t >= 0) put(static_cast<float>(row[t]), t);
+        }
+        __syncthreads();
+        const int equal = s_equal;
+        int count = s_count;
+        if (count > kCand) {
+            // More than are kept (many of the row's largest values with one
+            // thread): the largest keys one by one, each by a pass.
+            unsigned long long below = ~0ull;
+            for (int q = 0; q < want; ++q) {
+                unsigned long long top = 0;
+                for (int i = seg.lo + tid; i < seg.hi; i += kThreads) {
+                    const unsigned long long key = (static_cast<unsigned long long>(order_key(static_cast<float>(row[i]))) << 32) |
+                                                   (0xFFFFFFFFu - static_cast<uint32_t>(i));
+                    if (key < below && key > top) top = key;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const unsigned long long other = __shfl_xor_sync(kAll, top, o);
+                    top = other > top ? other : top;
+                }
+                __syncthreads();
+                if (lane == 0) s_cand[warp] = top;
+                __syncthreads();
+                top = 0;
+                for (int w = 0; w < kWarps; ++w) top = s_cand[w] > top ? s_cand[w] : top;
+                if (tid == 0) s_top[q] = top;
+                below = top;
+            }
+        } else {
+            // All of the few that equal it stand with the others; many are looked
+            // for in index order until there are enough. Where a row has fewer
+            // numbers than alternatives are asked for, those that are NaN follow.
+            const bool few = equal <= kTies && count + equal <= kCand;
+            if (few && count < want) {
+                for (int i = tid; i < equal; i += kThreads)
+                    s_cand[count + i] = (static_cast<unsigned long long>(bound) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(s_ties[i]));
+                count += equal;
+                __syncthreads();
+            }
+            for (uint32_t at = few ? 0u : bound; count < want; at = 0u) {
+                for (int i0 = seg.lo; i0 < seg.hi && count < want; i0 += kThreads) {
+                    const int i = i0 + tid;
+                    const bool tie = i < seg.hi && order_key(static_cast<float>(row[i])) == at;
+                    const unsigned vote = __ballot_sync(kAll, tie);
+                    if (lane == 0) s_scan[warp] = __popc(vote);
+                    if (__syncthreads_or(tie)) {
+                        int before = __popc(vote & ((1u << lane) - 1u)), all = 0;
+                        for (int w = 0; w < kWarps; ++w) {
+                            if (w < warp) before += s_scan[w];
+                            all += s_scan[w];
+                        }
+                        if (tie && count + before < want)
+                            s_cand[count + before] = (static_cast<unsigned long long>(at) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
+                        count = min(want, count + all);
+                    }
+                    __syncthreads();
+                }
+                if (at == 0u) break;
+            }
+            // each key to its rank
+            for (int i = tid; i < count; i += kThreads) {
+                const unsigned long long key = s_cand[i];
+                int ahead = 0;
+                for (int q = 0; q < count; ++q) ahead += s_cand[q] > key;
+                if (ahead < want) s_top[ahead] = key;
+            }
+        }
+    }
+    __syncthreads();
+
+    // the first CTA of the cluster joins the parts
+    if (parts > 1) {
+        cluster_wait();
+        if (part > 0) {
+            const uint32_t sums = dsmem_addr(smem_u32(&s_all[part]), 0), top = dsmem_addr(smem_u32(s_top + part * kMaxTop), 0);
+            if (tid == 0) {
+                dsmem_st2(sums, s_sums[0].m, s_sums[0].z);
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums + 8), "f"(s_sums[0].s) : "memory");
+            }
+            if (tid < p.k) {
+                const unsigned long long key = tid < want ? s_top[tid] : 0ull;
+                asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(top + tid * 8), "l"(key) : "memory");
+            }
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (part > 0) return;
+    }
+    Sums sum = s_sums[0];
+    for (int q = 1; q < parts; ++q) sum = join(sum, Sums{s_all[q].x, s_all[q].y, s_all[q].z}, c);
+    // NaN where the row has no probability: none above -inf, an infinity, a NaN
+    const float log_z = sum.z > 0.f ? logf(sum.z) : NAN;
+    if (tid == 0) {
+        const int t = p.tokens[r];
+        p.logprobs[r] = t >= 0 && t < p.V ? (static_cast<float>(row[t]) - sum.m) * p.inv_t - log_z : NAN;
+        if (p.entropy != nullptr) p.entropy[r] = log_z - sum.s / sum.z * p.inv_t;
+    }
+    if (p.k == 0) return;
+    // every part's are in order
+    for (int i = tid; i < parts * kMaxTop; i += kThreads) {
+        const int from = i / kMaxTop, at = i % kMaxTop;
+        if (at >= (from == 0 ? want : p.k) || s_top[i] == 0ull) continue;
+        const unsigned long long key = s_top[i];
+        int ahead = at;
+        for (int q = 0; q < parts; ++q)
+            if (q != from)
+                for (int x = 0; x < (q == 0 ? want : p.k) && s_top[q * kMaxTop + x] > key; ++x) ++ahead;
+        if (ahead >= p.k) continue;
+        const long long to = static_cast<long long>(r) * p.k + ahead;
+        p.top_tokens[to] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+        p.top_logprobs[to] = (key_value(static_cast<uint32_t>(key >> 32)) - sum.m) * p.inv_t - log_z;
+    }
+}
+
+template <typename T>
+int launch(const LogprobParams& p, int parts, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    const unsigned rows_y = static_cast<unsigned>(p.R < 32768 ? p.R : 32768);
+    cfg.gridDim = dim3(parts, rows_y, (p.R + rows_y - 1) / rows_y);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    PE_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_token_logprobs<T>, p));
+    return PE_OK;
+}
+
+}  // namespace
+}  // namespace pe
+
+using namespace pe;
+
+extern "C" int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void* logits, int64_t ld,
+                                 const int32_t* tokens, float temperature, float* logprobs, float* entropy,
+                                 int32_t top, int32_t* top_tokens, float* top_logprobs, void* stream) {
+    if (R < 1 || V < 1) { set_error("R and V must be >= 1"); return PE_ERR_ARG; }
+    if (dtype != PE_DTYPE_BF16 && dtype != PE_DTYPE_FP32) { set_error("logits must be bf16 or fp32"); return PE_ERR_ARG; }
+    if (top < 0 || top > kMaxTop || top > V) { set_error("top must lie in 0..32 and not exceed V"); return PE_ERR_ARG; }
+    if (R > (1 << 30)) { set_error("too many rows for one call"); return PE_ERR_ARG; }
+    const float inv_t = 1.f / temperature;
+    if (!(temperature > 0.f && temperature <= kMaxTemperature && inv_t * 2.f < INFINITY)) {
+        set_error("temperature must be positive and at most 2^64");
+        return PE_ERR_ARG;
+    }
+    if (!logits || !tokens || !logprobs || (top > 0 && (!top_tokens || !top_logprobs))) {
+        set_error("null tensor argument");
+        return PE_ERR_ARG;
+    }
+    if (ld < V && ld != 0) { set_error("row stride must be at least V, or 0"); return PE_ERR_ARG; }
+    if (reinterpret_cast<uintptr_t>(logits) % (dtype == PE_DTYPE_BF16 ? 2 : 4) != 0 ||
+        ((reinterpret_cast<uintptr_t>(logprobs) | reinterpret_cast<uintptr_t>(entropy) | reinterpret_cast<uintptr_t>(tokens) |
+          reinterpret_cast<uintptr_t>(top_tokens) | reinterpret_cast<uintptr_t>(top_logprobs)) & 3u) != 0) {
+        set_error("tensors must be aligned to their elements");
+        return PE_ERR_ARG;
+    }
+    int dev = 0, sms = 0;
+    const int rc = current_device(&dev, &sms);
+    if (rc != PE_OK) return rc;
+    LogprobParams p{R, V, top, logits, ld, tokens, inv_t, logprobs, entropy, top_tokens, top_logprobs};
+    // a cluster to a row while rows alone leave multiprocessors idle
+    int parts = 1;
+    while (parts < kMaxCluster && static_cast<long long>(R) * parts < 2ll * sms && V / (2 * parts) >= kMinSegment) parts *= 2;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == PE_DTYPE_BF16 ? launch<__nv_bfloat16>(p, parts, s) : launch<float>(p, parts, s);
+}
