@@ -50,7 +50,7 @@ extern "C" {
 #define PE_REQ_CAPACITY    1    /* entries needed exceed max_pages * page_size */
 #define PE_REQ_BAD_PAGE    2    /* a needed page-table entry is outside [0, num_pages) */
 #define PE_REQ_BAD_INPUT   3    /* token id outside [0, V), negative length */
-#define PE_REQ_TIMEOUT     4    /* pe_attention_kv8: a device-side wait gave up; all outputs of the call are zero */
+#define PE_REQ_TIMEOUT     4    /* pe_attention_kv8, pe_attention_kv4: a device-side wait gave up; all outputs of the call are zero */
 
 /* bits of the device error word (pe_device_errors) */
 #define PE_DEVERR_GEMM_TIMEOUT  1u
@@ -576,6 +576,8 @@ int pe_test_stall_chain(pe_handle* h, void* stream);
  * wait for one arrival more than there are, so its waits give up after their
  * limit (1 s) and the call reports PE_REQ_TIMEOUT. Later calls are not touched. */
 int pe_test_stall_attention_kv8(int32_t barrier);
+/* And for pe_attention_kv4 (its tensor-memory kernel: more than 16 query rows of a kv head). */
+int pe_test_stall_attention_kv4(int32_t barrier);
 
 /* Kernel kinds of the draft pass, for launch accounting and profiling. */
 #define PE_KERNEL_FC         0

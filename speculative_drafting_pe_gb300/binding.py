@@ -31,6 +31,7 @@ EXPORTS = (
     "pe_linear_w4", "pe_assign_pages", "pe_release_pages", "pe_kv8_append", "pe_attention_kv8_scratch",
     "pe_attention_kv8", "pe_test_stall_attention_kv8",
     "pe_kv4_append", "pe_attention_kv4_scratch", "pe_attention_kv4", "pe_token_logprobs",
+    "pe_test_stall_attention_kv4",
 )
 KERNEL_KINDS = ("fc", "row_build", "rmsnorm", "qkv", "attention", "o_proj", "gate_up", "down", "lm_head", "argmax",
                 "layer_chain")
@@ -165,6 +166,7 @@ def load():
              [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp]),
             ("pe_token_logprobs", [_i32] * 3 + [_vp, _i64, _vp, ctypes.c_float, _vp, _vp, _i32, _vp, _vp, _vp]),
             ("pe_test_stall_attention_kv8", [_i32]),
+            ("pe_test_stall_attention_kv4", [_i32]),
             ("pe_attention_kv8", [_i32] * 5 + [_vp, _i64, _vp, _vp, _vp, _i32, _i32] + [_vp] * 4 +
              [ctypes.c_float, _vp, _i64, _vp, _i64, _vp, _vp])):
         fn = getattr(lib, name)
@@ -930,3 +932,8 @@ def test_stall_attention_kv8(barrier):
     """Host-side fault injection (tests only): in the next attention_kv8 call by the tensor-memory kernel no wait for
     K codes (1), V tiles (2) or weights (3) can complete; they must give up."""
     _check(load().pe_test_stall_attention_kv8(barrier))
+
+
+def test_stall_attention_kv4(barrier):
+    """The same for attention_kv4."""
+    _check(load().pe_test_stall_attention_kv4(barrier))

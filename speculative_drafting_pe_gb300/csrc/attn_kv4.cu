@@ -564,9 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+constexpr int kFewRows = 16;   // query rows of a head up to which the register kernel is taken
+
 int plan_kv4(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const int rows = K * (nq / nkv);
-    if (rows > 16) { set_error("K * (n_q_heads / n_kv_heads) must be <= 16"); return PE_ERR_UNSUPPORTED; }
+    if (rows > kFewRows) return plan_umma(B, nkv, hd, max_pages, out);
     return plan_line(B, nkv, hd, max_pages, kPages, kPad, kMinUnits, rows <= 8 ? 8 : 16, out);
 }
 
@@ -655,7 +657,8 @@ extern "C" int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t
     // whole sectors: a 16-byte aligned `ws` may be half of one off
     p.part = ws + a.cut_floats + (reinterpret_cast<uintptr_t>(ws) % 32 != 0 ? 4 : 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (a.tr == 16) rc = head_dim == 128 ? launch_rows<128, 2>(p, a, s) : launch_rows<64, 2>(p, a, s);
+    if (a.tr > kFewRows) rc = launch_umma(p, a, head_dim, s);
+    else if (a.tr == 16) rc = head_dim == 128 ? launch_rows<128, 2>(p, a, s) : launch_rows<64, 2>(p, a, s);
     else rc = head_dim == 128 ? launch_rows<128, 1>(p, a, s) : launch_rows<64, 1>(p, a, s);
     return rc != PE_OK ? rc : launch_merge(p, a, head_dim, s);
 }

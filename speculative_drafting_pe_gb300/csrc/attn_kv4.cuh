@@ -41,5 +41,9 @@ __device__ __forceinline__ float mid_of(uint32_t par) {
     return fmaf(mid, 0.f, mid);
 }
 
+// the tensor-memory kernel, for more rows: its plan and launch
+int plan_umma(int B, int nkv, int hd, int max_pages, Plan* out);
+int launch_umma(const Kv4Params& p, const Plan& a, int hd, cudaStream_t s);
+
 }  // namespace kv4
 }  // namespace pe
