@@ -14,9 +14,10 @@
 // without a double on the device (FP64 runs at a few operations a cycle and
 // SM). Its first 24 bits go through sincospif, the rest is a first-order term.
 //
-// A CTA takes `block` rows of one request, a warp a head of a row at a time (two
-// 64-wide ones): four values a lane, 8-byte loads, kBatch heads in flight. The
-// rows' sines and cosines are computed once, for all heads.
+// A CTA takes `block` rows of one request, a warp two heads of a row at a time
+// (four 64-wide ones). A lane has four dimensions of the lower half of a head
+// and the four that they turn with, two 8-byte loads, and kBatch such pairs in
+// flight. The rows' sines and cosines are computed once, for all heads.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -53,12 +54,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// four bf16 values
+__device__ __forceinline__ void unpack4(const uint2& w, float* x) {
+    x[0] = __uint_as_float(w.x << 16);
+    x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(w.y << 16);
+    x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__ AppendParams p) {
-    constexpr int kLanes = HD / 4;          // lanes of a head, four values each
-    constexpr int kPer = 32 / kLanes;       // heads that a warp takes at a time
     constexpr int kHalf = HD / 2;
-    __shared__ float2 s_cs[kMaxBlock * kHalf];
+    constexpr int kLanes = HD / 8;          // lanes of a head
+    constexpr int kPer = 32 / kLanes;       // heads that a warp takes at a time
+    __shared__ float4 s_cs[kMaxBlock * kHalf / 2];   // (cos, sin) of two pairs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int blocks = (p.n_max + p.block - 1) / p.block;
     const int b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * p.block;
@@ -73,39 +82,42 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
 
     const int sub = lane / kLanes, l = lane % kLanes;
     const int heads = p.nq + 2 * p.nkv, groups = (heads + kPer - 1) / kPer;
-    const int rows = min(p.block, p.n_max - j0), tasks = rows * groups;
-    // this warp's tasks warp, warp + kWarps, ...: row and head of this lane's part
-    auto place = [&](int t, int& j, int& head) {
-        j = t / groups;
-        head = (t - j * groups) * kPer + sub;
-        j += j0;
+    const int end = min(p.n_max, j0 + p.block);
+    // this warp's heads: of row j, group g, then kWarps groups further
+    auto next = [&](int& j, int& g) {
+        for (g += kWarps; g >= groups; g -= groups) ++j;
     };
-    auto load = [&](int t) {
-        int j, head;
-        place(t, j, head);
-        uint2 v = make_uint2(0u, 0u);
-        if (t < tasks && head < heads && j < live) {
+    auto load = [&](int j, int g, uint2 (&v)[2]) {
+        const int head = g * kPer + sub;
+        v[0] = v[1] = make_uint2(0u, 0u);
+        if (j < min(end, live) && head < heads) {
             const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
             const int h = kind == 0 ? head : kind == 1 ? head - p.nq : head - p.nq - p.nkv;
-            const long long at = (static_cast<long long>(b) * p.n_max + j) * p.ld[kind] + h * HD + l * 4;
-            v = *reinterpret_cast<const uint2*>(p.x[kind] + at);
+            const __nv_bfloat16* x = p.x[kind] + (static_cast<long long>(b) * p.n_max + j) * p.ld[kind] + h * HD + l * 4;
+            v[0] = *reinterpret_cast<const uint2*>(x);
+            v[1] = *reinterpret_cast<const uint2*>(x + kHalf);
         }
-        return v;
     };
-    uint2 v[kBatch];
+    uint2 v[kBatch][2];
+    int j = j0, g = warp - kWarps;
+    next(j, g);
+    int jl = j, gl = g;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) v[i] = load(warp + i * kWarps);
+    for (int i = 0; i < kBatch; ++i) {
+        load(jl, gl, v[i]);
+        next(jl, gl);
+    }
 
     if (p.turn)
-        for (int x = tid; x < rows * kHalf; x += kThreads) {
-            const int j = x / kHalf, i = x - j * kHalf;
-            const unsigned long long turns = static_cast<unsigned long long>(static_cast<uint32_t>(first + j0 + j)) * p.freq[i];
+        for (int x = tid; x < (end - j0) * kHalf; x += kThreads) {
+            const int row = x / kHalf, i = x - row * kHalf;
+            const unsigned long long turns = static_cast<unsigned long long>(static_cast<uint32_t>(first + j0 + row)) * p.freq[i];
             // the remainder in half turns, -1 .. 1: 24 bits, which are a float, and the rest
             const int32_t top = static_cast<int32_t>(turns >> 32) & ~0xFF;
             const float rest = static_cast<float>(static_cast<uint32_t>(turns >> 8)) * 0x1p-55f * 3.14159265358979f;
             float sn, cs;
             sincospif(static_cast<float>(top) * 0x1p-31f, &sn, &cs);
-            s_cs[x] = make_float2(fmaf(-rest, sn, cs), fmaf(rest, cs, sn));
+            reinterpret_cast<float2*>(s_cs)[x] = make_float2(fmaf(-rest, sn, cs), fmaf(rest, cs, sn));
         }
     // every page that the request's new rows need, before any of them is written
     const int32_t* table = p.page_table + static_cast<size_t>(b) * p.max_pages;
@@ -115,71 +127,91 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
             bad |= table[i] < 0 || table[i] >= p.num_pages;
     if (__syncthreads_or(bad)) st = PE_REQ_BAD_PAGE;
     if (j0 == 0 && tid == 0) p.status[b] = st;
+    const int rows = st == PE_REQ_OK ? live : 0;
 
-    for (int t0 = warp; t0 < tasks; t0 += kBatch * kWarps) {
-        if (t0 != warp) {
+    for (bool front = true; j < end; front = false) {
+        if (!front) {
+            jl = j;
+            gl = g;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) v[i] = load(t0 + i * kWarps);
+            for (int i = 0; i < kBatch; ++i) {
+                load(jl, gl, v[i]);
+                next(jl, gl);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int t = t0 + i * kWarps;
-            if (t >= tasks) break;
-            int j, head;
-            place(t, j, head);
-            const bool there = head < heads;
+            if (j >= end) break;
+            const int head = g * kPer + sub, row = j;
+            next(j, g);
             const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
-            if (st != PE_REQ_OK || j >= live) {   // no row here
-                if (there && kind == 0)
-                    *reinterpret_cast<uint2*>(p.q_out + (static_cast<long long>(b) * p.n_max + j) * p.ld_q_out +
-                                              head * HD + l * 4) = make_uint2(0u, 0u);
+            __nv_bfloat16* q_to = p.q_out + (static_cast<long long>(b) * p.n_max + row) * p.ld_q_out + head * HD + l * 4;
+            if (row >= rows) {   // no row here
+                if (kind == 0) {
+                    *reinterpret_cast<uint2*>(q_to) = make_uint2(0u, 0u);
+                    *reinterpret_cast<uint2*>(q_to + kHalf) = make_uint2(0u, 0u);
+                }
                 continue;
             }
-            float x[4] = {__uint_as_float(v[i].x << 16), __uint_as_float(v[i].x & 0xFFFF0000u),
-                          __uint_as_float(v[i].y << 16), __uint_as_float(v[i].y & 0xFFFF0000u)};
-            if (p.turn) {
-                float other[4];
+            float x[8];   // dimensions 4l .., then hd/2 + 4l ..
+            unpack4(v[i][0], x);
+            unpack4(v[i][1], x + 4);
+            if (p.turn && kind != 2) {
+                const float4* cs = s_cs + ((row - j0) * kHalf + l * 4) / 2;
+                const float4 c0 = cs[0], c1 = cs[1];
+                const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) other[c] = __shfl_xor_sync(0xffffffffu, x[c], kLanes / 2);
-                if (kind != 2) {
-                    const bool upper = l >= kLanes / 2;
-                    const float4* cs = reinterpret_cast<const float4*>(s_cs + (j - j0) * kHalf + (l % (kLanes / 2)) * 4);
-                    const float4 c0 = cs[0], c1 = cs[1];
-                    const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) x[c] = fmaf(x[c], co[c], (upper ? other[c] : -other[c]) * si[c]);
+                for (int c = 0; c < 4; ++c) {
+                    const float lo = x[c], hi = x[4 + c];
+                    x[c] = fmaf(lo, co[c], -(hi * si[c]));
+                    x[4 + c] = fmaf(hi, co[c], lo * si[c]);
                 }
             }
-            if (kind == 0 && there)
-                *reinterpret_cast<uint2*>(p.q_out + (static_cast<long long>(b) * p.n_max + j) * p.ld_q_out + head * HD +
-                                          l * 4) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-            if (!__any_sync(0xffffffffu, kind != 0 && there)) continue;
-            float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            // NaN where a value is not finite: their difference is, and stays
-            // so (a plain minimum would lose it)
-            float odd = (x[0] - x[0]) + (x[1] - x[1]) + (x[2] - x[2]) + (x[3] - x[3]);
+            if (kind == 0) {
+                *reinterpret_cast<uint2*>(q_to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+                *reinterpret_cast<uint2*>(q_to + kHalf) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            }
+            const bool stores = kind != 0 && head < heads;
+            if (!__any_sync(0xffffffffu, stores)) continue;
+            float lo = x[0], hi = x[0], odd = x[0] - x[0];   // odd: NaN where a value is not finite
+#pragma unroll
+            for (int c = 1; c < 8; ++c) {
+                lo = fminf(lo, x[c]);
+                hi = fmaxf(hi, x[c]);
+                odd += x[c] - x[c];
+            }
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) {
                 lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
                 hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                odd += __shfl_xor_sync(0xffffffffu, odd, o);
             }
-            if (kind == 0 || !there) continue;
+            const unsigned who = __ballot_sync(0xffffffffu, odd != 0.f);
+            if (!stores) continue;
             uint32_t par = pack_bf16(0.f, lo);
             const float base = __uint_as_float(par & 0xFFFF0000u);
             par |= pack_bf16((hi - base) / 15.f, 0.f);
             const float scale = __uint_as_float(par << 16);
-            uint32_t code = 0;
-            if (odd != 0.f || !(scale < INFINITY)) {
+            uint32_t code[2] = {0u, 0u};
+            if (((who >> (sub * kLanes)) & ((1u << kLanes) - 1u)) != 0u || !(scale < INFINITY)) {
                 par = 0x7FC07FC0u;   // the entry is NaN
+            } else if (scale >= 0x1p-100f) {
+                // the quotient with its rounding error put right, as a division has it
+                const float inv = 1.f / scale;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float d = x[c] - base, near = d * inv;
+                    code[c >> 2] |= min(__float2uint_rn(fmaf(fmaf(-scale, near, d), inv, near)), 15u) << (4 * (c & 3));
+                }
             } else if (scale > 0.f) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) code |= min(__float2uint_rn((x[c] - base) / scale), 15u) << (4 * c);
+                for (int c = 0; c < 8; ++c) code[c >> 2] |= min(__float2uint_rn((x[c] - base) / scale), 15u) << (4 * (c & 3));
             }
-            const int side = kind - 1, e = S + j;
+            const int side = kind - 1, e = S + row;
             const int h = kind == 1 ? head - p.nq : head - p.nq - p.nkv;
             const size_t at = (static_cast<size_t>(table[e / kPage]) * p.nkv + h) * kPage + e % kPage;
-            *reinterpret_cast<uint16_t*>((side == 0 ? p.codes[0] : p.codes[1]) + at * kHalf + l * 2) = static_cast<uint16_t>(code);
+            uint8_t* to = (side == 0 ? p.codes[0] : p.codes[1]) + at * kHalf + l * 2;
+            *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
+            *reinterpret_cast<uint16_t*>(to + kHalf / 2) = static_cast<uint16_t>(code[1]);
             if (l == 0) (side == 0 ? p.params[0] : p.params[1])[at] = par;
         }
     }

@@ -40,7 +40,7 @@ struct LogprobParams {
     const void* logits;
     long long ld;
     const int32_t* tokens;
-    float inv_t;
+    float c, inv_t;              // log2(e) / temperature, 1 / temperature
     float* logprobs;
     float* entropy;
     int32_t* top_tokens;
@@ -56,34 +56,53 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t u) {
     return u == 0u ? NAN : __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// Sums relative to a maximum: z = sum e^{(x-m)/T}, s = sum e^{(x-m)/T} (x - m).
+// two floats in one instruction
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unf2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// In base 2, t_i = c x_i with c = log2(e) / T: sums relative to a maximum m of
+// the t, z = sum 2^(t - m) and s = sum 2^(t - m) (t - m). m is rounded, but every
+// difference with it is one rounding (the product is exact in fma).
 struct Sums {
     float m, z, s;
 };
-constexpr float kFloor = -FLT_MAX;   // the maximum of no value, and of values that are all a mask's lowest one
-constexpr float kFar = -1e30f;     // a difference below it is this one: its weight is 0 at every temperature (kMaxTemperature),
-                                   // and 0 times it is not NaN
-__device__ __forceinline__ void rescale(Sums& a, float m, float c) {   // to a maximum m >= a.m
-    const float d = fmaxf(a.m - m, kFar), f = exp2_fast(d * c);
+constexpr float kSafe = -1e15f;       // values from here on: times c (2^64 at most) they and their differences stay finite
+constexpr float kFloor = -FLT_MAX;   // the maximum of no value
+constexpr float kFar = -1e30f;       // a difference below it is this one: its weight is 0, and 0 times it is not NaN
+__device__ __forceinline__ void rescale(Sums& a, float m) {   // to a maximum m >= a.m
+    const float d = fmaxf(a.m - m, kFar), f = exp2_fast(d);
     a.s = f * fmaf(d, a.z, a.s);
     a.z *= f;
     a.m = m;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
     const float m = fmaxf(a.m, b.m);
-    if (a.z != 0.f) rescale(a, m, c);
-    if (b.z != 0.f) rescale(b, m, c);
+    if (a.z != 0.f) rescale(a, m);
+    if (b.z != 0.f) rescale(b, m);
     return Sums{m, a.z + b.z, a.s + b.s};
 }
 
@@ -108,19 +127,38 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// Values v of a row, the largest of which goes into `best`.
 template <int N>
 __device__ __forceinline__ void add(Sums& a, float& best, const float (&v)[N], float c) {
-    float top = v[0];
+    float top = v[0], low = v[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+    for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]), low = fminf(low, v[i]);
     best = fmaxf(best, top);
-    rescale(a, fmaxf(a.m, top), c);
+    // (a maximum of -inf stays the floor; the lowest value may leave fp32's range here)
+    rescale(a, fmaxf(a.m, top * c));
+    if (N % 2 == 0 && low >= kSafe) {
+        const uint64_t c2 = f2(c, c), m2 = f2(-a.m, -a.m);
+        uint64_t z = f2(a.z, 0.f), s = f2(a.s, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        // a NaN goes on into both sums
-        const float y = max_nan(v[i] - a.m, kFar), e = exp2_fast(y * c);
-        a.z += e;
-        a.s = fmaf(e, y, a.s);
+        for (int i = 0; i < N / 2; ++i) {
+            const uint64_t t = fma2(f2(v[2 * i], v[2 * i + 1]), c2, m2);
+            const float2 y = unf2(t);
+            const uint64_t e = f2(exp2_fast(y.x), exp2_fast(y.y));
+            z = add2(z, e);
+            s = fma2(e, t, s);
+        }
+        const float2 zz = unf2(z), ss = unf2(s);
+        a.z = zz.x + zz.y;
+        a.s = ss.x + ss.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // what lies far below adds nothing (-inf would be 0 * inf); a NaN goes on into both sums
+            const float t = v[i] < kSafe ? (v[i] == -INFINITY ? kFar : fmaxf(fmaxf(v[i] * c, kFloor) - a.m, kFar)) : fmaf(v[i], c, -a.m);
+            const float e = exp2_fast(t);
+            a.z += e;
+            a.s = fmaf(e, t, a.s);
+        }
     }
 }
 
@@ -154,13 +192,13 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
     __shared__ uint32_t s_best[kWarps];
     __shared__ int s_count, s_equal, s_ties[kTies], s_scan[kWarps];
     __shared__ unsigned long long s_cand[kCand];
-    __shared__ unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
+    __shared__ __align__(16) unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
     __shared__ float4 s_all[kMaxCluster];                         // the parts' sums (m, z, s), in the first CTA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int parts = static_cast<int>(gridDim.x), part = blockIdx.x, r = blockIdx.y + blockIdx.z * gridDim.y;
     if (r >= p.R) return;   // the whole cluster
     if (parts > 1) cluster_arrive();   // this CTA runs
-    const float c = p.inv_t * 1.4426950408889634f;
+    const float c = p.c;
     const T* row = static_cast<const T*>(p.logits) + static_cast<long long>(r) * p.ld;
     const int each = (p.V + parts - 1) / parts;
     const Segment<T> seg(row, min(p.V, part * each), min(p.V, part * each + each));
@@ -190,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
-        a = join(a, b, c);
+        a = join(a, b);
     }
     if (lane == 0) s_sums[warp] = a;
     if (p.k > 0) {
@@ -204,13 +242,14 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         if (lane == 0) s_best[warp] = best;
     }
     if (tid == 0) s_count = s_equal = 0;
+    if (tid < kMaxTop) s_top[tid] = 0ull;   // (no key)
     __syncthreads();
     if (warp == 0) {
         a = lane < kWarps ? s_sums[lane] : Sums{kFloor, 0.f, 0.f};
 #pragma unroll
         for (int o = kWarps / 2; o > 0; o >>= 1) {
             const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
-            a = join(a, b, c);
+            a = join(a, b);
         }
         if (lane == 0) s_sums[0] = a;
     }
@@ -333,8 +372,8 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
                 dsmem_st2(sums, s_sums[0].m, s_sums[0].z);
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(sums + 8), "f"(s_sums[0].s) : "memory");
             }
-            if (tid < p.k) {
-                const unsigned long long key = tid < want ? s_top[tid] : 0ull;
+            if (p.k > 0 && tid < kMaxTop) {
+                const unsigned long long key = s_top[tid];
                 asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(top + tid * 8), "l"(key) : "memory");
             }
         }
@@ -343,29 +382,37 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         if (part > 0) return;
     }
     Sums sum = s_sums[0];
-    for (int q = 1; q < parts; ++q) sum = join(sum, Sums{s_all[q].x, s_all[q].y, s_all[q].z}, c);
+    for (int q = 1; q < parts; ++q) sum = join(sum, Sums{s_all[q].x, s_all[q].y, s_all[q].z});
     // NaN where the row has no probability: none above -inf, an infinity, a NaN
-    const float log_z = sum.z > 0.f ? logf(sum.z) : NAN;
+    constexpr float kLn2 = 0.69314718055994531f;
+    const float log_z = sum.z > 0.f ? log2f(sum.z) : NAN;
+    auto logprob = [&](float x) {
+        if (x < kSafe && sum.m >= kSafe) return x * p.inv_t - (sum.m + log_z) * kLn2;   // x c may leave fp32's range
+        return ((x < kSafe ? fmaxf(x * c, kFloor) - sum.m : fmaf(x, c, -sum.m)) - log_z) * kLn2;
+    };
     if (tid == 0) {
         const int t = p.tokens[r];
-        p.logprobs[r] = t >= 0 && t < p.V ? (static_cast<float>(row[t]) - sum.m) * p.inv_t - log_z : NAN;
-        if (p.entropy != nullptr) p.entropy[r] = log_z - sum.s / sum.z * p.inv_t;
+        p.logprobs[r] = t >= 0 && t < p.V ? logprob(static_cast<float>(row[t])) : NAN;
+        if (p.entropy != nullptr) p.entropy[r] = (log_z - sum.s / sum.z) * kLn2;
     }
     if (p.k == 0) return;
-    // every part's are in order
-    for (int i = tid; i < parts * kMaxTop; i += kThreads) {
-        const int from = i / kMaxTop, at = i % kMaxTop;
-        if (at >= (from == 0 ? want : p.k) || s_top[i] == 0ull) continue;
-        const unsigned long long key = s_top[i];
-        int ahead = at;
-        for (int q = 0; q < parts; ++q)
-            if (q != from)
-                for (int x = 0; x < (q == 0 ? want : p.k) && s_top[q * kMaxTop + x] > key; ++x) ++ahead;
-        if (ahead >= p.k) continue;
-        const long long to = static_cast<long long>(r) * p.k + ahead;
-        p.top_tokens[to] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
-        p.top_logprobs[to] = (key_value(static_cast<uint32_t>(key >> 32)) - sum.m) * p.inv_t - log_z;
+    // two threads to a key, each with half of the others
+    constexpr int kKeys = kMaxCluster * kMaxTop;
+    static_assert(kThreads == 2 * kKeys, "a thread for half of a key's comparisons");
+    const int i = tid >> 1, half = parts * kMaxTop / 2;
+    const unsigned long long key = i < parts * kMaxTop ? s_top[i] : 0ull;
+    int ahead = 0;
+    const ulonglong2* others = reinterpret_cast<const ulonglong2*>(s_top + (tid & 1) * half);
+#pragma unroll 8
+    for (int q = 0; q < half / 2; ++q) {
+        const ulonglong2 o = others[q];
+        ahead += (o.x > key) + (o.y > key);
     }
+    ahead += __shfl_xor_sync(kAll, ahead, 1);
+    if (key == 0ull || ahead >= p.k || (tid & 1) != 0) return;
+    const long long to = static_cast<long long>(r) * p.k + ahead;
+    p.top_tokens[to] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+    p.top_logprobs[to] = logprob(key_value(static_cast<uint32_t>(key >> 32)));
 }
 
 template <typename T>
@@ -398,9 +445,9 @@ extern "C" int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void
     if (dtype != PE_DTYPE_BF16 && dtype != PE_DTYPE_FP32) { set_error("logits must be bf16 or fp32"); return PE_ERR_ARG; }
     if (top < 0 || top > kMaxTop || top > V) { set_error("top must lie in 0..32 and not exceed V"); return PE_ERR_ARG; }
     if (R > (1 << 30)) { set_error("too many rows for one call"); return PE_ERR_ARG; }
-    const float inv_t = 1.f / temperature;
-    if (!(temperature > 0.f && temperature <= kMaxTemperature && inv_t * 2.f < INFINITY)) {
-        set_error("temperature must be positive and at most 2^64");
+    const float c = 1.4426950408889634f / temperature;
+    if (!(temperature > 0.f && temperature <= kMaxTemperature && c <= kMaxTemperature)) {
+        set_error("temperature must lie in 2^-63 .. 2^64");
         return PE_ERR_ARG;
     }
     if (!logits || !tokens || !logprobs || (top > 0 && (!top_tokens || !top_logprobs))) {
@@ -417,7 +464,7 @@ extern "C" int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void
     int dev = 0, sms = 0;
     const int rc = current_device(&dev, &sms);
     if (rc != PE_OK) return rc;
-    LogprobParams p{R, V, top, logits, ld, tokens, inv_t, logprobs, entropy, top_tokens, top_logprobs};
+    LogprobParams p{R, V, top, logits, ld, tokens, c, 1.f / temperature, logprobs, entropy, top_tokens, top_logprobs};
     // a cluster to a row while rows alone leave multiprocessors idle
     int parts = 1;
     while (parts < kMaxCluster && static_cast<long long>(R) * parts < 2ll * sms && V / (2 * parts) >= kMinSegment) parts *= 2;
