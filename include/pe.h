@@ -512,9 +512,9 @@ int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  * A logit of -inf is a token that cannot be (ln p = -inf, and it adds nothing to
  * the entropy); -FLT_MAX is one like any other (ln p below fp32's range is -inf). A row that holds a NaN or +inf,
  * or only -inf, has no probabilities: NaN in the place of each, NaN logits
- * ordered behind all others. Finite logits have magnitudes up to 2^126 or are
- * -FLT_MAX; the temperature is positive, 2^64 at most. Sums in fp32, each weight
- * off by about 2^-22 of itself. */
+ * ordered behind all others. The temperature lies in 2^-63 .. 2^64; a finite
+ * logit over it has a magnitude up to 2^120, or the logit is -FLT_MAX. Sums in
+ * fp32, each weight off by about 2^-21 of itself. */
 int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void* logits, int64_t ld, const int32_t* tokens,
                       float temperature, float* logprobs, float* entropy, int32_t top, int32_t* top_tokens,
                       float* top_logprobs, void* stream);

@@ -33,6 +33,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kMinSegment = 8 * kThreads;   // values of a CTA at least, where a cluster shares a row
 constexpr int kCand = 2048 + 64;            // values above the bound that are kept; see `collect`
 constexpr int kTies = 512;                  // values equal to it that are
+constexpr int kBatch = 4;                   // vectors of a thread whose loads are in flight together
+constexpr int kAgain = 4;                   // the same where some are read again
 constexpr unsigned kAll = 0xffffffffu;
 
 struct LogprobParams {
@@ -106,18 +108,20 @@ __device__ __forceinline__ Sums join(Sums a, Sums b) {
     return Sums{m, a.z + b.z, a.s + b.s};
 }
 
+// 16 bytes of a row
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int kN = 4;
-    __device__ static __forceinline__ void load(const float* p, float (&v)[4]) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    __device__ static __forceinline__ void values(const uint4& x, float (&v)[4]) {
+        v[0] = __uint_as_float(x.x);
+        v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z);
+        v[3] = __uint_as_float(x.w);
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int kN = 8;
-    __device__ static __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    __device__ static __forceinline__ void values(const uint4& x, float (&v)[8]) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -187,12 +191,13 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams p) {
-    constexpr int kN = Vec<T>::kN, kBatch = kN == 4 ? 4 : 2;   // vectors whose loads are in flight together
+    constexpr int kN = Vec<T>::kN;
     __shared__ Sums s_sums[kWarps];
     __shared__ uint32_t s_best[kWarps];
     __shared__ int s_count, s_equal, s_ties[kTies], s_scan[kWarps];
+    __shared__ uint8_t s_who[kWarps][32];
     __shared__ unsigned long long s_cand[kCand];
-    __shared__ __align__(16) unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
+    __shared__ unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
     __shared__ float4 s_all[kMaxCluster];                         // the parts' sums (m, z, s), in the first CTA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int parts = static_cast<int>(gridDim.x), part = blockIdx.x, r = blockIdx.y + blockIdx.z * gridDim.y;
@@ -205,19 +210,31 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
 
     Sums a{kFloor, 0.f, 0.f};
     float mine = -INFINITY;   // this thread's largest value
-    const T* body = row + seg.body;
+    const uint4* body = reinterpret_cast<const uint4*>(row + seg.body);
     int x = tid;
     for (; x + (kBatch - 1) * kThreads < seg.vecs; x += kBatch * kThreads) {
-        float v[kBatch][kN];
+        uint4 w[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) Vec<T>::load(body + static_cast<size_t>(x + i * kThreads) * kN, v[i]);
+        for (int i = 0; i < kBatch; ++i) w[i] = __ldg(body + x + i * kThreads);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) add(a, mine, v[i], c);
+        for (int i = 0; i < kBatch; ++i) {
+            float v[kN];
+            Vec<T>::values(w[i], v);
+            add(a, mine, v, c);
+        }
     }
-    for (; x < seg.vecs; x += kThreads) {
-        float v[kN];
-        Vec<T>::load(body + static_cast<size_t>(x) * kN, v);
-        add(a, mine, v, c);
+    if (x < seg.vecs) {
+        uint4 w[kBatch - 1];
+#pragma unroll
+        for (int i = 0; i < kBatch - 1; ++i)
+            if (x + i * kThreads < seg.vecs) w[i] = __ldg(body + x + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < kBatch - 1; ++i)
+            if (x + i * kThreads < seg.vecs) {
+                float v[kN];
+                Vec<T>::values(w[i], v);
+                add(a, mine, v, c);
+            }
     }
     {
         const int f = seg.front(tid), t = seg.back(tid);
@@ -277,17 +294,36 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
                 if (n < kTies) s_ties[n] = i;
             }
         };
+        // All lanes read the vectors of the warp's threads that have some, kAgain in flight.
         const bool has = mine >= level;
-        unsigned who = __ballot_sync(kAll, has);
-        while (who != 0) {
-            const int of = __ffs(who) - 1;
-            who &= who - 1;
-            for (int y = warp * 32 + of + lane * kThreads; y < seg.vecs; y += 32 * kThreads) {
-                float v[kN];
-                Vec<T>::load(body + static_cast<size_t>(y) * kN, v);
+        const unsigned who = __ballot_sync(kAll, has);
+        const int those = __popc(who);
+        if (has) s_who[warp][__popc(who & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
+        __syncwarp();
+        const int work = those * ((seg.vecs + kThreads - 1) / kThreads);
+        for (int q0 = lane; q0 < work; q0 += 32 * kAgain) {
+            uint4 w[kAgain];
+            int y[kAgain];
 #pragma unroll
-                for (int i = 0; i < kN; ++i) put(v[i], seg.body + y * kN + i);
+            for (int i = 0; i < kAgain; ++i) {
+                const int q = q0 + 32 * i, at = q / those;
+                y[i] = q < work ? at * kThreads + warp * 32 + s_who[warp][q - at * those] : seg.vecs;
+                if (y[i] < seg.vecs) w[i] = __ldg(body + y[i]);
             }
+#pragma unroll
+            for (int i = 0; i < kAgain; ++i)
+                if (y[i] < seg.vecs) {
+                    float v[kN];
+                    Vec<T>::values(w[i], v);
+                    float top = v[0];
+#pragma unroll
+                    for (int e = 1; e < kN; ++e) top = fmaxf(top, v[e]);
+                    if (top >= level) {
+                        const int at = seg.body + y[i] * kN;
+#pragma unroll 1
+                        for (int e = 0; e < kN; ++e) put(static_cast<float>(row[at + e]), at + e);
+                    }
+                }
         }
         if (has) {
             const int f = seg.front(tid), t = seg.back(tid);
@@ -356,6 +392,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
             for (int i = tid; i < count; i += kThreads) {
                 const unsigned long long key = s_cand[i];
                 int ahead = 0;
+#pragma unroll 8
                 for (int q = 0; q < count; ++q) ahead += s_cand[q] > key;
                 if (ahead < want) s_top[ahead] = key;
             }
@@ -396,23 +433,27 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         if (p.entropy != nullptr) p.entropy[r] = (log_z - sum.s / sum.z) * kLn2;
     }
     if (p.k == 0) return;
-    // two threads to a key, each with half of the others
-    constexpr int kKeys = kMaxCluster * kMaxTop;
-    static_assert(kThreads == 2 * kKeys, "a thread for half of a key's comparisons");
-    const int i = tid >> 1, half = parts * kMaxTop / 2;
-    const unsigned long long key = i < parts * kMaxTop ? s_top[i] : 0ull;
-    int ahead = 0;
-    const ulonglong2* others = reinterpret_cast<const ulonglong2*>(s_top + (tid & 1) * half);
-#pragma unroll 8
-    for (int q = 0; q < half / 2; ++q) {
-        const ulonglong2 o = others[q];
-        ahead += (o.x > key) + (o.y > key);
+    // Every part's keys are in order: a key's rank is its place in its own part
+    // and what is ahead of it in each other one, which a lane of `parts` looks up.
+    for (int i0 = 0; i0 < parts * p.k; i0 += kThreads / parts) {
+        const int i = i0 + tid / parts, q = tid % parts, from = i / p.k, at = i - from * p.k;
+        const bool there = from < parts;
+        const unsigned long long key = there ? s_top[from * kMaxTop + at] : 0ull;
+        int ahead = at;
+        if (q != from) {
+            const unsigned long long* of = s_top + q * kMaxTop;
+            ahead = 0;
+#pragma unroll
+            for (int step = kMaxTop / 2; step > 0; step /= 2)
+                if (of[ahead + step - 1] > key) ahead += step;
+            ahead += of[ahead] > key;
+        }
+        for (int o = 1; o < parts; o <<= 1) ahead += __shfl_xor_sync(kAll, ahead, o);
+        if (!there || key == 0ull || ahead >= p.k || q != 0) continue;
+        const long long to = static_cast<long long>(r) * p.k + ahead;
+        p.top_tokens[to] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+        p.top_logprobs[to] = logprob(key_value(static_cast<uint32_t>(key >> 32)));
     }
-    ahead += __shfl_xor_sync(kAll, ahead, 1);
-    if (key == 0ull || ahead >= p.k || (tid & 1) != 0) return;
-    const long long to = static_cast<long long>(r) * p.k + ahead;
-    p.top_tokens[to] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key));
-    p.top_logprobs[to] = logprob(key_value(static_cast<uint32_t>(key >> 32)));
 }
 
 template <typename T>
