@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv4(const Kv4Params p) {
     using L = Smem<HD, NT>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sm = smem_raw + (1024u - smem_u32(smem_raw) % 1024u) % 1024u;   // (an offset: still known to be shared memory)
     int4* s_info = reinterpret_cast<int4*>(sm + L::kInfo);
     int* s_tile = reinterpret_cast<int*>(sm + L::kTab);
     __shared__ Window s_win;

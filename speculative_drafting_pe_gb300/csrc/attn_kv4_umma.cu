@@ -3,26 +3,41 @@
 //
 // A unit is 64 entries (4 pages) of one (request, kv head); all its query rows
 // (at most 128, the MMA's M) share every entry, so the cache is read once.
-// Roles (448 threads):
-//   warps 8-11  converters, kTeam warps to a unit. Each thread fetches 16-byte
-//               chunks of codes, kDepth units ahead, by asynchronous copies to
-//               a place of its own, and turns them into fp16 tiles of K and of
-//               V (128-byte swizzle, entry-major: K a K-major operand, V an
-//               MN-major one). A value is scale (n - 8) + mid, under a power of
-//               two of its page that puts the page's largest one below 2^15:
-//               n - 8 and the scale are exact, mid and the sum are rounded to
-//               fp16 (2^-11 each). V of entries that no row sees is zero. At
-//               the start of a segment the query rows, as fp16 after an exact
-//               shift by a power of two per row, to tensor memory.
-//   warp 12     one elected lane issues S_t = Q K_t^T (M=128, N=64, A = Q from
+// Roles (640 threads):
+//   warps 18, 19  fetch: the codes and parameters of a unit's pages, kDepth
+//               units ahead, by asynchronous copies.
+//   warps 8-15  converters, kTeam warps to a unit, two (64 wide: four) units at
+//               a time. They turn codes into fp16 tiles of K and of V (128-byte
+//               swizzle, entry-major: K a K-major operand, V an MN-major one)
+//               under a power of two of the page: K as scale n + base, rounded
+//               once, V as scale (n - 8) + mid, mid and the sum rounded (2^-11
+//               each). What falls below fp16's range is 2^-19 of the page's
+//               largest K and 2^-37 of its largest V. Where some row does not
+//               see all of the unit, an entry has a power of two to itself, so
+//               that none moves a row that does not see it. At the start of a
+//               segment the query rows, as fp16 after an exact shift by a power
+//               of two per row, to tensor memory.
+//   warp 16     one elected lane issues S_t = Q K_t^T (M=128, N=64, A = Q from
 //               tensor memory: from shared memory its reads alone would take the
 //               product's whole time)
-//   warp 13     one elected lane issues O += P_t V_t (A = P_t from tensor
+//   warp 17     one elected lane issues O += P_t V_t (A = P_t from tensor
 //               memory)
 //   warps 0-3, 4-7  two softmax groups, thread = query row = TMEM lane: group
 //               x takes the units t = x (mod 2), with a running maximum, sum
 //               and output accumulator of its own; they meet at the end of a
 //               segment.
+// What bounds it is the instructions' supply more than any pipe: five roles'
+// loops share the instruction cache and 54% of the issue slots go. So loops
+// that could be unrolled are not (the whole kernel unrolled: 333 us for 244 at
+// B=128 K=11, 512..8192 entries, 32/4 heads of 128; 13% more code by alternative
+// paths in it: 267), and shared memory is addressed as such, not by generic
+// pointers (248 for 222). Eight converter warps for four: 244 for 270. Now 219 us;
+// 64 requests of 10 rows, 64/8 heads of 64, 1024..4096 entries: 103. Without
+// the widening 187 and 93, without the softmax 183 and 70, without both 149 and
+// 67: the hand-over of a unit between the roles. Scores of a unit in one pass with
+// weights from the old maximum: 229 (a third of the units has a new one);
+// parameters by a warp of their own: 228; 136 registers for the softmax warps by
+// setmaxnreg and scores kept in them: 273.
 // kTurns S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t. Tiles of K
 // and V and S_t have as many places; "S_t is complete" frees K_t's, "P_t V_t is
 // complete" V_t's and S_t's: one commit for each product.
@@ -31,6 +46,8 @@
 // The queries follow it, and the output's columns are put back where they are
 // written.
 #include "attn_kv4.cuh"
+#include <type_traits>
+
 #include "attn_umma_line.cuh"
 
 namespace pe {
@@ -38,29 +55,30 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kThreads = 448;
+constexpr int kThreads = 640;
 constexpr int kUnitPages = 4;
 constexpr int kTile = kUnitPages * kPage;   // entries of a unit
 constexpr int kRows = 128;
 constexpr int kUnits = 640;                 // units of a window
 constexpr int kLeast = 3, kPad = 7;         // a share's positions at least, a segment's end in units
 constexpr int kSoft = 256;                  // softmax threads
-constexpr int kWarpConv = 8, kWarpS = 12, kWarpPv = 13;
-constexpr int kScales = 16;                 // units whose page factors are kept: written kTurns ahead, read a few behind
+constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17, kWarpFetch = 18;   // (and 19)
+constexpr int kScales = 16;                 // units whose factors are kept: written with K kTurns ahead at most, read a few behind
 constexpr int kScaleRec = 2 * kUnitPages;   // floats of a unit's
+constexpr float kHead = 4.f;                // a row's largest contribution stands that much (log2) below the one it moves to
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 template <int HD>
 struct Layout {
-    static constexpr int kTeam = HD == 64 ? 1 : 4;           // converter warps to a unit
+    static constexpr int kTeam = HD == 64 ? 2 : 4;           // converter warps to a unit
     static constexpr int kTurns = HD == 64 ? 5 : 3;          // places of K and V tiles and scores
     static constexpr int kQBufs = HD == 64 ? 2 : 1;          // places of the queries
     static constexpr int kDepth = HD == 64 ? 12 : 6;         // units whose codes are in flight
     static constexpr int kTileBytes = kTile * HD * 2;        // an fp16 tile
     static constexpr int kPageCodes = kPage * HD / 2;        // codes of K or V of a page
-    static constexpr int kPagePar = kPage * 4;
-    static constexpr int kPageBytes = 2 * (kPageCodes + kPagePar);   // codes of K, of V, parameters of K, of V
-    static constexpr int kUnitBytes = kUnitPages * kPageBytes;
+    static constexpr int kPageBytes = 2 * kPageCodes;        // codes of K, of V
+    static constexpr int kParams = kUnitPages * kPageBytes;  // behind the codes: [page][K, V][kPage]
+    static constexpr int kUnitBytes = kParams + kUnitPages * 2 * kPage * 4;
     static constexpr int kK = 0;
     static constexpr int kV = kK + kTurns * kTileBytes;
     static constexpr int kRing = kV + kTurns * kTileBytes;
@@ -69,9 +87,11 @@ struct Layout {
     static constexpr int kCs = kUnit + kUnits * kUnitPages * 4;      // [kCsTurns][kRows]
     static constexpr int kEx = kCs + kCsTurns * kRows * 4;   // [2][kRows] float4
     static constexpr int kScale = kEx + 2 * kRows * 16;      // [kScales][factors of 4 pages' K, exponents of their V]
-    static constexpr int kNan = kScale + kScales * kScaleRec * 4;    // [kTurns][kTile] bytes
-    static constexpr int kBar = kNan + kTurns * kTile;
-    static constexpr int kBars = 5 * kTurns + 2 * kQBufs;
+    static constexpr int kEnt = kScale + kScales * kScaleRec * 4;    // [kScales][kTile] (factor of K, exponent of V)
+    static constexpr int kPar = kEnt + kScales * kTile * 8;  // [kDepth][K, V][kTile] what widens an entry, as fp16
+    static constexpr int kBar = kPar + kDepth * 2 * kTile * 8;
+    static constexpr int kBars = 5 * kTurns + 2 * kQBufs + 2 * kDepth;
+    static_assert(2 * kTurns + 4 <= kScales, "factors that are in use");
     static constexpr int kTmem = kBar + kBars * 8;
     static constexpr int kBytes = kTmem + 16 + 1024;
     // tensor memory: S_t in columns 64 (t mod kTurns) .., group x's output x * HD behind them, then the queries
@@ -79,7 +99,7 @@ struct Layout {
     static_assert(kColQ + kQBufs * HD / 2 <= 512, "tensor memory");
     static_assert(kBytes <= 232448 - 2048, "shared memory of a block");
 };
-// the barriers of a window: k_full, v_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [kQBufs]
+// the barriers of a window: k_full, v_full, s_full, p_full, pv_done [kTurns], q_full, q_empty [kQBufs], full, empty [kDepth]
 template <int HD>
 __device__ __forceinline__ void init_bars(uint64_t* bars, int stall) {
     using L = Layout<HD>;
@@ -95,32 +115,84 @@ __device__ __forceinline__ void init_bars(uint64_t* bars, int stall) {
         mbar_init(&bars[5 * kTurns + s], 4);
         mbar_init(&bars[5 * kTurns + L::kQBufs + s], 1);
     }
+    for (int s = 0; s < L::kDepth; ++s) {
+        uint64_t* ring = bars + 5 * kTurns + 2 * L::kQBufs + s;
+        mbar_init(ring, 64);
+        mbar_init(ring + L::kDepth, L::kTeam);
+    }
     fence_mbar_init();
 }
+
+// A unit's place among N that are taken in turn, and the parity of its use.
+template <int N>
+struct Place {
+    int at;
+    uint32_t odd = 0;
+    __device__ __forceinline__ void step(int by) {
+        at += by;
+        if (at >= N) at -= N, odd ^= 1u;
+    }
+};
 
 // What the CTA has set going in this window, units of each kind.
 struct Issued {
     int s, pv;   // score products, P.V products
 };
 
-// Four words of codes of an entry as fp16, at the places of its chunk in a tile:
-// chunk positions j0 .. j0 + 3 of row r. far: of a block's second 64 bytes' twin
-// in the other block, written in another order so that no bank is met twice.
-__device__ __forceinline__ void widen_chunk(const uint4& codes, uint32_t scale, uint32_t mid, uint8_t* row, int r, int j0, bool far) {
-    const __half2 s2 = *reinterpret_cast<const __half2*>(&scale), c2 = *reinterpret_cast<const __half2*>(&mid);
-    const uint32_t w[4] = {far ? codes.z : codes.x, far ? codes.w : codes.y, far ? codes.x : codes.z, far ? codes.y : codes.w};
-    const int turn = (far ? 2 : 0) ^ j0 ^ (r & 7);
+// arrives once this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The eight codes n of a word as scale * n + base, one rounding: a code under
+// fp16's lowest exponent is n * 2^-24, one four bits further up n * 2^-20, and
+// by: scale * 2^24 and scale * 2^20 in its halves.
+__device__ __forceinline__ void widen_k(uint32_t w, uint32_t by, uint32_t base, uint32_t (&v)[4]) {
+    const __half2 lo = __low2half2(*reinterpret_cast<const __half2*>(&by)), hi = __high2half2(*reinterpret_cast<const __half2*>(&by));
+    const __half2 b2 = __low2half2(*reinterpret_cast<const __half2*>(&base));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t x = h == 0 ? w : w >> 8, n0 = x & 0x000F000Fu, n1 = x & 0x00F000F0u;
+        const __half2 v0 = __hfma2(*reinterpret_cast<const __half2*>(&n0), lo, b2);
+        const __half2 v1 = __hfma2(*reinterpret_cast<const __half2*>(&n1), hi, b2);
+        v[2 * h] = *reinterpret_cast<const uint32_t*>(&v0);
+        v[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&v1);
+    }
+}
+// As scale * (n - 8) + mid, two roundings (mid's, and the sum's).
+__device__ __forceinline__ void widen_v(uint32_t w, uint32_t scale, uint32_t mid, uint32_t (&v)[4]) {
+    uint32_t n[4];
+    widen(w, n);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&n[y]), *reinterpret_cast<const __half2*>(&scale),
+                                  *reinterpret_cast<const __half2*>(&mid));
+        v[y] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+// Four words of codes of an entry to the places x ^ turn of its chunk of a tile's row.
+template <int SIDE>
+__device__ __forceinline__ void widen_chunk(const uint2& w0, const uint2& w1, const uint2& by, uint8_t* row, int turn) {
+    const uint32_t w[4] = {w0.x, w0.y, w1.x, w1.y};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-        uint32_t n[4], v[4];
-        widen(w[x], n);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&n[y]), s2, c2);
-            v[y] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(row + ((x ^ turn) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+        uint32_t v[4];
+        if constexpr (SIDE == 0) widen_k(w[x], by.x, by.y, v);
+        else widen_v(w[x], by.x, by.y, v);
+        *reinterpret_cast<uint4*>(row + (turn ^ (x << 4))) = make_uint4(v[0], v[1], v[2], v[3]);
     }
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // The n units of a window by every role; FIRST: of the share's first one. false
@@ -135,7 +207,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
     float* s_cs = reinterpret_cast<float*>(sm + L::kCs);
     float4* s_ex = reinterpret_cast<float4*>(sm + L::kEx);
     float* s_scale = reinterpret_cast<float*>(sm + L::kScale);
-    uint8_t* s_nan = sm + L::kNan;
+    float2* s_ent = reinterpret_cast<float2*>(sm + L::kEnt);
     uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t* cv_full = k_full + kTurns;
     uint64_t* s_full = cv_full + kTurns;
@@ -143,13 +215,15 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
     uint64_t* pv_done = p_full + kTurns;
     uint64_t* q_full = pv_done + kTurns;
     uint64_t* q_empty = q_full + kQBufs;
+    uint64_t* full = q_empty + kQBufs;
+    uint64_t* empty = full + L::kDepth;
+    uint2* s_par = reinterpret_cast<uint2*>(sm + L::kPar);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.nq / p.nkv;
 
     const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L::kTmem);
     const uint32_t t_o = tmem + L::kColO, t_q = tmem + L::kColQ;
     bool ok = true;
-    auto turn = [](int i) { return static_cast<uint32_t>((i / kTurns) & 1); };   // parity of unit i's use of its place
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_ab(bar, parity, nullptr, 0u, abort); };
 
     if (warp == kWarpS || warp == kWarpPv) {
@@ -158,40 +232,42 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
         const bool scores = warp != kWarpPv;
         const uint32_t idesc_s = umma_idesc(0, kRows, kTile);   // format 0: fp16
         const uint32_t idesc_o = umma_idesc(0, kRows, HD) | kIdescBMnMajor;
-        const uint32_t k_base = smem_u32(sm + L::kK), v_base = smem_u32(sm + L::kV);
+        const uint64_t k_desc = umma_desc_sw128(smem_u32(sm + L::kK)), v_desc = umma_desc_sw128_mn(smem_u32(sm + L::kV), kTile * 128);
         int seg = 0, end = 0, no = -1, i = 0;
-        for (; i < n; ++i) {
-            const int x = i % kTurns;
+        Place<kTurns> c{0};
+        for (; i < n; ++i, c.step(1)) {
+            const int x = c.at;
             if (i == end) {
                 seg = i;
                 end = i + min(s_info[i].w - s_info[i].z, n - i);
                 ++no;
                 if (scores) ok = wait(&q_full[no % kQBufs], static_cast<uint32_t>((no / kQBufs) & 1));
             }
-            if (scores) ok = ok && wait(&k_full[x], turn(i)) && (i < kTurns || wait(&pv_done[x], turn(i) ^ 1u));
-            else ok = ok && wait(&cv_full[x], turn(i)) && wait(&p_full[x], turn(i));
+            if (scores) ok = ok && wait(&k_full[x], c.odd) && (i < kTurns || wait(&pv_done[x], c.odd ^ 1u));
+            else ok = ok && wait(&cv_full[x], c.odd) && wait(&p_full[x], c.odd);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
             const uint32_t t_s = tmem + static_cast<uint32_t>(x * kTile);
             if (scores) {
-                const uint32_t q_addr = t_q + static_cast<uint32_t>(no % kQBufs * (HD / 2)), k_addr = k_base + x * L::kTileBytes;
+                const uint32_t q_addr = t_q + static_cast<uint32_t>(no % kQBufs * (HD / 2));
+                const uint64_t k_at = k_desc + static_cast<uint32_t>(x * L::kTileBytes / 16);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk)
                         umma_bf16_a_tmem(t_s, q_addr + static_cast<uint32_t>(kk * 8),
-                                         umma_desc_sw128(k_addr + (kk >> 2) * kTile * 128 + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+                                         k_at + static_cast<uint32_t>(((kk >> 2) * kTile * 128 + (kk & 3) * 32) / 16), idesc_s, kk > 0 ? 1u : 0u);
                     umma_commit(&s_full[x]);
                     if (i + 1 == end) umma_commit(&q_empty[no % kQBufs]);
                 }
             } else {
-                const uint32_t v_addr = v_base + x * L::kTileBytes;
+                const uint64_t v_at = v_desc + static_cast<uint32_t>(x * L::kTileBytes / 16);
                 const uint32_t more = i - seg > 1 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         umma_bf16_a_tmem(t_o + static_cast<uint32_t>((i & 1) * HD), t_s + static_cast<uint32_t>(kk * 8),
-                                         umma_desc_sw128_mn(v_addr + kk * 16 * 128, kTile * 128), idesc_o,
+                                         v_at + static_cast<uint32_t>(kk * 16 * 128 / 16), idesc_o,
                                          kk > 0 ? 1u : more);
                     umma_commit(&pv_done[x]);
                 }
@@ -200,57 +276,32 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
         }
         if (lane == 0) (scores ? issued->s : issued->pv) = i;
         if (!FIRST && ok && win->more) {   // what this warp committed has arrived: the next window takes the barriers anew
-            for (int i = max(0, n - kTurns); i < n; ++i) ok = ok && wait(scores ? &s_full[i % kTurns] : &pv_done[i % kTurns], turn(i));
+            for (int i = max(0, n - kTurns); i < n; ++i)
+                ok = ok && wait(&(scores ? s_full : pv_done)[i % kTurns], static_cast<uint32_t>((i / kTurns) & 1));
             for (int x = max(0, no + 1 - kQBufs); scores && x <= no; ++x)
                 ok = ok && wait(&q_empty[x % kQBufs], static_cast<uint32_t>((x / kQBufs) & 1));
             ok = __all_sync(0xffffffffu, ok);
         }
         __syncwarp();
     } else if (warp >= kWarpConv && warp < kWarpS) {
-        constexpr int kTeam = L::kTeam, kTeams = 4 / kTeam, kAhead = L::kDepth / kTeams, kMine = kUnitPages / kTeam;
-        static_assert(L::kDepth % kTeams == 0, "a warp's units");
-        const int ct = tid & 127, team = (warp - kWarpConv) / kTeam, part = (warp - kWarpConv) % kTeam;
+        constexpr int kTeam = L::kTeam, kTeams = 8 / kTeam, kMine = kUnitPages / kTeam;
+        const int ct = tid & 127, quad = (warp - kWarpConv) / 4, team = (warp - kWarpConv) / kTeam, part = (warp - kWarpConv) % kTeam;
         constexpr int kChunks = HD / 32, kPasses = kPage * kChunks / 32, kPass = 32 / kChunks;   // chunks of an entry; passes over a page
         const int ch = lane % kChunks, row0 = lane / kChunks;
-        const uint64_t policy = l2_policy_evict_first();
-        const uint32_t ring_at = smem_u32(sm + L::kRing);
-        // page q of this warp's of unit i: codes of K and V by all lanes, parameters of K by lanes 0-3, of V by 4-7
-        auto fetch = [&](int i) {
-            if (i < n) {
-#pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                    const int page = part * kMine + q, tile = s_tile[i * kUnitPages + page];
-                    if (tile < 0) continue;
-                    const uint32_t at = ring_at + (i % L::kDepth) * L::kUnitBytes + page * L::kPageBytes;
-#pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-                        const uint8_t* from = (side == 0 ? p.k_codes : p.v_codes) + static_cast<long long>(tile) * L::kPageCodes + lane * 16;
-#pragma unroll
-                        for (int x = 0; x < kPasses; ++x)
-                            copy_async<16>(at + side * L::kPageCodes + x * 512 + lane * 16, from + x * 512, policy);
-                    }
-                    if (lane < 8)
-                        copy_async<16>(at + 2 * L::kPageCodes + lane * 16,
-                                       (lane < 4 ? p.k_params : p.v_params) + static_cast<long long>(tile) * kPage + (lane & 3) * 4, policy);
-                }
-            }
-            copies_commit();
-        };
-#pragma unroll
-        for (int x = 0; x < kAhead; ++x) fetch(team + x * kTeams);
-        int seg = 0, end = 0, no = -1, S = 0, last = 0;
+        int seg = 0, end = 0, no = -1, S = 0, last = 0, unit0 = 0;
         // the query rows of the segments up to the one of unit `upto`: every
         // warp has 32 of them
         auto queries = [&](int upto) {
             while (ok && end <= upto) {
                 const int4 info = s_info[end];
                 seg = end;
-                end = seg + min(info.w - info.z, n - seg);
-                ++no;
+                unit0 = info.z;
+                end += min(info.w - info.z, n - end);
                 const int b = info.x;
-                S = p.seq_lens[b];
                 const int rows = p.rows != nullptr ? p.rows[b] : p.K;
+                S = p.seq_lens[b];
                 last = S + rows - 1;
+                if ((++no & 1) != quad) continue;   // the other four warps'
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
@@ -264,7 +315,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     for (int x = 0; x < HD / 64; ++x) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + x * 64));
                 }
                 uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
                 for (int x = 0; x < HD / 8; ++x) {
                     const uint4 q = load(x);
                     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -275,9 +326,9 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                 if (no >= kQBufs) ok = wait(&q_empty[no % kQBufs], static_cast<uint32_t>((no / kQBufs) & 1) ^ 1u);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
-                // the row times 2^(127 - E): its largest value lies in [1, 2)
-                const int E = min(max(static_cast<int>(top >> 23), 1), 253);
-                const float down = __uint_as_float(static_cast<uint32_t>(254 - E) << 23);
+                // the row times 2^(141 - E): its largest value lies in [2^14, 2^15)
+                const int E = min(max(static_cast<int>(top >> 23), 14), 253);
+                const float down = __uint_as_float(static_cast<uint32_t>(268 - E) << 23);
                 const uint32_t to = t_q + static_cast<uint32_t>(no % kQBufs * (HD / 2)) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll 1
                 for (int half = 0; half < HD / 64; ++half) {
@@ -298,81 +349,127 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     __syncwarp();
                     tmem_st32(to + static_cast<uint32_t>(half * 32), v);
                 }
-                // a row that holds an infinity (or a NaN) is NaN
+                // back from there (and K from 2^15 below its factor); a row
+                // that holds an infinity (or a NaN) is NaN
                 s_cs[(no & (kCsTurns - 1)) * kRows + ct] =
-                    top >= 0x7F800000u ? NAN : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E) << 23);
+                    top >= 0x7F800000u ? NAN : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(E + 1) << 23);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[no % kQBufs]);
             }
         };
-        for (int i = team; i < n; i += kTeams) {
-            const int c = i % kTurns;
-            queries(i);
-            copies_wait<kAhead - 1>();
-            __syncwarp();   // the parameters come by eight lanes
-            const uint8_t* unit = sm + L::kRing + (i % L::kDepth) * L::kUnitBytes;
-            const int e0 = (s_info[seg].z + i - seg) * kTile;
-            const bool inner = e0 + kTile - 1 <= S;
-            // Powers of two that put the pages' K and V below 2^15: of the
-            // exponents of base and 15 scale, of entries that some row sees.
-            float up[kMine][2];
+        Place<kTurns> at{team};
+        Place<L::kDepth> ring{team};
+        for (int i = team;; i += kTeams, at.step(kTeams), ring.step(kTeams)) {
+            queries(min(i, n - 1));
+            if (i >= n) break;
+            const int c = at.at, d = ring.at;
+            ok = ok && wait(&full[d], ring.odd);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // What widens the entries of this warp's pages: lanes 0-15 K's, 16-31 V's
+            const int e0 = (unit0 + i - seg) * kTile;
+            const bool alone = e0 + kTile - 1 > S || p.scale_log2 < 0.f;
+            const bool v_side = lane >= kPage;
 #pragma unroll
             for (int q = 0; q < kMine; ++q) {
-                const int page = part * kMine + q;
-                const uint32_t par = reinterpret_cast<const uint32_t*>(unit + page * L::kPageBytes + 2 * L::kPageCodes)[lane];
-                const uint32_t eb = (par >> 23) & 0xFFu, es = (par >> 7) & 0xFFu;
-                uint32_t e = e0 + page * kPage + (lane & 15) > last || eb == 255u || es == 255u ? 0u : max(eb, es + 4u);
-                const uint32_t ek = __reduce_max_sync(0xffffffffu, lane < 16 ? e : 0u), ev = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : e);
-                // stored = value * 2^(14 - (e - 126)), |value| < 2^(e - 125)
-                const uint32_t fk = min(max(ek, 24u), 254u), fv = min(max(ev, 24u), 254u);
-                up[q][0] = __uint_as_float((267u - fk) << 23);
-                up[q][1] = __uint_as_float((267u - fv) << 23);
-                if (lane == 0) {
-                    float* rec = s_scale + (i % kScales) * kScaleRec + page;
-                    rec[0] = __uint_as_float((fk - 13u) << 23);
-                    rec[kUnitPages] = static_cast<float>(static_cast<int>(fv) - 140);
+                const int page = part * kMine + q, e = page * kPage + lane % kPage;
+                const uint32_t pr = reinterpret_cast<const uint32_t*>(sm + L::kRing + d * L::kUnitBytes + L::kParams)[page * 32 + lane];
+                // of base and of 15 scale
+                const uint32_t eb = (pr >> 23) & 0xFFu, es = (pr >> 7) & 0xFFu;
+                uint32_t f = e0 + e > last || eb == 255u || es == 255u ? 0u : max(eb, es + 4u);
+                // Where some row does not see all of the unit an entry has a power of
+                // two to itself: what a row does not see does not move its outputs.
+                if (!alone) {
+                    const uint32_t of_k = __reduce_max_sync(0xffffffffu, v_side ? 0u : f), of_v = __reduce_max_sync(0xffffffffu, v_side ? f : 0u);
+                    f = v_side ? of_v : of_k;
+                }
+                // |base| and 16 scale are below 2^(f - 126). K is stored times
+                // 2^(122 - f) (below 2^-3, its scale below 2^-8), V times
+                // 2^(140 - f) (below 2^15).
+                f = min(max(f, 24u), 254u);
+                const float up = __uint_as_float((267u - f) << 23), mid = mid_of(pr), scale = scale_of(pr) * up;
+                const float back = __uint_as_float((f - 10u) << 23), lg = static_cast<float>(static_cast<int>(f) - 140);
+                const bool odd = mid != mid;
+                uint2 by;
+                if (!v_side) {
+                    const float base = odd ? NAN : __uint_as_float(pr & 0xFFFF0000u) * up * 0x1p-18f;
+                    by = make_uint2(pack_f16(scale * 64.f, scale * 4.f), pack_f16(base, base));
+                } else {
+                    by = make_uint2(pack_f16(scale, scale), pack_f16(mid * up, mid * up));
+                    if (alone && (odd || e0 + e > last)) by = make_uint2(0u, 0u);
+                }
+                s_par[(d * 2 + v_side) * kTile + e] = by;
+                if (alone) {
+                    // A V that is not finite enters through the score, and only of the rows that see it.
+                    const bool v_odd = __shfl_down_sync(0xffffffffu, static_cast<int>(odd), kPage) != 0;
+                    float* ent = reinterpret_cast<float*>(s_ent + (i % kScales) * kTile + e);
+                    ent[v_side] = v_side ? lg : v_odd ? NAN : back;
+                } else if (lane % kPage == 0) {
+                    s_scale[(i % kScales) * kScaleRec + v_side * kUnitPages + page] = v_side ? lg : back;
                 }
             }
-            auto widen_page = [&](int q, int side, uint8_t* tile_at, bool keep_all) {
-                const int page = part * kMine + q;
-                const uint8_t* codes = unit + page * L::kPageBytes + side * L::kPageCodes;
-                const uint32_t* par = reinterpret_cast<const uint32_t*>(unit + page * L::kPageBytes + 2 * L::kPageCodes) + side * kPage;
-#pragma unroll
-                for (int x = 0; x < kPasses; ++x) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + x * 512 + lane * 16);
-                    const int r = row0 + x * kPass, e = page * kPage + r;
-                    const uint32_t pr = par[r];
-                    float s = scale_of(pr) * up[q][side], m = mid_of(pr) * up[q][side];
-                    if (!keep_all) {
-                        // no one's, or not finite: it enters through the score
-                        const bool odd = m != m, out = e0 + e > last;
-                        if (odd || out) s = m = 0.f;
-                        if (ch == 0) s_nan[c * kTile + e] = static_cast<uint8_t>(odd && !out);
-                    }
-                    const uint32_t s2 = pack_f16(s, s), c2 = pack_f16(m, m);
-                    widen_chunk(w, s2, c2, tile_at + (ch >> 1) * kTile * 128 + e * 128, e, (ch & 1) * 4, (ch >> 1) != 0);
+            __syncwarp();
+            // far: words in another order, so that the lanes of a store meet no bank twice
+            const bool far = (ch >> 1) != 0;
+            const uint8_t* codes = sm + L::kRing + d * L::kUnitBytes + part * kMine * L::kPageBytes + lane * 16;
+            const uint2* par = s_par + d * 2 * kTile + part * kMine * kPage + row0;
+            uint8_t* tile = sm + c * L::kTileBytes + (ch >> 1) * kTile * 128 + (part * kMine * kPage + row0) * 128;
+            const int place = ((far ? 2 : 0) ^ ((ch & 1) * 4) ^ (row0 & 7)) << 4;
+            auto widen_side = [&](auto of) {
+                constexpr int kSide = decltype(of)::value;
+                // the last reader of the place: S, or P V, of the unit kTurns back
+                if (i >= kTurns) ok = ok && wait(&(kSide == 0 ? s_full : pv_done)[c], at.odd ^ 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+#pragma unroll 1
+                for (int x = 0; x < kMine * kPasses; ++x) {
+                    static_assert(kPass % 8 == 0, "the swizzle of a thread's rows");
+                    const int r = x * kPass;
+                    const uint8_t* from = codes + kSide * L::kPageCodes + (r / kPage) * L::kPageBytes + (r % kPage) * (HD / 2);
+                    const uint2 w0 = *reinterpret_cast<const uint2*>(from + (far ? 8 : 0)), w1 = *reinterpret_cast<const uint2*>(from + (far ? 0 : 8));
+                    widen_chunk<kSide>(w0, w1, par[kSide * kTile + r], tile + kSide * (L::kV - L::kK) + r * 128, place);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&(kSide == 0 ? k_full : cv_full)[c]);
             };
-            if (i >= kTurns) ok = ok && wait(&s_full[c], turn(i) ^ 1u);   // S of the unit before it in this place
-            ok = __all_sync(0xffffffffu, ok);
+            widen_side(std::integral_constant<int, 0>{});
+            if (ok) widen_side(std::integral_constant<int, 1>{});
             if (!ok) break;
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) widen_page(q, 0, sm + L::kK + c * L::kTileBytes, true);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_full[c]);
-            if (i >= kTurns) ok = ok && wait(&pv_done[c], turn(i) ^ 1u);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) widen_page(q, 1, sm + L::kV + c * L::kTileBytes, inner);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&cv_full[c]);
-            fetch(i + L::kDepth);   // (all lanes have read the unit's)
+            if (lane == 0) mbar_arrive(&empty[d]);
         }
-        queries(n - 1);
+    } else if (warp >= kWarpFetch) {
+        // a warp for the codes of K, and one for V's and both sides' parameters
+        const bool v_side = warp > kWarpFetch;
+        const uint64_t policy = l2_policy_evict_first();
+        const uint8_t* codes = (v_side ? p.v_codes : p.k_codes) + lane * 16;
+        const uint32_t* params = ((lane >> 2) & 1 ? p.v_params : p.k_params) + (lane & 3) * 4;
+        const uint32_t to = smem_u32(sm + L::kRing) + v_side * L::kPageCodes + lane * 16;
+        const uint32_t to_params = smem_u32(sm + L::kRing) + L::kParams + lane * 16;
+        Place<L::kDepth> at{0};
+        for (int i = 0; i < n; ++i, at.step(1)) {
+            const int d = at.at;
+            if (i >= L::kDepth) ok = wait(&empty[d], at.odd ^ 1u);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUnitPages);
+            const int tile[kUnitPages] = {tl.x, tl.y, tl.z, tl.w};
+#pragma unroll
+            for (int q = 0; q < kUnitPages; ++q) {
+                if (tile[q] < 0) continue;
+                const uint8_t* from = codes + static_cast<size_t>(tile[q]) * L::kPageCodes;
+#pragma unroll
+                for (int x = 0; x < L::kPageCodes; x += 512)
+                    copy_async<16>(to + d * L::kUnitBytes + q * L::kPageBytes + x, from + x, policy);
+            }
+            if (v_side) {
+                const int mine = s_tile[i * kUnitPages + (lane >> 3)];
+                if (mine >= 0) copy_async<16>(to_params + d * L::kUnitBytes, params + static_cast<size_t>(mine) * kPage, policy);
+            }
+            copies_arrive(&full[d]);
+        }
+        copies_commit();
         copies_wait<0>();
     } else if (warp < kWarpConv) {
         // ------------------------------------------------ softmax: thread = query row
@@ -381,6 +478,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
         const uint32_t t_mine = t_o + lane_off + static_cast<uint32_t>(grp * HD);
         const bool flip = p.scale_log2 < 0.f;
         int no = 0;
+        Place<kTurns> c{grp}, had{grp};   // of this group's next unit, and of its last one
         for (int seg = 0; seg < n; ++no) {
             const int4 info = s_info[seg];
             const int b = info.x, head = info.y;
@@ -391,64 +489,59 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
             const bool busy = (warp & 3) * 32 < R;      // some row of this warp is live
             const int j = row / G, lim = S + j;
             const int first = seg + ((seg ^ grp) & 1);  // this group's first unit of the segment
-            const int count = first < seg + len ? (seg + len - first + 1) / 2 : 0;
             float m = -INFINITY, md = -INFINITY, l = 0.f, mark = 0.f, cs = 0.f;
-            for (int i = first; i < seg + len; i += 2) {
-                const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i % kTurns) * kTile);
-                if (ok) ok = wait(&s_full[i % kTurns], turn(i));
+            for (int i = first; i < seg + len; i += 2, had = c, c.step(2)) {
+                const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>(c.at * kTile);
+                if (ok) ok = wait(&s_full[c.at], c.odd);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after_sync();
                 if (busy) {
                     if (i == first) cs = s_cs[(no & (kCsTurns - 1)) * kRows + row];
-                    const float4* sc = reinterpret_cast<const float4*>(s_scale + (i % kScales) * kScaleRec);
-                    const float4 ks = sc[0], vlg = sc[1];   // factors of the pages' K, exponents of their V
                     const int4 tl = *reinterpret_cast<const int4*>(s_tile + i * kUnitPages);
-                    float s[kTile];
-                    tmem_ld64(t_s, s);
                     if (tl.x == -1 || tl.y == -1 || tl.z == -1 || tl.w == -1) mark = kMarkBadPage;
-                    float kf[4] = {cs * ks.x, cs * ks.y, cs * ks.z, cs * ks.w};
                     const int e0 = (info.z + i - seg) * kTile;
-                    const bool inner = e0 + kTile - 1 <= S;
-                    if (!inner || flip) {
-                        // the page factors first: a masked score must not meet
-                        // a factor of 0, nor a maximum a negative one
+                    const bool alone = e0 + kTile - 1 > S || flip;   // factors of entries, not of pages
+                    const float2* ent = s_ent + (i % kScales) * kTile;
+                    // 16 of the unit's scores with their entries' factors, -inf where the row does not see them
+                    auto scores = [&](int at, float (&s)[16]) {
+                        tmem_ld16(t_s + static_cast<uint32_t>(at), s);
 #pragma unroll
-                        for (int x = 0; x < kTile; ++x) s[x] *= kf[x >> 4];
-                        kf[0] = kf[1] = kf[2] = kf[3] = 1.f;
-                        if (!inner) {
-                            // Some row does not see all of it. A NaN in a V
-                            // that only some rows see enters through the score
-                            // (the converters cleared it, before V.P needs it).
-                            ok = wait(&cv_full[i % kTurns], turn(i));
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) continue;
-                            const uint4* nan = reinterpret_cast<const uint4*>(s_nan + (i % kTurns) * kTile);
-#pragma unroll 1
-                            for (int q = 0; q < kTile / 16; ++q) {
-                                const uint4 f = nan[q];
-                                if ((f.x | f.y | f.z | f.w) == 0u) continue;   // as good as always
-#pragma unroll
-                                for (int x = 0; x < kTile; ++x) {
-                                    const uint32_t w = (x & 12) == 0 ? f.x : (x & 12) == 4 ? f.y : (x & 12) == 8 ? f.z : f.w;
-                                    if ((x >> 4) == q && ((w >> (8 * (x & 3))) & 0xFFu)) s[x] = NAN;
-                                }
-                            }
-#pragma unroll
-                            for (int x = 0; x < kTile; ++x)
-                                if (e0 + x > lim) s[x] = -INFINITY;
+                        for (int x = 0; x < 16; ++x) {
+                            s[x] = s[x] * cs * ent[at + x].x;
+                            if (e0 + at + x > lim) s[x] = -INFINITY;
                         }
-                    }
-                    const float vl[4] = {vlg.x, vlg.y, vlg.z, vlg.w};
-                    float t[4], top = -INFINITY;
+                        __syncwarp();
+                    };
+                    // largest score, largest score + exponent of its V
+                    float top = -INFINITY, most = -INFINITY, kf[4], vl[4];
+                    if (!alone) {
+                        const float4* sc = reinterpret_cast<const float4*>(s_scale + (i % kScales) * kScaleRec);
+                        const float4 ks = sc[0], vlg = sc[1];   // of the pages
+                        kf[0] = cs * ks.x; kf[1] = cs * ks.y; kf[2] = cs * ks.z; kf[3] = cs * ks.w;
+                        vl[0] = vlg.x; vl[1] = vlg.y; vl[2] = vlg.z; vl[3] = vlg.w;
+                        float s[kTile];
+                        tmem_ld64(t_s, s);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float* sq = s + q * 16;
-                        float t4[4];
+                        for (int q = 0; q < 4; ++q) {
+                            const float* sq = s + q * 16;
+                            const float a = max3(max3(sq[0], sq[1], sq[2]), max3(sq[3], sq[4], sq[5]), max3(sq[6], sq[7], sq[8]));
+                            const float b = max3(max3(sq[9], sq[10], sq[11]), max3(sq[12], sq[13], sq[14]), sq[15]);
+                            const float t = fmaxf(a, b) * kf[q];
+                            top = fmaxf(top, t);
+                            most = fmaxf(most, t + vl[q]);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int at = 0; at < kTile; at += 16) {
+                            float s[16];
+                            scores(at, s);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) t4[x] = fmaxf(fmaxf(sq[x], sq[x + 4]), fmaxf(sq[x + 8], sq[x + 12]));
-                        t[q] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q];
-                        top = fmaxf(top, t[q]);
+                            for (int x = 0; x < 16; ++x) {
+                                top = fmaxf(top, s[x]);
+                                most = fmaxf(most, s[x] + ent[at + x].y);
+                            }
+                        }
                     }
                     if (top > m + kRescale) {
                         l *= m == -INFINITY ? 0.f : ex2(m - top);
@@ -457,55 +550,82 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     }
                     // 0 in the place of the maximum where a row has seen no entry
                     const float mm = m == -INFINITY ? 0.f : -m;
-                    const float most = fmaxf(fmaxf(t[0] + mm + vl[0], t[1] + mm + vl[1]), fmaxf(t[2] + mm + vl[2], t[3] + mm + vl[3]));
+                    most += mm;
                     float f = 1.f;
                     if (most > md + kRescale) {
-                        f = md == -INFINITY ? 0.f : ex2(md - most);
-                        md = most;
+                        f = md == -INFINITY ? 0.f : ex2(md - most - kHead);
+                        md = most + kHead;
                     }
                     if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
                         // this group's last P.V has to be done
-                        ok = wait(&pv_done[(i - 2) % kTurns], turn(i - 2));
+                        ok = wait(&pv_done[had.at], had.odd);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) continue;
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int c = 0; c < HD / 16; ++c) {
-                            float o[16];
-                            tmem_ld16(t_mine + static_cast<uint32_t>(c * 16), o);
+                        for (int c = 0; c < HD / 32; ++c) {
+                            float o[32];
+                            uint32_t v[32];
+                            tmem_ld32(t_mine + static_cast<uint32_t>(c * 32), o);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] *= f;
-                            tmem_st16(t_mine + static_cast<uint32_t>(c * 16), o);
+                            for (int x = 0; x < 32; x += 2) {
+                                const float2 y = unf2(mul2(f2(o[x], o[x + 1]), f2(f, f)));
+                                v[x] = __float_as_uint(y.x);
+                                v[x + 1] = __float_as_uint(y.y);
+                            }
+                            tmem_st32(t_mine + static_cast<uint32_t>(c * 32), v);
                         }
                     }
-                    const uint64_t m2 = f2(mm, mm);
                     const float from = kLift - md;
-                    const float vr[4] = {lift(from, vl[0]), lift(from, vl[1]), lift(from, vl[2]), lift(from, vl[3])};
                     uint64_t sum[2] = {0ull, 0ull};
-                    uint32_t pk[32];
+                    // P of a half goes where S of the first half stood
+                    if (!alone) {
+                        const uint64_t m2 = f2(mm, mm);
+                        const float vr[4] = {lift(from, vl[0]), lift(from, vl[1]), lift(from, vl[2]), lift(from, vl[3])};
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            float s[32], pk[16];   // pk: pairs of fp16
+                            tmem_ld32(t_s + static_cast<uint32_t>(half * 32), s);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint64_t k2 = f2(kf[q], kf[q]), r2 = f2(vr[q], vr[q]);
+                            for (int q = 0; q < 2; ++q) {
+                                const float kq = half == 0 ? kf[q] : kf[2 + q], rq = half == 0 ? vr[q] : vr[2 + q];
+                                const uint64_t k2 = f2(kq, kq), r2 = f2(rq, rq);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const float2 a = unf2(fma2(f2(s[q * 16 + 2 * x], s[q * 16 + 2 * x + 1]), k2, m2));
-                            const uint64_t w = f2(ex2(a.x), ex2(a.y));
-                            sum[x & 1] = add2(sum[x & 1], w);
-                            const float2 r = unf2(mul2(w, r2));
-                            pk[q * 8 + x] = pack_f16(r.x, r.y);
+                                for (int x = 0; x < 8; ++x) {
+                                    const float2 a = unf2(fma2(f2(s[q * 16 + 2 * x], s[q * 16 + 2 * x + 1]), k2, m2));
+                                    const uint64_t w = f2(ex2(a.x), ex2(a.y));
+                                    sum[x & 1] = add2(sum[x & 1], w);
+                                    const float2 r = unf2(mul2(w, r2));
+                                    pk[q * 8 + x] = __uint_as_float(pack_f16(r.x, r.y));
+                                }
+                            }
+                            __syncwarp();
+                            tmem_st16(t_s + static_cast<uint32_t>(half * 16), pk);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int at = 0; at < kTile; at += 16) {
+                            float s[16];
+                            uint32_t pk[8];
+                            scores(at, s);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float2 w = make_float2(ex2(s[2 * x] + mm), ex2(s[2 * x + 1] + mm));
+                                sum[x & 1] = add2(sum[x & 1], f2(w.x, w.y));
+                                pk[x] = pack_f16(w.x * lift(from, ent[at + 2 * x].y), w.y * lift(from, ent[at + 2 * x + 1].y));
+                            }
+                            __syncwarp();
+                            tmem_st8(t_s + static_cast<uint32_t>(at / 2), pk);
                         }
                     }
                     const float2 sa = unf2(add2(sum[0], sum[1]));
                     l += sa.x + sa.y;
-                    __syncwarp();
-                    tmem_st32(t_s, pk);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[i % kTurns]);
+                if (lane == 0) mbar_arrive(&p_full[c.at]);
             }
-            const int final = first + 2 * (count - 1);
-            if (ok && count > 0) ok = wait(&pv_done[final % kTurns], turn(final));
+            if (ok && first < seg + len) ok = wait(&pv_done[had.at], had.odd);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after_sync();
             // the two groups' sums of each row; each group writes half of the dimensions
@@ -531,7 +651,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
             // which groups had a tile: the same for the whole segment
             const bool has_a = (seg & 1) == 0 || len > 1, has_b = (seg & 1) == 1 || len > 1;
             if (busy) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < HD / 2; c += 32) {
                     float v[32];
 #pragma unroll
@@ -624,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_attn_kv4_umma(const Kv4Params p) {
     using L = Layout<HD>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sm = smem_raw + (1024u - smem_u32(smem_raw) % 1024u) % 1024u;   // (an offset: still known to be shared memory)
     __shared__ int s_abort;
     __shared__ Window s_win;
     __shared__ Issued s_issued;
@@ -678,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) p.cut[blockIdx.x].z = -1;   // the merge refuses the call's results
         if (warp == kWarpS) {
             // what is in flight lands before the shared and tensor memory go
-            // (the lanes' own copies have been waited for)
+            // (the copies have been waited for)
             constexpr int kTurns = L::kTurns;
             auto last = [&](uint64_t* of, int i) { settle(&of[i % kTurns], static_cast<uint32_t>((i / kTurns) & 1)); };
             if (s_issued.s > 0) last(bars + 2 * kTurns, s_issued.s - 1);
