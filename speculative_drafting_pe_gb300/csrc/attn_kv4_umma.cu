@@ -285,6 +285,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
         __syncwarp();
     } else if (warp >= kWarpConv && warp < kWarpS) {
         constexpr int kTeam = L::kTeam, kTeams = 8 / kTeam, kMine = kUnitPages / kTeam;
+        static_assert(L::kDepth % kTeams == 0 && kTeams <= kTurns && (kQBufs == 1 || kQBufs == 2), "phases that a team does not see");
         const int ct = tid & 127, quad = (warp - kWarpConv) / 4, team = (warp - kWarpConv) / kTeam, part = (warp - kWarpConv) % kTeam;
         constexpr int kChunks = HD / 32, kPasses = kPage * kChunks / 32, kPass = 32 / kChunks;   // chunks of an entry; passes over a page
         const int ch = lane % kChunks, row0 = lane / kChunks;
@@ -301,7 +302,15 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                 const int rows = p.rows != nullptr ? p.rows[b] : p.K;
                 S = p.seq_lens[b];
                 last = S + rows - 1;
-                if ((++no & 1) != quad) continue;   // the other four warps'
+                // the place's last reader: S of the segment kQBufs back
+                auto free_place = [&]() {
+                    if (no >= kQBufs) ok = wait(&q_empty[no % kQBufs], static_cast<uint32_t>((no / kQBufs) & 1) ^ 1u);
+                };
+                if ((++no & 1) != quad) {   // the other four warps'
+                    // (a single place's barrier is seen in every phase: a parity alone stands for two)
+                    if (kQBufs == 1) free_place();
+                    continue;
+                }
                 const int j = ct / G;
                 const __nv_bfloat16* src = p.q + (static_cast<long long>(b) * p.K + j) * p.ld_q +
                                            static_cast<long long>(info.y * G + ct - j * G) * HD;
@@ -322,8 +331,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
 #pragma unroll
                     for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
                 }
-                // the place's last reader: S of the segment kQBufs back
-                if (no >= kQBufs) ok = wait(&q_empty[no % kQBufs], static_cast<uint32_t>((no / kQBufs) & 1) ^ 1u);
+                free_place();
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after_sync();
                 // the row times 2^(141 - E): its largest value lies in [2^14, 2^15)
