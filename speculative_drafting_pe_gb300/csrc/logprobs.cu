@@ -8,16 +8,24 @@
 // from the same Z.
 //
 // One pass over a row: every thread keeps a running maximum of its own and its
-// sums relative to it, rescaled once for kVec values. A cluster of CTAs takes a
+// sums relative to it, rescaled once for a vector. A cluster of CTAs takes a
 // row where rows are few; the first CTA joins their sums through distributed
 // shared memory.
 //
-// The likeliest tokens cost the pass nothing. Each thread's maximum is known
-// behind it; of the warps' largest (for more than 16 alternatives: second
-// largest) ones the k-th (k/2-th) gives a bound that at least k values reach.
-// Only threads whose maximum reaches that bound can hold such values, a few of
-// 512, and only theirs are read again (from L2). Many values that equal the
-// bound are looked for in index order until there are k.
+// The likeliest tokens cost the pass one store for kBatch vectors. Each thread's
+// maximum is known behind it; of the warps' n-th largest ones (n times the warps
+// make k) the k/n-th gives a bound that at least k values reach. Only cells (a
+// thread's kBatch vectors, or a power of two as many) whose maximum reaches that
+// bound can hold such values, a few dozen of thousands, and only theirs are read
+// again, shared by all threads. (All vectors of the threads whose maximum
+// reaches it, a sixth of a row's bytes at 20 alternatives, took 86 us where
+// this takes 58.) Many values that equal the bound are looked for in index order
+// until there are k.
+//
+// Memory bounds it in fp32 (1408 x 151936: 128 us, 98% of the copy rate; with 5
+// alternatives 136, with 20 157), memory and the exponentials together in bf16
+// (704 x 201088: 49 us, 85%; 54 and 58); a launch and the latency of a row's
+// end where rows are few (one 5.2, 8 with 5 alternatives 8.5).
 #include <cfloat>
 
 #include "lowbit.cuh"
@@ -25,16 +33,15 @@
 namespace pe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kFew = 512, kMany = 256;      // threads of a CTA: rows that are split, rows with one each
 constexpr int kMaxTop = 32;
 constexpr float kMaxTemperature = 0x1p64f;
 constexpr int kMaxCluster = 8;
-constexpr int kMinSegment = 8 * kThreads;   // values of a CTA at least, where a cluster shares a row
-constexpr int kCand = 2048 + 64;            // values above the bound that are kept; see `collect`
+constexpr int kMinSegment = 8 * kFew;   // values of a CTA at least, where a cluster shares a row
+constexpr int kCand = 1024 + 64;            // values above the bound that are kept; see `collect`
 constexpr int kTies = 512;                  // values equal to it that are
 constexpr int kBatch = 4;                   // vectors of a thread whose loads are in flight together
-constexpr int kAgain = 4;                   // the same where some are read again
+constexpr int kCells = 8;                  // cells of a thread at most
 constexpr unsigned kAll = 0xffffffffu;
 
 struct LogprobParams {
@@ -106,6 +113,20 @@ __device__ __forceinline__ Sums join(Sums a, Sums b) {
     if (a.z != 0.f) rescale(a, m);
     if (b.z != 0.f) rescale(b, m);
     return Sums{m, a.z + b.z, a.s + b.s};
+}
+// of the first N lanes of a warp, in each of them
+template <int N>
+__device__ __forceinline__ Sums join_lanes(Sums a) {
+    float m = a.m;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (a.z != 0.f) rescale(a, m);
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        a.z += __shfl_xor_sync(kAll, a.z, o);
+        a.s += __shfl_xor_sync(kAll, a.s, o);
+    }
+    return Sums{m, a.z, a.s};
 }
 
 // 16 bytes of a row
@@ -189,16 +210,18 @@ struct Segment {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams p) {
-    constexpr int kN = Vec<T>::kN;
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1536 / kThreads) k_token_logprobs(const LogprobParams p) {
+    constexpr int kN = Vec<T>::kN, kWarps = kThreads / 32;
     __shared__ Sums s_sums[kWarps];
     __shared__ uint32_t s_best[kWarps];
     __shared__ int s_count, s_equal, s_ties[kTies], s_scan[kWarps];
-    __shared__ uint8_t s_who[kWarps][32];
     __shared__ unsigned long long s_cand[kCand];
     __shared__ unsigned long long s_top[kMaxCluster * kMaxTop];   // this CTA's, in the first CTA everybody's
     __shared__ float4 s_all[kMaxCluster];                         // the parts' sums (m, z, s), in the first CTA
+    __shared__ int s_work;
+    extern __shared__ float s_cell[];                             // [kCells][kThreads] the cells' maxima
+    uint16_t* s_list = reinterpret_cast<uint16_t*>(s_cell + kCells * kThreads);   // those that are read again
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int parts = static_cast<int>(gridDim.x), part = blockIdx.x, r = blockIdx.y + blockIdx.z * gridDim.y;
     if (r >= p.R) return;   // the whole cluster
@@ -208,11 +231,17 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
     const int each = (p.V + parts - 1) / parts;
     const Segment<T> seg(row, min(p.V, part * each), min(p.V, part * each + each));
 
+    const int token = tid == 0 && part == 0 ? p.tokens[r] : -1;   // (needed last, loaded first)
+
     Sums a{kFloor, 0.f, 0.f};
     float mine = -INFINITY;   // this thread's largest value
     const uint4* body = reinterpret_cast<const uint4*>(row + seg.body);
-    int x = tid;
-    for (; x + (kBatch - 1) * kThreads < seg.vecs; x += kBatch * kThreads) {
+    int shift = 0;            // batches of a cell: 2^shift
+    while ((seg.vecs / (kBatch * kThreads)) >> shift >= kCells) ++shift;
+    const int last = (1 << shift) - 1;
+    float cell = -INFINITY;
+    int x = tid, batch = 0;
+    for (; x + (kBatch - 1) * kThreads < seg.vecs; x += kBatch * kThreads, ++batch) {
         uint4 w[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) w[i] = __ldg(body + x + i * kThreads);
@@ -220,7 +249,12 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         for (int i = 0; i < kBatch; ++i) {
             float v[kN];
             Vec<T>::values(w[i], v);
-            add(a, mine, v, c);
+            add(a, cell, v, c);
+        }
+        if ((batch & last) == last) {
+            if (p.k > 0) s_cell[(batch >> shift) * kThreads + tid] = cell;
+            mine = fmaxf(mine, cell);
+            cell = -INFINITY;
         }
     }
     if (x < seg.vecs) {
@@ -233,48 +267,46 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
             if (x + i * kThreads < seg.vecs) {
                 float v[kN];
                 Vec<T>::values(w[i], v);
-                add(a, mine, v, c);
+                add(a, cell, v, c);
             }
+        ++batch;
     }
+    // the last cell, where it is not a whole one (a row of few values: none at all)
+    if (p.k > 0 && ((batch & last) != 0 || (batch > 0 && x < seg.vecs))) s_cell[((batch - 1) >> shift) * kThreads + tid] = cell;
+    mine = fmaxf(mine, cell);
+    const int cells = (batch + last) >> shift;   // of this thread
     {
         const int f = seg.front(tid), t = seg.back(tid);
         float v[1];
         if (f >= 0) { v[0] = static_cast<float>(row[f]); add(a, mine, v, c); }
         if (t >= 0) { v[0] = static_cast<float>(row[t]); add(a, mine, v, c); }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
-        a = join(a, b);
-    }
+    T asked = static_cast<T>(NAN);
+    if (token >= 0 && token < p.V) asked = row[token];
+    a = join_lanes<32>(a);
     if (lane == 0) s_sums[warp] = a;
     if (p.k > 0) {
-        // the warp's largest, or second largest, maximum
-        const uint32_t key = order_key(mine);
-        uint32_t best = __reduce_max_sync(kAll, key);
-        if (p.k > kWarps) {
-            const unsigned who = __ballot_sync(kAll, key == best);
-            best = __reduce_max_sync(kAll, lane == __ffs(who) - 1 ? 0u : key);
+        // the warp's largest maximum, or its n-th, where n of each warp make k
+        uint32_t key = order_key(mine), best = __reduce_max_sync(kAll, key);
+        for (int n = kWarps; n < p.k; n += kWarps) {
+            if (lane == __ffs(__ballot_sync(kAll, key == best)) - 1) key = 0u;
+            best = __reduce_max_sync(kAll, key);
         }
         if (lane == 0) s_best[warp] = best;
     }
-    if (tid == 0) s_count = s_equal = 0;
+    if (tid == 0) s_count = s_equal = s_work = 0;
     if (tid < kMaxTop) s_top[tid] = 0ull;   // (no key)
     __syncthreads();
-    if (warp == 0) {
-        a = lane < kWarps ? s_sums[lane] : Sums{kFloor, 0.f, 0.f};
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) {
-            const Sums b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.z, o), __shfl_xor_sync(kAll, a.s, o)};
-            a = join(a, b);
-        }
+    if (warp == kWarps - 1) {
+        a = join_lanes<kWarps>(lane < kWarps ? s_sums[lane] : Sums{kFloor, 0.f, 0.f});
+        __syncwarp();
         if (lane == 0) s_sums[0] = a;
     }
 
     const int want = min(p.k, seg.hi - seg.lo);
     if (want > 0) {
-        // the bound: so many warps have one (or two) maxima that are as large
-        const int rank = p.k > kWarps ? (p.k + 1) / 2 : p.k;
+        // the bound: so many warps have n maxima that are as large
+        const int n = (p.k + kWarps - 1) / kWarps, rank = (p.k + n - 1) / n;
         const uint32_t b = s_best[lane % kWarps];
         int ahead = 0;
 #pragma unroll
@@ -285,50 +317,46 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         const uint32_t bound = __shfl_sync(kAll, b, __ffs(__ballot_sync(kAll, ahead == rank - 1)) - 1);
         // values above the bound, and some that equal it, of the threads that have such
         const float level = key_value(bound);
-        auto put = [&](float v, int i) {
-            if (v > level) {
-                const int n = atomicAdd(&s_count, 1);
-                if (n < kCand) s_cand[n] = (static_cast<unsigned long long>(order_key(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
-            } else if (v == level && *static_cast<volatile int*>(&s_equal) <= kTies) {
-                const int n = atomicAdd(&s_equal, 1);
-                if (n < kTies) s_ties[n] = i;
-            }
+        auto above = [&](float v, int i) {
+            const int n = atomicAdd(&s_count, 1);
+            if (n < kCand) s_cand[n] = (static_cast<unsigned long long>(order_key(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
         };
-        // All lanes read the vectors of the warp's threads that have some, kAgain in flight.
+        auto equal_one = [&](int i) {
+            if (*static_cast<volatile int*>(&s_equal) > kTies) return;
+            const int n = atomicAdd(&s_equal, 1);
+            if (n < kTies) s_ties[n] = i;
+        };
         const bool has = mine >= level;
-        const unsigned who = __ballot_sync(kAll, has);
-        const int those = __popc(who);
-        if (has) s_who[warp][__popc(who & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
-        __syncwarp();
-        const int work = those * ((seg.vecs + kThreads - 1) / kThreads);
-        for (int q0 = lane; q0 < work; q0 += 32 * kAgain) {
-            uint4 w[kAgain];
-            int y[kAgain];
+        if (has)
+            for (int q = 0; q < cells; ++q)
+                if (s_cell[q * kThreads + tid] >= level) s_list[atomicAdd(&s_work, 1)] = static_cast<uint16_t>(q * kThreads + tid);
+        __syncthreads();
+        const int each_vecs = kBatch << shift, work = s_work * each_vecs;
+        for (int q = tid; q < work; q += kThreads) {
+            const int of = q / each_vecs, id = s_list[of];
+            const int y = id % kThreads + (id / kThreads * each_vecs + q - of * each_vecs) * kThreads;
+            if (y >= seg.vecs) continue;
+            float v[kN];
+            Vec<T>::values(__ldg(body + y), v);
+            unsigned more = 0, same = 0;
 #pragma unroll
-            for (int i = 0; i < kAgain; ++i) {
-                const int q = q0 + 32 * i, at = q / those;
-                y[i] = q < work ? at * kThreads + warp * 32 + s_who[warp][q - at * those] : seg.vecs;
-                if (y[i] < seg.vecs) w[i] = __ldg(body + y[i]);
+            for (int e = 0; e < kN; ++e) {
+                more |= v[e] > level ? 1u << e : 0u;
+                same |= v[e] == level ? 1u << e : 0u;
             }
-#pragma unroll
-            for (int i = 0; i < kAgain; ++i)
-                if (y[i] < seg.vecs) {
-                    float v[kN];
-                    Vec<T>::values(w[i], v);
-                    float top = v[0];
-#pragma unroll
-                    for (int e = 1; e < kN; ++e) top = fmaxf(top, v[e]);
-                    if (top >= level) {
-                        const int at = seg.body + y[i] * kN;
-#pragma unroll 1
-                        for (int e = 0; e < kN; ++e) put(static_cast<float>(row[at + e]), at + e);
-                    }
-                }
+            const int at = seg.body + y * kN - 1;
+            for (; more != 0; more &= more - 1) above(static_cast<float>(row[at + __ffs(more)]), at + __ffs(more));
+            for (; same != 0; same &= same - 1) equal_one(at + __ffs(same));
         }
         if (has) {
-            const int f = seg.front(tid), t = seg.back(tid);
-            if (f >= 0) put(static_cast<float>(row[f]), f);
-            if (t >= 0) put(static_cast<float>(row[t]), t);
+            const int ends[2] = {seg.front(tid), seg.back(tid)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (ends[i] < 0) continue;
+                const float v = static_cast<float>(row[ends[i]]);
+                if (v > level) above(v, ends[i]);
+                else if (v == level) equal_one(ends[i]);
+            }
         }
         __syncthreads();
         const int equal = s_equal;
@@ -428,8 +456,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
         return ((x < kSafe ? fmaxf(x * c, kFloor) - sum.m : fmaf(x, c, -sum.m)) - log_z) * kLn2;
     };
     if (tid == 0) {
-        const int t = p.tokens[r];
-        p.logprobs[r] = t >= 0 && t < p.V ? logprob(static_cast<float>(row[t])) : NAN;
+        p.logprobs[r] = logprob(static_cast<float>(asked));
         if (p.entropy != nullptr) p.entropy[r] = (log_z - sum.s / sum.z) * kLn2;
     }
     if (p.k == 0) return;
@@ -456,13 +483,18 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const LogprobParams
     }
 }
 
-template <typename T>
-int launch(const LogprobParams& p, int parts, cudaStream_t s) {
+template <typename T, int kThreads>
+int launch(const LogprobParams& p, int parts, int dev, cudaStream_t s) {
+    if (p.k > 0) {
+        const int rc = allow_smem<k_token_logprobs<T, kThreads>>(dev, kCells * kThreads * 6);
+        if (rc != PE_OK) return rc;
+    }
     cudaLaunchConfig_t cfg = {};
     const unsigned rows_y = static_cast<unsigned>(p.R < 32768 ? p.R : 32768);
     cfg.gridDim = dim3(parts, rows_y, (p.R + rows_y - 1) / rows_y);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
+    cfg.dynamicSmemBytes = p.k > 0 ? kCells * kThreads * 6 : 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = parts;
@@ -470,7 +502,7 @@ int launch(const LogprobParams& p, int parts, cudaStream_t s) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    PE_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_token_logprobs<T>, p));
+    PE_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_token_logprobs<T, kThreads>, p));
     return PE_OK;
 }
 
@@ -510,5 +542,10 @@ extern "C" int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void
     int parts = 1;
     while (parts < kMaxCluster && static_cast<long long>(R) * parts < 2ll * sms && V / (2 * parts) >= kMinSegment) parts *= 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == PE_DTYPE_BF16 ? launch<__nv_bfloat16>(p, parts, s) : launch<float>(p, parts, s);
+    // Small CTAs once there are rows for most of them, so that what a row does behind its last value (a few
+    // dependent reads) falls into others' streaming: 704 rows of 201088 bf16, 20 alternatives, 58 us for 66 with
+    // large ones; 456 rows 43 for 38, and 36 for 31 without alternatives.
+    if (parts == 1 && R >= 4 * sms && V >= kMinSegment)
+        return dtype == PE_DTYPE_BF16 ? launch<__nv_bfloat16, kMany>(p, parts, dev, s) : launch<float, kMany>(p, parts, dev, s);
+    return dtype == PE_DTYPE_BF16 ? launch<__nv_bfloat16, kFew>(p, parts, dev, s) : launch<float, kFew>(p, parts, dev, s);
 }

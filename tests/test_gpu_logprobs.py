@@ -101,9 +101,43 @@ def test_masks_and_values_that_are_not_finite(V, top, dtype):
     _check(x, tokens, top, 0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [4096, 5003, 33001])
+@pytest.mark.parametrize("top", [0, 1, 8, 9, 20, 32])
+def test_rows_for_every_small_block(V, top, dtype):
+    # more rows than large blocks are used for; rows of every kind among them
+    rng = np.random.default_rng(V + top)
+    R = 4 * torch.cuda.get_device_properties(0).multi_processor_count + 13
+    x = _logits(rng, R, V + 3, dtype)[:, :V]
+    x[0], x[1], x[2] = 0.0, -float("inf"), torch.finfo(dtype).min
+    x[3, 7:] = -float("inf")
+    x[4, 5], x[5, 6] = float("inf"), float("nan")
+    x[6] = (torch.arange(V) % 256 == 3).float() * 4        # many of the largest with one thread
+    x[7] = -torch.arange(V) * 2.0 ** -10
+    x[8] = torch.as_tensor(rng.integers(0, 3, V)).float()
+    x[9, :V - 20] = -1e4
+    x[10] = torch.where(torch.arange(V) % 512 < 3, 9.0, 1.0) + torch.arange(V) % 7 * 0.125
+    _check(x, rng.integers(0, V, R), top, 0.7)
+
+
+@pytest.mark.parametrize("R", [1, 700])
+def test_long_rows(R):
+    # cells of several batches
+    rng = np.random.default_rng(R)
+    x = torch.randn(R, 300007, device="cuda", generator=torch.Generator("cuda").manual_seed(R)).to(torch.bfloat16)
+    at = rng.choice(R, min(R, 40), replace=False)
+    tokens = torch.as_tensor(rng.integers(0, 300007, R), dtype=torch.int32, device="cuda")
+    o = binding.token_logprobs(x, tokens, top=20)
+    some = torch.as_tensor(at).cuda()
+    lp, h, ids, best = kv4.token_logprobs(x[some].double().cpu().numpy(), tokens[some].cpu().numpy(), 20, 1.0)
+    np.testing.assert_array_equal(o["top_tokens"][some].cpu().numpy(), ids)
+    for got, ref in ((o["logprobs"], lp), (o["entropy"], h), (o["top_logprobs"], best)):
+        np.testing.assert_allclose(got[some].double().cpu().numpy(), ref, rtol=2.0 ** -19, atol=2.0 ** -19)
+
+
 def test_results_do_not_change_from_call_to_call():
     rng = np.random.default_rng(3)
-    for R in (1, 9, 400):
+    for R in (1, 9, 400, 700):
         x = _logits(rng, R, 30000, torch.bfloat16)
         t = torch.as_tensor(rng.integers(0, 30000, R), dtype=torch.int32, device="cuda")
         first = binding.token_logprobs(x, t, top=20)
