@@ -30,10 +30,10 @@ constexpr int kPage = 16;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBatch = 4;        // heads of a warp whose loads are in flight together
-constexpr int kMaxBlock = 4;     // rows of a CTA
+constexpr int kMaxBlock = 2;     // rows of a CTA
 
 struct AppendParams {
-    int n_max, nq, nkv, block, max_pages, num_pages;
+    int B, n_max, nq, nkv, block, max_pages, num_pages;
     const __nv_bfloat16* x[3];   // q, k, v
     long long ld[3];
     const int32_t* seq_lens;
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
     constexpr int kPer = 32 / kLanes;       // heads that a warp takes at a time
     __shared__ float4 s_cs[kMaxBlock * kHalf / 2];   // (cos, sin) of two pairs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int blocks = (p.n_max + p.block - 1) / p.block;
-    const int b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * p.block;
+    // (requests in turn: of ragged ones, blocks of rows run beside blocks that only zero)
+    const int b = blockIdx.x % p.B, j0 = blockIdx.x / p.B * p.block;
     const int S = p.seq_lens[b];
     const int n = p.rows != nullptr ? p.rows[b] : p.n_max;
     const int first = p.positions != nullptr ? p.positions[b] : S;
@@ -78,7 +78,25 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
     if (S < 0 || n < 0 || n > p.n_max || (p.turn && (first < 0 || first > 0x7FFFFFFF - n))) st = PE_REQ_BAD_INPUT;
     else if (static_cast<long long>(S) + n > static_cast<long long>(p.max_pages) * kPage) st = PE_REQ_CAPACITY;
     const int live = st == PE_REQ_OK ? n : 0;
-    if (j0 > 0 && j0 >= live && p.q_out == nullptr) return;
+    if (j0 >= live) {
+        // No row of the block is live: its queries' places are zeroed, 16 bytes
+        // a store where they are aligned, as one run where they are one (8
+        // prompts of 6 to 2048 rows in room for 2048, most of whose bytes
+        // these are: 36 us by the loop below, 29 so).
+        if (j0 == 0 && tid == 0) p.status[b] = st;
+        if (p.q_out == nullptr) return;
+        int count = min(p.n_max, j0 + p.block) - j0, bytes = p.nq * HD * 2;
+        if (p.ld_q_out * 2 == bytes) bytes *= count, count = 1;
+        for (int j = 0; j < count; ++j) {
+            uint8_t* row = reinterpret_cast<uint8_t*>(p.q_out + (static_cast<long long>(b) * p.n_max + j0 + j) * p.ld_q_out);
+            if (reinterpret_cast<uintptr_t>(row) % 16 == 0)
+#pragma unroll 4
+                for (int x = tid * 16; x < bytes; x += kThreads * 16) *reinterpret_cast<uint4*>(row + x) = make_uint4(0u, 0u, 0u, 0u);
+            else
+                for (int x = tid * 8; x < bytes; x += kThreads * 8) *reinterpret_cast<uint2*>(row + x) = make_uint2(0u, 0u);
+        }
+        return;
+    }
 
     const int sub = lane / kLanes, l = lane % kLanes;
     const int heads = p.nq + 2 * p.nkv, groups = (heads + kPer - 1) / kPer;
@@ -279,6 +297,7 @@ extern "C" int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_
     const int rc = current_device(&dev, &sms);
     if (rc != PE_OK) return rc;
     AppendParams p{};
+    p.B = B;
     p.n_max = n_max;
     p.nq = nq;
     p.nkv = nkv;
