@@ -24,6 +24,10 @@
 // masks of `widen` leave (Q's fragments follow that order), and its transposed
 // form four dimensions of two V rows in the two halves of a word, which is what
 // a fragment of V^T wants. P^T comes out of S^T's layout by 8x8 transposes.
+// Issue slots bound it (58% of them go, ALU 54%): widening is 288 of some 900
+// instructions of a unit's warp. 64 single tokens over 512..8192 entries, 32/4
+// heads of 128: 50.5 us, 2.4 TB/s; one of 131072 entries 29. 16 warps of 128
+// registers instead: 56 and 31.
 // Queries enter as fp16 after an exact shift by a power of two per row;
 // weights times V's scale go to fp16 (2^-11) relative to the row's largest such
 // product so far (kLift).
@@ -564,7 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-constexpr int kFewRows = 16;   // query rows of a head up to which the register kernel is taken
+// Query rows of a head up to which the register kernel is taken. At 16 of them, 64 requests of 512..8192 entries: 83 us,
+// by the tensor-memory kernel 107 (64-wide heads 102, 164); one request of 2048: 13.2, 13.6.
+constexpr int kFewRows = 16;
 
 int plan_kv4(int B, int K, int nq, int nkv, int hd, int max_pages, Plan* out) {
     const int rows = K * (nq / nkv);
