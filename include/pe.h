@@ -489,8 +489,17 @@ int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_head
  * cache's arrays 16-byte aligned) and its rules for rows, masks, scratch (of
  * pe_attention_kv4_scratch floats), pages and status.
  * Entries that no row sees may hold anything. An entry whose parameters are not
- * finite makes the rows that see it NaN, and no other row. A row of q that
- * holds an infinity or a NaN is NaN. */
+ * finite makes the rows that see it NaN, and no other row; one that a row does
+ * not see does not move it, whatever its size. A row of q that holds an infinity
+ * or a NaN is NaN. Scales are not negative and below 2^124, values below 2^127.
+ * Rounded to fewer than 32 bits, besides the output: the queries, to fp16 under a
+ * power of two of their row (a value is off by 2^-25 of its row's largest at
+ * most), and the weights times V's scale, to fp16 relative to the row's largest
+ * such product (2^-11 of each; small ones by 2^-26 of the largest). With more than
+ * 16 rows for a kv head, K * (nq/nkv), also K and V, to fp16 under a power of two
+ * of their page where every row sees the unit of 64 entries that it stands in:
+ * 2^-11 of a value of K, 2^-10 of scale |n - 8| + |base + 8 scale| for V, and
+ * 2^-18 of the page's largest K, 2^-36 of its largest V. */
 int pe_attention_kv4_scratch(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                              int32_t max_pages, int64_t* ws_floats);
 int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,

@@ -11,8 +11,8 @@
 //               swizzle, entry-major: K a K-major operand, V an MN-major one)
 //               under a power of two of the page: K as scale n + base, rounded
 //               once, V as scale (n - 8) + mid, mid and the sum rounded (2^-11
-//               each). What falls below fp16's range is 2^-19 of the page's
-//               largest K and 2^-37 of its largest V. Where some row does not
+//               each); fp16's smallest step is 2^-18 of the page's largest K
+//               and 2^-36 of its largest V at most. Where some row does not
 //               see all of the unit, an entry has a power of two to itself, so
 //               that none moves a row that does not see it. At the start of a
 //               segment the query rows, as fp16 after an exact shift by a power

@@ -18,6 +18,12 @@
 // (four 64-wide ones). A lane has four dimensions of the lower half of a head
 // and the four that they turn with, two 8-byte loads, and kBatch such pairs in
 // flight. The rows' sines and cosines are computed once, for all heads.
+//
+// Few rows take a launch and three dependent loads, length, page and row (one
+// row 3.5 us, 32 x 8 rows of 32 + 2 * 4 128-wide heads 4.0). Prompts are bound by
+// issue slots (60% of them go) and by the stores of rows that are not there:
+// 2240 rows of 64 + 2 * 8 64-wide heads in room for 16384 29 us, 4.6 TB/s; one to
+// two rows a CTA, with four 31 and with eight 34.
 #include <cmath>
 #include <cuda_fp16.h>
 
