@@ -475,7 +475,9 @@ int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  * where scale is 0. A turned key is not rounded before. Angles are exact to
  * 2^-31 of a turn at every position. A head of a row that holds an infinity or
  * NaN, or magnitudes beyond 2^126, stands as NaN (scale and base). An entry
- * depends on its row alone; nothing else of the cache is touched.
+ * depends on its row alone; nothing else of the cache is touched. Requests whose
+ * new entries are the same places of the cache race. q_out over q has q's row
+ * stride; otherwise no output shares memory with an input.
  * q, k, v and q_out 8-byte aligned, their strides multiples of 4, the cache's
  * arrays 16-byte aligned. */
 int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,
@@ -487,7 +489,7 @@ int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_head
 /* Attention of the K rows of each request over that cache, with the arguments
  * of pe_attention_kv8 (k_params and v_params in the place of the scales, the
  * cache's arrays 16-byte aligned) and its rules for rows, masks, scratch (of
- * pe_attention_kv4_scratch floats), pages and status.
+ * pe_attention_kv4_scratch floats), pages and status. out shares no memory with q.
  * Entries that no row sees may hold anything. An entry whose parameters are not
  * finite makes the rows that see it NaN, and no other row; one that a row does
  * not see does not move it, whatever its size. A row of q that holds an infinity
@@ -521,7 +523,7 @@ int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  * A logit of -inf is a token that cannot be (ln p = -inf, and it adds nothing to
  * the entropy); -FLT_MAX is one like any other (ln p below fp32's range is -inf). A row that holds a NaN or +inf,
  * or only -inf, has no probabilities: NaN in the place of each, NaN logits
- * ordered behind all others. The temperature lies in 2^-63 .. 2^64; a finite
+ * ordered behind all others. The temperature lies in 2^-63 .. 2^64, R and V are 2^30 at most; a finite
  * logit over it has a magnitude up to 2^120, or the logit is -FLT_MAX. Sums in
  * fp32, each weight off by about 2^-21 of itself. */
 int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void* logits, int64_t ld, const int32_t* tokens,

@@ -623,6 +623,10 @@ extern "C" int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t
         set_error("null tensor argument");
         return PE_ERR_ARG;
     }
+    if (out == q || status == seq_lens || (rows != nullptr && status == rows)) {
+        set_error("out must not be q, status neither seq_lens nor rows");
+        return PE_ERR_ARG;
+    }
     const int64_t width = static_cast<int64_t>(n_q_heads) * head_dim;
     if (ld_q < width || ld_out < width || ld_q % 8 != 0 || ld_out % 8 != 0) {
         set_error("row strides must be multiples of 8 and at least n_q_heads * head_dim");

@@ -299,6 +299,11 @@ extern "C" int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_
         set_error("q, k, v and q_out must be 8-byte aligned, the code and parameter arrays 16-byte aligned");
         return PE_ERR_ARG;
     }
+    if ((nq > 0 && q_out == q && ld_q_out != ld_q) || status == seq_lens || (rows != nullptr && status == rows) ||
+        (positions != nullptr && status == positions)) {
+        set_error("q_out over q must have its row stride, status must be none of the inputs");
+        return PE_ERR_ARG;
+    }
     int dev = 0, sms = 0;
     const int rc = current_device(&dev, &sms);
     if (rc != PE_OK) return rc;

@@ -517,7 +517,7 @@ extern "C" int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void
     if (R < 1 || V < 1) { set_error("R and V must be >= 1"); return PE_ERR_ARG; }
     if (dtype != PE_DTYPE_BF16 && dtype != PE_DTYPE_FP32) { set_error("logits must be bf16 or fp32"); return PE_ERR_ARG; }
     if (top < 0 || top > kMaxTop || top > V) { set_error("top must lie in 0..32 and not exceed V"); return PE_ERR_ARG; }
-    if (R > (1 << 30)) { set_error("too many rows for one call"); return PE_ERR_ARG; }
+    if (R > (1 << 30) || V > (1 << 30)) { set_error("R and V must be at most 2^30"); return PE_ERR_ARG; }
     const float c = 1.4426950408889634f / temperature;
     if (!(temperature > 0.f && temperature <= kMaxTemperature && c <= kMaxTemperature)) {
         set_error("temperature must lie in 2^-63 .. 2^64");

@@ -155,6 +155,23 @@ def test_any_number_of_rows(rows, hd):
                 _check(got[2 * c:2 * c + 2].double().cpu().numpy(), ref, size, reach, v, 131 + K, rows)
 
 
+@pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)
+def test_batches_with_next_to_nothing(K, nq, nkv, hd):
+    # no live row at all, then one row of one request whose cache is its own entry
+    rng = np.random.default_rng(hd)
+    k, v = _cache(rng, 4, nkv, hd), _cache(rng, 4, nkv, hd)
+    _, qt = _bf16(rng.standard_normal((3, K, nq, hd)))
+    args = [qt, _i([5, 0, 40]), _i([[0, 1, 2], [3, -1, -1], [0, 1, -1]]), *_on_device(k, v)]
+    out, status = binding.attention_kv4(*args, rows=_i([0, 0, 0]), out=torch.full_like(qt, 2.0))
+    assert (status == 0).all() and (out == 0).all()
+    out, status = binding.attention_kv4(*args, rows=_i([0, 1, 0]), out=torch.full_like(qt, 2.0))
+    assert (status == 0).all() and (out[0] == 0).all() and (out[2] == 0).all() and (out[1, 1:] == 0).all()
+    own, _ = kv4.values(v[0][3, :, 0], v[1][3, :, 0])       # its only entry has all the weight
+    got = out[1, 0].double().cpu().numpy().reshape(nkv, nq // nkv, hd)
+    size = np.abs(own).max(-1, keepdims=True) * 2
+    assert (np.abs(got - own[:, None]) <= 2.0 ** -8 * np.abs(own)[:, None] + 2.0 ** -9 * size[:, None]).all()
+
+
 # ---------------------------------------------------------------- what a row does not see
 
 @pytest.mark.parametrize("K,nq,nkv,hd", KERNELS, ids=NAMES)

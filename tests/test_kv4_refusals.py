@@ -16,33 +16,36 @@ def lib():
     return binding.load()
 
 
-P = ctypes.c_void_p(64)      # an aligned address that nothing reads
+P = ctypes.c_void_p(64)      # aligned addresses that nothing reads
+P2, P3 = ctypes.c_void_p(128), ctypes.c_void_p(192)
 ODD = ctypes.c_void_p(68)
 INF, NAN = float("inf"), float("nan")
 
 
 def test_append_refusals(lib):
     def call(B=1, n=1, nq=4, nkv=2, hd=64, q=P, ldq=256, k=P, ldk=128, v=P, ldv=128, theta=1e4, pos=None, s=P, rows=None,
-             t=P, mp=1, pages=1, kc=P, vc=P, kp=P, vp=P, qo=P, ldo=256, st=P):
+             t=P, mp=1, pages=1, kc=P, vc=P, kp=P, vp=P, qo=P2, ldo=256, st=P3):
         return lib.pe_kv4_append(B, n, nq, nkv, hd, q, ldq, k, ldk, v, ldv, theta, pos, s, rows, t, mp, pages, kc, vc, kp,
                                  vp, qo, ldo, st, None)
     for bad in (dict(B=0), dict(n=0), dict(nkv=0), dict(nq=-1), dict(mp=0), dict(pages=0), dict(ldk=127), dict(ldv=130),
                 dict(ldq=252), dict(ldq=258), dict(ldo=255), dict(q=None), dict(qo=None), dict(k=None), dict(v=None),
                 dict(s=None), dict(t=None), dict(kc=None), dict(vp=None), dict(st=None), dict(k=ODD), dict(qo=ODD),
                 dict(kc=ODD), dict(vp=ODD), dict(mp=1 << 28), dict(n=1 << 28), dict(nq=1 << 21, ldq=1 << 30, ldo=1 << 30),
-                dict(theta=-1.0), dict(theta=0.5), dict(theta=INF), dict(theta=NAN)):
+                dict(theta=-1.0), dict(theta=0.5), dict(theta=INF), dict(theta=NAN),
+                dict(qo=P, ldo=512), dict(st=P), dict(rows=P2, st=P2), dict(pos=P2, st=P2)):
         assert call(**bad) == -1, bad
     assert call(hd=96) == -2 and call(hd=32) == -2
 
 
 def test_attention_refusals(lib):
-    def call(B=1, K=1, nq=4, nkv=2, hd=64, q=P, ldq=256, s=P, t=P, mp=1, pages=1, kc=P, vc=P, kp=P, vp=P, scale=1.0, o=P,
-             ldo=256, ws=P, floats=1 << 30, st=P):
-        return lib.pe_attention_kv4(B, K, nq, nkv, hd, q, ldq, s, None, t, mp, pages, kc, vc, kp, vp, scale, o, ldo, ws,
+    def call(B=1, K=1, nq=4, nkv=2, hd=64, q=P, ldq=256, s=P, t=P, mp=1, pages=1, kc=P, vc=P, kp=P, vp=P, scale=1.0, o=P2,
+             ldo=256, ws=P, floats=1 << 30, st=P3, rows=None):
+        return lib.pe_attention_kv4(B, K, nq, nkv, hd, q, ldq, s, rows, t, mp, pages, kc, vc, kp, vp, scale, o, ldo, ws,
                                     floats, st, None)
     for bad in (dict(B=0), dict(K=0), dict(mp=0), dict(pages=0), dict(ldq=252), dict(ldq=255), dict(ldo=248),
                 dict(q=None), dict(o=None), dict(ws=None), dict(st=None), dict(kp=None), dict(q=ODD), dict(o=ODD),
-                dict(ws=ODD), dict(vc=ODD), dict(vp=ODD), dict(pages=1 << 26), dict(mp=1 << 28)):
+                dict(ws=ODD), dict(vc=ODD), dict(vp=ODD), dict(pages=1 << 26), dict(mp=1 << 28), dict(o=P), dict(st=P),
+                dict(rows=P2, st=P2)):
         assert call(**bad) == -1, bad
     for bad in (dict(nq=5), dict(nkv=0), dict(hd=32), dict(K=65), dict(nq=260, ldq=260 * 64, ldo=260 * 64)):
         assert call(**bad) == -2, bad
@@ -56,7 +59,7 @@ def test_logprob_refusals(lib):
     for bad in (dict(R=0), dict(V=0), dict(dtype=7), dict(top=-1), dict(top=33, V=100, ld=100), dict(top=9), dict(ld=7),
                 dict(ld=-8), dict(temp=0.0), dict(temp=-1.0), dict(temp=NAN), dict(temp=INF), dict(temp=2.0 ** -64),
                 dict(temp=2.0 ** 65), dict(x=None), dict(t=None), dict(lp=None), dict(ids=None), dict(best=None),
-                dict(x=v(65)), dict(t=v(66)), dict(h=v(66)), dict(R=(1 << 30) + 1)):
+                dict(x=v(65)), dict(t=v(66)), dict(h=v(66)), dict(R=(1 << 30) + 1), dict(V=(1 << 30) + 1, ld=1 << 31)):
         assert call(**bad) == -1, bad
 
 
