@@ -27,17 +27,18 @@
 //               and output accumulator of its own; they meet at the end of a
 //               segment.
 // What bounds it is the instructions' supply more than any pipe: five roles'
-// loops share the instruction cache and 54% of the issue slots go. So loops
-// that could be unrolled are not (the whole kernel unrolled: 333 us for 244 at
-// B=128 K=11, 512..8192 entries, 32/4 heads of 128; 13% more code by alternative
-// paths in it: 267), and shared memory is addressed as such, not by generic
-// pointers (248 for 222). Eight converter warps for four: 244 for 270. Now 219 us;
-// 64 requests of 10 rows, 64/8 heads of 64, 1024..4096 entries: 103. Without
-// the widening 187 and 93, without the softmax 183 and 70, without both 149 and
-// 67: the hand-over of a unit between the roles. Scores of a unit in one pass with
-// weights from the old maximum: 229 (a third of the units has a new one);
-// parameters by a warp of their own: 228; 136 registers for the softmax warps by
-// setmaxnreg and scores kept in them: 273.
+// loops share the instruction cache and 54% of the issue slots go. So only the
+// two innermost loops are unrolled (the whole kernel unrolled: 333 us for 244 at
+// B=128 K=11, 512..8192 entries, 32/4 heads of 128; those two: 210 for 219), and
+// shared memory is addressed as such, not by generic pointers (222 for 248).
+// Eight converter warps for four: 244 for 270. Now 208 us; 64 requests of 10
+// rows, 64/8 heads of 64, 1024..4096 entries: 96. At 225 and 103 it took
+// without the widening 187 and 93, without the softmax 183 and 70, without both
+// 149 and 67: the hand-over of a unit between the roles. Scores of a unit in one
+// pass with weights from the old maximum: 229 for 219 (a third of the units has a
+// new one); parameters by warps of their own: 228 for 219, or a unit ahead 221 for
+// 214; 136 registers for the softmax warps by setmaxnreg and scores kept in
+// them: 273 for 244; query rows staged in shared memory 221 for 220.
 // kTurns S_t buffers: P_t (fp16 pairs) overwrites the columns of S_t. Tiles of K
 // and V and S_t have as many places; "S_t is complete" frees K_t's, "P_t V_t is
 // complete" V_t's and S_t's: one commit for each product.
@@ -65,7 +66,9 @@ constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17, kWarpFetch = 18;   // (and 19)
 constexpr int kScales = 16;                 // units whose factors are kept: written with K kTurns ahead at most, read a few behind
 constexpr int kScaleRec = 2 * kUnitPages;   // floats of a unit's
-constexpr float kHead = 4.f;                // a row's largest contribution stands that much (log2) below the one it moves to
+// A row's largest contribution stands at 2^(kLift - kHead) in fp16 when it is
+// taken as the reference, which moves once one stands kTall above it.
+constexpr float kHead = 5.f, kTall = 10.f;
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 template <int HD>
@@ -430,7 +433,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                 if (i >= kTurns) ok = ok && wait(&(kSide == 0 ? s_full : pv_done)[c], at.odd ^ 1u);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
-#pragma unroll 1
+#pragma unroll 2
                 for (int x = 0; x < kMine * kPasses; ++x) {
                     static_assert(kPass % 8 == 0, "the swizzle of a thread's rows");
                     const int r = x * kPass;
@@ -560,7 +563,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     const float mm = m == -INFINITY ? 0.f : -m;
                     most += mm;
                     float f = 1.f;
-                    if (most > md + kRescale) {
+                    if (most > md + kTall) {
                         f = md == -INFINITY ? 0.f : ex2(md - most - kHead);
                         md = most + kHead;
                     }
@@ -590,7 +593,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     if (!alone) {
                         const uint64_t m2 = f2(mm, mm);
                         const float vr[4] = {lift(from, vl[0]), lift(from, vl[1]), lift(from, vl[2]), lift(from, vl[3])};
-#pragma unroll 1
+#pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             float s[32], pk[16];   // pk: pairs of fp16
                             tmem_ld32(t_s + static_cast<uint32_t>(half * 32), s);

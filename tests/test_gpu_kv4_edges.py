@@ -43,7 +43,7 @@ def _on_device(k, v):
 
 def _lim(ref, size, reach, top, L, rows):
     """Half a step of bf16; weights times V's scale in fp16, and L products below fp16's normal range, off by 2^-25
-    where the row's largest stands at 2^1 or above; scores in fp32, off by some 2^-21 of what they add up. With more
+    where the row's largest stands at 1 or above; scores in fp32, off by some 2^-21 of what they add up. With more
     than 16 rows K and V go to fp16, a value by two roundings at most."""
     scores, value = 2.0 ** -21 * reach[..., None], 0.0
     if rows > 16:
