@@ -20,10 +20,11 @@
 // flight. The rows' sines and cosines are computed once, for all heads.
 //
 // Few rows take a launch and three dependent loads, length, page and row (one
-// row 3.5 us, 32 x 8 rows of 32 + 2 * 4 128-wide heads 4.0). Prompts are bound by
-// issue slots (60% of them go) and by the stores of rows that are not there:
-// 2240 rows of 64 + 2 * 8 64-wide heads in room for 16384 29 us, 4.6 TB/s; one to
-// two rows a CTA, with four 31 and with eight 34.
+// row 3.2 us, 32 x 8 rows of 32 + 2 * 4 128-wide heads 3.6). Prompts are bound by
+// memory and issue slots: 8 x 2048 rows of 64 + 2 * 8 64-wide heads 58 us, 78% of
+// the copy rate (77 with queries, keys and values in one loop), one prompt of
+// 32768 112 us, 82%; 2240 rows in room for 16384, most of whose bytes are zeros,
+// 27 us. One to two rows a CTA: with four 31 for 29, with eight 34.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -36,7 +37,7 @@ constexpr int kPage = 16;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBatch = 4;        // heads of a warp whose loads are in flight together
-constexpr int kMaxBlock = 2;     // rows of a CTA
+constexpr int kMaxBlock = 2;     // rows of a CTA (its items are counted for one or two)
 
 struct AppendParams {
     int B, n_max, nq, nkv, block, max_pages, num_pages;
@@ -104,33 +105,46 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
         return;
     }
 
+    // Items: a row's heads of one kind, kPer at a time. Queries first, then keys
+    // and values, so that neither pays for the other's steps; a warp's first ones
+    // are on their way before anything else.
     const int sub = lane / kLanes, l = lane % kLanes;
-    const int heads = p.nq + 2 * p.nkv, groups = (heads + kPer - 1) / kPer;
-    const int end = min(p.n_max, j0 + p.block);
-    // this warp's heads: of row j, group g, then kWarps groups further
-    auto next = [&](int& j, int& g) {
-        for (g += kWarps; g >= groups; g -= groups) ++j;
-    };
-    auto load = [&](int j, int g, uint2 (&v)[2]) {
-        const int head = g * kPer + sub;
+    const int end = min(p.n_max, j0 + p.block), there = min(end, live) - j0;   // rows that may be read
+    const int of_q = (p.nq + kPer - 1) / kPer, of_kv = (p.nkv + kPer - 1) / kPer;
+    const int q_items = of_q * (end - j0), kv_items = 2 * of_kv * there;
+    const long long row0 = static_cast<long long>(b) * p.n_max + j0;
+    auto load = [&](const __nv_bfloat16* x, bool ok, uint2 (&v)[2]) {
         v[0] = v[1] = make_uint2(0u, 0u);
-        if (j < min(end, live) && head < heads) {
-            const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
-            const int h = kind == 0 ? head : kind == 1 ? head - p.nq : head - p.nq - p.nkv;
-            const __nv_bfloat16* x = p.x[kind] + (static_cast<long long>(b) * p.n_max + j) * p.ld[kind] + h * HD + l * 4;
+        if (ok) {
             v[0] = *reinterpret_cast<const uint2*>(x);
             v[1] = *reinterpret_cast<const uint2*>(x + kHalf);
         }
     };
-    uint2 v[kBatch][2];
-    int j = j0, g = warp - kWarps;
-    next(j, g);
-    int jl = j, gl = g;
+    const __nv_bfloat16* xq = p.x[0] + row0 * p.ld[0] + l * 4;
+    auto load_q = [&](int t, uint2 (&v)[2]) {
+        const int row = t >= of_q, head = (t - (row ? of_q : 0)) * kPer + sub;
+        load(xq + (row ? p.ld[0] : 0) + head * HD, t < q_items && row < there && head < p.nq, v);
+    };
+    struct Item {
+        int row, side, head;
+    };
+    auto kv_item = [&](int t) {
+        Item it{t >= 2 * of_kv, 0, 0};
+        t -= it.row ? 2 * of_kv : 0;
+        it.side = t >= of_kv;
+        it.head = (t - (it.side ? of_kv : 0)) * kPer + sub;
+        return it;
+    };
+    auto load_kv = [&](int t, uint2 (&v)[2]) {
+        const Item it = kv_item(t);
+        const long long ld = it.side ? p.ld[2] : p.ld[1];
+        load((it.side ? p.x[2] : p.x[1]) + (row0 + it.row) * ld + it.head * HD + l * 4, t < kv_items && it.head < p.nkv, v);
+    };
+    uint2 v[kBatch][2], kv[2];
+    load_kv(warp, kv);
+    if (warp < q_items)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-        load(jl, gl, v[i]);
-        next(jl, gl);
-    }
+        for (int i = 0; i < kBatch; ++i) load_q(warp + i * kWarps, v[i]);
 
     if (p.turn)
         for (int x = tid; x < (end - j0) * kHalf; x += kThreads) {
@@ -153,91 +167,85 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
     if (j0 == 0 && tid == 0) p.status[b] = st;
     const int rows = st == PE_REQ_OK ? live : 0;
 
-    for (bool front = true; j < end; front = false) {
-        if (!front) {
-            jl = j;
-            gl = g;
+    auto turn = [&](int row, float (&x)[8]) {
+        const float4* cs = s_cs + (row * kHalf + l * 4) / 2;
+        const float4 c0 = cs[0], c1 = cs[1];
+        const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                load(jl, gl, v[i]);
-                next(jl, gl);
-            }
+        for (int c = 0; c < 4; ++c) {
+            const float lo = x[c], hi = x[4 + c];
+            x[c] = fmaf(lo, co[c], -(hi * si[c]));
+            x[4 + c] = fmaf(hi, co[c], lo * si[c]);
         }
+    };
+    __nv_bfloat16* to_q = p.q_out + row0 * p.ld_q_out + l * 4;
+    for (int t0 = warp; t0 < q_items; t0 += kBatch * kWarps) {
+        if (t0 != warp)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) load_q(t0 + i * kWarps, v[i]);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (j >= end) break;
-            const int head = g * kPer + sub, row = j;
-            next(j, g);
-            const int kind = head < p.nq ? 0 : head < p.nq + p.nkv ? 1 : 2;
-            __nv_bfloat16* q_to = p.q_out + (static_cast<long long>(b) * p.n_max + row) * p.ld_q_out + head * HD + l * 4;
-            if (row >= rows) {   // no row here
-                if (kind == 0) {
-                    *reinterpret_cast<uint2*>(q_to) = make_uint2(0u, 0u);
-                    *reinterpret_cast<uint2*>(q_to + kHalf) = make_uint2(0u, 0u);
-                }
-                continue;
-            }
+            const int t = t0 + i * kWarps, row = t >= of_q, head = (t - (row ? of_q : 0)) * kPer + sub;
+            if (t >= q_items || head >= p.nq) continue;
             float x[8];   // dimensions 4l .., then hd/2 + 4l ..
             unpack4(v[i][0], x);
             unpack4(v[i][1], x + 4);
-            if (p.turn && kind != 2) {
-                const float4* cs = s_cs + ((row - j0) * kHalf + l * 4) / 2;
-                const float4 c0 = cs[0], c1 = cs[1];
-                const float co[4] = {c0.x, c0.z, c1.x, c1.z}, si[4] = {c0.y, c0.w, c1.y, c1.w};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float lo = x[c], hi = x[4 + c];
-                    x[c] = fmaf(lo, co[c], -(hi * si[c]));
-                    x[4 + c] = fmaf(hi, co[c], lo * si[c]);
-                }
-            }
-            if (kind == 0) {
-                *reinterpret_cast<uint2*>(q_to) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-                *reinterpret_cast<uint2*>(q_to + kHalf) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            }
-            const bool stores = kind != 0 && head < heads;
-            if (!__any_sync(0xffffffffu, stores)) continue;
-            float lo = x[0], hi = x[0], odd = x[0] - x[0];   // odd: NaN where a value is not finite
-#pragma unroll
-            for (int c = 1; c < 8; ++c) {
-                lo = fminf(lo, x[c]);
-                hi = fmaxf(hi, x[c]);
-                odd += x[c] - x[c];
-            }
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            }
-            const unsigned who = __ballot_sync(0xffffffffu, odd != 0.f);
-            if (!stores) continue;
-            uint32_t par = pack_bf16(0.f, lo);
-            const float base = __uint_as_float(par & 0xFFFF0000u);
-            par |= pack_bf16((hi - base) / 15.f, 0.f);
-            const float scale = __uint_as_float(par << 16);
-            uint32_t code[2] = {0u, 0u};
-            if (((who >> (sub * kLanes)) & ((1u << kLanes) - 1u)) != 0u || !(scale < INFINITY)) {
-                par = 0x7FC07FC0u;   // the entry is NaN
-            } else if (scale >= 0x1p-100f) {
-                // the quotient with its rounding error put right, as a division has it
-                const float inv = 1.f / scale;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float d = x[c] - base, near = d * inv;
-                    code[c >> 2] |= min(__float2uint_rn(fmaf(fmaf(-scale, near, d), inv, near)), 15u) << (4 * (c & 3));
-                }
-            } else if (scale > 0.f) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) code[c >> 2] |= min(__float2uint_rn((x[c] - base) / scale), 15u) << (4 * (c & 3));
-            }
-            const int side = kind - 1, e = S + row;
-            const int h = kind == 1 ? head - p.nq : head - p.nq - p.nkv;
-            const size_t at = (static_cast<size_t>(table[e / kPage]) * p.nkv + h) * kPage + e % kPage;
-            uint8_t* to = (side == 0 ? p.codes[0] : p.codes[1]) + at * kHalf + l * 2;
-            *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
-            *reinterpret_cast<uint16_t*>(to + kHalf / 2) = static_cast<uint16_t>(code[1]);
-            if (l == 0) (side == 0 ? p.params[0] : p.params[1])[at] = par;
+            if (p.turn) turn(row, x);
+            uint2 lo = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+            uint2 hi = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            if (j0 + row >= rows) lo = hi = make_uint2(0u, 0u);   // no row here
+            __nv_bfloat16* to = to_q + (row ? p.ld_q_out : 0) + head * HD;
+            *reinterpret_cast<uint2*>(to) = lo;
+            *reinterpret_cast<uint2*>(to + kHalf) = hi;
         }
+    }
+    if (rows == 0) return;   // refused
+    for (int t = warp; t < kv_items; t += kWarps) {
+        if (t != warp) load_kv(t, kv);
+        const Item it = kv_item(t);
+        float x[8];
+        unpack4(kv[0], x);
+        unpack4(kv[1], x + 4);
+        if (p.turn && it.side == 0) turn(it.row, x);
+        float lo = x[0], hi = x[0], odd = x[0] - x[0];   // odd: NaN where a value is not finite
+#pragma unroll
+        for (int c = 1; c < 8; ++c) {
+            lo = fminf(lo, x[c]);
+            hi = fmaxf(hi, x[c]);
+            odd += x[c] - x[c];
+        }
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, odd != 0.f);
+        if (it.head >= p.nkv) continue;
+        uint32_t par = pack_bf16(0.f, lo);
+        const float base = __uint_as_float(par & 0xFFFF0000u);
+        par |= pack_bf16((hi - base) / 15.f, 0.f);
+        const float scale = __uint_as_float(par << 16);
+        uint32_t code[2] = {0u, 0u};
+        if (((who >> (sub * kLanes)) & ((1u << kLanes) - 1u)) != 0u || !(scale < INFINITY)) {
+            par = 0x7FC07FC0u;   // the entry is NaN
+        } else if (scale >= 0x1p-100f) {
+            // the quotient with its rounding error put right, as a division has it
+            const float inv = 1.f / scale;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float d = x[c] - base, near = d * inv;
+                code[c >> 2] |= min(__float2uint_rn(fmaf(fmaf(-scale, near, d), inv, near)), 15u) << (4 * (c & 3));
+            }
+        } else if (scale > 0.f) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) code[c >> 2] |= min(__float2uint_rn((x[c] - base) / scale), 15u) << (4 * (c & 3));
+        }
+        const int e = S + j0 + it.row;
+        const size_t at = (static_cast<size_t>(table[e / kPage]) * p.nkv + it.head) * kPage + e % kPage;
+        uint8_t* to = (it.side == 0 ? p.codes[0] : p.codes[1]) + at * kHalf + l * 2;
+        *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code[0]);
+        *reinterpret_cast<uint16_t*>(to + kHalf / 2) = static_cast<uint16_t>(code[1]);
+        if (l == 0) (it.side == 0 ? p.params[0] : p.params[1])[at] = par;
     }
 }
 
