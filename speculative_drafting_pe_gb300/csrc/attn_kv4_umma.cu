@@ -61,7 +61,9 @@ constexpr int kUnitPages = 4;
 constexpr int kTile = kUnitPages * kPage;   // entries of a unit
 constexpr int kRows = 128;
 constexpr int kUnits = 640;                 // units of a window
-constexpr int kLeast = 3, kPad = 7;         // a share's positions at least, a segment's end in units
+// A share's positions at least (one request of 2048 entries, 4 heads of 56 rows: 1 14.8 us, 2 14.1, 3 15.1, 5 15.6; 5
+// of some 500 with 32: 15.5, 15.5, 15.1, 16.3), a segment's end in units.
+constexpr int kLeast = 2, kPad = 7;
 constexpr int kSoft = 256;                  // softmax threads
 constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17, kWarpFetch = 18;   // (and 19)
 constexpr int kScales = 16;                 // units whose factors are kept: written with K kTurns ahead at most, read a few behind
