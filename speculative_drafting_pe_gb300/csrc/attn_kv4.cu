@@ -389,7 +389,8 @@ __device__ __forceinline__ void attend_window(const Kv4Params& p, uint8_t* sm, i
                 uint32_t pb[kPages][NT][2];
 #pragma unroll
                 for (int a = 0; a < NT; ++a) {
-                    // (nothing seen: weights of 0)
+                    // (nothing seen: weights of 0). A weight meets its scale first: 0 times any scale is 0, where scale
+                    // times lift, of values far above all that has weight, would be an infinity and 0 times it NaN.
                     const float r0 = md[a][0] == -INFINITY ? 0.f : ex2(kLift - md[a][0]);
                     const float r1 = md[a][1] == -INFINITY ? 0.f : ex2(kLift - md[a][1]);
 #pragma unroll
@@ -402,7 +403,7 @@ __device__ __forceinline__ void attend_window(const Kv4Params& p, uint8_t* sm, i
                             l[a][1] += w1;
                             u[a][0] = fmaf(w0, vc, u[a][0]);
                             u[a][1] = fmaf(w1, vc, u[a][1]);
-                            pb[q][a][h] = transpose8x8(pack_f16(w0 * (vs * r0), w1 * (vs * r1)));
+                            pb[q][a][h] = transpose8x8(pack_f16(w0 * vs * r0, w1 * vs * r1));
                         }
                 }
 #pragma unroll
