@@ -515,13 +515,18 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     if (tl.x == -1 || tl.y == -1 || tl.z == -1 || tl.w == -1) mark = kMarkBadPage;
                     const int e0 = (info.z + i - seg) * kTile;
                     const bool alone = e0 + kTile - 1 > S || flip;   // factors of entries, not of pages
-                    const float2* ent = s_ent + (i % kScales) * kTile;
-                    // 16 of the unit's scores with their entries' factors, -inf where the row does not see them
-                    auto scores = [&](int at, float (&s)[16]) {
+                    const float* page = s_scale + (i % kScales) * kScaleRec;
+                    const float* ent = reinterpret_cast<const float*>(s_ent + (i % kScales) * kTile);
+                    // 16 of the unit's scores, rounded, with their entries' or their page's factors; -inf where the row
+                    // does not see them. v: the exponents of their V, a step apart
+                    const int step = alone ? 2 : 0;
+                    auto scores = [&](int at, float (&s)[16], const float*& v) {
                         tmem_ld16(t_s + static_cast<uint32_t>(at), s);
+                        const float* k = alone ? ent + 2 * at : page + at / kPage;
+                        v = alone ? k + 1 : k + kUnitPages;
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            s[x] = s[x] * cs * ent[at + x].x;
+                            s[x] *= cs * k[x * step];
                             if (e0 + at + x > lim) s[x] = -INFINITY;
                         }
                         __syncwarp();
@@ -529,7 +534,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     // largest score, largest score + exponent of its V
                     float top = -INFINITY, most = -INFINITY, kf[4], vl[4];
                     if (!alone) {
-                        const float4* sc = reinterpret_cast<const float4*>(s_scale + (i % kScales) * kScaleRec);
+                        const float4* sc = reinterpret_cast<const float4*>(page);
                         const float4 ks = sc[0], vlg = sc[1];   // of the pages
                         kf[0] = cs * ks.x; kf[1] = cs * ks.y; kf[2] = cs * ks.z; kf[3] = cs * ks.w;
                         vl[0] = vlg.x; vl[1] = vlg.y; vl[2] = vlg.z; vl[3] = vlg.w;
@@ -548,11 +553,12 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
 #pragma unroll 1
                         for (int at = 0; at < kTile; at += 16) {
                             float s[16];
-                            scores(at, s);
+                            const float* v;
+                            scores(at, s, v);
 #pragma unroll
                             for (int x = 0; x < 16; ++x) {
                                 top = fmaxf(top, s[x]);
-                                most = fmaxf(most, s[x] + ent[at + x].y);
+                                most = fmaxf(most, s[x] + v[x * step]);
                             }
                         }
                     }
@@ -592,7 +598,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     const float from = kLift - md;
                     uint64_t sum[2] = {0ull, 0ull};
                     // P of a half goes where S of the first half stood
-                    if (!alone) {
+                    if (!alone && !__any_sync(0xffffffffu, fabsf(mm) > kFine)) {
                         const uint64_t m2 = f2(mm, mm);
                         const float vr[4] = {lift(from, vl[0]), lift(from, vl[1]), lift(from, vl[2]), lift(from, vl[3])};
 #pragma unroll
@@ -619,13 +625,14 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
 #pragma unroll 1
                         for (int at = 0; at < kTile; at += 16) {
                             float s[16];
+                            const float* v;
                             uint32_t pk[8];
-                            scores(at, s);
+                            scores(at, s, v);
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
                                 const float2 w = make_float2(ex2(s[2 * x] + mm), ex2(s[2 * x + 1] + mm));
                                 sum[x & 1] = add2(sum[x & 1], f2(w.x, w.y));
-                                pk[x] = pack_f16(w.x * lift(from, ent[at + 2 * x].y), w.y * lift(from, ent[at + 2 * x + 1].y));
+                                pk[x] = pack_f16(w.x * lift(from, v[2 * x * step]), w.y * lift(from, v[(2 * x + 1) * step]));
                             }
                             __syncwarp();
                             tmem_st8(t_s + static_cast<uint32_t>(at / 2), pk);

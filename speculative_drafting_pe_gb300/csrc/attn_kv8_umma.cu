@@ -506,9 +506,12 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
                     float kf[4] = {cs * ks.x, cs * ks.y, cs * ks.z, cs * ks.w};
                     const int e0 = (info.z + i - seg) * kTile;
                     const bool inner = e0 + kTile - 1 <= S;
-                    if (!inner || flip || ks.x < 0.f || ks.y < 0.f || ks.z < 0.f || ks.w < 0.f) {
+                    // a product is below 2^24, two terms of a query of 256 at most by 448, 128 times
+                    const bool rough = fmaxf(fmaxf(kf[0], kf[1]), fmaxf(kf[2], kf[3])) > kFine * 0x1p-24f;
+                    if (!inner || flip || rough || ks.x < 0.f || ks.y < 0.f || ks.z < 0.f || ks.w < 0.f) {
                         // the page factors first: a masked score must not meet
-                        // a factor of 0, nor a maximum a negative one
+                        // a factor of 0, nor a maximum a negative one, and
+                        // large scores are rounded
 #pragma unroll
                         for (int x = 0; x < kTile; ++x) s[x] *= kf[x >> 4];
                         kf[0] = kf[1] = kf[2] = kf[3] = 1.f;

@@ -83,6 +83,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// A row's maximum is of scores as they are rounded, product by factor; its weights take the product into an fma with
+// the maximum exactly, whose result then lies half a step of the score above 0 where the maximum was rounded down, or
+// below. Up to scores (log2) of kFine that is 2^-4 at most and does not count. Beyond (from 2^26 or so a weight left
+// fp16, from 2^31 fp32) the scores are rounded first.
+constexpr float kFine = 0x1p20f;
+
 // Waits for the phase a millisecond at most.
 __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer_ns();

@@ -1,10 +1,11 @@
-"""Attention over the 4-bit cache where one entry has all of a row's weight and others' values are far larger."""
+"""Attention over the 4-bit and the 8-bit cache where one entry has all of a row's weight: scores that lie far apart,
+in requests long enough for pages and units that every row sees whole, and values of V that do."""
 
 import numpy as np
 import pytest
 import torch
 
-from oracle import kv4
+from oracle import e4m3_decode, kv4, lowbit
 from speculative_drafting_pe_gb300 import binding
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +70,63 @@ def test_large_values_without_weight_next_to_one_that_has_it_all(K, G, hd, S, wi
     floor = 2.0 ** -37 * np.abs(v[:16]).max() if K * G > 16 else 0.0
     lim = 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * size + floor
     assert np.isfinite(got).all() and (np.abs(got - want) <= lim).all()
+
+
+def _clear(k, q, S, reach, part):
+    """Of each row of q [K, G, hd] the entry with the largest score, and whether it stands `part` of `reach`, the
+    largest sum of |q| |k|, above the next: more than scores, queries and keys are rounded by, and by so much that the
+    next has no weight."""
+    best, clear = np.zeros(q.shape[:2], dtype=int), np.zeros(q.shape[:2], dtype=bool)
+    for j in range(len(q)):
+        x = k[:S + j + 1] @ q[j].T
+        best[j] = x.argmax(0)
+        top = np.sort(x, axis=0)[-2:]
+        clear[j] = top[1] - top[0] > part * reach[j]
+    assert clear.mean() > 0.3
+    return best, clear
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("K,G", ROWS)
+@pytest.mark.parametrize("S", [130, 900, 6000])
+@pytest.mark.parametrize("up", [15, 24, 26, 28, 31, 40, 60])
+@pytest.mark.parametrize("spread", [0])
+def test_kv4_scores_far_apart(K, G, hd, S, up, spread):
+    rng = np.random.default_rng(hd + up + S)
+    kk = _store(rng.standard_normal((S + K, hd)))
+    far = np.exp2(rng.integers(-spread, spread + 1, (-(-(S + K) // PAGE), 1, 1))).repeat(PAGE, 1).reshape(-1, 1)[:S + K]
+    vv = _store(rng.standard_normal((S + K, hd)) * far)
+    qx, qt = _bf16(rng.standard_normal((1, K, G, hd)) * 2.0 ** up)
+    (k, ka), (v, va) = _flat(*kk), _flat(*vv)
+    best, clear = _clear(k, qx[0], S, (np.abs(qx[0]) @ ka.T).max(-1), 2.0 ** (-9 if K * G > 16 else -11))
+    got = _attend4(qt, S, kk, vv)
+    want = v[best]
+    lim = 2.0 ** -8 * np.abs(want) + 2.0 ** -9 * va[best]
+    if K * G > 16:
+        lim = lim + 2.0 ** -36 * va.reshape(-1, PAGE, hd).max((1, 2))[best // PAGE][..., None]
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want)[clear] <= lim[clear]).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("K,G", ROWS)
+@pytest.mark.parametrize("S", [130, 900, 6000])
+@pytest.mark.parametrize("up", [15, 24, 26, 28, 31, 40, 60])
+@pytest.mark.parametrize("spread", [0])
+def test_kv8_scores_far_apart(K, G, hd, S, up, spread):
+    rng = np.random.default_rng(hd + up + S)
+    pages = -(-(S + K) // PAGE)
+    codes = [lowbit.e4m3_encode(rng.standard_normal((pages, 1, PAGE, hd))) for _ in range(2)]
+    scale = np.ones((pages, 1), dtype=np.float32)
+    v_scale = np.exp2(rng.integers(-spread, spread + 1, (pages, 1))).astype(np.float32)
+    qx, qt = _bf16(rng.standard_normal((1, K, G, hd)) * 2.0 ** up)
+    k = e4m3_decode(codes[0])[:, 0].reshape(-1, hd)
+    v = (e4m3_decode(codes[1]) * v_scale[..., None, None])[:, 0].reshape(-1, hd)
+    best, clear = _clear(k, qx[0], S, (np.abs(qx[0]) @ np.abs(k).T).max(-1), 2.0 ** -11)
+    dev = [torch.as_tensor(c).cuda() for c in (*codes, scale, v_scale)]
+    out, status = binding.attention_kv8(qt, _i([S]), _i(np.arange(pages)[None]), *dev)
+    assert int(status[0]) == 0
+    got, want = out.double().cpu().numpy()[0], v[best]
+    assert np.isfinite(got).all()
+    # the output's rounding, and the weight's
+    assert (np.abs(got - want)[clear] <= ((2.0 ** -8 + 2.0 ** -10) * np.abs(want))[clear]).all()
