@@ -451,7 +451,7 @@ __device__ __forceinline__ void attend_window(const Kv4Params& p, uint8_t* sm, i
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
-                const float f = md[a][x] == -INFINITY ? 0.f : ex2(m[a][x] - M + md[a][x] - kLift);
+                const float f = unlift(m[a][x], md[a][x], M);
 #pragma unroll
                 for (int j = 0; j < kMt; ++j) {
                     o[j][a][x] *= f;

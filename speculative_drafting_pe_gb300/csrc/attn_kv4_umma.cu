@@ -531,37 +531,43 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                         }
                         __syncwarp();
                     };
-                    // largest score, largest score + exponent of its V
+                    // largest score; largest score + exponent of its V, relative to the larger of m and the scores
                     float top = -INFINITY, most = -INFINITY, kf[4], vl[4];
                     if (!alone) {
                         const float4* sc = reinterpret_cast<const float4*>(page);
                         const float4 ks = sc[0], vlg = sc[1];   // of the pages
                         kf[0] = cs * ks.x; kf[1] = cs * ks.y; kf[2] = cs * ks.z; kf[3] = cs * ks.w;
                         vl[0] = vlg.x; vl[1] = vlg.y; vl[2] = vlg.z; vl[3] = vlg.w;
-                        float s[kTile];
+                        float s[kTile], t[4];
                         tmem_ld64(t_s, s);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const float* sq = s + q * 16;
                             const float a = max3(max3(sq[0], sq[1], sq[2]), max3(sq[3], sq[4], sq[5]), max3(sq[6], sq[7], sq[8]));
                             const float b = max3(max3(sq[9], sq[10], sq[11]), max3(sq[12], sq[13], sq[14]), sq[15]);
-                            const float t = fmaxf(a, b) * kf[q];
-                            top = fmaxf(top, t);
-                            most = fmaxf(most, t + vl[q]);
+                            t[q] = fmaxf(a, b) * kf[q];
+                            top = fmaxf(top, t[q]);
                         }
+                        const float high = fmaxf(top, m);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) most = fmaxf(most, t[q] - high + vl[q]);
                     } else {
+                        float high = m;
 #pragma unroll 1
                         for (int at = 0; at < kTile; at += 16) {
                             float s[16];
                             const float* v;
                             scores(at, s, v);
+                            const float had = high;
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                top = fmaxf(top, s[x]);
-                                most = fmaxf(most, s[x] + v[x * step]);
-                            }
+                            for (int x = 0; x < 16; ++x) top = fmaxf(top, s[x]);
+                            high = fmaxf(high, top);
+                            most += had - high;   // (NaN while a row has seen no entry, and no maximum of what follows)
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) most = fmaxf(most, s[x] - high + v[x * step]);
                         }
                     }
+                    const float high = fmaxf(top, m);
                     if (top > m + kRescale) {
                         l *= m == -INFINITY ? 0.f : ex2(m - top);
                         md += m - top;
@@ -569,7 +575,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     }
                     // 0 in the place of the maximum where a row has seen no entry
                     const float mm = m == -INFINITY ? 0.f : -m;
-                    most += mm;
+                    most += high - m;   // (a row that has seen no entry: NaN, which moves nothing)
                     float f = 1.f;
                     if (most > md + kTall) {
                         f = md == -INFINITY ? 0.f : ex2(md - most - kHead);
@@ -662,8 +668,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
             const float sum = (xa.y <= 0.f ? 0.f : xa.y * fa) + (xb.y <= 0.f ? 0.f : xb.y * fb) + (sum0 <= 0.f ? 0.f : sum0 * f0);
             const bool whole = !early && info.z + len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            const float ga = xa.z == -INFINITY ? 0.f : ex2(xa.x - M + xa.z - kLift) * inv;
-            const float gb = xb.z == -INFINITY ? 0.f : ex2(xb.x - M + xb.z - kLift) * inv;
+            const float ga = unlift(xa.x, xa.z, M) * inv, gb = unlift(xb.x, xb.z, M) * inv;
             __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
                                  static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
             const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;

@@ -139,9 +139,9 @@ __device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, i
         for (int j = 0; j < kMt; ++j)
 #pragma unroll
             for (int a = 0; a < NT; ++a) o[j][a][0] = o[j][a][1] = o[j][a][2] = o[j][a][3] = 0.f;
-        float m[NT][2], l[NT][2], mo[NT][2];
+        float m[NT][2], l[NT][2], md[NT][2];   // maximum of the scores; of their products with V's scale, relative to it
 #pragma unroll
-        for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = mo[a][0] = mo[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
+        for (int a = 0; a < NT; ++a) m[a][0] = m[a][1] = md[a][0] = md[a][1] = -INFINITY, l[a][0] = l[a][1] = 0.f;
 
         if (i < seg + len) {
             // queries: row a * 8 + g, this lane's quarter of the dimensions
@@ -274,7 +274,7 @@ __device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, i
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 4));
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 8));
                         top[a][x] = fmaxf(top[a][x], __shfl_xor_sync(0xffffffffu, top[a][x], 16));
-                        up |= top[a][x] > m[a][x] + kRescale || top[a][x] + vlg > mo[a][x] + kRescale;
+                        up |= top[a][x] > m[a][x] + kRescale || top[a][x] - m[a][x] + vlg > md[a][x] + kRescale;
                     }
                 if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -283,12 +283,14 @@ __device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, i
                         for (int x = 0; x < 2; ++x) {
                             if (top[a][x] > m[a][x] + kRescale) {
                                 l[a][x] *= m[a][x] == -INFINITY ? 0.f : ex2(m[a][x] - top[a][x]);
+                                md[a][x] += m[a][x] - top[a][x];
                                 m[a][x] = top[a][x];
                             }
                             float f = 1.f;
-                            if (top[a][x] + vlg > mo[a][x] + kRescale) {
-                                f = mo[a][x] == -INFINITY ? 0.f : ex2(mo[a][x] - (top[a][x] + vlg));
-                                mo[a][x] = top[a][x] + vlg;
+                            const float most = top[a][x] - m[a][x] + vlg;   // (a row that has seen no entry: NaN)
+                            if (most > md[a][x] + kRescale) {
+                                f = md[a][x] == -INFINITY ? 0.f : ex2(md[a][x] - most);
+                                md[a][x] = most;
                             }
 #pragma unroll
                             for (int j = 0; j < kMt; ++j) {
@@ -303,8 +305,8 @@ __device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, i
                 for (int a = 0; a < NT; ++a) {
                     // 0 in the place of both maxima where a row has seen no entry
                     const float m0 = m[a][0] == -INFINITY ? 0.f : m[a][0], m1 = m[a][1] == -INFINITY ? 0.f : m[a][1];
-                    const float o0 = mo[a][0] == -INFINITY ? 0.f : mo[a][0], o1 = mo[a][1] == -INFINITY ? 0.f : mo[a][1];
-                    const float r0 = vpart * lift(m0 - o0 + kLift, vlg), r1 = vpart * lift(m1 - o1 + kLift, vlg);
+                    const float d0 = md[a][0] == -INFINITY ? 0.f : md[a][0], d1 = md[a][1] == -INFINITY ? 0.f : md[a][1];
+                    const float r0 = vpart * lift(kLift - d0, vlg), r1 = vpart * lift(kLift - d1, vlg);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float w0 = ex2(s[a][2 * h] - m0), w1 = ex2(s[a][2 * h + 1] - m1);
@@ -361,7 +363,7 @@ __device__ __forceinline__ void attend_window(const Kv8Params& p, uint8_t* sm, i
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w * kRows + r].x);
-                const float f = unlift(mo[a][x], M);
+                const float f = unlift(m[a][x], md[a][x], M);
 #pragma unroll
                 for (int j = 0; j < kMt; ++j) {
                     o[j][a][x] *= f;

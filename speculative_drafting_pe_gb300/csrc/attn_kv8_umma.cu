@@ -488,7 +488,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
             const int j = row / G, lim = S + j;
             const int first = seg + ((seg ^ grp) & 1);  // this group's first unit of the segment
             const int count = first < seg + len ? (seg + len - first + 1) / 2 : 0;
-            float m = -INFINITY, mo = -INFINITY, l = 0.f, mark = 0.f, cs = 0.f;
+            float m = -INFINITY, md = -INFINITY, l = 0.f, mark = 0.f, cs = 0.f;
             for (int i = first; i < seg + len; i += 2) {
                 const uint32_t t_s = tmem + lane_off + static_cast<uint32_t>((i % kTurns) * kTile);
                 if (ok) ok = wait(&s_full[i % kTurns], turn(i));
@@ -539,25 +539,29 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
                         }
                     }
                     const float vl[4] = {vlg.x, vlg.y, vlg.z, vlg.w};
-                    float top = -INFINITY, most = -INFINITY;
+                    float top = -INFINITY, most = -INFINITY, t[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float* sq = s + q * 16;
                         float t4[4];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) t4[x] = fmaxf(fmaxf(sq[x], sq[x + 4]), fmaxf(sq[x + 8], sq[x + 12]));
-                        const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q];
-                        top = fmaxf(top, t);
-                        most = fmaxf(most, t + vl[q]);
+                        t[q] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * kf[q];
+                        top = fmaxf(top, t[q]);
                     }
+                    const float high = fmaxf(top, m);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) most = fmaxf(most, t[q] - high + vl[q]);
                     if (top > m + kRescale) {
                         l *= m == -INFINITY ? 0.f : ex2(m - top);
+                        md += m - top;
                         m = top;
                     }
+                    most += high - m;   // (a row that has seen no entry: NaN, which moves nothing)
                     float f = 1.f;
-                    if (most > mo + kRescale) {
-                        f = mo == -INFINITY ? 0.f : ex2(mo - most);
-                        mo = most;
+                    if (most > md + kRescale) {
+                        f = md == -INFINITY ? 0.f : ex2(md - most);
+                        md = most;
                     }
                     if (i > first && __any_sync(0xffffffffu, f != 1.f)) {
                         // this group's last P.V has to be done
@@ -574,10 +578,10 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
                             tmem_st16(t_mine + static_cast<uint32_t>(c * 16), o);
                         }
                     }
+                    // 0 in the place of the maximum where a row has seen no entry
                     const float mm = m == -INFINITY ? 0.f : -m;
                     const uint64_t m2 = f2(mm, mm);
-                    // 0 in the place of both maxima where a row has seen no entry
-                    const float from = (mo == -INFINITY ? 0.f : -mo) - mm + kLift;
+                    const float from = kLift - (md == -INFINITY ? 0.f : md);
                     const float vr[4] = {vpart.x * lift(from, vl[0]), vpart.y * lift(from, vl[1]),
                                          vpart.z * lift(from, vl[2]), vpart.w * lift(from, vl[3])};
                     uint64_t sum[2] = {0ull, 0ull};
@@ -612,7 +616,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
             const bool early = FIRST ? info.z > 0 : seg == 0 && win->early, carry = !FIRST && seg == 0 && win->carry && row < R;
             float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (early ? 0 : 1)) * part_floats(kRows, HD);
             const float M0 = carry ? part[kRows * HD + row] : -INFINITY, sum0 = carry ? part[kRows * HD + kRows + row] : 0.f;
-            s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, mo, 0.f);
+            s_ex[grp * kRows + row] = make_float4(m, mark != 0.f ? mark : l, md, 0.f);
             named_bar_sync(1, kSoft);
             const float4 xa = s_ex[row], xb = s_ex[kRows + row];
             const float bad = fminf(fminf(fminf(xa.y, xb.y), sum0), 0.f);   // a NaN sum is not less than 0
@@ -621,7 +625,7 @@ __device__ __forceinline__ bool attend_window(const CUtensorMap& tmK, const Kv8P
             const float sum = (xa.y <= 0.f ? 0.f : xa.y * fa) + (xb.y <= 0.f ? 0.f : xb.y * fb) + (sum0 <= 0.f ? 0.f : sum0 * f0);
             const bool whole = !early && info.z + len == info.w;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-            const float ga = unlift(xa.z, M) * inv, gb = unlift(xb.z, M) * inv;
+            const float ga = unlift(xa.x, xa.z, M) * inv, gb = unlift(xb.x, xb.z, M) * inv;
             __nv_bfloat16* out = p.out + (static_cast<long long>(b) * p.K + j) * p.ld_out +
                                  static_cast<long long>(head * G + row - j * G) * HD + grp * (HD / 2);
             const bool sectors = ((reinterpret_cast<uintptr_t>(p.out) | static_cast<uintptr_t>(p.ld_out) * 2) & 31u) == 0;

@@ -77,12 +77,13 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // Weights meet V as fp16. What a row sums up is w * scale of v, and the scales
 // of V's pages may lie far apart, so next to the scores' running maximum m a
-// row has one of its contributions, mo, the maximum of score + log2(scale) over
-// the pages, and the fp16 weights are w * scale * 2^(m - mo + kLift): the
+// row has one of its contributions, md, the maximum of score - m + log2(scale)
+// over the pages, and the fp16 weights are w * scale * 2^(kLift - md): the
 // largest one stands between 2^kLift and 2^(kLift + kRescale + 2), and what
 // falls below fp16's normal range, 2^-14, is 2^-19 of it at most. (Taken
 // relative to the largest scale alone, a page of values below 2^-14 of the
-// largest lost its bits even where it had all the weight.)
+// largest lost its bits even where it had all the weight; as a maximum of
+// score + log2(scale), scores of 2^25 and more lost the scale beside them.)
 constexpr float kLift = 5.f;
 // v = part * 2^lg exactly, |part| in [1, 2) for scales of 2^-104 to 2^127 (a
 // smaller one is a smaller part, so that 2^-lg and what is summed stay normal)
@@ -91,11 +92,11 @@ __device__ __forceinline__ void split_scale(float v, float& part, float& lg) {
     part = v * __uint_as_float((254u - e) << 23);
     lg = static_cast<float>(static_cast<int>(e) - 127);
 }
-// what scales a weight 2^(score - m) by, next to `part`; from: m - mo + kLift.
+// what scales a weight 2^(score - m) by, next to `part`; from: kLift - md.
 // Never an infinity, which would meet weights of 0
 __device__ __forceinline__ float lift(float from, float lg) { return ex2(fminf(from + lg, 127.f)); }
 // a sum of such products back to the values that belong to M
-__device__ __forceinline__ float unlift(float mo, float M) { return mo == -INFINITY ? 0.f : ex2(mo - M - kLift); }
+__device__ __forceinline__ float unlift(float m, float md, float M) { return md == -INFINITY ? 0.f : ex2(m - M + md - kLift); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);

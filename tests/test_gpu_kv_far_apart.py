@@ -90,7 +90,7 @@ def _clear(k, q, S, reach, part):
 @pytest.mark.parametrize("K,G", ROWS)
 @pytest.mark.parametrize("S", [130, 900, 6000])
 @pytest.mark.parametrize("up", [15, 24, 26, 28, 31, 40, 60])
-@pytest.mark.parametrize("spread", [0])
+@pytest.mark.parametrize("spread", [0, 24])
 def test_kv4_scores_far_apart(K, G, hd, S, up, spread):
     rng = np.random.default_rng(hd + up + S)
     kk = _store(rng.standard_normal((S + K, hd)))
@@ -112,7 +112,7 @@ def test_kv4_scores_far_apart(K, G, hd, S, up, spread):
 @pytest.mark.parametrize("K,G", ROWS)
 @pytest.mark.parametrize("S", [130, 900, 6000])
 @pytest.mark.parametrize("up", [15, 24, 26, 28, 31, 40, 60])
-@pytest.mark.parametrize("spread", [0])
+@pytest.mark.parametrize("spread", [0, 24])
 def test_kv8_scores_far_apart(K, G, hd, S, up, spread):
     rng = np.random.default_rng(hd + up + S)
     pages = -(-(S + K) // PAGE)
