@@ -497,7 +497,7 @@ int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_head
  * Rounded to fewer than 32 bits, besides the output: the queries, to fp16 under a
  * power of two of their row (a value is off by 2^-25 of its row's largest at
  * most), and the weights times V's scale, to fp16 relative to the row's largest
- * such product (2^-11 of each; small ones by 2^-25 of the largest). With more than
+ * such product (2^-11 of each; small ones by 2^-26 of the largest). With more than
  * 16 rows for a kv head, K * (nq/nkv), also K and V, to fp16 under a power of two
  * of their page where every row sees the unit of 64 entries that it stands in:
  * 2^-11 of a value of K, 2^-10 of scale |n - 8| + |base + 8 scale| for V, and

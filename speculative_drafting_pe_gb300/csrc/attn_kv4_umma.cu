@@ -69,8 +69,10 @@ constexpr int kWarpConv = 8, kWarpS = 16, kWarpPv = 17, kWarpFetch = 18;   // (a
 constexpr int kScales = 16;                 // units whose factors are kept: written with K kTurns ahead at most, read a few behind
 constexpr int kScaleRec = 2 * kUnitPages;   // floats of a unit's
 // A row's largest contribution stands at 2^(kLift - kHead) in fp16 when it is
-// taken as the reference, which moves once one stands kTall above it.
-constexpr float kHead = 5.f, kTall = 10.f;
+// taken as the reference, which moves once one stands kRescale above it: by 2^12
+// at least. (Moves by 2^15, from 10 above with a head of 5: 212 us for 215 at B=128
+// K=11, 97.5 for 99 with 64-wide heads, and small products lose a bit.)
+constexpr float kHead = 4.f;
 constexpr int kCsTurns = 8;                 // segments whose row factors are kept: the converters run fewer ahead
 
 template <int HD>
@@ -577,7 +579,7 @@ __device__ __forceinline__ bool attend_window(const Kv4Params& p, uint8_t* sm, i
                     const float mm = m == -INFINITY ? 0.f : -m;
                     most += high - m;   // (a row that has seen no entry: NaN, which moves nothing)
                     float f = 1.f;
-                    if (most > md + kTall) {
+                    if (most > md + kRescale) {
                         f = md == -INFINITY ? 0.f : ex2(md - most - kHead);
                         md = most + kHead;
                     }

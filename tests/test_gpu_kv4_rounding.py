@@ -128,3 +128,38 @@ def test_the_bound_notices_one_percent(K, G, hd, what):
     for (want, lim), (off, _) in zip(_wants(case, lens, hd), _wants(wrong, lens, hd, scale)):
         off = kv4.bf16(off)
         assert (np.abs(off - want) > lim).mean() > 0.02
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,G,hd", [(1, 8, 128), (2, 8, 64), (11, 8, 64), (11, 8, 128)])
+def test_products_far_below_the_largest(K, G, hd):
+    """Two entries have nearly all of the weight and no V in half of the dimensions, where 598 others of 2^-25.4 each
+    make the output: small products are off by 2^-26 of the row's largest at most (a register kernel's by 2^-30)."""
+    B, S = 1500, 599
+    entries = 608
+    at = np.arange(entries)
+    heavy = (at == 0) | (at == UNIT)                  # one for either softmax group
+    # scores in base 2: k is one value throughout, q picks a dimension of it
+    kp = np.zeros((entries // PAGE, 1, PAGE, 2))
+    kp[..., 1] = np.where(heavy, 0.0, -25.375).reshape(-1, 1, PAGE)
+    vp, code = np.zeros_like(kp), np.zeros((entries, hd), dtype=np.uint8)
+    vp[..., 0] = kv4.bf16(np.where(heavy, 1 / 15, 0.0)).reshape(-1, 1, PAGE)
+    vp[..., 1] = np.where(heavy, 0.0, 1.0).reshape(-1, 1, PAGE)
+    code[heavy, :hd // 2] = 15
+    codes = kv4.pack(code).reshape(entries // PAGE, 1, PAGE, hd // 2)
+    q = torch.zeros(B, K, G, hd, dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = 1.0
+    dev = [torch.as_tensor(np.zeros_like(codes)).cuda(), torch.as_tensor(codes).cuda()]
+    dev += [torch.as_tensor(p).to(torch.bfloat16).cuda() for p in (kp, vp)]
+    table = torch.arange(entries // PAGE, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    # the last row sees all: entries 0 .. S + j
+    lens = torch.full((B,), S - K + 1, dtype=torch.int32, device="cuda")
+    out, status = binding.attention_kv4(q, lens, table, *dev, scale=float(np.log(2.0)))
+    assert (status == 0).all()
+    got = out.double().cpu().numpy()
+    for j in range(K):
+        small = S - K + 1 + j + 1 - 2
+        want = small * 2.0 ** -25.375 / (2 + small * 2.0 ** -25.375)
+        part = 2.0 ** -26 if K * G > 16 else 2.0 ** -30
+        lim = 2.0 ** -8 * want + 2.0 ** -11 * want + small * part / 2 + 2.0 ** -40
+        assert (np.abs(got[:, j, :, hd // 2:] - want) <= lim).all(), (got[:, j, :, hd // 2:].min(), want)
