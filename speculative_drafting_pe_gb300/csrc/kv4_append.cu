@@ -10,9 +10,10 @@
 // written does not depend on how the rows came in calls.
 //
 // The angle is p times a frequency that is held as a fraction of a turn in 64
-// bits: the product's lower half is the turn's remainder for every position,
-// without a double on the device (FP64 runs at a few operations a cycle and
-// SM). Its first 24 bits go through sincospif, the rest is a first-order term.
+// bits (rotation.h): the product's lower half is the turn's remainder for every
+// position, to 2^-34 of a turn, without a double on the device (FP64 runs at a
+// few operations a cycle and SM). Its first 24 bits go through sincospif, the
+// rest is a first-order term.
 //
 // A CTA takes `block` rows of one request, a warp two heads of a row at a time
 // (four 64-wide ones). A lane has four dimensions of the lower half of a head
@@ -29,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include "lowbit.cuh"
+#include "rotation.h"
 
 namespace pe {
 namespace {
@@ -249,17 +251,13 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
     }
 }
 
-// Turns per position of pair i, theta^(-2i/hd) / 2 pi, in 2^-64. The powers are
-// kept for the calls that follow with the same base and width.
+// The frequencies of a base and width, kept for the calls that follow with the same.
 const unsigned long long* frequencies(float theta, int hd) {
     static thread_local float had_theta = 0.f;
     static thread_local int had_hd = 0;
     static thread_local unsigned long long freq[64];
     if (had_theta != theta || had_hd != hd) {
-        for (int i = 0; i < hd / 2; ++i) {
-            const double turns = std::pow(static_cast<double>(theta), -2.0 * i / hd) * 0.15915494309189533577;
-            freq[i] = static_cast<unsigned long long>(std::ldexp(turns, 64));
-        }
+        rotation_turns(theta, hd, freq);
         had_theta = theta;
         had_hd = hd;
     }
