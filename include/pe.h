@@ -470,11 +470,12 @@ int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  *          the turned queries; zero past rows[b] and in requests that are not OK
  *  status  [B] OUT; a request that is not OK writes nothing else.
  *          PE_REQ_BAD_INPUT: a length or position below 0 or rows[b] above n_max
- * Of the values x of a head of a row: base = bf16(min x), scale = bf16((max x -
- * base) / 15), n the nearest (ties to even) to (x - base) / scale in 0..15, 0
+ * Of the values x of a head of a row: base = bf16(min x), scale = bf16(max(max x -
+ * base, 0) / 15), n the nearest (ties to even) to (x - base) / scale in 0..15, 0
  * where scale is 0. A turned key is not rounded before. Angles are off by 2^-33
  * of a turn at most at every position, sines and cosines are fp32. A head of a row that holds an infinity or
- * NaN, or magnitudes beyond 2^126, stands as NaN (scale and base). An entry
+ * NaN, or whose largest value and base lie 2^128 or more apart, stands as NaN
+ * (scale and base). An entry
  * depends on its row alone; nothing else of the cache is touched. Requests whose
  * new entries are the same places of the cache race. q_out over q has q's row
  * stride; otherwise no output shares memory with an input.

@@ -38,7 +38,7 @@ def quantise(x):
     whole = np.isfinite(x).all(-1)
     y = np.where(whole[..., None], x, 0.0)
     base = bf16(y.min(-1))
-    scale = bf16((y.max(-1) - base) / 15)
+    scale = bf16(np.maximum(y.max(-1) - base, 0) / 15)
     part = (y - base[..., None]) / np.where(scale > 0, scale, 1.0)[..., None]
     part = np.where((scale > 0)[..., None], part, 0.0)
     codes = np.clip(np.rint(part), 0, 15).astype(np.uint8)

@@ -3,7 +3,7 @@
 // a scale and a base for each (entry, kv head), queries go back in bf16.
 //
 //   (a_i, b_i) = (x_i, x_{i+hd/2}) -> (a cos - b sin, b cos + a sin), angle p * theta^(-2i/hd)
-//   base = bf16(min x), scale = bf16((max x - base) / 15), code = rn((x - base) / scale) in 0..15
+//   base = bf16(min x), scale = bf16(max(max x - base, 0) / 15), code = rn((x - base) / scale) in 0..15
 //
 // over the values x of one head of one row. An entry's codes depend on its row
 // alone, so an append never touches an entry that is there, and what is
@@ -225,10 +225,12 @@ __global__ void __launch_bounds__(kThreads) k_kv4_append(const __grid_constant__
         if (it.head >= p.nkv) continue;
         uint32_t par = pack_bf16(0.f, lo);
         const float base = __uint_as_float(par & 0xFFFF0000u);
-        par |= pack_bf16((hi - base) / 15.f, 0.f);
+        // (base may be rounded up past the largest value: the entry is one value throughout)
+        const float range = hi - base;
+        par |= pack_bf16(fmaxf(range, 0.f) / 15.f, 0.f);
         const float scale = __uint_as_float(par << 16);
         uint32_t code[2] = {0u, 0u};
-        if (((who >> (sub * kLanes)) & ((1u << kLanes) - 1u)) != 0u || !(scale < INFINITY)) {
+        if (((who >> (sub * kLanes)) & ((1u << kLanes) - 1u)) != 0u || !(fabsf(range) < INFINITY)) {
             par = 0x7FC07FC0u;   // the entry is NaN
         } else if (scale >= 0x1p-100f) {
             // the quotient with its rounding error put right, as a division has it

@@ -1,4 +1,4 @@
-"""The rotation of pe_kv4_append to the last bits of its angles."""
+"""The rotation of pe_kv4_append to the last bits of its angles, and keys whose turned values all but agree."""
 
 from decimal import Decimal, getcontext
 
@@ -65,3 +65,44 @@ def test_angles_of_far_positions(theta, hd, position):
     size = np.tile(np.abs(ab).sum(1), 2)
     lim = size * (1.5 * 2.0 ** -24 + 2 * np.pi * 2.0 ** -32) + 2.0 ** -25 + 2.0 ** -8 * np.abs(want)
     assert (np.abs(got - want) <= lim).all(), ((np.abs(got - want) / lim).max(), (np.abs(got - want) / lim).argmax())
+
+
+def _agreeing(theta, hd):
+    """A position and bf16 a, b whose turned values, the same for every pair at a base of 1, lie between two bf16
+    values, nearer to the upper one."""
+    for position in range(1, 4000):
+        c, s = np.cos(float(position)), np.sin(float(position))
+        a = np.arange(128, 256)[:, None] / 128.0
+        b = kv4.bf16(a * (c - s) / (c + s))              # both would be a / (cos + sin)
+        x, y = a * c - b * s, b * c + a * s
+        lo, hi = np.minimum(x, y), np.maximum(x, y)
+        at = np.argwhere((kv4.bf16(lo) > hi + 1e-5 * np.abs(hi)) & (lo > 0.1))
+        if len(at):
+            i = at[0][0]
+            return position, float(a[i, 0]), float(b[i, 0]), float(kv4.bf16(lo[i])[0])
+    raise AssertionError("none found")
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_a_scale_is_never_negative(hd):
+    """All values of a key below the bf16 value that their smallest rounds to: the scale is 0, not below it."""
+    position, a, b, base = _agreeing(1.0, hd)
+    k = np.concatenate([np.full(hd // 2, a), np.full(hd // 2, b)])[None, None, None]
+    _, codes, params = _append(None, k, 1.0, position)
+    np.testing.assert_array_equal(params[0, 0, 0], [0.0, base])
+    assert not codes[0, 0, 0].any()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_the_largest_magnitudes(hd):
+    """What lies farther apart than fp32 holds stands as NaN, one value throughout as it is."""
+    k = np.full((1, 1, 4, hd), 2.0 ** 127)
+    k[0, 0, 1] *= -1
+    k[0, 0, 2, ::2] *= -1                              # 2^128 apart
+    k[0, 0, 3, ::2] *= -0.5
+    _, codes, params = _append(None, k, 0.0, 0)
+    got = params[0, :, 0]
+    np.testing.assert_array_equal(got[:2], [[0.0, 2.0 ** 127], [0.0, -2.0 ** 127]])
+    assert np.isnan(got[2]).all()
+    assert got[3, 1] == -2.0 ** 126 and got[3, 0] == kv4.bf16(1.5 * 2.0 ** 127 / 15)
+    assert not codes[0, :2, 0].any() and (kv4.unpack(codes[0, 3, 0]) == np.where(np.arange(hd) % 2, 15, 0)).all()
