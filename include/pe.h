@@ -494,7 +494,9 @@ int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_head
  * Entries that no row sees may hold anything. An entry whose parameters are not
  * finite makes the rows that see it NaN, and no other row; one that a row does
  * not see does not move it, whatever its size. A row of q that holds an infinity
- * or a NaN is NaN. Scales are not negative and below 2^124, values below 2^127.
+ * or a NaN is NaN. Scales are not negative, and values of V times the entries that
+ * a row sees stay below 2^119: sums are of weights up to 2^8. Scores may be of any
+ * size that fp32 holds. Below 2^-104 scales of V have fewer bits in the products.
  * Rounded to fewer than 32 bits, besides the output: the queries, to fp16 under a
  * power of two of their row (a value is off by 2^-25 of its row's largest at
  * most), and the weights times V's scale, to fp16 relative to the row's largest

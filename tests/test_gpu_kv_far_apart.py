@@ -130,3 +130,18 @@ def test_kv8_scores_far_apart(K, G, hd, S, up, spread):
     assert np.isfinite(got).all()
     # the output's rounding, and the weight's
     assert (np.abs(got - want)[clear] <= ((2.0 ** -8 + 2.0 ** -10) * np.abs(want))[clear]).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("K,G", ROWS)
+@pytest.mark.parametrize("S", [60, 600, 6000])
+@pytest.mark.parametrize("power", [-100, -60, 60, 104])
+def test_kv4_values_times_a_power_of_two(K, G, hd, S, power):
+    """Outputs follow V's power of two, to the ends of the range that the header gives (6000 values below 2^106)."""
+    rng = np.random.default_rng(hd + S)
+    kk, vv = _store(rng.standard_normal((S + K, hd))), _store(rng.standard_normal((S + K, hd)))
+    qt = _bf16(2.0 * rng.standard_normal((1, K, G, hd)))[1]
+    plain = _attend4(qt, S, kk, vv)
+    moved = _attend4(qt, S, kk, (vv[0], np.ldexp(vv[1], power)))
+    # a step of the output apart at most, where reference points fall on either side of a rounding; fp16 products
+    assert (np.abs(np.ldexp(moved, -power) - plain) <= 2.0 ** -7 * np.abs(plain) + 2.0 ** -11).all()
