@@ -473,12 +473,12 @@ int pe_attention_kv8(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  * Of the values x of a head of a row: base = bf16(min x), scale = bf16(max(max x -
  * base, 0) / 15), n the nearest (ties to even) to (x - base) / scale in 0..15, 0
  * where scale is 0. A turned key is not rounded before. Angles are off by 2^-33
- * of a turn at most at every position, sines and cosines are fp32. A head of a row that holds an infinity or
- * NaN, or whose largest value and base lie 2^128 or more apart, stands as NaN
- * (scale and base). An entry
- * depends on its row alone; nothing else of the cache is touched. Requests whose
- * new entries are the same places of the cache race. q_out over q has q's row
- * stride; otherwise no output shares memory with an input.
+ * of a turn at most at every position, sines and cosines are fp32. A head of a
+ * row that holds an infinity or NaN, or whose largest value and base lie 2^128 or
+ * more apart, stands as NaN (scale and base). An entry depends on its row alone;
+ * nothing else of the cache is touched. Requests whose new entries are the same
+ * places of the cache race. q_out over q has q's row stride; otherwise no output
+ * shares memory with an input.
  * q, k, v and q_out 8-byte aligned, their strides multiples of 4, the cache's
  * arrays 16-byte aligned. */
 int pe_kv4_append(int32_t B, int32_t n_max, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const void* q,
@@ -528,7 +528,8 @@ int pe_attention_kv4(int32_t B, int32_t K, int32_t n_q_heads, int32_t n_kv_heads
  * or only -inf, has no probabilities: NaN in the place of each, NaN logits
  * ordered behind all others. The temperature lies in 2^-63 .. 2^64, R and V are 2^30 at most; a finite
  * logit over it has a magnitude up to 2^120, or the logit is -FLT_MAX. Sums in
- * fp32, each weight off by about 2^-21 of itself. */
+ * fp32, each weight off by about 2^-21 of itself. No output shares memory with an
+ * input. */
 int pe_token_logprobs(int32_t R, int32_t V, int32_t dtype, const void* logits, int64_t ld, const int32_t* tokens,
                       float temperature, float* logprobs, float* entropy, int32_t top, int32_t* top_tokens,
                       float* top_logprobs, void* stream);

@@ -24,10 +24,12 @@
 // masks of `widen` leave (Q's fragments follow that order), and its transposed
 // form four dimensions of two V rows in the two halves of a word, which is what
 // a fragment of V^T wants. P^T comes out of S^T's layout by 8x8 transposes.
-// Issue slots bound it (58% of them go, ALU 54%): widening is 288 of some 900
-// instructions of a unit's warp. 64 single tokens over 512..8192 entries, 32/4
-// heads of 128: 50.5 us, 2.4 TB/s; one of 131072 entries 29. 16 warps of 128
-// registers instead: 56 and 31.
+// What bounds it is instructions and their latency: some 900 for a unit's warp,
+// 288 of them widening, of three warps a scheduler, which issue one in 54% of the
+// cycles (ALU 49%). 64 single tokens over 512..8192 entries, 32/4 heads of 128:
+// 50.4 us, 2.4 TB/s; one of 131072 entries 29; 64 single tokens over 1024..4096,
+// 64/8 heads of 64: 47. 16 warps of 128 registers instead: 56 and 31 of the first
+// two.
 // Queries enter as fp16 after an exact shift by a power of two per row;
 // weights times V's scale go to fp16 (2^-11) relative to the row's largest such
 // product so far (kLift).

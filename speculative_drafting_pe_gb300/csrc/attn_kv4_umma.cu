@@ -27,12 +27,14 @@
 //               and output accumulator of its own; they meet at the end of a
 //               segment.
 // What bounds it is the instructions' supply more than any pipe: five roles'
-// loops share the instruction cache and 54% of the issue slots go. So only the
+// loops share the instruction cache and 51% of the issue slots go. So only the
 // two innermost loops are unrolled (the whole kernel unrolled: 333 us for 244 at
 // B=128 K=11, 512..8192 entries, 32/4 heads of 128; those two: 210 for 219), and
 // shared memory is addressed as such, not by generic pointers (222 for 248).
-// Eight converter warps for four: 244 for 270. Now 208 us; 64 requests of 10
-// rows, 64/8 heads of 64, 1024..4096 entries: 96. At 225 and 103 it took
+// Eight converter warps for four: 244 for 270. Now 215 us; 64 requests of 10
+// rows, 64/8 heads of 64, 1024..4096 entries: 99 (208 and 96 before large scores
+// were rounded, contributions kept relative to them, and small products kept a bit
+// more: about a third of it each). At 225 and 103 it took
 // without the widening 187 and 93, without the softmax 183 and 70, without both
 // 149 and 67: the hand-over of a unit between the roles. Scores of a unit in one
 // pass with weights from the old maximum: 229 for 219 (a third of the units has a

@@ -51,7 +51,7 @@
 // then, 128-wide ones 250 for 190), a third softmax group for 64-wide heads
 // (100 for 87) and scores of two units in one product (242 for 235) did not
 // help. 128 requests of 512 to 8192 entries, 11 rows of 8 heads to each of 4
-// of 128: 181 us, 3.3 TB/s, 49% of the measured copy; 64 of 1024 to 4096, up
+// of 128: 182 us, 3.3 TB/s, 49% of the measured copy; 64 of 1024 to 4096, up
 // to 10 rows of 8 heads to each of 8 of 64: 81 us, 29%.
 #include "attn_kv8.cuh"
 #include "attn_umma_line.cuh"

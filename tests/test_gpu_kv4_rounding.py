@@ -163,3 +163,19 @@ def test_products_far_below_the_largest(K, G, hd):
         part = 2.0 ** -26 if K * G > 16 else 2.0 ** -30
         lim = 2.0 ** -8 * want + 2.0 ** -11 * want + small * part / 2 + 2.0 ** -40
         assert (np.abs(got[:, j, :, hd // 2:] - want) <= lim).all(), (got[:, j, :, hd // 2:].min(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,G,hd", [(1, 8, 128), (2, 8, 128), (1, 8, 64), (11, 8, 64), (11, 8, 128)])
+def test_outputs_do_not_change_from_call_to_call(K, G, hd):
+    """Nor with what scratch held before: whatever part of a head a block has, its sums are joined in one order."""
+    lens = [2000, 3, 900, 15, 4100]
+    qt, table, _, k, v = _case(K, G, hd, 2, lens, 2)
+    dev = [torch.as_tensor(c).cuda() for c in (k[0], v[0])] + [torch.as_tensor(p).to(torch.bfloat16).cuda() for p in (k[1], v[1])]
+    args = (qt.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.as_tensor(table).cuda(), *dev)
+    first, _ = binding.attention_kv4(*args)
+    for fill in (float("nan"), 0.0, -1.0, 1e30):
+        junk = [torch.full((n,), fill, device="cuda") for n in (1 << 10, 1 << 16, 1 << 21, 6000000)]
+        del junk
+        again, _ = binding.attention_kv4(*args)
+        assert torch.equal(first, again)
